@@ -41,6 +41,8 @@
  *      PA_DEV_OVERFLOW    the plan needs more split partials than the workspace
  *                         holds (only if seq_lens exceed max_seq_len); every row is 0
  *      PA_DEV_TIMEOUT     a bounded wait inside a kernel gave up (never expected)
+ *      PA_DEV_NO_PAGES    pa_block_tables ran out of free pages; the requests
+ *                         that got none have no slots
  *      PA_DEV_INTERNAL    a kernel found its launch set-up unusable (its shared
  *                         memory window not 1024-byte aligned) and wrote
  *                         nothing (never expected)
@@ -86,6 +88,7 @@ typedef enum {
 #define PA_DEV_OVERFLOW 0x10u
 #define PA_DEV_TIMEOUT 0x20u
 #define PA_DEV_INTERNAL 0x40u
+#define PA_DEV_NO_PAGES 0x80u
 
 /*
  * pa_forward -- unified paged attention over a mixed batch.
@@ -410,6 +413,155 @@ pa_status pa_cache_write(const void *k_new, const void *v_new, void *k_cache,
                          pa_kv_layout kv_layout);
 
 /*
+ * pa_forward_shared_prefix -- pa_forward for a batch whose requests share long
+ * prefixes: requests on one system prompt or document, or samples of one
+ * prompt.  The requests of a group see the same first prefix_lens[g]
+ * positions, held once in the cache; their keys and values are read once for
+ * 256 query rows of the group (a row: one token x one query head) instead of
+ * once for every request.  The result is that of pa_forward on the same
+ * contexts, up to rounding.
+ *
+ *  q, k_cache, v_cache, seq_lens, query_start_loc, num_heads, num_kv_heads,
+ *  head_dim, block_size, scale, out, dtype, max_seq_len: as for pa_forward.
+ *  seq_lens count the shared positions too.
+ *  group_start_loc [num_groups + 1] int32: group g is the requests
+ *                  group_start_loc[g] .. group_start_loc[g + 1] - 1;
+ *                  group_start_loc[0] = 0, non-decreasing, ends at num_seqs
+ *  prefix_lens     [num_groups] int32: shared positions of each group, a
+ *                  multiple of block_size (whole pages; 0: the group shares
+ *                  nothing).  Every request's new tokens lie behind them:
+ *                  seq_len - q_len >= prefix_len
+ *  block_table     [num_seqs, max_blocks_per_seq]: the shared pages are read
+ *                  from the row of the group's first request; the other rows'
+ *                  first prefix_len / block_size entries are never read
+ *  max_prefix_len  host-known bound on prefix_lens
+ *  options         sinks, kv_layout and max_query_len as for pa_forward_ex (a
+ *                  max_query_len of 1 spares the tile launch; it does not
+ *                  require num_tokens == num_seqs here); a sliding window or
+ *                  ALiBi is PA_ERR_UNSUPPORTED.  NULL: none
+ *  workspace       device memory of the caller, 256-byte aligned, at least
+ *                  pa_forward_shared_prefix_workspace_bytes() for the same
+ *                  extents, for this call alone until its kernels have run:
+ *                  calls on several streams, or several captured graphs, that
+ *                  may overlap need one each.  Its contents need not be set
+ *
+ * Bad device metadata: as for pa_forward; besides,
+ *   PA_DEV_BAD_QSL     also for a bad group_start_loc: every row is 0
+ *   PA_DEV_BAD_SEQLEN  also for a prefix_len that is negative, above
+ *                      max_prefix_len, no multiple of block_size or longer
+ *                      than a block-table row (the group's rows are 0), and
+ *                      for a request whose new tokens begin inside its
+ *                      group's prefix (its rows are 0)
+ * Errors: as for pa_forward; PA_ERR_INVALID_ARG also for num_tokens > 0 with
+ * no group, or a workspace that is not 256-byte aligned; PA_ERR_WORKSPACE when
+ * the workspace is NULL or too small, or when the first call on a device is
+ * made during capture.  num_tokens == 0 launches nothing.
+ */
+pa_status pa_forward_shared_prefix(
+    const void *q, const void *k_cache, const void *v_cache,
+    const int32_t *block_table, const int32_t *seq_lens,
+    const int32_t *query_start_loc, const int32_t *group_start_loc,
+    const int32_t *prefix_lens, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, void *out, void *stream, pa_dtype dtype,
+    int num_seqs, int num_groups, int num_tokens, int max_blocks_per_seq,
+    int num_blocks, int max_seq_len, int max_prefix_len,
+    const pa_forward_options *options, void *workspace,
+    size_t workspace_bytes);
+
+/* Workspace bytes pa_forward_shared_prefix needs for these host-known extents
+ * (0 for extents it refuses as PA_ERR_INVALID_ARG). */
+size_t pa_forward_shared_prefix_workspace_bytes(pa_dtype dtype, int num_seqs,
+                                                int num_groups, int num_tokens,
+                                                int num_heads, int num_kv_heads,
+                                                int head_dim, int max_seq_len);
+
+/*
+ * pa_block_tables -- a step's block-table rows and slot map, built on the
+ * device from the request lengths: request s, with q_s = qsl[s+1] - qsl[s] new
+ * tokens among its seq_lens[s] positions, holds ceil((seq_len - q_s) /
+ * block_size) pages and takes the pages it lacks from a list of free ones, in
+ * request order; every new token gets the cache slot of its position,
+ *   slot = block_table[s][pos / block_size] * block_size + pos % block_size,
+ *   pos = seq_lens[s] - q_s + i.
+ *
+ *  seq_lens        [num_seqs] int32, the new tokens included
+ *  query_start_loc [num_seqs + 1] int32, qsl[0] = 0, non-decreasing,
+ *                  qsl[num_seqs] <= num_tokens: token rows behind the last
+ *                  request (a batch padded to a captured size) get slot -1
+ *  free_pages      [num_free] int32 page ids; may be NULL when num_free is 0
+ *  free_start      device pointer to one int32: the index of the first page
+ *                  not yet taken.  NULL: the block table is complete already,
+ *                  no page is taken and only the slots are made (free_end and
+ *                  free_pages NULL, num_free 0 then)
+ *  free_end        device pointer to one int32, written: free_start plus the
+ *                  pages taken, which is the next step's free_start.  It must
+ *                  be another word than free_start (a chain of steps
+ *                  alternates two)
+ *  block_table     [num_seqs, max_blocks_per_seq] int32: entries of pages
+ *                  taken are written, all others left as they are
+ *  slot_mapping    [num_tokens] int64, fully written: -1 for a token that has
+ *                  no slot
+ *  positions       [num_tokens] int32, fully written, or NULL: each token's
+ *                  pos (0 for padded rows and requests with bad metadata)
+ *  block_size >= 1; num_seqs <= 16384 (PA_ERR_UNSUPPORTED above)
+ *
+ * When the free pages run out, requests are served in order up to the first
+ * whose pages are not all there; it and the later ones that need pages take
+ * none: PA_DEV_NO_PAGES, their slots are -1 and their rows unchanged.
+ * Requests that need no page are always served.  Other bad metadata:
+ *   PA_DEV_BAD_QSL     bad query_start_loc: no page taken, every slot -1
+ *   PA_DEV_BAD_QLEN / PA_DEV_BAD_SEQLEN  q_s > seq_len / seq_len < 0 or beyond
+ *                      max_blocks_per_seq pages: that request takes no page,
+ *                      its slots are -1
+ *   PA_DEV_BAD_BLOCK   a page id outside [0, num_blocks): its tokens' slots
+ *                      are -1, and a table entry to be written becomes -1
+ *                      (the page counts as taken)
+ * Asynchronous on `stream`, one launch, no workspace; capturable after the
+ * first call on a device.  Errors: PA_ERR_INVALID_ARG for null pointers with
+ * nonzero sizes, negative sizes, misaligned pointers (to their element size)
+ * or free_end == free_start; PA_ERR_CUDA when the launch fails.
+ */
+pa_status pa_block_tables(const int32_t *seq_lens,
+                          const int32_t *query_start_loc,
+                          const int32_t *free_pages, const int32_t *free_start,
+                          int32_t *free_end, int32_t *block_table,
+                          int64_t *slot_mapping, int32_t *positions,
+                          int block_size, void *stream, int num_seqs,
+                          int num_tokens, int max_blocks_per_seq,
+                          int num_blocks, int num_free);
+
+/*
+ * pa_cache_write_slots -- the paged KV-cache write by a slot map (as
+ * pa_block_tables makes it): token t's K and V rows are copied, bit for bit,
+ * to slot slot_mapping[t] % block_size of page slot_mapping[t] / block_size.
+ *
+ *  k_new, v_new     [num_tokens, num_kv_heads, head_dim] dtype, the heads of a
+ *                   token contiguous, consecutive tokens k_token_stride /
+ *                   v_token_stride elements apart (slices of a fused
+ *                   projection; 0 repeats one row)
+ *  k_cache, v_cache as for pa_cache_write, written in place
+ *  slot_mapping     [num_tokens] int64; a negative slot skips its token.  The
+ *                   slots of one call must differ from one another: a slot
+ *                   named twice ends up with either row's values, 16 bytes
+ *                   by 16 bytes
+ *  head_dim x element size and the strides x element size multiples of 16
+ *  bytes, num_kv_heads x head_dim at most 2^26 (PA_ERR_UNSUPPORTED otherwise);
+ *  any block_size >= 1
+ *
+ * A slot of num_blocks x block_size or more sets PA_DEV_BAD_BLOCK and its
+ * token is not written.  Asynchronous on `stream`, one launch, no workspace;
+ * capturable after the first call on a device.  Errors as for pa_cache_write.
+ */
+pa_status pa_cache_write_slots(const void *k_new, const void *v_new,
+                               void *k_cache, void *v_cache,
+                               const int64_t *slot_mapping, int num_kv_heads,
+                               int head_dim, int block_size, void *stream,
+                               pa_dtype dtype, int num_tokens,
+                               long long k_token_stride,
+                               long long v_token_stride, int num_blocks,
+                               pa_kv_layout kv_layout);
+
+/*
  * pa_debug_gather -- the page-gather indexing alone (PA_KV_NHD), for
  * bit-exact tests:
  *   dense_out[s][j][:] = k_cache[block_table[s][j / bs]][j % bs][0:row_elems]
@@ -439,8 +591,8 @@ pa_status pa_debug_gather(const void *k_cache, const int32_t *block_table,
 pa_status pa_debug_wait_timeout(uint64_t limit_ns, int *done, void *stream);
 
 /*
- * Kernel timing.  While enabled, every kernel that pa_forward, pa_mla_decode
- * and pa_debug_gather launch is bracketed by a pair of CUDA events recorded
+ * Kernel timing.  While enabled, every kernel that pa_forward, pa_mla_decode,
+ * pa_forward_shared_prefix and pa_debug_gather launch is bracketed by a pair of CUDA events recorded
  * on the caller's stream (nothing is recorded for a stream that is being
  * captured).  pa_profile_read synchronises on those events, writes for each
  * kernel id below the summed milliseconds and the launch count (arrays of
@@ -457,6 +609,7 @@ enum {
   PA_K_GATHER = 6,    /* debug gather                               */
   PA_K_UPPROJ = 7,    /* MLA prefill up-projection (tensor cores)   */
   PA_K_MLA_ROPE = 8,  /* MLA prefill rotary-key copy                */
+  PA_K_PREFIX = 9,    /* prefix part of pa_forward_shared_prefix    */
   PA_K_COUNT = 10
 };
 pa_status pa_profile_enable(int on);

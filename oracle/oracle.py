@@ -274,6 +274,81 @@ def cache_write(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_sta
     return k_store, v_store, status
 
 
+DEV_BAD_SEQLEN, DEV_NO_PAGES = 0x4, 0x80
+
+
+def block_tables(seq_lens, query_start_loc, block_table, block_size, num_blocks, num_tokens,
+                 free_pages=None, free_start=None):
+    """A step's block-table rows and slot map, request by request and token by
+    token.  Request s holds the pages of its positions before this step and,
+    when free_start is given, takes the pages it lacks from
+    free_pages[free_start:] in request order; the first request whose pages are
+    not all there, and the later ones that need any, take none (their demand
+    still counts).  Returns (table, slots, positions, free_end, status)."""
+    table = np.array(block_table, dtype=np.int64)
+    qsl = [int(x) for x in query_start_loc]
+    slots = np.full(num_tokens, -1, np.int64)
+    positions = np.zeros(num_tokens, np.int64)
+    S, status = len(seq_lens), 0
+    end = free_start
+    if S and (qsl[0] != 0 or qsl[S] > num_tokens or any(b < a for a, b in zip(qsl, qsl[1:]))):
+        return table, slots, positions, end, DEV_BAD_QSL
+    asked = 0
+    for s in range(S):
+        length, q_len = int(seq_lens[s]), qsl[s + 1] - qsl[s]
+        if length < 0 or -(-length // block_size) > table.shape[1]:
+            status |= DEV_BAD_SEQLEN
+            continue
+        if q_len > length:
+            status |= DEV_BAD_QLEN
+            continue
+        prefix = length - q_len
+        held, total = -(-prefix // block_size), -(-length // block_size)
+        served = True
+        if free_start is not None and total > held:
+            first = free_start + asked
+            asked += total - held
+            room = len(free_pages) - free_start if free_start >= 0 else 0
+            served = asked <= room
+            if served:
+                end = free_start + asked
+                for j in range(held, total):
+                    page = int(free_pages[first + j - held])
+                    table[s, j] = page if 0 <= page < num_blocks else -1
+            else:
+                status |= DEV_NO_PAGES
+        for i in range(q_len):
+            pos = prefix + i
+            positions[qsl[s] + i] = pos
+            if not served:
+                continue
+            page = int(table[s, pos // block_size])
+            if 0 <= page < num_blocks:
+                slots[qsl[s] + i] = page * block_size + pos % block_size
+            else:
+                status |= DEV_BAD_BLOCK
+    return table, slots, positions, end, status
+
+
+def cache_write_slots(k_new, v_new, k_cache, v_cache, slot_mapping, block_size, kv_layout="nhd"):
+    """The cache write by a slot map: token t's rows go to slot
+    slot_mapping[t] % block_size of page slot_mapping[t] // block_size; a
+    negative slot is skipped, one past the pool too (DEV_BAD_BLOCK).  Returns
+    the two new caches (copies) and the status bits."""
+    k_store, v_store = k_cache.copy(), v_cache.copy()
+    k_out, v_out = nhd_view(k_store, kv_layout), nhd_view(v_store, kv_layout)
+    status = 0
+    for t, slot in enumerate(int(x) for x in slot_mapping):
+        if slot < 0:
+            continue
+        if slot >= k_out.shape[0] * block_size:
+            status |= DEV_BAD_BLOCK
+            continue
+        k_out[slot // block_size, slot % block_size] = k_new[t]
+        v_out[slot // block_size, slot % block_size] = v_new[t]
+    return k_store, v_store, status
+
+
 def widen(a):
     """Stored values as float64: float32 as is, uint16 bf16 bit patterns as
     the exact binary32 they encode."""

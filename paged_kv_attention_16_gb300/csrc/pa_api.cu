@@ -952,6 +952,108 @@ size_t fwd_workspace_bytes(const FwdCall &c) {
       .total;
 }
 
+int row_ctas_per_sm(int dtype, int head_dim, int group) {
+  return row_ctas_per_sm_cached(dtype, head_dim, group);
+}
+
+pa_status launch_rows_and_tiles(const FwdCall &c, FwdParams &p, int num_sms, cudaStream_t st,
+                                bool timed) {
+  if (c.num_seqs <= 0) return PA_OK;
+  const int group = c.num_heads / c.num_kv_heads;
+  const int dqk = c.head_dim_qk > 0 ? c.head_dim_qk : c.head_dim;
+  const bool tile_ok = p.tile_ok != 0;
+  const int row_ctas = p.row_ctas;
+  const bool mma_rows = row_mma_supported(c.dtype, c.head_dim, group);
+  // bf16 K/V boxes of 16 slots x both 64-dim halves of one KV head:
+  // dims {64 dims, slots, halves, kv heads, pages} (the slot stride is
+  // larger than the half stride; TMA takes strides in any order).  The row
+  // kernel reads K and V through them, the tile kernel V.  In the HND
+  // layout a box is one contiguous run of 16 x head_dim elements.
+  CUtensorMap tm_kr, tm_vr;
+  // (all-tile calls have no row items: their K rows may be wider than V's)
+  if (c.dtype == PA_BF16 && !encode_row_maps(c, c.all_tile ? nullptr : &tm_kr, &tm_vr))
+    return PA_ERR_CUDA;
+  // The tile kernel's K: one 64-element (128-byte) swizzled box per half
+  // and 16 slots, so the S product sees a uniform row stride.
+  // When every 64-position tile lies in one page (block_size a multiple of
+  // 64; tiles start at multiples of 64: no window, splits of a multiple of
+  // 64), the tile kernel loads a whole tile's K chunk or V rows as one box.
+  const bool page_boxes = tile_ok && c.dtype == PA_BF16 && c.block_size % 64 == 0 &&
+                          c.sliding_window == 0 && c.kv_split_tokens % 64 == 0;
+  p.tile_page_boxes = page_boxes ? 1 : 0;
+  // Split keys (MLA prefill): the key tensor holds dqk - 64 columns per
+  // (position, head) and the last 64 come from one row per position.
+  CUtensorMap tm_kt, tm_vt, tm_krope;
+  p.k_rope_split = c.k_rope ? 1 : 0;
+  if (tile_ok && !encode_cache_map(&tm_kt, c.k_cache, c.dtype, c.kv_layout, c.num_blocks,
+                                   c.block_size, c.num_kv_heads, c.k_rope ? dqk - 64 : dqk, 64,
+                                   page_boxes ? 64 : 16, CU_TENSOR_MAP_SWIZZLE_128B))
+    return PA_ERR_CUDA;
+  if (c.k_rope && !encode_cache_map(&tm_krope, c.k_rope, c.dtype, PA_KV_NHD, c.num_blocks,
+                                    c.block_size, 1, 64, 64, page_boxes ? 64 : 16,
+                                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return PA_ERR_CUDA;
+  if (!c.k_rope) tm_krope = tm_kt;
+  if (page_boxes) {
+    const unsigned long long es = 2, row = (unsigned long long)c.head_dim * es;
+    const bool hnd = c.kv_layout == PA_KV_HND;
+    const unsigned long long dims[5] = {64, (unsigned long long)c.block_size,
+                                        (unsigned long long)(c.head_dim / 64),
+                                        (unsigned long long)c.num_kv_heads,
+                                        (unsigned long long)c.num_blocks};
+    const unsigned long long strides[4] = {
+        hnd ? row : (unsigned long long)c.num_kv_heads * row, 64 * es,
+        hnd ? (unsigned long long)c.block_size * row : row,
+        (unsigned long long)c.block_size * c.num_kv_heads * row};
+    const unsigned int box[5] = {64, 64, (unsigned int)(c.head_dim / 64), 1, 1};
+    if (!encode_tiled(&tm_vt, c.v_cache, c.dtype, 5, dims, strides, box, true))
+      return PA_ERR_CUDA;
+  }
+  cudaError_t row_err = cudaSuccess;
+  int slot = timed ? prof_begin(PA_K_ROW, st) : -1;
+  if (c.all_tile) {
+    // no row items: the row kernel is not launched
+  } else if (mma_rows) {
+    row_err = launch_row_mma_kernel(p, tm_kr, tm_vr, row_ctas, st);
+  } else {
+    // fp32: whole rows of head_dim elements, no swizzle (CUDA-core kernel)
+    CUtensorMap tm_k, tm_v;
+    if (!encode_cache_map(&tm_k, c.k_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
+                          c.num_kv_heads, c.head_dim, c.head_dim, 16,
+                          CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_cache_map(&tm_v, c.v_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
+                          c.num_kv_heads, c.head_dim, c.head_dim, 16,
+                          CU_TENSOR_MAP_SWIZZLE_NONE))
+      return PA_ERR_CUDA;
+    row_err = launch_row_kernel(p, tm_k, tm_v, row_ctas, st);
+  }
+  prof_end(slot, st);
+  if (row_err != cudaSuccess) return PA_ERR_CUDA;
+  // A decode-only batch (the caller's bound max_query_len == 1; a request
+  // above it is zeroed as bad metadata) has no tile items: no launch.
+  if (tile_ok && c.max_query_len != 1) {
+    // Q as [tokens, heads, dim] with 64-element (128-byte) swizzled boxes of
+    // G heads x (128 / G) tokens.
+    CUtensorMap tm_q;
+    EncodeTiledFn fn = encode_fn();
+    cuuint64_t qd[3] = {(cuuint64_t)dqk, (cuuint64_t)c.num_heads, (cuuint64_t)c.num_tokens};
+    cuuint64_t qs[2] = {(cuuint64_t)dqk * 2, (cuuint64_t)c.num_heads * dqk * 2};
+    cuuint32_t qb[3] = {64, (cuuint32_t)group, (cuuint32_t)(kTileRows / group)};
+    cuuint32_t qe[3] = {1, 1, 1};
+    if (!fn ||
+        fn(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(c.q), qd, qs, qb, qe,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return PA_ERR_CUDA;
+    slot = timed ? prof_begin(PA_K_TILE, st) : -1;
+    const cudaError_t tile_err =
+        launch_tile_kernel(p, tm_q, tm_kt, page_boxes ? tm_vt : tm_vr, tm_krope, num_sms, st);
+    prof_end(slot, st);
+    if (tile_err != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
 pa_status fwd_launch(const FwdCall &c, void *workspace, unsigned int *status, int num_sms,
                      cudaStream_t st, bool timed) {
   const int group = c.num_heads / c.num_kv_heads;
@@ -1010,96 +1112,8 @@ pa_status fwd_launch(const FwdCall &c, void *workspace, unsigned int *status, in
   prof_end(slot, st);
   if (plan_err != cudaSuccess) return PA_ERR_CUDA;
 
-  if (c.num_seqs > 0) {
-    const bool mma_rows = row_mma_supported(c.dtype, c.head_dim, group);
-    // bf16 K/V boxes of 16 slots x both 64-dim halves of one KV head:
-    // dims {64 dims, slots, halves, kv heads, pages} (the slot stride is
-    // larger than the half stride; TMA takes strides in any order).  The row
-    // kernel reads K and V through them, the tile kernel V.  In the HND
-    // layout a box is one contiguous run of 16 x head_dim elements.
-    CUtensorMap tm_kr, tm_vr;
-    // (all-tile calls have no row items: their K rows may be wider than V's)
-    if (c.dtype == PA_BF16 && !encode_row_maps(c, c.all_tile ? nullptr : &tm_kr, &tm_vr))
-      return PA_ERR_CUDA;
-    // The tile kernel's K: one 64-element (128-byte) swizzled box per half
-    // and 16 slots, so the S product sees a uniform row stride.
-    // When every 64-position tile lies in one page (block_size a multiple of
-    // 64; tiles start at multiples of 64: no window, splits of a multiple of
-    // 64), the tile kernel loads a whole tile's K chunk or V rows as one box.
-    const bool page_boxes = tile_ok && c.dtype == PA_BF16 && c.block_size % 64 == 0 &&
-                            c.sliding_window == 0 && c.kv_split_tokens % 64 == 0;
-    p.tile_page_boxes = page_boxes ? 1 : 0;
-    // Split keys (MLA prefill): the key tensor holds dqk - 64 columns per
-    // (position, head) and the last 64 come from one row per position.
-    CUtensorMap tm_kt, tm_vt, tm_krope;
-    p.k_rope_split = c.k_rope ? 1 : 0;
-    if (tile_ok && !encode_cache_map(&tm_kt, c.k_cache, c.dtype, c.kv_layout, c.num_blocks,
-                                     c.block_size, c.num_kv_heads, c.k_rope ? dqk - 64 : dqk, 64,
-                                     page_boxes ? 64 : 16, CU_TENSOR_MAP_SWIZZLE_128B))
-      return PA_ERR_CUDA;
-    if (c.k_rope && !encode_cache_map(&tm_krope, c.k_rope, c.dtype, PA_KV_NHD, c.num_blocks,
-                                      c.block_size, 1, 64, 64, page_boxes ? 64 : 16,
-                                      CU_TENSOR_MAP_SWIZZLE_128B))
-      return PA_ERR_CUDA;
-    if (!c.k_rope) tm_krope = tm_kt;
-    if (page_boxes) {
-      const unsigned long long es = 2, row = (unsigned long long)c.head_dim * es;
-      const bool hnd = c.kv_layout == PA_KV_HND;
-      const unsigned long long dims[5] = {64, (unsigned long long)c.block_size,
-                                          (unsigned long long)(c.head_dim / 64),
-                                          (unsigned long long)c.num_kv_heads,
-                                          (unsigned long long)c.num_blocks};
-      const unsigned long long strides[4] = {
-          hnd ? row : (unsigned long long)c.num_kv_heads * row, 64 * es,
-          hnd ? (unsigned long long)c.block_size * row : row,
-          (unsigned long long)c.block_size * c.num_kv_heads * row};
-      const unsigned int box[5] = {64, 64, (unsigned int)(c.head_dim / 64), 1, 1};
-      if (!encode_tiled(&tm_vt, c.v_cache, c.dtype, 5, dims, strides, box, true))
-        return PA_ERR_CUDA;
-    }
-    cudaError_t row_err = cudaSuccess;
-    slot = timed ? prof_begin(PA_K_ROW, st) : -1;
-    if (c.all_tile) {
-      // no row items: the row kernel is not launched
-    } else if (mma_rows) {
-      row_err = launch_row_mma_kernel(p, tm_kr, tm_vr, row_ctas, st);
-    } else {
-      // fp32: whole rows of head_dim elements, no swizzle (CUDA-core kernel)
-      CUtensorMap tm_k, tm_v;
-      if (!encode_cache_map(&tm_k, c.k_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
-                            c.num_kv_heads, c.head_dim, c.head_dim, 16,
-                            CU_TENSOR_MAP_SWIZZLE_NONE) ||
-          !encode_cache_map(&tm_v, c.v_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
-                            c.num_kv_heads, c.head_dim, c.head_dim, 16,
-                            CU_TENSOR_MAP_SWIZZLE_NONE))
-        return PA_ERR_CUDA;
-      row_err = launch_row_kernel(p, tm_k, tm_v, row_ctas, st);
-    }
-    prof_end(slot, st);
-    if (row_err != cudaSuccess) return PA_ERR_CUDA;
-    // A decode-only batch (the caller's bound max_query_len == 1; a request
-    // above it is zeroed as bad metadata) has no tile items: no launch.
-    if (tile_ok && c.max_query_len != 1) {
-      // Q as [tokens, heads, dim] with 64-element (128-byte) swizzled boxes of
-      // G heads x (128 / G) tokens.
-      CUtensorMap tm_q;
-      EncodeTiledFn fn = encode_fn();
-      cuuint64_t qd[3] = {(cuuint64_t)dqk, (cuuint64_t)c.num_heads, (cuuint64_t)c.num_tokens};
-      cuuint64_t qs[2] = {(cuuint64_t)dqk * 2, (cuuint64_t)c.num_heads * dqk * 2};
-      cuuint32_t qb[3] = {64, (cuuint32_t)group, (cuuint32_t)(kTileRows / group)};
-      cuuint32_t qe[3] = {1, 1, 1};
-      if (!fn ||
-          fn(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(c.q), qd, qs, qb, qe,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return PA_ERR_CUDA;
-      slot = timed ? prof_begin(PA_K_TILE, st) : -1;
-      const cudaError_t tile_err =
-          launch_tile_kernel(p, tm_q, tm_kt, page_boxes ? tm_vt : tm_vr, tm_krope, num_sms, st);
-      prof_end(slot, st);
-      if (tile_err != cudaSuccess) return PA_ERR_CUDA;
-    }
-  }
+  const pa_status work = launch_rows_and_tiles(c, p, num_sms, st, timed);
+  if (work != PA_OK) return work;
   slot = timed ? prof_begin(PA_K_MERGE, st) : -1;
   const cudaError_t merge_err =
       c.dtype == PA_BF16

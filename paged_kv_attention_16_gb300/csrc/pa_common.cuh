@@ -100,6 +100,9 @@ struct FwdParams {
                             // [pages, slots, 1, 64] tensor shared by all heads
   int max_qlen;             // the caller's bound on q_len (0: none); a request
                             // above it is bad metadata (PA_DEV_BAD_QLEN)
+  int partial_only;         // 1: every row's splits, a single one included, are
+                            // stored as partials (positions below kv_base are
+                            // another kernel's and join in the merge)
   // Decode-only batches declared by the caller (one launch, no planner): the
   // row kernel sizes the splits itself from seq_lens (at most fast_nsmax a
   // row); partial rows (s * H + head) * fast_nsmax + split; fast_work: [0]

@@ -120,6 +120,13 @@ size_t fwd_workspace_bytes(const FwdCall &c);
 pa_status fwd_launch(const FwdCall &c, void *workspace, unsigned int *status, int num_sms,
                      cudaStream_t stream, bool timed);
 
+// The row and the tile kernel over the lists a planner has left in `p`
+// (row_ctas and tile_ok set): their tensor maps and launches.
+pa_status launch_rows_and_tiles(const FwdCall &c, FwdParams &p, int num_sms, cudaStream_t stream,
+                                bool timed);
+// Resident CTAs per SM of the row kernel that serves these rows.
+int row_ctas_per_sm(int dtype, int head_dim, int group);
+
 // True while `stream` is capturing a CUDA graph.
 bool stream_capturing(cudaStream_t stream);
 // The calling thread's current device in *dev; PA_ERR_INVALID_ARG when

@@ -1,0 +1,719 @@
+// pa_prefix.cu -- attention for a batch whose requests share long prefixes
+// (pa_forward_shared_prefix): argument checks, the planner, the prefix kernel
+// on CUDA cores and the merge.
+//
+// Requests come in consecutive groups; the requests of group g see the same
+// first P_g positions.  A row's softmax over [0, P_g) and its own positions is
+// the log-sum-exp join of two parts:
+//   prefix part   all rows of the group (its tokens x the G heads of a KV
+//                 head) against [0, P_g): every key is visible to every row,
+//                 so it is a dense product of many rows, and a tile of keys is
+//                 read once for 256 rows instead of once for each request;
+//   own part      each request's rows against its own positions, causal: the
+//                 row and tile kernels of pa_forward, their splits starting
+//                 at P_g, every split stored as a partial.
+// The merge joins a row's partials of both parts, and its sink.
+//
+// Planner: the prefix part is cut into items (KV head, 256-row block, split).
+// Splits are whole 128-position tiles of equal length, sized by a cost model
+// over the whole grid (see plan_splits).  Items that read the same keys are
+// neighbours, so that they run at the same time and share them through L2.
+#include <algorithm>
+
+#include "pa_prefix.h"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeCache = 1024;       // requests whose starts the merge keeps in shared memory
+constexpr int kModelGroups = 128;       // groups up to which the split model is evaluated
+constexpr int kRowItemTarget = 2560;    // most row-kernel items the own part aims at
+// What an item costs beside its tiles (query loads, the first scores' and the
+// last products' latency, storing and merging 256 partial rows), in tiles.
+constexpr int kItemOverhead = 2;
+
+// ---------------------------------------------------------------------------
+// planner: one block
+// ---------------------------------------------------------------------------
+
+// Tiles per split.  Each thread tries one number of splits of the longest
+// prefix: its length L gives every group ceil(n_g / L) splits, the items run in
+// ceil(items / SMs) waves, and a wave lasts L + kItemOverhead tiles.
+__device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const int *s_w, int nmax,
+                                  long long tiles, int *s_best) {
+  const int NG = p.num_groups, tid = threadIdx.x;
+  if (nmax <= 0) return 1;
+  if (NG > kModelGroups) {
+    // enough units to fill the SMs in most batches: about two items per SM
+    const long long L = ceil_div_ll(tiles, 2ll * p.num_sms);
+    return (int)(L < 1 ? 1 : L > nmax ? nmax : L);
+  }
+  const int s = tid + 1;
+  long long cost = 0x7fffffffffffll;
+  const int L = (nmax + s - 1) / s;
+  if (s <= nmax) {
+    long long items = 0;
+    for (int g = 0; g < NG; ++g) items += (long long)s_w[g] * ((s_n[g] + L - 1) / L);
+    if (s == 1 || items <= p.item_cap)
+      cost = ceil_div_ll(items, p.num_sms) * (L + kItemOverhead);
+  }
+  __shared__ long long s_cost[kPlanThreads / 32];
+  long long best = cost << 10 | tid;  // ties: the fewest splits
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if ((tid & 31) == 0) s_cost[tid >> 5] = best;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kPlanThreads / 32; ++w) best = min(best, s_cost[w]);
+    *s_best = (int)(best & 1023) + 1;
+  }
+  __syncthreads();
+  return (nmax + *s_best - 1) / *s_best;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
+  __shared__ long long scratch[3 * 33];
+  __shared__ int s_n[kModelGroups], s_w[kModelGroups];
+  __shared__ int s_best, s_nmax;
+  __shared__ unsigned long long s_tiles;
+  const FwdParams &f = p.f;
+  const int S = f.num_seqs, NG = p.num_groups, T = f.num_tokens, tid = threadIdx.x;
+  const int Hk = f.num_kv_heads, G = f.num_heads / Hk, H = f.num_heads, bs = f.block_size;
+  pdl_trigger();
+  pdl_wait();
+
+  // -- starts: query_start_loc over the tokens, group_start_loc over the requests
+  int bad = 0;
+  if (tid == 0) {
+    bad = f.qsl[0] != 0 || f.qsl[S] != T || p.group_start[0] != 0 || p.group_start[NG] != S;
+    s_nmax = 0;
+    s_tiles = 0;
+  }
+  for (int s = tid; s < S; s += kPlanThreads)
+    if (f.qsl[s + 1] < f.qsl[s]) bad = 1;
+  for (int g = tid; g < NG; g += kPlanThreads)
+    if (p.group_start[g + 1] < p.group_start[g]) bad = 1;
+  const bool starts_bad = __syncthreads_or(bad) != 0;
+  if (starts_bad) {
+    if (tid == 0) {
+      atomicOr(f.status, PA_DEV_BAD_QSL);
+      p.plan->n_items = 0;
+      p.plan->all_bad = 1;
+      for (int x = 0; x < kNumLists; ++x) f.plan->n[x] = 0;
+      for (int x = 0; x < 8; ++x) f.plan->counter[x] = 0;
+      f.plan->qsl_bad = 1;
+    }
+    return;
+  }
+
+  // -- groups: rows and prefix tiles
+  auto group_prefix = [&](int g) {  // -1: bad
+    const int P = p.prefix_lens[g];
+    const bool ok = P >= 0 && P <= p.max_prefix_len && P % bs == 0 &&
+                    P / bs <= f.max_blocks_per_seq;
+    return ok ? P : -1;
+  };
+  unsigned flags = 0;
+  for (int g = tid; g < NG; g += kPlanThreads) {
+    const int r0 = p.group_start[g], r1 = p.group_start[g + 1];
+    const int q0 = f.qsl[r0], nq = f.qsl[r1] - q0;
+    int P = group_prefix(g);
+    if (P < 0) {
+      if (r1 > r0) flags |= PA_DEV_BAD_SEQLEN;
+      P = 0;
+    }
+    const int nrp = nq > 0 ? (int)ceil_div_ll((long long)nq * G, kPrefixRows) : 0;
+    const int n = nq > 0 ? (P + kPrefixTile - 1) / kPrefixTile : 0;
+    p.grp[g] = PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0, 0};
+    if (NG <= kModelGroups) {
+      s_n[g] = n;
+      s_w[g] = n > 0 ? Hk * nrp : 0;
+    }
+    atomicMax(&s_nmax, n);
+    atomicAdd(&s_tiles, (unsigned long long)n * Hk * nrp);
+  }
+  __syncthreads();
+  const int L = plan_splits(p, s_n, s_w, s_nmax, (long long)s_tiles, &s_best);
+  long long run = 0;
+  for (int base = 0; base < NG; base += kPlanThreads) {
+    const int g = base + tid;
+    PrefixGroup gr{};
+    long long items = 0;
+    if (g < NG) {
+      gr = p.grp[g];
+      const int n = gr.q_len > 0 ? (gr.prefix + kPrefixTile - 1) / kPrefixTile : 0;
+      const int ns = (n + L - 1) / L;
+      // equal splits; as many as have tiles
+      const int len = ns > 0 ? (n + ns - 1) / ns : 1;
+      gr.nsplit = (n + len - 1) / len;
+      gr.split_len = len * kPrefixTile;
+      items = (long long)Hk * gr.nrp * gr.nsplit;
+    }
+    long long tot;
+    const long long end = block_inclusive_scan(items, scratch, &tot) + run;
+    run += tot;
+    if (g < NG) {
+      gr.item0 = end - items;
+      p.grp[g] = gr;
+      p.grp_end[g] = end;
+    }
+  }
+  const long long n_items = run;
+
+  // -- requests: the own part's lists
+  auto classify = [&](int s, int &g, ReqInfo &r) {
+    int lo = 0, hi = NG - 1;
+    while (lo < hi) {  // the last group that starts at or before s
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.group_start[mid] <= s) lo = mid; else hi = mid - 1;
+    }
+    g = lo;
+    const int P = group_prefix(g);
+    r.q_start = f.qsl[s];
+    r.q_len = f.qsl[s + 1] - r.q_start;
+    r.ctx = f.seq_lens[s];
+    r.kv_base = P < 0 ? 0 : P;
+    const bool len_ok = r.ctx >= 0 && r.ctx <= f.max_seq_len &&
+                        ceil_div_ll(r.ctx, bs) <= (long long)f.max_blocks_per_seq;
+    const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen);
+    const bool own_ok = P >= 0 && r.ctx - r.q_len >= P;
+    unsigned fl = 0;
+    if (r.q_len > 0) {
+      if (!len_ok || !own_ok) fl |= PA_DEV_BAD_SEQLEN;
+      if (!q_ok) fl |= PA_DEV_BAD_QLEN;
+    }
+    const bool valid = r.q_len > 0 && len_ok && q_ok && own_ok;
+    r.flags = (r.q_len == 1 ? kDecode : kExtend) | (valid ? kFlagValid : 0) |
+              (!f.tile_ok || r.q_len == 1 ? kFlagRowPath : 0);
+    return fl;
+  };
+  long long v[1] = {0}, t[1];
+  for (int s = tid; s < S; s += kPlanThreads) {
+    int g;
+    ReqInfo r{};
+    flags |= classify(s, g, r);
+    if ((r.flags & kFlagValid) && r.q_len == 1) v[0] += r.ctx - r.kv_base;
+  }
+  if (flags) atomicOr(f.status, flags);
+  block_scan_multi<1>(v, scratch, t);
+  // Decode rows: splits as the one-launch decode sizes them, about 8 (4 from
+  // G = 8 on) items a resident block, down to one 64-position stage.
+  const long long target = min((G >= 8 ? 4ll : 8ll) * max(f.row_ctas, 1), (long long)kRowItemTarget);
+  const long long Lw = ceil_div_ll(ceil_div_ll(t[0] * Hk, target), 64) * 64;
+  const int Ld = (int)min(max(Lw, (long long)kFastMinSplit), (long long)kRowMaxSplit);
+  // rows of longer requests on the row path (fp32): at most about 4 splits
+  const int Lr = (int)min(max((long long)Ld, ceil_div_ll(ceil_div_ll(f.max_seq_len, 4), 16) * 16),
+                          (long long)kRowMaxSplit);
+  long long sum[3] = {0, 0, 0};  // row items, tile items, partial rows
+  for (int base = 0; base < S; base += kPlanThreads) {
+    const int s = base + tid;
+    long long cnt[3] = {0, 0, 0};
+    ReqInfo r{};
+    int g = 0;
+    if (s < S) {
+      classify(s, g, r);
+      const int own = r.ctx - r.kv_base;
+      r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : max(own, 1);
+      r.nsplit = max((int)ceil_div_ll(own, r.split_len), 1);
+      if (r.flags & kFlagValid) {
+        if (r.flags & kFlagRowPath) cnt[0] = (long long)Hk * r.q_len * r.nsplit;
+        else cnt[1] = (long long)Hk * ceil_div_ll((long long)r.q_len * G, kTileRows) * r.nsplit;
+        cnt[2] = (long long)r.q_len * H * r.nsplit;
+      }
+    }
+    const long long part = cnt[2];
+    long long tot[3];
+    block_scan_multi<3>(cnt, scratch, tot);
+    if (s < S) {
+      r.partial_base = cnt[2] + sum[2] - part;
+      f.list_end[(size_t)kListRow * S + s] = cnt[0] + sum[0];
+      f.list_end[(size_t)kListTile * S + s] = cnt[1] + sum[1];
+      f.ord[s] = s;
+      f.req[s] = r;
+      p.req_grp[s] = g;
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) sum[x] += tot[x];
+  }
+  if (tid == 0) {
+    const bool overflow = sum[2] > f.part_cap || n_items > p.item_cap;
+    if (overflow) atomicOr(f.status, PA_DEV_OVERFLOW);
+    p.plan->n_items = overflow ? 0 : n_items;
+    p.plan->all_bad = overflow ? 1 : 0;
+    for (int x = 0; x < kNumLists; ++x) f.plan->n[x] = 0;
+    f.plan->n[kListRow] = overflow ? 0 : sum[0];
+    f.plan->n[kListTile] = overflow ? 0 : sum[1];
+    for (int x = 0; x < 8; ++x) f.plan->counter[x] = 0;
+    f.plan->qsl_bad = overflow ? 1 : 0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// prefix part on CUDA cores
+// ---------------------------------------------------------------------------
+// Four threads share a row (each every fourth 16-byte group of its head_dim
+// values), 64 rows a pass; 32 keys and values at a time in shared memory as
+// fp32.  A row's scores of 8 keys are reduced over its four threads, then
+// join the running maximum and sum.  Every key costs 4 D fp32 operations a
+// row: the FMA units bound it.
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 32;
+
+template <typename T>
+__device__ inline void load16(const T *src, float *dst);
+template <>
+__device__ inline void load16<float>(const float *src, float *dst) {
+  *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src);
+}
+template <>
+__device__ inline void load16<__nv_bfloat16>(const __nv_bfloat16 *src, float *dst) {
+  const uint4 w = *reinterpret_cast<const uint4 *>(src);
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    dst[2 * i] = bf16lo(x[i]);
+    dst[2 * i + 1] = bf16hi(x[i]);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixParams p, int hnd) {
+  constexpr int VEC = 16 / sizeof(T);
+  __shared__ __align__(16) float s_k[kSimtKeys][D], s_v[kSimtKeys][D];
+  __shared__ int s_page[kSimtKeys];
+  const FwdParams &f = p.f;
+  const int tid = threadIdx.x, c = tid & 3, G = f.num_heads / f.num_kv_heads, bs = f.block_size;
+  const int Hk = f.num_kv_heads;
+  pdl_trigger();
+  pdl_wait();
+  const long long n_items = p.plan->n_items;
+  const T *kc = static_cast<const T *>(p.k_cache), *vc = static_cast<const T *>(p.v_cache);
+  for (long long item = blockIdx.x; item < n_items; item += gridDim.x) {
+    const PrefixItem it = prefix_item(p, item, G);
+    const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
+    const int rows = min(kPrefixRows, (it.q_len - it.t0) * G);
+    for (int pass = 0; pass * 64 < rows; ++pass) {
+      const int r = pass * 64 + (tid >> 2);  // row of the item
+      const bool in = r < rows;
+      const int tok = it.q_start + it.t0 + (in ? r / G : 0), head = it.kvh * G + (in ? r % G : 0);
+      const T *q = static_cast<const T *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
+      float qv[D / 4], o[D / 4];
+#pragma unroll
+      for (int i = 0; i < D / 4; i += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          qv[i + e] = (float)q[i * 4 + c * 4 + e] * f.scale_log2;
+          o[i + e] = 0.f;
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+      int bad = 0;
+      for (int lo = it.kv_lo; lo < it.kv_hi; lo += kSimtKeys) {
+        __syncthreads();  // the tile before is read
+        if (tid < kSimtKeys) {
+          const int pos = lo + tid;
+          int page = -1;
+          if (pos < it.kv_hi) {
+            page = __ldg(bt + pos / bs);
+            if (page < 0 || page >= f.num_blocks) {
+              atomicOr(f.status, PA_DEV_BAD_BLOCK);
+              page = -2;
+            }
+          }
+          s_page[tid] = page;
+        }
+        __syncthreads();
+        for (int e = tid; e < kSimtKeys * (D / VEC); e += kSimtThreads) {
+          const int j = e / (D / VEC), x = e % (D / VEC) * VEC, page = s_page[j];
+          float kf[VEC] = {}, vf[VEC] = {};
+          if (page >= 0) {
+            const int slot = (lo + j) % bs;
+            const size_t row = hnd ? ((size_t)page * Hk + it.kvh) * bs + slot
+                                   : ((size_t)page * bs + slot) * Hk + it.kvh;
+            load16<T>(kc + row * D + x, kf);
+            load16<T>(vc + row * D + x, vf);
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            s_k[j][x + i] = kf[i];
+            s_v[j][x + i] = vf[i];
+          }
+        }
+        __syncthreads();
+        for (int j0 = 0; j0 < kSimtKeys && lo + j0 < it.kv_hi; j0 += 8) {
+          float sc[8];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float acc = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 4; i += 4) {
+              const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[j0 + j][i * 4 + c * 4]);
+              acc = fmaf(qv[i], k4.x, acc);
+              acc = fmaf(qv[i + 1], k4.y, acc);
+              acc = fmaf(qv[i + 2], k4.z, acc);
+              acc = fmaf(qv[i + 3], k4.w, acc);
+            }
+            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+            if (s_page[j0 + j] == -2) bad = 1;
+            sc[j] = lo + j0 + j < it.kv_hi ? acc : -INFINITY;
+            mx = fmaxf(mx, sc[j]);
+          }
+          if (mx > m) {
+            const float a = m == -INFINITY ? 0.f : exp2f(m - mx);
+            l *= a;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) o[i] *= a;
+            m = mx;
+          }
+          const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float w = exp2f(sc[j] - mu);
+            l += w;
+#pragma unroll
+            for (int i = 0; i < D / 4; i += 4) {
+              const float4 v4 = *reinterpret_cast<const float4 *>(&s_v[j0 + j][i * 4 + c * 4]);
+              o[i] = fmaf(w, v4.x, o[i]);
+              o[i + 1] = fmaf(w, v4.y, o[i + 1]);
+              o[i + 2] = fmaf(w, v4.z, o[i + 2]);
+              o[i + 3] = fmaf(w, v4.w, o[i + 3]);
+            }
+          }
+        }
+      }
+      if (in) {
+        const long long prow = item * kPrefixRows + r;
+        const float inv = l > 0.f && !bad ? 1.f / l : 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; i += 4)
+          *reinterpret_cast<float4 *>(p.part_o + prow * D + i * 4 + c * 4) =
+              make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        if (c == 0)
+          p.part_lse[prow] = bad ? __int_as_float(0x7fc00000) : l > 0.f ? m + log2f(l) : -INFINITY;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge: one warp per (token, query head)
+// ---------------------------------------------------------------------------
+
+template <typename T>
+__device__ inline void store_vec(T *dst, const float (&v)[4], int n);
+template <>
+__device__ inline void store_vec<float>(float *dst, const float (&v)[4], int n) {
+  for (int x = 0; x < n; ++x) dst[x] = v[x];
+}
+template <>
+__device__ inline void store_vec<__nv_bfloat16>(__nv_bfloat16 *dst, const float (&v)[4], int n) {
+  // one rounding to nearest even, of the finished output
+  for (int x = 0; x < n; x += 2)
+    *reinterpret_cast<__nv_bfloat162 *>(dst + x) = __floats2bfloat162_rn(v[x], v[x + 1]);
+}
+
+// out = sum_i w_i O_i with w_i = 2^(lse_i - M) / (sum_j 2^(lse_j - M) + 2^(sink - M)):
+// the row's prefix partials, then its own.
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const PrefixParams p) {
+  __shared__ int s_qsl[kMergeCache];
+  const FwdParams &f = p.f;
+  const int S = f.num_seqs, H = f.num_heads, D = f.head_dim, G = H / f.num_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, dpl = D / 32;
+  pdl_trigger();
+  pdl_wait();
+  T *out = static_cast<T *>(f.out);
+  const long long rows = (long long)f.num_tokens * H;
+  const long long gw = ((long long)blockIdx.x * kMergeThreads + tid) >> 5;
+  const long long nw = ((long long)gridDim.x * kMergeThreads) >> 5;
+  const bool all_bad = p.plan->all_bad != 0;
+  const bool cached = S <= kMergeCache;
+  if (cached) {
+    for (int s = tid; s < S; s += kMergeThreads) s_qsl[s] = f.qsl[s];
+    __syncthreads();
+  }
+  for (long long row = gw; row < rows; row += nw) {
+    const int tok = (int)(row / H), h = (int)(row % H);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    T *dst = out + row * D + lane * dpl;
+    if (all_bad) {
+      store_vec<T>(dst, acc, dpl);
+      continue;
+    }
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {  // the last request that starts at or before tok: its own
+      const int mid = (lo + hi + 1) >> 1;
+      if ((cached ? s_qsl[mid] : f.qsl[mid]) <= tok) lo = mid; else hi = mid - 1;
+    }
+    const ReqInfo r = f.req[lo];
+    if (!(r.flags & kFlagValid)) {
+      store_vec<T>(dst, acc, dpl);
+      continue;
+    }
+    const PrefixGroup g = p.grp[p.req_grp[lo]];
+    const int np = g.nsplit, i = tok - r.q_start, pos = r.ctx - r.q_len + i;
+    const int n = np + (pos - r.kv_base) / r.split_len + 1;
+    const long long own0 = r.partial_base + ((long long)i * H + h) * r.nsplit;
+    // row of the prefix part's blocks, and the step between its splits
+    const long long pr = (long long)(tok - g.q_start) * G + h % G;
+    const long long step = (long long)g.nrp * kPrefixRows;
+    const long long pre0 =
+        (g.item0 + (long long)(h / G) * np * g.nrp + pr / kPrefixRows) * kPrefixRows + pr % kPrefixRows;
+    auto lse_of = [&](int e) {
+      return e < np ? __ldg(p.part_lse + pre0 + e * step) : __ldg(f.part_lse + own0 + e - np);
+    };
+    float M = -INFINITY;
+    int bad = 0;
+    for (int e = lane; e < n; e += 32) {
+      const float v = lse_of(e);
+      if (isnan(v)) bad = 1; else M = fmaxf(M, v);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    const float sink2 = f.sinks ? __ldg(f.sinks + h) * kLog2eF : -INFINITY;
+    M = fmaxf(M, sink2);
+    if (bad || M == -INFINITY) {
+      store_vec<T>(dst, acc, dpl);
+      continue;
+    }
+    float L = 0.f;
+    for (int e0 = 0; e0 < n; e0 += 32) {
+      const float w_own = e0 + lane < n ? fast_exp2(lse_of(e0 + lane) - M) : 0.f;
+      L += w_own;
+      const int cnt = min(32, n - e0);
+      for (int u0 = 0; u0 < cnt; u0 += 8) {
+        float v[8][4];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int e = e0 + u0 + u;
+          const float *src = (e < np ? p.part_o + (pre0 + e * step) * D
+                                     : f.part_o + (own0 + e - np) * D) + lane * dpl;
+          if (u0 + u < cnt) {
+            if (dpl == 4) {
+              const float4 x = __ldg(reinterpret_cast<const float4 *>(src));
+              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+            } else {
+              const float2 x = __ldg(reinterpret_cast<const float2 *>(src));
+              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = v[u][3] = 0.f;
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (u0 + u >= cnt) break;
+          const float w = __shfl_sync(0xffffffffu, w_own, u0 + u);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[x] = fmaf(w, v[u][x], acc[x]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (f.sinks) L += fast_exp2(sink2 - M);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] *= inv;
+    store_vec<T>(dst, acc, dpl);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct PrefixLayout {
+  size_t plan, req, ord, list_end, pplan, grp, grp_end, req_grp, pre_o, pre_lse, own_o, own_lse,
+      total;
+  long long item_cap, part_cap;
+};
+
+// Host-side bounds of what the planner lays out, from the extents alone.
+PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_tokens, int num_heads,
+                           int num_kv_heads, int head_dim, int max_seq_len) {
+  PrefixLayout l{};
+  const long long S = num_seqs > 0 ? num_seqs : 1, NG = num_groups > 0 ? num_groups : 1;
+  const long long T = num_tokens, H = num_heads, Hk = num_kv_heads, G = H / Hk;
+  const long long msl = max_seq_len > 0 ? max_seq_len : 1;
+  // one item per (KV head, 256-row block, group) unsplit, and what splitting
+  // adds, but no more than one a tile
+  const long long units = Hk * (ceil_div_ll(T * G, kPrefixRows) + NG);
+  l.item_cap = std::min(units + kPrefixSplitItems, units * ceil_div_ll(msl, kPrefixTile));
+  // own part: decode rows ceil(len / Ld) splits each, Ld sized to the item
+  // target; longer rows one split (tile kernel) or about four (fp32)
+  const long long dec = std::min(S, T);
+  long long cap = H * dec * (1 + ceil_div_ll(msl, kRowMaxSplit)) + G * kRowItemTarget;
+  long long per_row = 1;
+  if (dtype == PA_F32) {
+    long long lr = ceil_div_ll(ceil_div_ll(msl, 4), 16) * 16;
+    lr = std::min(std::max(lr, (long long)kFastMinSplit), (long long)kRowMaxSplit);
+    per_row = ceil_div_ll(msl, lr);
+  }
+  cap += T * H * per_row;
+  l.part_cap = cap;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  l.plan = take(sizeof(PlanHeader));
+  l.req = take(S * sizeof(ReqInfo));
+  l.ord = take(S * sizeof(int));
+  l.list_end = take(S * kNumLists * sizeof(long long));
+  l.pplan = take(sizeof(PrefixPlan));
+  l.grp = take(NG * sizeof(PrefixGroup));
+  l.grp_end = take(NG * sizeof(long long));
+  l.req_grp = take(S * sizeof(int));
+  l.pre_o = take((size_t)l.item_cap * kPrefixRows * head_dim * sizeof(float));
+  l.pre_lse = take((size_t)l.item_cap * kPrefixRows * sizeof(float));
+  l.own_o = take((size_t)cap * head_dim * sizeof(float));
+  l.own_lse = take((size_t)cap * sizeof(float));
+  l.total = off;
+  return l;
+}
+
+template <typename T>
+cudaError_t launch_simt(const PrefixParams &p, int hnd, int num_sms, cudaStream_t st) {
+  auto kern = p.f.head_dim == 128 ? prefix_simt_kernel<T, 128> : prefix_simt_kernel<T, 64>;
+  return launch_dependent(kern, dim3(num_sms * 2), dim3(kSimtThreads), 0, st, p, hnd);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_forward_shared_prefix_workspace_bytes(pa_dtype dtype, int num_seqs, int num_groups,
+                                                int num_tokens, int num_heads, int num_kv_heads,
+                                                int head_dim, int max_seq_len) {
+  if (num_seqs < 0 || num_groups < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+      num_heads % num_kv_heads || head_dim <= 0 || max_seq_len < 0)
+    return 0;
+  return prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads, num_kv_heads, head_dim,
+                       max_seq_len)
+      .total;
+}
+
+pa_status pa_forward_shared_prefix(
+    const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+    const int32_t *seq_lens, const int32_t *query_start_loc, const int32_t *group_start_loc,
+    const int32_t *prefix_lens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+    float scale, void *out, void *stream, pa_dtype dtype, int num_seqs, int num_groups,
+    int num_tokens, int max_blocks_per_seq, int num_blocks, int max_seq_len, int max_prefix_len,
+    const pa_forward_options *options, void *workspace, size_t workspace_bytes) {
+  FwdCall c{q, k_cache, v_cache, block_table, seq_lens, query_start_loc, num_heads,
+            num_kv_heads, head_dim, block_size, scale, out, dtype, num_seqs, num_tokens,
+            max_blocks_per_seq, num_blocks, max_seq_len, 0};
+  if (num_groups < 0 || max_prefix_len < 0) return PA_ERR_INVALID_ARG;
+  if (options) {
+    if (options->sinks && (reinterpret_cast<uintptr_t>(options->sinks) & 3))
+      return PA_ERR_INVALID_ARG;
+    if ((options->kv_layout != PA_KV_NHD && options->kv_layout != PA_KV_HND) ||
+        options->sliding_window < 0 || options->max_query_len < 0 ||
+        (options->alibi_sqrt != 0 && options->alibi_sqrt != 1))
+      return PA_ERR_INVALID_ARG;
+    // every prefix key is visible to every row, whatever its position
+    if (options->sliding_window || options->alibi_slopes) return PA_ERR_UNSUPPORTED;
+    c.sinks = options->sinks;
+    c.kv_layout = options->kv_layout;
+    c.max_query_len = options->max_query_len;
+  }
+  pa_status s = fwd_check(c);
+  if (s != PA_OK || num_tokens == 0) return s;
+  if (num_groups == 0 || num_seqs == 0 || !group_start_loc || !prefix_lens)
+    return PA_ERR_INVALID_ARG;
+  const PrefixLayout lay = prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads,
+                                         num_kv_heads, head_dim, max_seq_len);
+  if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return PA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  PrefixParams p{};
+  void *lib_ws = nullptr;
+  int num_sms = 0;
+  s = device_resources(st, 0, &lib_ws, &p.f.status, &num_sms);
+  if (s != PA_OK) return s;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const int group = num_heads / num_kv_heads;
+  FwdParams &f = p.f;
+  f.q = q;
+  f.out = out;
+  f.block_table = block_table;
+  f.seq_lens = seq_lens;
+  f.qsl = query_start_loc;
+  f.num_seqs = num_seqs;
+  f.num_tokens = num_tokens;
+  f.num_heads = num_heads;
+  f.num_kv_heads = num_kv_heads;
+  f.head_dim = head_dim;
+  f.head_dim_qk = head_dim;
+  f.block_size = block_size;
+  f.max_blocks_per_seq = max_blocks_per_seq;
+  f.num_blocks = num_blocks;
+  f.max_seq_len = max_seq_len;
+  f.scale = scale;
+  f.scale_log2 = scale * kLog2eF;
+  f.tile_ok = tile_kernel_supported(dtype, head_dim, group) ? 1 : 0;
+  f.row_ctas = row_ctas_per_sm(dtype, head_dim, group) * num_sms;
+  f.tile_ctas = 2 * num_sms;
+  f.dtype = dtype;
+  f.plan = reinterpret_cast<PlanHeader *>(ws + lay.plan);
+  f.req = reinterpret_cast<ReqInfo *>(ws + lay.req);
+  f.ord = reinterpret_cast<int *>(ws + lay.ord);
+  f.list_end = reinterpret_cast<long long *>(ws + lay.list_end);
+  f.part_o = reinterpret_cast<float *>(ws + lay.own_o);
+  f.part_lse = reinterpret_cast<float *>(ws + lay.own_lse);
+  f.part_cap = lay.part_cap;
+  f.sinks = c.sinks;
+  f.max_qlen = c.max_query_len;
+  f.partial_only = 1;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.group_start = group_start_loc;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = num_groups;
+  p.max_prefix_len = max_prefix_len;
+  p.num_sms = num_sms;
+  p.plan = reinterpret_cast<PrefixPlan *>(ws + lay.pplan);
+  p.grp = reinterpret_cast<PrefixGroup *>(ws + lay.grp);
+  p.grp_end = reinterpret_cast<long long *>(ws + lay.grp_end);
+  p.req_grp = reinterpret_cast<int *>(ws + lay.req_grp);
+  p.part_o = reinterpret_cast<float *>(ws + lay.pre_o);
+  p.part_lse = reinterpret_cast<float *>(ws + lay.pre_lse);
+  p.item_cap = lay.item_cap;
+
+  int slot = prof_begin(PA_K_PLAN, st);
+  cudaError_t err = launch_dependent(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p);
+  prof_end(slot, st);
+  if (err != cudaSuccess) return PA_ERR_CUDA;
+  slot = prof_begin(PA_K_PREFIX, st);
+  const int hnd = c.kv_layout == PA_KV_HND;
+  err = dtype == PA_BF16 ? launch_simt<__nv_bfloat16>(p, hnd, num_sms, st)
+                         : launch_simt<float>(p, hnd, num_sms, st);
+  prof_end(slot, st);
+  if (err != cudaSuccess) return PA_ERR_CUDA;
+  s = launch_rows_and_tiles(c, f, num_sms, st, true);
+  if (s != PA_OK) return s;
+  slot = prof_begin(PA_K_MERGE, st);
+  const long long warps = (long long)num_tokens * num_heads;
+  const int blocks = (int)std::min(ceil_div_ll(warps, kMergeThreads / 32), (long long)num_sms * 8);
+  err = dtype == PA_BF16
+            ? launch_dependent(prefix_merge_kernel<__nv_bfloat16>, dim3(blocks),
+                               dim3(kMergeThreads), 0, st, p)
+            : launch_dependent(prefix_merge_kernel<float>, dim3(blocks), dim3(kMergeThreads), 0,
+                               st, p);
+  prof_end(slot, st);
+  return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -106,6 +106,7 @@ const char *pa_kernel_name(int kernel_id) {
     case PA_K_GATHER: return "gather";
     case PA_K_UPPROJ: return "upproj";
     case PA_K_MLA_ROPE: return "mla_rope";
+    case PA_K_PREFIX: return "prefix";
   }
   return "unknown";
 }

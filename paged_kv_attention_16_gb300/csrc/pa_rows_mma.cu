@@ -324,7 +324,8 @@ __global__ void __maxnreg__(168) row_mma_kernel(const __grid_constant__ CUtensor
         d.kv_hi = min(d.qpos + 1, s_lo + r.split_len);
         if (max(s_lo, d.mask_lo) >= d.kv_hi) continue;  // no visible position in this split
         d.kv_lo = max(s_lo, d.mask_lo & ~15);  // copy boxes start on 16-slot bounds
-        d.direct = (d.mask_lo - r.kv_base) / r.split_len == (d.qpos - r.kv_base) / r.split_len;
+        d.direct = !p.partial_only &&
+                   (d.mask_lo - r.kv_base) / r.split_len == (d.qpos - r.kv_base) / r.split_len;
         d.nsplit = r.nsplit;
         d.prow0 = r.partial_base + ((long long)d.i * H + d.kvh * G) * r.nsplit + d.split;
         pfirst = d.kv_lo / bs;

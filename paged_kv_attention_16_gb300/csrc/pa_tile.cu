@@ -687,6 +687,7 @@ __global__ void __launch_bounds__((TileCfg<DQK, DV>::THREADS), 2)
       tc_fence_after();
       const bool write = row_in;
       const bool direct =
+          !p.partial_only &&
           (row_lo - it.kv_base) / it.split_len == (qpos - it.kv_base) / it.split_len;
       // partials are normalised by their own l; a row's own output also
       // counts its head's sink

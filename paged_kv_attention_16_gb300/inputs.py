@@ -255,6 +255,71 @@ def mla_prefill_batch(q_lens, ctx_lens, num_heads=128, kv_lora_rank=512, qk_nope
                            kv_split_tokens=kv_split_tokens)
 
 
+@dataclass
+class SharedPrefixBatch(PagedBatch):
+    """A PagedBatch in groups of requests that share their first positions.
+    block_table names the shared pages in each group's first row only;
+    full_table names every page of every request, as pa_forward reads it."""
+    group_start_loc: torch.Tensor = None
+    prefix_lens: torch.Tensor = None
+    full_table: torch.Tensor = None
+    max_prefix_len: int = 0
+
+
+def shared_prefix_batch(groups, num_heads, num_kv_heads, head_dim, block_size, dtype="bf16",
+                        seed=0, poison=True, slack=0.1, scale=None):
+    """groups: [(prefix, [(q_len, own_len), ...]), ...] -- each group's shared
+    positions (a multiple of block_size) and its requests' new tokens and
+    positions behind the prefix (new tokens included).  Pages are placed and
+    values drawn as in paged_batch; with poison, unused pages, the slots past
+    each request's end and the entries the library must not read are NaN / bad."""
+    g_layout, g_vals = _gen(seed * 7919 + 7), _gen(seed * 104729 + 8)
+    reqs = [(g, q, own) for g, (_, rs) in enumerate(groups) for q, own in rs]
+    for p, rs in groups:
+        if p % block_size or any(q > own or q < 0 for q, own in rs):
+            raise ValueError("prefixes are whole pages, q_len lies in [0, own_len]")
+    S = len(reqs)
+    ctx = [groups[g][0] + own for g, _, own in reqs]
+    own_pages = [-(-own // block_size) for _, _, own in reqs]
+    used = sum(p // block_size for p, _ in groups) + sum(own_pages)
+    pool = used + max(1, math.ceil(slack * used))
+    perm = torch.randperm(pool, generator=g_layout).to(torch.int32)
+    width = max([-(-c // block_size) for c in ctx] + [1])
+    full = torch.full((S, width), -1 if poison else 0, dtype=torch.int32)
+    if poison and width > 1:
+        full[:, 1::2] = pool + 1000
+    table, at, s = full.clone(), 0, 0
+    for p, rs in groups:
+        n = p // block_size
+        for i, _ in enumerate(rs):
+            full[s + i, :n] = perm[at:at + n]
+        if rs:
+            table[s, :n] = perm[at:at + n]
+        at, s = at + n, s + len(rs)
+    for s, (g, _, _) in enumerate(reqs):
+        n = groups[g][0] // block_size
+        for t in (full, table):
+            t[s, n:n + own_pages[s]] = perm[at:at + own_pages[s]]
+        at += own_pages[s]
+    T = sum(q for _, q, _ in reqs)
+    q = _normal((T, num_heads, head_dim), g_vals, dtype)
+    k = _normal((pool, block_size, num_kv_heads, head_dim), g_vals, dtype)
+    v = _normal((pool, block_size, num_kv_heads, head_dim), g_vals, dtype)
+    if poison:
+        _poison_cache([k, v], full, ctx, block_size, pool)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    return SharedPrefixBatch(
+        q=q, k_cache=k, v_cache=v, block_table=table, seq_lens=i32(ctx),
+        query_start_loc=i32(np.cumsum([0] + [x for _, x, _ in reqs]).tolist()),
+        num_heads=num_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, block_size=block_size,
+        scale=scale if scale is not None else 1.0 / math.sqrt(head_dim), dtype=dtype,
+        max_seq_len=max(ctx + [1]),
+        kinds=["decode" if x == 1 else "extend" for _, x, _ in reqs],
+        group_start_loc=i32(np.cumsum([0] + [len(rs) for _, rs in groups]).tolist()),
+        prefix_lens=i32([p for p, _ in groups]), full_table=full,
+        max_prefix_len=max([p for p, _ in groups] + [0]))
+
+
 def _uniform_ints(gen, n, lo, hi):
     """n integers uniform on [lo, hi] (both ends included)."""
     if n == 0:

@@ -24,6 +24,7 @@ PA_DEV_BAD_QSL = 0x8
 PA_DEV_OVERFLOW = 0x10
 PA_DEV_TIMEOUT = 0x20
 PA_DEV_INTERNAL = 0x40
+PA_DEV_NO_PAGES = 0x80
 PA_KV_NHD, PA_KV_HND = 0, 1  # pa_kv_layout
 
 # Every entry point declared in include/pa.h.
@@ -31,7 +32,9 @@ EXPORTS = ("pa_forward", "pa_forward_workspace_bytes", "pa_mla_decode", "pa_cach
            "pa_mla_decode_workspace_bytes", "pa_reserve", "pa_get_device_status",
            "pa_status_string", "pa_num_sms", "pa_debug_gather", "pa_profile_enable",
            "pa_profile_read", "pa_kernel_name", "pa_forward_static_scratch", "pa_forward_ex",
-           "pa_mla_prefill", "pa_mla_prefill_workspace_bytes", "pa_debug_wait_timeout")
+           "pa_mla_prefill", "pa_mla_prefill_workspace_bytes", "pa_debug_wait_timeout",
+           "pa_forward_shared_prefix", "pa_forward_shared_prefix_workspace_bytes",
+           "pa_block_tables", "pa_cache_write_slots")
 PA_K_COUNT = 10
 
 
@@ -110,6 +113,17 @@ def lib():
         L.pa_mla_prefill_workspace_bytes.restype = ctypes.c_size_t
         L.pa_debug_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
         L.pa_debug_wait_timeout.restype = c_int
+        L.pa_forward_shared_prefix.argtypes = (
+            [vp] * 8 + [c_int] * 4 + [c_float, vp, vp] + [c_int] * 8
+            + [ctypes.POINTER(ForwardOptions), vp, ctypes.c_size_t])
+        L.pa_forward_shared_prefix.restype = c_int
+        L.pa_forward_shared_prefix_workspace_bytes.argtypes = [c_int] * 8
+        L.pa_forward_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
+        L.pa_block_tables.argtypes = [vp] * 8 + [c_int, vp] + [c_int] * 5
+        L.pa_block_tables.restype = c_int
+        L.pa_cache_write_slots.argtypes = ([vp] * 5 + [c_int] * 3 + [vp, c_int, c_int]
+                                           + [ctypes.c_longlong] * 2 + [c_int, c_int])
+        L.pa_cache_write_slots.restype = c_int
         L.pa_kernel_name.argtypes = [c_int]
         L.pa_kernel_name.restype = ctypes.c_char_p
         _lib = L
@@ -303,6 +317,171 @@ def pa_cache_write(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_
     return st
 
 
+def _on_device(device, **tensors):
+    """Every tensor given lies on CUDA device `device`, the current one."""
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError("the tensors must lie on the current CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} lies on another device")
+
+
+def _contiguous(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def pa_block_tables(seq_lens, query_start_loc, block_table, slot_mapping, block_size, stream=None,
+                    *, num_blocks, free_pages=None, free_start=None, free_end=None,
+                    positions=None, check=True):
+    """A step's block-table rows and slot map from the request lengths (see
+    include/pa.h).  slot_mapping [T] int64 and, if given, positions [T] int32
+    are written; with free_pages [num_free], free_start [1] and free_end [1]
+    (int32) the pages the requests lack are taken from free_pages[free_start:]
+    and written into block_table [S, max_blocks] in place."""
+    S, T = int(seq_lens.shape[0]), int(slot_mapping.shape[0])
+    _contiguous(torch.int32, seq_lens=seq_lens, query_start_loc=query_start_loc,
+                block_table=block_table, free_pages=free_pages, free_start=free_start,
+                free_end=free_end, positions=positions)
+    _contiguous(torch.int64, slot_mapping=slot_mapping)
+    if query_start_loc.numel() != S + 1 or block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("query_start_loc [S + 1] and block_table [S, max_blocks] go with seq_lens [S]")
+    if positions is not None and positions.numel() != T:
+        raise ValueError("positions must have slot_mapping's length")
+    if (free_start is None) != (free_end is None) or (free_start is None and free_pages is not None):
+        raise ValueError("free_pages, free_start and free_end go together")
+    for t in (free_start, free_end):
+        if t is not None and t.numel() != 1:
+            raise ValueError("free_start and free_end are one int32 each")
+    device = slot_mapping.get_device()
+    _on_device(device, seq_lens=seq_lens, query_start_loc=query_start_loc, block_table=block_table,
+               free_pages=free_pages, free_start=free_start, free_end=free_end,
+               positions=positions)
+    st = lib().pa_block_tables(
+        _ptr(seq_lens), _ptr(query_start_loc), _ptr(free_pages), _ptr(free_start), _ptr(free_end),
+        _ptr(block_table), _ptr(slot_mapping), _ptr(positions), int(block_size),
+        _stream_ptr(stream, device), S, T, int(block_table.shape[1]), int(num_blocks),
+        0 if free_pages is None else int(free_pages.numel()))
+    if check:
+        _check(st, "pa_block_tables")
+    return st
+
+
+def _token_stride(t, name):
+    """Elements from one token's [heads, dim] row to the next; the row itself
+    must be contiguous."""
+    T, Hk, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (Hk > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return int(t.stride(0)) if T > 1 else Hk * D
+
+
+def pa_cache_write_slots(k_new, v_new, k_cache, v_cache, slot_mapping, block_size, stream=None,
+                         kv_layout="nhd", check=True):
+    """The cache write by a slot map (see include/pa.h): k_new / v_new
+    [T, Hk, D], each token's row contiguous and any number of elements from the
+    next (slices of a fused projection); slot_mapping [T] int64, negative slots
+    skipped."""
+    T, Hk, D = (int(x) for x in k_new.shape)
+    dt, layout = _dtype_code(k_new), layout_code(kv_layout)
+    _contiguous(torch.int64, slot_mapping=slot_mapping)
+    _contiguous(k_new.dtype, k_cache=k_cache, v_cache=v_cache)
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or slot_mapping.numel() != T:
+        raise ValueError("k_new and v_new [T, Hk, D] of one type go with slot_mapping [T]")
+    page = (block_size, Hk, D) if layout != PA_KV_HND else (Hk, block_size, D)
+    if tuple(k_cache.shape[1:]) != page or k_cache.shape != v_cache.shape:
+        raise ValueError("the caches' shape does not fit the rows, block_size and kv_layout")
+    device = k_new.get_device()
+    _on_device(device, v_new=v_new, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
+    st = lib().pa_cache_write_slots(
+        _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), Hk, D,
+        int(block_size), _stream_ptr(stream, device), dt, T, _token_stride(k_new, "k_new"),
+        _token_stride(v_new, "v_new"), int(k_cache.shape[0]), layout)
+    if check:
+        _check(st, "pa_cache_write_slots")
+    return st
+
+
+def pa_forward_shared_prefix_workspace_bytes(dtype, num_seqs, num_groups, num_tokens, num_heads,
+                                             num_kv_heads, head_dim, max_seq_len):
+    return lib().pa_forward_shared_prefix_workspace_bytes(
+        int(dtype), int(num_seqs), int(num_groups), int(num_tokens), int(num_heads),
+        int(num_kv_heads), int(head_dim), int(max_seq_len))
+
+
+def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                             group_start_loc, prefix_lens, num_heads, num_kv_heads, head_dim,
+                             block_size, scale, out, stream=None, *, max_seq_len, max_prefix_len,
+                             num_blocks=None, sinks=None, kv_layout="nhd", sliding_window=0,
+                             alibi_slopes=None, alibi_sqrt=False, max_query_len=0,
+                             workspace=None, check=True):
+    """Attention for a batch whose requests share prefixes group by group (see
+    include/pa.h).  workspace: a uint8 tensor of at least
+    pa_forward_shared_prefix_workspace_bytes, for this call alone until it has
+    run; None takes one from torch's allocator for this call, so calls on
+    several streams and captured graphs each have their own."""
+    dt, layout = _dtype_code(q), layout_code(kv_layout)
+    _contiguous(q.dtype, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
+    _contiguous(torch.int32, block_table=block_table, seq_lens=seq_lens,
+                query_start_loc=query_start_loc, group_start_loc=group_start_loc,
+                prefix_lens=prefix_lens)
+    S, NG, T = int(seq_lens.numel()), int(prefix_lens.numel()), int(q.shape[0])
+    page = (block_size, num_kv_heads, head_dim)
+    if layout == PA_KV_HND:
+        page = (num_kv_heads, block_size, head_dim)
+    if tuple(q.shape[1:]) != (num_heads, head_dim) or out.shape != q.shape:
+        raise ValueError("q and out must be [T, num_heads, head_dim]")
+    if tuple(k_cache.shape[1:]) != page or v_cache.shape[1:] != k_cache.shape[1:]:
+        raise ValueError("the caches' shape does not fit the heads, block_size and kv_layout")
+    if (query_start_loc.numel() != S + 1 or group_start_loc.numel() != NG + 1
+            or block_table.dim() != 2 or block_table.shape[0] != S):
+        raise ValueError("query_start_loc [S + 1], block_table [S, max_blocks] and "
+                         "group_start_loc [groups + 1] go with seq_lens [S] and prefix_lens [groups]")
+    for name, t in (("sinks", sinks), ("alibi_slopes", alibi_slopes)):
+        if isinstance(t, torch.Tensor):
+            _contiguous(torch.float32, **{name: t})
+            if t.numel() != num_heads:
+                raise TypeError(f"{name} must be a float32 tensor of num_heads elements")
+    blocks = min(int(k_cache.shape[0]), int(v_cache.shape[0]))
+    if num_blocks is not None:
+        if num_blocks > blocks:
+            raise ValueError("num_blocks exceeds the caches")
+        blocks = int(num_blocks)
+    device = q.get_device()
+    _on_device(device, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+               seq_lens=seq_lens, query_start_loc=query_start_loc,
+               group_start_loc=group_start_loc, prefix_lens=prefix_lens, out=out,
+               workspace=workspace)
+    raw = _stream_ptr(stream, device)
+    need = pa_forward_shared_prefix_workspace_bytes(dt, S, NG, T, num_heads, num_kv_heads,
+                                                    head_dim, max_seq_len)
+    if workspace is None:
+        if raw == _stream_ptr(None, device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:  # allocated for the stream that uses it, so that its reuse is ordered there
+            owner = (torch.cuda.ExternalStream(raw, device=q.device) if raw
+                     else torch.cuda.default_stream(q.device))
+            with torch.cuda.stream(owner):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _contiguous(torch.uint8, workspace=workspace)
+    opts = _forward_options(sinks, layout, sliding_window, alibi_slopes, alibi_sqrt, max_query_len)
+    st = lib().pa_forward_shared_prefix(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+        _ptr(query_start_loc), _ptr(group_start_loc), _ptr(prefix_lens), int(num_heads),
+        int(num_kv_heads), int(head_dim), int(block_size), float(scale), _ptr(out), raw, dt, S,
+        NG, T, int(block_table.shape[1]), blocks, int(max_seq_len), int(max_prefix_len),
+        ctypes.byref(opts), _ptr(workspace), int(workspace.numel()))
+    if check:
+        _check(st, "pa_forward_shared_prefix")
+    return st
+
+
 def pa_debug_gather(k_cache, block_table, seq_lens, block_size, max_seq_len, dense_out,
                     stream=None):
     row_elems = int(k_cache[0, 0].numel())
@@ -352,6 +531,20 @@ def forward(b, out=None, stream=None, kv_split_tokens=None, sinks=None, sliding_
                kv_split_tokens=b.kv_split_tokens if kv_split_tokens is None else kv_split_tokens,
                sinks=sinks, kv_layout=b.kv_layout, sliding_window=sliding_window,
                alibi_slopes=alibi_slopes, alibi_sqrt=alibi_sqrt, max_query_len=max_query_len)
+    return out
+
+
+def forward_shared_prefix(b, out=None, stream=None, sinks=None, max_query_len=0, workspace=None):
+    """pa_forward_shared_prefix on a device-resident SharedPrefixBatch;
+    returns `out`."""
+    if out is None:
+        out = torch.empty_like(b.q)
+    pa_forward_shared_prefix(b.q, b.k_cache, b.v_cache, b.block_table, b.seq_lens,
+                             b.query_start_loc, b.group_start_loc, b.prefix_lens, b.num_heads,
+                             b.num_kv_heads, b.head_dim, b.block_size, b.scale, out, stream,
+                             max_seq_len=b.max_seq_len, max_prefix_len=b.max_prefix_len,
+                             sinks=sinks, kv_layout=b.kv_layout, max_query_len=max_query_len,
+                             workspace=workspace)
     return out
 
 

@@ -1,0 +1,395 @@
+"""pa_forward_shared_prefix against the fp64 oracle on the same contexts
+written out in full (every request's block-table row naming its prefix's pages).
+
+Tolerances, per output element, with A = sum_j p_j |v_j| of the exact row (the
+oracle run on |V|), out the exact output:
+  bf16: every weight is rounded to bf16 once (half a step, 2^-8 relative) before
+        the value product while the sum of weights is kept in fp32, and the
+        output is rounded once: 2^-8 (A + |out|).
+  both: a score is a sum of D products in fp32, off by at most (D + 2) 2^-24
+        s_max with s_max = scale max|q| max|k| (2-norms bound sum |q_d k_d|); a
+        weight is then off by that, times 2 for weight and denominator; sums
+        over N keys of weights and of weighted values are each off by N 2^-24,
+        and 64 more roundings cover exponentials, rescaling and the merge:
+        2^-24 (2 (D + 2) s_max + 2 N + 64) A.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import oracle as orc
+from paged_kv_attention_16_gb300 import inputs, pa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from paged_kv_attention_16_gb300 import build
+    build.build()
+    pa.lib()
+    pa.pa_get_device_status()  # clear
+
+
+def oracle(b, rows=None, sinks=None, absolute=False):
+    v = b.v_cache.abs() if absolute else b.v_cache
+    return orc.paged_attention(
+        inputs.storage_array(b.q), inputs.storage_array(b.k_cache), inputs.storage_array(v),
+        b.full_table.numpy(), b.seq_lens.numpy(), b.query_start_loc.numpy(), b.num_heads,
+        b.num_kv_heads, b.head_dim, b.block_size, b.scale, rows=rows, kv_layout=b.kv_layout,
+        sinks=None if sinks is None else np.asarray(sinks, np.float64))
+
+
+def tolerance(b, want, absolute):
+    q, k = b.q.float(), torch.nan_to_num(b.k_cache.float())
+    s_max = abs(b.scale) * float(q.norm(dim=-1).max()) * float(k.norm(dim=-1).max())
+    N = int(b.seq_lens.max())
+    tol = 2.0 ** -24 * (2 * (b.head_dim + 2) * s_max + 2 * N + 64) * absolute
+    if b.dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (absolute + np.abs(want))
+    return tol
+
+
+def check(b, got, rows=None, sinks=None, what=""):
+    want, absolute = oracle(b, rows, sinks), oracle(b, rows, sinks, absolute=True)
+    g = got.float().cpu().numpy().astype(np.float64).reshape(-1, b.head_dim)
+    w, a = want.reshape(g.shape), absolute.reshape(g.shape)
+    if rows is not None:
+        g, w, a = g[rows], w[rows], a[rows]
+    assert np.isfinite(g).all(), what
+    over = np.abs(g - w) - tolerance(b, w, a)
+    assert over.max(initial=-1.0) <= 0, f"{what}: {int((over > 0).sum())} elements off, worst {over.max()}"
+
+
+def run(b, status=0, sinks=None, **kw):
+    d = pa.to_device(b)
+    out = torch.full_like(d.q, float("nan"))
+    s = None if sinks is None else torch.as_tensor(np.asarray(sinks), dtype=torch.float32).cuda()
+    pa.forward_shared_prefix(d, out=out, sinks=s, **kw)
+    got = pa.pa_get_device_status()
+    assert got == status, f"device status {got:#x}"
+    return out
+
+
+def make(groups, H, Hk, D, bs, dtype="bf16", layout="nhd", seed=0, **kw):
+    b = inputs.shared_prefix_batch(groups, H, Hk, D, bs, dtype=dtype, seed=seed, **kw)
+    return inputs.as_hnd(b) if layout == "hnd" else b
+
+
+def decodes(n, lo, hi, seed):
+    rng = np.random.default_rng(seed)
+    return [(1, int(x)) for x in rng.integers(lo, hi + 1, n)]
+
+
+BATCHES = {
+    # one group of decodes; own parts from a single position on
+    "decode": lambda bs: [(20 * bs, [(1, 1), (1, 2), (1, bs), (1, bs + 1), (1, 70)])],
+    # groups with and without a prefix, of one request, empty, with idle requests
+    "groups": lambda bs: [(0, [(1, 5), (3, 9)]), (bs, [(1, 1)]), (3 * bs, []),
+                          (7 * bs, [(0, 0), (1, 33), (0, 8), (1, 4)]), (11 * bs, [(0, 3)])],
+    # extends: own part all new, one token, many tokens, mixed with decodes
+    "extend": lambda bs: [(5 * bs, [(40, 40), (1, 17), (2, 300), (130, 150)]), (bs, [(9, 9), (1, 1)])],
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk,D,bs,layout", [
+    (8, 2, 128, 16, "nhd"), (4, 4, 64, 16, "hnd"), (16, 1, 64, 64, "nhd"), (8, 4, 128, 128, "hnd"),
+    (16, 2, 128, 48, "nhd"), (2, 1, 64, 256, "nhd"),
+])
+@pytest.mark.parametrize("kind", sorted(BATCHES))
+def test_equals_the_oracle(kind, H, Hk, D, bs, layout, dtype):
+    b = make(BATCHES[kind](bs), H, Hk, D, bs, dtype, layout, seed=H + D + bs)
+    check(b, run(b), what=kind)
+
+
+@pytest.mark.parametrize("n,H,Hk,D,bs", [
+    (3, 8, 8, 128, 16), (31, 8, 2, 64, 16), (33, 8, 2, 128, 16), (64, 16, 4, 64, 64),
+    (65, 16, 4, 128, 16), (130, 16, 1, 128, 64), (257, 2, 2, 64, 16),
+])
+def test_row_block_edges(n, H, Hk, D, bs):
+    """Row counts around the 128-row tiles and the 256-row items."""
+    b = make([(9 * bs, decodes(n, 1, 40, n))], H, Hk, D, bs, seed=n)
+    check(b, run(b, max_query_len=1))
+
+
+@pytest.mark.parametrize("pages", [1, 7, 8, 9, 15, 16, 17, 63, 64, 65, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_lengths_around_the_tiles(pages, dtype):
+    b = make([(16 * pages, decodes(4, 1, 30, pages))], 8, 1, 128, 16, dtype, seed=pages)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("D,bs,layout", [(128, 16, "nhd"), (64, 64, "hnd"), (128, 128, "nhd")])
+def test_long_prefix_is_split_over_the_grid(D, bs, layout):
+    b = make([(24576, decodes(20, 1, 600, 4))], 8, 1, D, bs, layout=layout, seed=4)
+    rows = np.random.default_rng(0).choice(160, 24, replace=False)
+    check(b, run(b, max_query_len=1), rows=np.sort(rows).astype(np.int64))
+
+
+def test_many_groups():
+    """More groups than the split model looks at, more requests than the merge caches."""
+    rng = np.random.default_rng(8)
+    groups = [(16 * int(rng.integers(0, 30)), decodes(int(rng.integers(1, 11)), 1, 30, i))
+              for i in range(220)]
+    b = make(groups, 4, 2, 64, 16, seed=8)
+    assert b.num_seqs > 1024
+    check(b, run(b), rows=np.sort(rng.choice(b.num_tokens * 4, 600, replace=False)).astype(np.int64))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sinks(dtype):
+    b = make(BATCHES["extend"](16), 8, 2, 128, 16, dtype, seed=3)
+    sinks = np.linspace(-60, 60, 8).astype(np.float32)
+    check(b, run(b, sinks=sinks), sinks=sinks)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 2.0])
+def test_scales(scale):
+    b = make(BATCHES["extend"](16), 8, 2, 128, 16, seed=6, scale=scale)
+    check(b, run(b))
+
+
+def test_agrees_with_pa_forward_on_the_full_table():
+    b = make([(640, decodes(9, 1, 200, 1)), (48, [(20, 60), (1, 5)])], 16, 4, 128, 16, seed=9)
+    got = run(b).float()
+    d = pa.to_device(b)
+    d.block_table = d.full_table
+    want = pa.forward(d).float()
+    # both within the stated distance of the exact rows, so within twice that of each other
+    w, a = oracle(b), oracle(b, absolute=True)
+    assert (np.abs((got - want).cpu().numpy()) <= 2 * tolerance(b, w, a)).all()
+
+
+def test_largest_values_and_masked_garbage():
+    """Scores spread over hundreds of units; NaN and infinities everywhere the
+    call must not look."""
+    b = make([(512, decodes(6, 1, 40, 2)), (16, [(30, 31)])], 8, 2, 128, 16, seed=12, scale=3.0)
+    k = b.k_cache
+    k[torch.isnan(k)] = float("inf")
+    check(b, run(b))
+
+
+def test_rows_with_no_finite_score_are_zero():
+    """Every key -inf away from every query: no weight is left."""
+    b = make([(64, [(1, 3), (4, 9)])], 4, 2, 64, 16, seed=13, poison=False)
+    b.q[:], b.k_cache[:] = 0.0, 0.0
+    b.q[..., 0], b.k_cache[..., 0] = 3e38, -3e38
+    assert (run(b).float() == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# bad metadata: a status bit, and zeros in the rows it concerns
+# ---------------------------------------------------------------------------
+
+def _zero_and_right(b, out, dead, what):
+    """Rows of the requests in `dead` are zero, the others the oracle's."""
+    H, qsl = b.num_heads, b.query_start_loc.tolist()
+    zero = [t for s in dead for t in range(qsl[s], qsl[s + 1])]
+    assert (out[zero].float() == 0).all(), what
+    live = [t * H + h for s in range(b.num_seqs) if s not in dead
+            for t in range(qsl[s], qsl[s + 1]) for h in range(H)]
+    check(b, out, rows=np.asarray(live, np.int64), what=what)
+
+
+def _bad(dtype):
+    return make([(96, [(1, 5), (6, 20)]), (160, [(1, 40), (1, 1), (12, 12)]), (0, [(1, 9)])],
+                8, 2, 64, 16, dtype, seed=21)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["prefix_page", "own_page", "not_whole_pages", "negative", "above_bound",
+                                  "tokens_inside", "q_len", "q_bound", "length"])
+def test_bad_group_or_request(what, dtype):
+    b, kw, good = _bad(dtype), {}, _bad(dtype)
+    if what == "prefix_page":
+        b.block_table[2, 4] = b.num_blocks + 3
+        dead, bit = [2, 3, 4], pa.PA_DEV_BAD_BLOCK
+    elif what == "own_page":
+        b.block_table[4, 10] = -1
+        dead, bit = [4], pa.PA_DEV_BAD_BLOCK
+    elif what in ("not_whole_pages", "negative", "above_bound"):
+        b.prefix_lens[1] = {"not_whole_pages": 152, "negative": -16, "above_bound": 176}[what]
+        dead, bit = [2, 3, 4], pa.PA_DEV_BAD_SEQLEN
+    elif what == "tokens_inside":
+        b.seq_lens[1] = 96 + 5  # six new tokens
+        dead, bit = [1], pa.PA_DEV_BAD_SEQLEN
+    elif what == "q_len":
+        b.seq_lens[4] = 11
+        dead, bit = [4], pa.PA_DEV_BAD_QLEN | pa.PA_DEV_BAD_SEQLEN
+    elif what == "q_bound":
+        kw, dead, bit = dict(max_query_len=6), [4], pa.PA_DEV_BAD_QLEN
+    else:
+        b.seq_lens[0] = b.max_seq_len + 1
+        dead, bit = [0], pa.PA_DEV_BAD_SEQLEN
+    _zero_and_right(good, run(b, status=bit, **kw), dead, what)
+
+
+@pytest.mark.parametrize("field,at,value", [
+    ("query_start_loc", 0, 1), ("query_start_loc", 6, 99), ("query_start_loc", 2, 30),
+    ("group_start_loc", 0, 1), ("group_start_loc", 3, 5), ("group_start_loc", 1, 6),
+])
+def test_bad_starts_zero_every_row(field, at, value):
+    b = _bad("bf16")
+    getattr(b, field)[at] = value
+    assert (run(b, status=pa.PA_DEV_BAD_QSL).float() == 0).all()
+
+
+def test_lengths_beyond_the_bound_do_not_leave_the_workspace():
+    """max_seq_len sizes the workspace; longer requests are refused one by one."""
+    b = _bad("bf16")
+    b.max_seq_len = 100  # the last request alone is shorter
+    _zero_and_right(_bad("bf16"), run(b, status=pa.PA_DEV_BAD_SEQLEN), [0, 1, 2, 3, 4], "bound")
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, repeated calls
+# ---------------------------------------------------------------------------
+
+def test_two_calls_give_the_same_bits():
+    b = make([(2048, decodes(40, 1, 500, 3)), (16, [(30, 80)])], 16, 4, 128, 16, seed=30)
+    assert torch.equal(run(b).view(torch.int16), run(b).view(torch.int16))
+
+
+def test_calls_on_two_streams_at_once():
+    made = [make([(4096, decodes(24, 1, 300, i))], 16, 4, 128, 16, seed=40 + i) for i in range(2)]
+    d = [pa.to_device(b) for b in made]
+    want = [pa.forward_shared_prefix(x).clone() for x in d]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in d]
+    outs = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(pa.forward_shared_prefix(d[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+    # an explicit stream that is not the current one
+    out = torch.empty_like(d[0].q)
+    streams[0].wait_stream(torch.cuda.current_stream())
+    pa.forward_shared_prefix(d[0], out=out, stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(out, want[0])
+    assert pa.pa_get_device_status() == 0
+
+
+def test_two_captured_graphs_replayed_at_once():
+    made = [make([(4096, decodes(24, 1, 300, i))], 16, 4, 128, 16, seed=50 + i) for i in range(2)]
+    d = [pa.to_device(b) for b in made]
+    want = [pa.forward_shared_prefix(x).clone() for x in d]
+    outs, graphs = [torch.empty_like(x.q) for x in d], []
+    torch.cuda.synchronize()
+    for x, o in zip(d, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.forward_shared_prefix(x, out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in d]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    # the graph reads its metadata when it runs: shorter own parts
+    b = made[0]
+    b.seq_lens -= (b.seq_lens - b.max_prefix_len - 1) // 2
+    d[0].seq_lens.copy_(b.seq_lens)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    check(b, outs[0])
+    assert pa.pa_get_device_status() == 0
+
+
+def test_a_workspace_of_the_caller():
+    b = make([(320, decodes(7, 1, 50, 5))], 8, 2, 128, 16, seed=60)
+    need = pa.pa_forward_shared_prefix_workspace_bytes(pa.PA_BF16, b.num_seqs, 1, b.num_tokens, 8, 2,
+                                                       128, b.max_seq_len)
+    ws = torch.full((need + 512,), 0xAB, dtype=torch.uint8, device="cuda")
+    check(b, run(b, workspace=ws[:need]))
+    assert (ws[need:] == 0xAB).all()
+    with pytest.raises(pa.PaError, match="workspace"):
+        run(b, workspace=ws[:need - 256])
+
+
+# ---------------------------------------------------------------------------
+# a serving loop: block tables, cache write and attention together
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout,block_size,padded", [("nhd", 16, 0), ("hnd", 64, 3)])
+def test_serving_steps_together(layout, block_size, padded):
+    """Two prompts are written once (each by its group's first request), then
+    every request of both groups extends and decodes a few steps: pages and
+    slots from pa_block_tables, rows sliced from a fused projection and written
+    by pa_cache_write_slots, attention by pa_forward_shared_prefix.  Every
+    step's output is the oracle's on the whole history."""
+    H, Hk, D, bs = 8, 2, 64, block_size
+    sizes, prefix = [3, 4], [5 * bs, 2 * bs]
+    S, nb = sum(sizes), 80
+    g = torch.Generator().manual_seed(77)
+    shape = (nb, bs, Hk, D) if layout == "nhd" else (nb, Hk, bs, D)
+    kc = torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    free = torch.randperm(nb, generator=g).to(torch.int32).cuda()
+    counters = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2)]
+    table = torch.full((S, 12), -1, dtype=torch.int32, device="cuda")
+    first = [0, sizes[0]]
+    group_start = torch.tensor([0, sizes[0], S], dtype=torch.int32, device="cuda")
+    prefix_lens = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    groups = [0] * sizes[0] + [1] * sizes[1]
+    history = [[] for _ in range(S)]  # (k, v) rows of the request behind the prefix
+    shared = [None, None]
+    turn = 0
+
+    def step(q_lens, lens, pad):
+        nonlocal turn
+        T = sum(q_lens) + pad
+        qsl = torch.tensor(np.cumsum([0] + q_lens), dtype=torch.int32, device="cuda")
+        seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        slots = torch.empty(T, dtype=torch.int64, device="cuda")
+        pa.pa_block_tables(seq, qsl, table, slots, bs, num_blocks=nb, free_pages=free,
+                           free_start=counters[turn], free_end=counters[1 - turn])
+        turn = 1 - turn
+        rows = torch.randn((T, H + 2 * Hk, D), generator=g).to(torch.bfloat16).cuda()
+        pa.pa_cache_write_slots(rows[:, H:H + Hk], rows[:, H + Hk:], kc, vc, slots, bs,
+                                kv_layout=layout)
+        return rows, qsl, seq
+
+    # the prompts, by the groups' first requests
+    q_lens = [prefix[groups[s]] if s in first else 0 for s in range(S)]
+    rows, qsl, _ = step(q_lens, q_lens, 0)
+    at = 0
+    for gi in range(2):
+        n = prefix[gi]
+        shared[gi] = rows[at:at + n].float().cpu().numpy().astype(np.float64)
+        at += n
+    lens = [prefix[groups[s]] for s in range(S)]
+    for q_lens in ([5, 1, 40, 2, 1, 17, 3], [1] * S, [1, 1, 0, 1, 1, 1, 1], [1] * S):
+        lens = [a + b for a, b in zip(lens, q_lens)]
+        rows, qsl, seq = step(q_lens, lens, padded)
+        T = sum(q_lens)
+        q = rows[:T, :H].contiguous()
+        out = torch.empty_like(q)
+        pa.pa_forward_shared_prefix(q, kc, vc, table, seq, qsl, group_start, prefix_lens, H, Hk, D,
+                                    bs, 0.125, out, max_seq_len=max(lens),
+                                    max_prefix_len=max(prefix), kv_layout=layout)
+        r = rows.float().cpu().numpy().astype(np.float64)
+        got = out.float().cpu().numpy().astype(np.float64)
+        at = 0
+        for s in range(S):
+            history[s].append(r[at:at + q_lens[s], H:])
+            ctx = np.concatenate([shared[groups[s]][:, H:]] + history[s])
+            assert len(ctx) == lens[s]
+            k, v = ctx[:, :Hk], ctx[:, Hk:]
+            for i in range(q_lens[s]):
+                seen = lens[s] - q_lens[s] + i + 1
+                for h in range(H):
+                    x = k[:seen, h // 4] @ r[at + i, h] * 0.125
+                    w = np.exp(x - x.max())
+                    w /= w.sum()
+                    want = w @ v[:seen, h // 4]
+                    tol = 2.0 ** -8 * (w @ np.abs(v[:seen, h // 4]) + np.abs(want)) + 1e-4
+                    assert (np.abs(got[at + i, h] - want) <= tol).all()
+            at += q_lens[s]
+    assert pa.pa_get_device_status() == 0
