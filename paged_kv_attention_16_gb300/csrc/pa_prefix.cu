@@ -1,6 +1,6 @@
 // pa_prefix.cu -- attention for a batch whose requests share long prefixes
-// (pa_forward_shared_prefix): argument checks, the planner, the prefix kernel
-// on CUDA cores and the merge.
+// (pa_forward_shared_prefix): argument checks, the planner, the fp32
+// prefix kernel and the merge (pa_prefix_mma.cu holds the bf16 prefix kernel).
 //
 // Requests come in consecutive groups; the requests of group g see the same
 // first P_g positions.  A row's softmax over [0, P_g) and its own positions is
@@ -251,36 +251,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
 }
 
 // ---------------------------------------------------------------------------
-// prefix part on CUDA cores
+// prefix part on CUDA cores (fp32)
 // ---------------------------------------------------------------------------
 // Four threads share a row (each every fourth 16-byte group of its head_dim
-// values), 64 rows a pass; 32 keys and values at a time in shared memory as
-// fp32.  A row's scores of 8 keys are reduced over its four threads, then
+// values), 64 rows a pass; 32 keys and values at a time in shared memory.  A row's scores of 8 keys are reduced over its four threads, then
 // join the running maximum and sum.  Every key costs 4 D fp32 operations a
 // row: the FMA units bound it.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 32;
 
-template <typename T>
-__device__ inline void load16(const T *src, float *dst);
-template <>
-__device__ inline void load16<float>(const float *src, float *dst) {
-  *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src);
-}
-template <>
-__device__ inline void load16<__nv_bfloat16>(const __nv_bfloat16 *src, float *dst) {
-  const uint4 w = *reinterpret_cast<const uint4 *>(src);
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    dst[2 * i] = bf16lo(x[i]);
-    dst[2 * i + 1] = bf16hi(x[i]);
-  }
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixParams p, int hnd) {
-  constexpr int VEC = 16 / sizeof(T);
   __shared__ __align__(16) float s_k[kSimtKeys][D], s_v[kSimtKeys][D];
   __shared__ int s_page[kSimtKeys];
   const FwdParams &f = p.f;
@@ -289,7 +270,8 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
   pdl_trigger();
   pdl_wait();
   const long long n_items = p.plan->n_items;
-  const T *kc = static_cast<const T *>(p.k_cache), *vc = static_cast<const T *>(p.v_cache);
+  const float *kc = static_cast<const float *>(p.k_cache);
+  const float *vc = static_cast<const float *>(p.v_cache);
   for (long long item = blockIdx.x; item < n_items; item += gridDim.x) {
     const PrefixItem it = prefix_item(p, item, G);
     const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
@@ -298,13 +280,13 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
       const int r = pass * 64 + (tid >> 2);  // row of the item
       const bool in = r < rows;
       const int tok = it.q_start + it.t0 + (in ? r / G : 0), head = it.kvh * G + (in ? r % G : 0);
-      const T *q = static_cast<const T *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
+      const float *q = static_cast<const float *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
       float qv[D / 4], o[D / 4];
 #pragma unroll
       for (int i = 0; i < D / 4; i += 4) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          qv[i + e] = (float)q[i * 4 + c * 4 + e] * f.scale_log2;
+          qv[i + e] = q[i * 4 + c * 4 + e] * f.scale_log2;
           o[i + e] = 0.f;
         }
       }
@@ -325,21 +307,18 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
           s_page[tid] = page;
         }
         __syncthreads();
-        for (int e = tid; e < kSimtKeys * (D / VEC); e += kSimtThreads) {
-          const int j = e / (D / VEC), x = e % (D / VEC) * VEC, page = s_page[j];
-          float kf[VEC] = {}, vf[VEC] = {};
+        for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
+          const int j = e / (D / 4), x = e % (D / 4) * 4, page = s_page[j];
+          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
           if (page >= 0) {
             const int slot = (lo + j) % bs;
             const size_t row = hnd ? ((size_t)page * Hk + it.kvh) * bs + slot
                                    : ((size_t)page * bs + slot) * Hk + it.kvh;
-            load16<T>(kc + row * D + x, kf);
-            load16<T>(vc + row * D + x, vf);
+            k4 = *reinterpret_cast<const float4 *>(kc + row * D + x);
+            v4 = *reinterpret_cast<const float4 *>(vc + row * D + x);
           }
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            s_k[j][x + i] = kf[i];
-            s_v[j][x + i] = vf[i];
-          }
+          *reinterpret_cast<float4 *>(&s_k[j][x]) = k4;
+          *reinterpret_cast<float4 *>(&s_v[j][x]) = v4;
         }
         __syncthreads();
         for (int j0 = 0; j0 < kSimtKeys && lo + j0 < it.kv_hi; j0 += 8) {
@@ -581,9 +560,8 @@ PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_toke
   return l;
 }
 
-template <typename T>
 cudaError_t launch_simt(const PrefixParams &p, int hnd, int num_sms, cudaStream_t st) {
-  auto kern = p.f.head_dim == 128 ? prefix_simt_kernel<T, 128> : prefix_simt_kernel<T, 64>;
+  auto kern = p.f.head_dim == 128 ? prefix_simt_kernel<128> : prefix_simt_kernel<64>;
   return launch_dependent(kern, dim3(num_sms * 2), dim3(kSimtThreads), 0, st, p, hnd);
 }
 
@@ -697,9 +675,8 @@ pa_status pa_forward_shared_prefix(
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
   slot = prof_begin(PA_K_PREFIX, st);
-  const int hnd = c.kv_layout == PA_KV_HND;
-  err = dtype == PA_BF16 ? launch_simt<__nv_bfloat16>(p, hnd, num_sms, st)
-                         : launch_simt<float>(p, hnd, num_sms, st);
+  err = dtype == PA_BF16 ? launch_prefix_mma(p, c.kv_layout, num_sms, st)
+                         : launch_simt(p, c.kv_layout == PA_KV_HND, num_sms, st);
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
   s = launch_rows_and_tiles(c, f, num_sms, st, true);

@@ -69,4 +69,8 @@ __device__ inline PrefixItem prefix_item(const PrefixParams &p, long long item, 
   return it;
 }
 
+// The prefix part of bf16 calls (tensor cores).
+cudaError_t launch_prefix_mma(const PrefixParams &p, int kv_layout, int num_sms,
+                              cudaStream_t stream);
+
 }  // namespace pa
