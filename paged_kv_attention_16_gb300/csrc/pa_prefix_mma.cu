@@ -3,19 +3,20 @@
 //
 // Mathematics: for an item's 256 rows (128 / G tokens x the G heads of one KV
 // head, twice) and the positions [kv_lo, kv_hi) of its split,
-//   S = Q K^T,  m = running row maximum of scale S,  P = 2^(scale log2e S - m),
-//   l = sum P,  O = sum P V,
-// tile by tile of 128 positions, one pass over K and V.  Every position is
+//   S = Q K^T,  P = 2^(scale log2e S - ref),  l = sum P,  O = sum P V,
+// tile by tile of 128 positions, one pass over K and V, with a reference ref for
+// each row that moves (O and l rescaled) only when weights outgrow it.  Every position is
 // visible to every row: no causal mask; only the last tile of a prefix may be
 // short, its missing positions masked by select.
 //
 // One CTA per SM (224 KB of shared memory, all 512 TMEM columns), 16 warps:
 //   warps 0-3, 4-7  softmax of the two 128-row tiles, thread = row (TMEM lane):
-//                   S read once into 128 registers, lazy rescaling of O in
-//                   TMEM (only when the maximum grows by more than 8, base 2),
-//                   P as bf16 over the tile's own S
-//   warps 8, 9      each issues one tile's products (one thread): S of tile j
-//                   (M = 128, N = 128), then O += P V (P from TMEM)
+//                   P stored as bf16 over the
+//                   tile's own S.  The sum of a tile's weights tells whether
+//                   the reference still holds: the maximum of 128 scores and
+//                   its latency leave the loop
+//   warp 8          issues S = Q K^T (M = 128, N = 128) and O += P V (P from
+//                   TMEM, N = head_dim), one row tile after the other
 //   warps 10-13     TMA: K boxes (10, 11) and V boxes (12, 13) into rings that
 //                   both row tiles read
 // While one row tile's softmax runs, the other's products do.  K and V are
@@ -30,11 +31,14 @@ namespace pa {
 namespace {
 
 constexpr int kBN = kPrefixTile;
-constexpr float kTau = 8.0f;  // lazy-rescale headroom (base 2)
+// Half a tile's weights may sum to this much before the reference moves up to its
+// maximum: far from overflow in bf16 and in the fp32 sums, so a row's reference
+// is mostly its first tile's maximum, and no maximum is taken of the others.
+constexpr float kMostSum = 1048576.f;
 constexpr int kThreads = 512;
-constexpr int kIssue0 = 8, kLoad0 = 10, kNumLoad = 4;  // issuing warps 8, 9; loading warps 10 .. 13
-// launch registers 512 x 128; the softmax warpgroups take 200, the others keep 56
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
+constexpr int kIssueWarp = 8, kLoad0 = 10, kLoadEnd = 14;  // 9, 14, 15 idle
+// launch registers 512 x 128; the softmax warpgroups take 176, the others keep 80
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S of row tile x at 128 x, O at 256 + 128 x
 
 template <int D>
@@ -47,9 +51,9 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
   // barriers
-  static constexpr int Q_FULL = 0, Q_FREE = 1, S_FULL = 2, P_FULL = 4, O_DONE = 6, O_FREE = 8,
-                       K_FULL = 10, K_FREE = K_FULL + KST, V_FULL = K_FREE + KST,
-                       V_FREE = V_FULL + VST, NBAR = V_FREE + VST;
+  static constexpr int Q_FULL = 0, Q_FREE = 1, S_FULL = 2, O_HALF = 4, O_DONE = 6, P_HALF = 8,
+                       P_FULL = 10, O_FREE = 12, K_FULL = 14, V_FULL = K_FULL + KST, K_FREE = V_FULL + VST,
+                       V_FREE = K_FREE + KST, NBAR = V_FREE + VST;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 32;
   static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kBN, 0);
@@ -77,6 +81,74 @@ __device__ inline void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// tcgen05.wait::ld, which the uses of these registers stay behind.
+__device__ inline void wait_ld(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));
+}
+
+// 32 bytes in one store.
+__device__ inline void store32(float *dst, const uint32_t (&v)[32], int at, float scale) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[at + i]) * scale;
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]),
+               "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
+// Matrix descriptors of 128-byte-swizzled tiles by their two words: the high
+// one (8-row groups 1024 bytes apart) is the same for every operand here, the
+// low one is the address and the leading offset, both in 16-byte units.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ inline uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
+  return ((saddr >> 4) & 0x3FFFu) | (leading >> 4) << 16;
+}
+
+// The products and commits are run by a whole warp, one lane of it issuing
+// (always the same one).  Run by one lane in a branch of its own, an issue
+// held the thread for 85 clocks (A from shared memory) or 120 (from tensor
+// memory): the operands then pass from ordinary to uniform registers one by
+// one, while in converged code they are uniform from the start.
+
+// tmem_d (+)= A B^T, A and B from shared memory.
+__device__ inline void mma_ss(uint32_t tmem_d, uint32_t alo, uint32_t blo, uint32_t idesc,
+                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+
+// tmem_d (+)= A B, A (bf16 pairs) from tensor memory.
+__device__ inline void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t blo, uint32_t idesc,
+                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+
+// Arrive on `bar` when every product issued so far by the electing lane is done.
+__device__ inline void commit(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_mma_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -100,14 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensor_map(&tm_k);
     prefetch_tensor_map(&tm_v);
     for (int b = 0; b < C::NBAR; ++b) {
-      int n = 1;
-      if (b == C::Q_FREE || (b >= C::K_FULL)) n = 2;  // two issuers / two loading warps
-      if ((b >= C::P_FULL && b < C::P_FULL + 2) || (b >= C::O_FREE && b < C::O_FREE + 2)) n = 4;
-      mbar_init(&bar[b], n);
+      // P and O: the row tile's four warps; a full ring stage: two loading warps
+      const bool softmax = b >= C::P_HALF && b < C::K_FULL, loads = b >= C::K_FULL && b < C::K_FREE;
+      mbar_init(&bar[b], softmax ? 4 : loads ? 2 : 1);
     }
     fence_mbar_init();
   }
-  if (warp == kIssue0) tc_alloc(s_tmem, kTmemCols);
+  if (warp == kIssueWarp) tc_alloc(s_tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -116,9 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long n_items = p.plan->n_items;
   bool dead = false;
 
-  if (warp >= kIssue0) {
+  if (warp >= kIssueWarp) {
     reg_dec<kOtherRegs>();
-    if (warp >= kLoad0 && warp < kLoad0 + kNumLoad) {
+    if (warp >= kLoad0 && warp < kLoadEnd) {
       // ------------------------------------------------------------- loads
       // Two warps for K and two for V, each half of a tile's boxes, one box a
       // lane: K one box per 64-wide chunk and run of `box` positions (the S
@@ -178,69 +249,80 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if (warp < kLoad0 && lane == 0) {
+    } else if (warp == kIssueWarp) {
       // ------------------------------------------------------------- products
-      const int x = warp - kIssue0;  // row tile
-      const uint32_t sq = smem_u32(smem) + x * C::Q_TILE, sk = smem_u32(smem) + C::OFF_K,
-                     sv = smem_u32(smem) + C::OFF_V;
-      const uint32_t tm_s = tmem + x * 128, tm_o = tmem + kTmemO + x * 128;
+      // Row tile 0 then 1: the value product of its weights, and behind it the
+      // scores of the next tile of positions, so that each softmax has the
+      // other row tile's two products to run beside.
+      const uint32_t sq = smem_u32(smem), sk = sq + C::OFF_K, sv = sq + C::OFF_V;
       uint32_t ks = 0, kr = 0, vs = 0, vr = 0;  // ring stage and round
-      uint32_t n = 0, items = 0, mine = 0;      // this tile's S products; items; items with rows here
+      uint32_t items = 0, n0 = 0, n1 = 0;       // value products issued for each row tile
+      uint32_t two_items = 0;                   // items with rows in row tile 1
+      auto scores = [&](int x) {
+        const uint32_t a = desc_lo(sq + x * C::Q_TILE, 16), b = desc_lo(sk + ks * C::KV_BYTES, 16);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {  // 16 columns: 32 bytes, 4 to a chunk
+          const uint32_t off = (kk / 4) * (128 * 128 / 16) + (kk % 4) * 2;
+          mma_ss(tmem + x * 128, a + off, b + off, C::IDESC_S, kk > 0);
+        }
+        commit(&bar[C::S_FULL + x]);
+      };
+      auto free_k = [&]() {
+        commit(&bar[C::K_FREE + ks]);
+        if (++ks == C::KST) ks = 0, ++kr;
+      };
       for (long long item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
         const PrefixItem it = prefix_item(p, item, G);
-        const bool active = (it.q_len - it.t0) * G > x * 128;
+        const bool two = (it.q_len - it.t0) * G > 128;
         mbar_wait(&bar[C::Q_FULL], items & 1, dead, f.status);
+        mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
+        // (the weights of the item before have been read: O_DONE was awaited)
+        scores(0);
+        if (two) scores(1);
+        free_k();
         for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN) {
-          mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
-          if (active) {
-            // the S buffer holds P until the product that reads it is done
-            if (n > 0) mbar_wait(&bar[C::O_DONE + x], (n - 1) & 1, dead, f.status);
-            tc_fence_after();
-            const uint32_t kb = sk + ks * C::KV_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const int h = kk / 4, sub = kk % 4;
-              tc_mma_bf16(tm_s, umma_desc_sw128(sq + h * 128 * 128 + sub * 32, 16, 1024),
-                          umma_desc_sw128(kb + h * kBN * 128 + sub * 32, 16, 1024), C::IDESC_S,
-                          kk > 0);
-            }
-            tc_commit(&bar[C::S_FULL + x]);
-            tc_commit(&bar[C::K_FREE + ks]);
-          } else {
-            mbar_arrive(&bar[C::K_FREE + ks]);
-          }
-          if (++ks == C::KST) ks = 0, ++kr;
-          if (active) mbar_wait(&bar[C::P_FULL + x], n & 1, dead, f.status);
+          const bool more = lo + kBN < it.kv_hi;
           mbar_wait(&bar[C::V_FULL + vs], vr & 1, dead, f.status);
-          if (active) {
-            if (lo == it.kv_lo && mine > 0)
-              mbar_wait(&bar[C::O_FREE + x], (mine - 1) & 1, dead, f.status);
-            tc_fence_after();
-            const uint32_t vb = sv + vs * C::KV_BYTES;
+          // the leading offset steps to the next 64-wide chunk of the box
+          const uint32_t b = desc_lo(sv + vs * C::KV_BYTES, box * 128);
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk) {
-              // 16 V rows; the leading offset steps to the next 64-wide chunk
-              const int r = kk * 16;
-              const uint32_t a = vb + (r / box) * C::NH * box * 128 + (r % box) * 128;
-              tc_mma_bf16_ts(tm_o, tm_s + kk * 8, umma_desc_sw128(a, box * 128, 1024), C::IDESC_PV,
-                             lo > it.kv_lo || kk > 0);
+          for (int x = 0; x < 2; ++x) {
+            if (x && !two) break;
+            const bool last = x || !two;
+            uint32_t &n = x ? n1 : n0;
+            const uint32_t before = x ? two_items : items;  // items with rows here
+            if (lo == it.kv_lo && before > 0)
+              mbar_wait(&bar[C::O_FREE + x], (before - 1) & 1, dead, f.status);
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk) {  // 16 V rows
+              if (kk == 0 || kk == kBN / 32) {
+                mbar_wait(&bar[(kk ? C::P_FULL : C::P_HALF) + x], n & 1, dead, f.status);
+                tc_fence_after();
+              }
+              // row r of the box r / box, each box holding all chunks of its rows
+              const uint32_t r = kk * 16, off = r * 8 + (C::NH - 1) * (r & ~(uint32_t)(box - 1)) * 8;
+              mma_ts(tmem + kTmemO + x * 128, tmem + x * 128 + kk * 8, b + off, C::IDESC_PV,
+                     lo > it.kv_lo || kk > 0);
+              if (kk == kBN / 32 - 1) commit(&bar[C::O_HALF + x]);
             }
-            tc_commit(&bar[C::O_DONE + x]);
-            tc_commit(&bar[C::V_FREE + vs]);
+            commit(&bar[C::O_DONE + x]);
+            if (last) commit(&bar[C::V_FREE + vs]);
+            if (more && x == 0) mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
+            // the scores go over the weights that the product reads
+            mbar_wait(&bar[C::O_DONE + x], n & 1, dead, f.status);
             ++n;
-          } else {
-            mbar_arrive(&bar[C::V_FREE + vs]);
+            if (more) {
+              scores(x);
+              if (last) free_k();
+            }
           }
           if (++vs == C::VST) vs = 0, ++vr;
         }
-        if (active) {
-          tc_commit(&bar[C::Q_FREE]);
-          ++mine;
-        } else {
-          mbar_arrive(&bar[C::Q_FREE]);
-        }
+        two_items += two;
+        commit(&bar[C::Q_FREE]);
       }
-      // no commit of this thread may land after the CTA is gone
+      // no commit may land after the CTA is gone
       if (items > 0) mbar_wait(&bar[C::Q_FREE], (items - 1) & 1, dead, f.status);
     }
     __syncwarp();
@@ -251,8 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + lane_off + x * 128, tm_o = tmem + lane_off + kTmemO + x * 128;
     const float c2 = f.scale_log2;
-    // 2^(c s - m) as one multiply-add needs c > 0 (the maximum is then c max s)
+    // 2^(c s - ref) as one multiply-add needs c > 0 (the maximum is then c max s)
     const bool fold = c2 > 0.f;
+    const float cs = fold ? c2 : 1.f;
     uint32_t n = 0;
     for (long long item = blockIdx.x; item < n_items; item += gridDim.x) {
       const PrefixItem it = prefix_item(p, item, G);
@@ -274,75 +357,123 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool item_bad = s_bad[x] != 0;
       const bool warp_active = (warp & 3) * 32 < rows;  // its other rows are padding
-      float m = -INFINITY, l = 0.f;
+      float ref = 0.f, l = 0.f;  // the weights' reference exponent and their sum
       for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN, ++n) {
         mbar_wait(&bar[C::S_FULL + x], n & 1, dead, f.status);
         tc_fence_after();
         if (warp_active) {
-          float s[kBN];
+          // 64 columns from h0 on: scaled where the scale does not fold, masked
+          // past the split.
+          auto finish = [&](uint32_t(&u)[2][32], int h0) {
+            if (!fold) {
 #pragma unroll
-          for (int c0 = 0; c0 < kBN; c0 += 32)
-            tc_ld32(tm_s + c0, *reinterpret_cast<uint32_t(*)[32]>(s + c0));
-          tc_wait_ld();
-          if (!fold) {
-#pragma unroll
-            for (int c = 0; c < kBN; ++c) s[c] *= c2;
-          }
-          if (lo + kBN > it.kv_hi) {
-#pragma unroll
-            for (int c = 0; c < kBN; ++c) s[c] = lo + c < it.kv_hi ? s[c] : -INFINITY;
-          }
-          float mxa[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) mxa[c] = s[c];
-#pragma unroll
-          for (int c = 8; c < kBN; c += 2)
-            mxa[(c >> 1) & 7] = fmax3(mxa[(c >> 1) & 7], s[c], s[c + 1]);
-          float mx = fmax3(fmax3(mxa[0], mxa[1], mxa[2]), fmax3(mxa[3], mxa[4], mxa[5]),
-                           fmaxf(mxa[6], mxa[7]));
-          if (fold && mx != -INFINITY) mx *= c2;
-          float alpha = 1.f;
-          bool rescale = false;
-          if (mx > m + kTau) {
-            alpha = fast_exp2(m - mx);
-            l *= alpha;
-            m = mx;
-            rescale = lo > it.kv_lo;
-          }
-          if (__any_sync(0xffffffffu, rescale)) {
-            // (S of this tile was issued after the last product on O was done)
-            const float a = rescale ? alpha : 1.f;
-#pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              uint32_t raw[16];
-              tc_ld16(tm_o + c0, raw);
-              tc_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
-              tc_st16(tm_o + c0, raw);
+              for (int c = 0; c < 64; ++c)
+                u[c / 32][c % 32] = __float_as_uint(__uint_as_float(u[c / 32][c % 32]) * c2);
             }
-            tc_wait_st();
-          }
-          const float mu = m == -INFINITY ? 0.f : m;
-          const float cs = fold ? c2 : 1.f;
-          float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (lo + h0 + 64 > it.kv_hi) {
 #pragma unroll
-          for (int c0 = 0; c0 < kBN; c0 += 32) {
-            uint32_t pw[16];
+              for (int c = 0; c < 64; ++c)
+                if (lo + h0 + c >= it.kv_hi) u[c / 32][c % 32] = 0xff800000u;  // -inf
+            }
+          };
+          // Their weights as bf16 pairs (the tensor core's operand); the sum,
+          // of the weights before that rounding, stays fp32.
+          auto weights = [&](const uint32_t(&u)[2][32], uint32_t(&pw)[32]) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < 16; ++w) {
-              float a0 = -mu, a1 = -mu;
-              ffma2(a0, a1, s[c0 + 2 * w], s[c0 + 2 * w + 1], cs, cs);
+            for (int w = 0; w < 32; ++w) {
+              float a0 = -ref, a1 = -ref;
+              ffma2(a0, a1, __uint_as_float(u[w / 16][2 * w % 32]),
+                    __uint_as_float(u[w / 16][2 * w % 32 + 1]), cs, cs);
               const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-              ffma2(sum[2 * (w & 3)], sum[2 * (w & 3) + 1], p0, p1, 1.f, 1.f);
-              // weights to bf16 for the tensor core; their sum stays fp32
+              ffma2(acc[2 * (w & 1)], acc[2 * (w & 1) + 1], p0, p1, 1.f, 1.f);
               const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
               pw[w] = *reinterpret_cast<const uint32_t *>(&h2);
             }
-            tc_st16(tm_s + c0 / 2, pw);
+            return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          };
+          // The reference stands until weights outgrow it (or there is none
+          // yet, or a score is not finite).  Then it becomes the maximum of the
+          // columns from h0 on, O and l are rescaled, and the caller makes the
+          // weights again.  O is whole: these scores were issued after the last
+          // tile's product, and for h0 > 0 this tile's first half is awaited.
+          auto rebase = [&](bool redo, int h0) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int h = h0; h < kBN; h += 64) {
+              uint32_t u[2][32];
+              tc_ld32(tm_s + h, u[0]);
+              tc_ld32(tm_s + h + 32, u[1]);
+              wait_ld(u[0], u[1]);
+              finish(u, h);
+#pragma unroll
+              for (int c = 0; c < 64; c += 2)
+                mx = fmax3(mx, __uint_as_float(u[c / 32][c % 32]), __uint_as_float(u[c / 32][c % 32 + 1]));
+            }
+            if (fold && mx != -INFINITY) mx *= c2;
+            float a = 1.f;
+            if (redo && mx != -INFINITY) {
+              if (l != 0.f) a = fast_exp2(ref - mx);
+              l *= a;
+              ref = mx;
+            }
+            if (h0 > 0) {
+              mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
+              tc_fence_after();
+            }
+            if (lo > it.kv_lo || h0 > 0) {
+#pragma unroll
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t raw[16];
+                tc_ld16(tm_o + c0, raw);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
+                tc_st16(tm_o + c0, raw);
+              }
+              tc_wait_st();
+            }
+          };
+          uint32_t ua[2][32], ub[2][32], pw[32];
+          tc_ld32(tm_s, ua[0]);
+          tc_ld32(tm_s + 32, ua[1]);
+          wait_ld(ua[0], ua[1]);
+          tc_ld32(tm_s + 64, ub[0]);
+          tc_ld32(tm_s + 96, ub[1]);
+          finish(ua, 0);
+          float sum = weights(ua, pw);
+          bool redo = !(sum <= kMostSum) || l == 0.f;
+          if (__any_sync(0xffffffffu, redo)) {
+            rebase(redo, 0);
+            tc_ld32(tm_s, ua[0]);
+            tc_ld32(tm_s + 32, ua[1]);
+            wait_ld(ua[0], ua[1]);
+            finish(ua, 0);
+            sum = weights(ua, pw);
           }
+          wait_ld(ub[0], ub[1]);
+          tc_st32(tm_s, pw);  // over columns 0 - 31, read
+          l += sum;
           tc_wait_st();
-          l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::P_HALF + x]);
+          finish(ub, 64);
+          sum = weights(ub, pw);
+          redo = !(sum <= kMostSum) || l == 0.f;
+          if (__any_sync(0xffffffffu, redo)) {
+            rebase(redo, 64);
+            tc_ld32(tm_s + 64, ub[0]);
+            tc_ld32(tm_s + 96, ub[1]);
+            wait_ld(ub[0], ub[1]);
+            finish(ub, 64);
+            sum = weights(ub, pw);
+          }
+          tc_st32(tm_s + 32, pw);
+          l += sum;
+          tc_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&bar[C::P_HALF + x]);
         }
         tc_fence_before();
         __syncwarp();
@@ -360,18 +491,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t raw[32];
           tc_ld32(tm_o + c0, raw);
           tc_wait_ld();
-          if (r < rows) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c0);
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              dst[v] = make_float4(__uint_as_float(raw[4 * v] & keep) * inv,
-                                   __uint_as_float(raw[4 * v + 1] & keep) * inv,
-                                   __uint_as_float(raw[4 * v + 2] & keep) * inv,
-                                   __uint_as_float(raw[4 * v + 3] & keep) * inv);
+          for (int i = 0; i < 32; ++i) raw[i] &= keep;
+          if (r < rows) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) store32(p.part_o + prow * D + c0 + i, raw, i, inv);
           }
         }
         if (r < rows)
-          p.part_lse[prow] = item_bad ? __int_as_float(0x7fc00000) : l > 0.f ? m + log2f(l) : -INFINITY;
+          p.part_lse[prow] = item_bad ? __int_as_float(0x7fc00000) : l > 0.f ? ref + log2f(l) : -INFINITY;
       }
       tc_fence_before();
       __syncwarp();
@@ -381,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kIssue0) tc_dealloc(tmem, kTmemCols);
+  if (warp == kIssueWarp) tc_dealloc(tmem, kTmemCols);
 }
 
 template <int D>
