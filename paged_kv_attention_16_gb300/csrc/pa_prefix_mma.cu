@@ -15,8 +15,8 @@
 //                   tile's own S.  The sum of a tile's weights tells whether
 //                   the reference still holds: the maximum of 128 scores and
 //                   its latency leave the loop
-//   warp 8          issues S = Q K^T (M = 128, N = 128) and O += P V (P from
-//                   TMEM, N = head_dim), one row tile after the other
+//   warps 8, 9      each issues one row tile's S = Q K^T (M = 128, N = 128) and
+//                   O += P V (P from TMEM, N = head_dim), taking turns
 //   warps 10-13     TMA: K boxes (10, 11) and V boxes (12, 13) into rings that
 //                   both row tiles read
 // While one row tile's softmax runs, the other's products do.  K and V are
@@ -36,7 +36,7 @@ constexpr int kBN = kPrefixTile;
 // is mostly its first tile's maximum, and no maximum is taken of the others.
 constexpr float kMostSum = 1048576.f;
 constexpr int kThreads = 512;
-constexpr int kIssueWarp = 8, kLoad0 = 10, kLoadEnd = 14;  // 9, 14, 15 idle
+constexpr int kIssueWarp = 8, kLoad0 = 10, kLoadEnd = 14;  // 14, 15 idle
 // launch registers 512 x 128; the softmax warpgroups take 176, the others keep 80
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S of row tile x at 128 x, O at 256 + 128 x
@@ -52,7 +52,7 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
   // barriers
   static constexpr int Q_FULL = 0, Q_FREE = 1, S_FULL = 2, O_HALF = 4, O_DONE = 6, P_HALF = 8,
-                       P_FULL = 10, O_FREE = 12, K_FULL = 14, V_FULL = K_FULL + KST, K_FREE = V_FULL + VST,
+                       P_FULL = 10, O_FREE = 12, TURN = 14, K_FULL = 16, V_FULL = K_FULL + KST, K_FREE = V_FULL + VST,
                        V_FREE = K_FREE + KST, NBAR = V_FREE + VST;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 32;
@@ -172,9 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensor_map(&tm_k);
     prefetch_tensor_map(&tm_v);
     for (int b = 0; b < C::NBAR; ++b) {
-      // P and O: the row tile's four warps; a full ring stage: two loading warps
-      const bool softmax = b >= C::P_HALF && b < C::K_FULL, loads = b >= C::K_FULL && b < C::K_FREE;
-      mbar_init(&bar[b], softmax ? 4 : loads ? 2 : 1);
+      // P and O: the row tile's four warps; a ring stage: two loading warps,
+      // two issuing ones
+      const bool softmax = b >= C::P_HALF && b < C::TURN, ring = b >= C::K_FULL;
+      mbar_init(&bar[b], softmax ? 4 : ring || b == C::Q_FREE ? 2 : 1);
     }
     fence_mbar_init();
   }
@@ -249,77 +250,100 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if (warp == kIssueWarp) {
+    } else if (warp < kLoad0) {
       // ------------------------------------------------------------- products
-      // Row tile 0 then 1: the value product of its weights, and behind it the
-      // scores of the next tile of positions, so that each softmax has the
-      // other row tile's two products to run beside.
-      const uint32_t sq = smem_u32(smem), sk = sq + C::OFF_K, sv = sq + C::OFF_V;
+      // The warp of row tile x: the value product of its weights, and behind it
+      // the scores of the next tile of positions.  The two warps take turns,
+      // two products a turn, so that each softmax has the other row tile's
+      // products to run beside; a turn ends when its products are issued, so the
+      // other's next ones queue up behind them.  Both warps take every stage of
+      // the rings and free it, by a commit or, without rows, by an arrival.
+      const int x = warp - kIssueWarp;
+      const uint32_t sq = smem_u32(smem) + x * C::Q_TILE, sk = smem_u32(smem) + C::OFF_K,
+                     sv = smem_u32(smem) + C::OFF_V;
+      const uint32_t tm_s = tmem + x * 128, tm_o = tmem + kTmemO + x * 128;
       uint32_t ks = 0, kr = 0, vs = 0, vr = 0;  // ring stage and round
-      uint32_t items = 0, n0 = 0, n1 = 0;       // value products issued for each row tile
-      uint32_t two_items = 0;                   // items with rows in row tile 1
-      auto scores = [&](int x) {
-        const uint32_t a = desc_lo(sq + x * C::Q_TILE, 16), b = desc_lo(sk + ks * C::KV_BYTES, 16);
+      uint32_t items = 0, n = 0, mine = 0;      // items, value products, items with rows here
+      uint32_t turn = 0;
+      auto take_turn = [&]() {
+        if (x == 1 || turn > 0) mbar_wait(&bar[C::TURN + x], (turn - 1 + x) & 1, dead, f.status);
+        ++turn;
+      };
+      auto pass_turn = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[C::TURN + (x ^ 1)]);
+      };
+      auto scores = [&]() {
+        const uint32_t a = desc_lo(sq, 16), b = desc_lo(sk + ks * C::KV_BYTES, 16);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {  // 16 columns: 32 bytes, 4 to a chunk
           const uint32_t off = (kk / 4) * (128 * 128 / 16) + (kk % 4) * 2;
-          mma_ss(tmem + x * 128, a + off, b + off, C::IDESC_S, kk > 0);
+          mma_ss(tm_s, a + off, b + off, C::IDESC_S, kk > 0);
         }
-        commit(&bar[C::S_FULL + x]);
       };
-      auto free_k = [&]() {
+      auto scores_done = [&]() {
+        commit(&bar[C::S_FULL + x]);
         commit(&bar[C::K_FREE + ks]);
         if (++ks == C::KST) ks = 0, ++kr;
       };
       for (long long item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
         const PrefixItem it = prefix_item(p, item, G);
-        const bool two = (it.q_len - it.t0) * G > 128;
+        const int rows = (it.q_len - it.t0) * G;
+        const bool two = rows > 128;
         mbar_wait(&bar[C::Q_FULL], items & 1, dead, f.status);
+        if (x == 1 && !two) {
+          for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN) {
+            mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
+            mbar_wait(&bar[C::V_FULL + vs], vr & 1, dead, f.status);
+            if (lane == 0) {
+              mbar_arrive(&bar[C::K_FREE + ks]);
+              mbar_arrive(&bar[C::V_FREE + vs]);
+            }
+            if (++ks == C::KST) ks = 0, ++kr;
+            if (++vs == C::VST) vs = 0, ++vr;
+          }
+          if (lane == 0) mbar_arrive(&bar[C::Q_FREE]);
+          continue;
+        }
         mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
         // (the weights of the item before have been read: O_DONE was awaited)
-        scores(0);
-        if (two) scores(1);
-        free_k();
-        for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN) {
+        if (two) take_turn();
+        scores();
+        if (two) pass_turn();
+        scores_done();
+        for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN, ++n) {
           const bool more = lo + kBN < it.kv_hi;
           mbar_wait(&bar[C::V_FULL + vs], vr & 1, dead, f.status);
+          if (more) mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
+          if (lo == it.kv_lo && mine > 0)
+            mbar_wait(&bar[C::O_FREE + x], (mine - 1) & 1, dead, f.status);
           // the leading offset steps to the next 64-wide chunk of the box
           const uint32_t b = desc_lo(sv + vs * C::KV_BYTES, box * 128);
+          mbar_wait(&bar[C::P_HALF + x], n & 1, dead, f.status);
+          if (two) take_turn();
+          tc_fence_after();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (x && !two) break;
-            const bool last = x || !two;
-            uint32_t &n = x ? n1 : n0;
-            const uint32_t before = x ? two_items : items;  // items with rows here
-            if (lo == it.kv_lo && before > 0)
-              mbar_wait(&bar[C::O_FREE + x], (before - 1) & 1, dead, f.status);
-#pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk) {  // 16 V rows
-              if (kk == 0 || kk == kBN / 32) {
-                mbar_wait(&bar[(kk ? C::P_FULL : C::P_HALF) + x], n & 1, dead, f.status);
-                tc_fence_after();
-              }
-              // row r of the box r / box, each box holding all chunks of its rows
-              const uint32_t r = kk * 16, off = r * 8 + (C::NH - 1) * (r & ~(uint32_t)(box - 1)) * 8;
-              mma_ts(tmem + kTmemO + x * 128, tmem + x * 128 + kk * 8, b + off, C::IDESC_PV,
-                     lo > it.kv_lo || kk > 0);
-              if (kk == kBN / 32 - 1) commit(&bar[C::O_HALF + x]);
+          for (int kk = 0; kk < kBN / 16; ++kk) {  // 16 V rows
+            if (kk == kBN / 32) {
+              commit(&bar[C::O_HALF + x]);
+              mbar_wait(&bar[C::P_FULL + x], n & 1, dead, f.status);
+              tc_fence_after();
             }
-            commit(&bar[C::O_DONE + x]);
-            if (last) commit(&bar[C::V_FREE + vs]);
-            if (more && x == 0) mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
-            // the scores go over the weights that the product reads
-            mbar_wait(&bar[C::O_DONE + x], n & 1, dead, f.status);
-            ++n;
-            if (more) {
-              scores(x);
-              if (last) free_k();
-            }
+            // row r of the box r / box, each box holding all chunks of its rows
+            const uint32_t r = kk * 16, off = r * 8 + (C::NH - 1) * (r & ~(uint32_t)(box - 1)) * 8;
+            mma_ts(tm_o, tm_s + kk * 8, b + off, C::IDESC_PV, lo > it.kv_lo || kk > 0);
           }
+          commit(&bar[C::O_DONE + x]);
+          commit(&bar[C::V_FREE + vs]);
           if (++vs == C::VST) vs = 0, ++vr;
+          // the scores go over the weights that the product reads
+          mbar_wait(&bar[C::O_DONE + x], n & 1, dead, f.status);
+          if (more) scores();
+          if (two) pass_turn();
+          if (more) scores_done();
         }
-        two_items += two;
+        ++mine;
         commit(&bar[C::Q_FREE]);
       }
       // no commit may land after the CTA is gone
