@@ -26,10 +26,14 @@ namespace pa {
 namespace {
 
 constexpr int kPlanThreads = 256;
+constexpr int kPlanCache = 1024;        // requests, and groups, planned from shared memory
 constexpr int kMergeThreads = 256;
 constexpr int kMergeCache = 1024;       // requests whose starts the merge keeps in shared memory
 constexpr int kModelGroups = 128;       // groups up to which the split model is evaluated
-constexpr int kRowItemTarget = 2560;    // most row-kernel items the own part aims at
+// The own part's decode rows are cut into about this many items a resident
+// block of the row kernel, and kRowItemTarget at most (it bounds the partials).
+constexpr int kRowItems = 4;
+constexpr int kRowItemTarget = 2560;
 // What an item costs beside its tiles (query loads, the first scores' and the
 // last products' latency, storing and merging 256 partial rows), in tiles.
 constexpr int kItemOverhead = 2;
@@ -42,7 +46,8 @@ constexpr int kItemOverhead = 2;
 // prefix: its length L gives every group ceil(n_g / L) splits, the items run in
 // ceil(items / SMs) waves, and a wave lasts L + kItemOverhead tiles.
 __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const int *s_w, int nmax,
-                                  long long tiles, int *s_best) {
+                                  long long tiles) {
+  __shared__ long long s_cost[kPlanThreads / 32];
   const int NG = p.num_groups, tid = threadIdx.x;
   if (nmax <= 0) return 1;
   if (NG > kModelGroups) {
@@ -50,53 +55,66 @@ __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const i
     const long long L = ceil_div_ll(tiles, 2ll * p.num_sms);
     return (int)(L < 1 ? 1 : L > nmax ? nmax : L);
   }
-  const int s = tid + 1;
+  const int s = tid + 1, L = (nmax + s - 1) / s;
   long long cost = 0x7fffffffffffll;
-  const int L = (nmax + s - 1) / s;
   if (s <= nmax) {
     long long items = 0;
     for (int g = 0; g < NG; ++g) items += (long long)s_w[g] * ((s_n[g] + L - 1) / L);
     if (s == 1 || items <= p.item_cap)
       cost = ceil_div_ll(items, p.num_sms) * (L + kItemOverhead);
   }
-  __shared__ long long s_cost[kPlanThreads / 32];
   long long best = cost << 10 | tid;  // ties: the fewest splits
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
   if ((tid & 31) == 0) s_cost[tid >> 5] = best;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kPlanThreads / 32; ++w) best = min(best, s_cost[w]);
-    *s_best = (int)(best & 1023) + 1;
-  }
-  __syncthreads();
-  return (nmax + *s_best - 1) / *s_best;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) best = min(best, s_cost[w]);
+  const int ns = (int)(best & 1023) + 1;
+  return (nmax + ns - 1) / ns;
 }
 
+// A chain of short steps: what it takes is the latency of each.  The metadata
+// is read once, into shared memory, and every step after that works from there
+// (batches beyond kPlanCache read it again from L2).
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   __shared__ long long scratch[3 * 33];
+  __shared__ int s_qsl[kPlanCache + 1], s_len[kPlanCache], s_gsl[kPlanCache + 1], s_pre[kPlanCache];
   __shared__ int s_n[kModelGroups], s_w[kModelGroups];
-  __shared__ int s_best, s_nmax;
-  __shared__ unsigned long long s_tiles;
+  __shared__ int s_nmax;
+  __shared__ unsigned long long s_tiles, s_work;
   const FwdParams &f = p.f;
   const int S = f.num_seqs, NG = p.num_groups, T = f.num_tokens, tid = threadIdx.x;
   const int Hk = f.num_kv_heads, G = f.num_heads / Hk, H = f.num_heads, bs = f.block_size;
+  const bool cached = S <= kPlanCache && NG <= kPlanCache;
   pdl_trigger();
   pdl_wait();
+  if (cached) {
+    for (int s = tid; s <= S; s += kPlanThreads) {
+      s_qsl[s] = f.qsl[s];
+      if (s < S) s_len[s] = f.seq_lens[s];
+    }
+    for (int g = tid; g <= NG; g += kPlanThreads) {
+      s_gsl[g] = p.group_start[g];
+      if (g < NG) s_pre[g] = p.prefix_lens[g];
+    }
+  }
+  if (tid == 0) {
+    s_nmax = 0;
+    s_tiles = s_work = 0;
+  }
+  __syncthreads();
+  auto qsl = [&](int s) { return cached ? s_qsl[s] : f.qsl[s]; };
+  auto gsl = [&](int g) { return cached ? s_gsl[g] : p.group_start[g]; };
 
   // -- starts: query_start_loc over the tokens, group_start_loc over the requests
   int bad = 0;
-  if (tid == 0) {
-    bad = f.qsl[0] != 0 || f.qsl[S] != T || p.group_start[0] != 0 || p.group_start[NG] != S;
-    s_nmax = 0;
-    s_tiles = 0;
-  }
+  if (tid == 0) bad = qsl(0) != 0 || qsl(S) != T || gsl(0) != 0 || gsl(NG) != S;
   for (int s = tid; s < S; s += kPlanThreads)
-    if (f.qsl[s + 1] < f.qsl[s]) bad = 1;
+    if (qsl(s + 1) < qsl(s)) bad = 1;
   for (int g = tid; g < NG; g += kPlanThreads)
-    if (p.group_start[g + 1] < p.group_start[g]) bad = 1;
-  const bool starts_bad = __syncthreads_or(bad) != 0;
-  if (starts_bad) {
+    if (gsl(g + 1) < gsl(g)) bad = 1;
+  if (__syncthreads_or(bad)) {
     if (tid == 0) {
       atomicOr(f.status, PA_DEV_BAD_QSL);
       p.plan->n_items = 0;
@@ -108,100 +126,102 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     return;
   }
 
-  // -- groups: rows and prefix tiles
   auto group_prefix = [&](int g) {  // -1: bad
-    const int P = p.prefix_lens[g];
+    const int P = cached ? s_pre[g] : p.prefix_lens[g];
     const bool ok = P >= 0 && P <= p.max_prefix_len && P % bs == 0 &&
                     P / bs <= f.max_blocks_per_seq;
     return ok ? P : -1;
   };
+  auto classify = [&](int s, int &g, ReqInfo &r) {  // returns the status bits
+    int lo = 0, hi = NG - 1;
+    while (lo < hi) {  // the last group that starts at or before s
+      const int mid = (lo + hi + 1) >> 1;
+      if (gsl(mid) <= s) lo = mid; else hi = mid - 1;
+    }
+    g = lo;
+    const int P = group_prefix(g);
+    r.q_start = qsl(s);
+    r.q_len = qsl(s + 1) - r.q_start;
+    r.ctx = cached ? s_len[s] : f.seq_lens[s];
+    r.kv_base = P < 0 ? 0 : P;
+    const bool len_ok = r.ctx >= 0 && r.ctx <= f.max_seq_len &&
+                        ceil_div_ll(r.ctx, bs) <= (long long)f.max_blocks_per_seq;
+    const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen);
+    const bool own_ok = P >= 0 && r.ctx - r.q_len >= P;
+    const bool valid = r.q_len > 0 && len_ok && q_ok && own_ok;
+    r.flags = (r.q_len == 1 ? kDecode : kExtend) | (valid ? kFlagValid : 0) |
+              (!f.tile_ok || r.q_len == 1 ? kFlagRowPath : 0);
+    if (r.q_len == 0) return 0u;
+    return (len_ok && own_ok ? 0u : PA_DEV_BAD_SEQLEN) | (q_ok ? 0u : PA_DEV_BAD_QLEN);
+  };
+
+  // -- groups: rows and prefix tiles; requests: the decode rows' own work
   unsigned flags = 0;
-  for (int g = tid; g < NG; g += kPlanThreads) {
-    const int r0 = p.group_start[g], r1 = p.group_start[g + 1];
-    const int q0 = f.qsl[r0], nq = f.qsl[r1] - q0;
+  auto group_of = [&](int g) {
+    const int r0 = gsl(g), r1 = gsl(g + 1), q0 = qsl(r0), nq = qsl(r1) - q0;
     int P = group_prefix(g);
     if (P < 0) {
       if (r1 > r0) flags |= PA_DEV_BAD_SEQLEN;
       P = 0;
     }
     const int nrp = nq > 0 ? (int)ceil_div_ll((long long)nq * G, kPrefixRows) : 0;
-    const int n = nq > 0 ? (P + kPrefixTile - 1) / kPrefixTile : 0;
-    p.grp[g] = PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0, 0};
+    return PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0, 0};
+  };
+  auto tiles_of = [&](const PrefixGroup &g) {
+    return g.q_len > 0 ? (g.prefix + kPrefixTile - 1) / kPrefixTile : 0;
+  };
+  for (int g = tid; g < NG; g += kPlanThreads) {
+    const PrefixGroup gr = group_of(g);
+    const int n = tiles_of(gr);
     if (NG <= kModelGroups) {
       s_n[g] = n;
-      s_w[g] = n > 0 ? Hk * nrp : 0;
+      s_w[g] = n > 0 ? Hk * gr.nrp : 0;
     }
     atomicMax(&s_nmax, n);
-    atomicAdd(&s_tiles, (unsigned long long)n * Hk * nrp);
+    atomicAdd(&s_tiles, (unsigned long long)n * Hk * gr.nrp);
   }
-  __syncthreads();
-  const int L = plan_splits(p, s_n, s_w, s_nmax, (long long)s_tiles, &s_best);
-  long long run = 0;
-  for (int base = 0; base < NG; base += kPlanThreads) {
-    const int g = base + tid;
-    PrefixGroup gr{};
-    long long items = 0;
-    if (g < NG) {
-      gr = p.grp[g];
-      const int n = gr.q_len > 0 ? (gr.prefix + kPrefixTile - 1) / kPrefixTile : 0;
-      const int ns = (n + L - 1) / L;
-      // equal splits; as many as have tiles
-      const int len = ns > 0 ? (n + ns - 1) / ns : 1;
-      gr.nsplit = (n + len - 1) / len;
-      gr.split_len = len * kPrefixTile;
-      items = (long long)Hk * gr.nrp * gr.nsplit;
-    }
-    long long tot;
-    const long long end = block_inclusive_scan(items, scratch, &tot) + run;
-    run += tot;
-    if (g < NG) {
-      gr.item0 = end - items;
-      p.grp[g] = gr;
-      p.grp_end[g] = end;
-    }
-  }
-  const long long n_items = run;
-
-  // -- requests: the own part's lists
-  auto classify = [&](int s, int &g, ReqInfo &r) {
-    int lo = 0, hi = NG - 1;
-    while (lo < hi) {  // the last group that starts at or before s
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.group_start[mid] <= s) lo = mid; else hi = mid - 1;
-    }
-    g = lo;
-    const int P = group_prefix(g);
-    r.q_start = f.qsl[s];
-    r.q_len = f.qsl[s + 1] - r.q_start;
-    r.ctx = f.seq_lens[s];
-    r.kv_base = P < 0 ? 0 : P;
-    const bool len_ok = r.ctx >= 0 && r.ctx <= f.max_seq_len &&
-                        ceil_div_ll(r.ctx, bs) <= (long long)f.max_blocks_per_seq;
-    const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen);
-    const bool own_ok = P >= 0 && r.ctx - r.q_len >= P;
-    unsigned fl = 0;
-    if (r.q_len > 0) {
-      if (!len_ok || !own_ok) fl |= PA_DEV_BAD_SEQLEN;
-      if (!q_ok) fl |= PA_DEV_BAD_QLEN;
-    }
-    const bool valid = r.q_len > 0 && len_ok && q_ok && own_ok;
-    r.flags = (r.q_len == 1 ? kDecode : kExtend) | (valid ? kFlagValid : 0) |
-              (!f.tile_ok || r.q_len == 1 ? kFlagRowPath : 0);
-    return fl;
-  };
-  long long v[1] = {0}, t[1];
+  unsigned long long work = 0;
   for (int s = tid; s < S; s += kPlanThreads) {
     int g;
     ReqInfo r{};
     flags |= classify(s, g, r);
-    if ((r.flags & kFlagValid) && r.q_len == 1) v[0] += r.ctx - r.kv_base;
+    if ((r.flags & kFlagValid) && r.q_len == 1) work += r.ctx - r.kv_base;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  if ((tid & 31) == 0 && work) atomicAdd(&s_work, work);
+  __syncthreads();
+  const int L = plan_splits(p, s_n, s_w, s_nmax, (long long)s_tiles);
+  long long n_items = 0;
+  for (int base = 0; base < NG; base += kPlanThreads) {
+    const int g = base + tid;
+    PrefixGroup gr{};
+    long long v[1] = {0}, tot[1];
+    if (g < NG) {
+      gr = group_of(g);
+      const int n = tiles_of(gr), ns = (n + L - 1) / L;
+      // equal splits; as many as have tiles
+      const int len = ns > 0 ? (n + ns - 1) / ns : 1;
+      gr.nsplit = (n + len - 1) / len;
+      gr.split_len = len * kPrefixTile;
+      v[0] = (long long)Hk * gr.nrp * gr.nsplit;
+    }
+    const long long items = v[0];
+    block_scan_multi<1>(v, scratch, tot);
+    if (g < NG) {
+      gr.item0 = n_items + v[0] - items;
+      p.grp[g] = gr;
+      p.grp_end[g] = n_items + v[0];
+    }
+    n_items += tot[0];
   }
   if (flags) atomicOr(f.status, flags);
-  block_scan_multi<1>(v, scratch, t);
-  // Decode rows: splits as the one-launch decode sizes them, about 8 (4 from
-  // G = 8 on) items a resident block, down to one 64-position stage.
-  const long long target = min((G >= 8 ? 4ll : 8ll) * max(f.row_ctas, 1), (long long)kRowItemTarget);
-  const long long Lw = ceil_div_ll(ceil_div_ll(t[0] * Hk, target), 64) * 64;
+
+  // -- requests: the own part's lists.  Decode rows: splits as the one-launch
+  // decode sizes them, about kRowItems items a resident block, down to one
+  // 64-position stage.
+  const long long target = min((long long)kRowItems * max(f.row_ctas, 1), (long long)kRowItemTarget);
+  const long long Lw = ceil_div_ll(ceil_div_ll((long long)s_work * Hk, target), 64) * 64;
   const int Ld = (int)min(max(Lw, (long long)kFastMinSplit), (long long)kRowMaxSplit);
   // rows of longer requests on the row path (fp32): at most about 4 splits
   const int Lr = (int)min(max((long long)Ld, ceil_div_ll(ceil_div_ll(f.max_seq_len, 4), 16) * 16),
@@ -216,7 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       classify(s, g, r);
       const int own = r.ctx - r.kv_base;
       r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : max(own, 1);
-      r.nsplit = max((int)ceil_div_ll(own, r.split_len), 1);
+      r.nsplit = max((own + r.split_len - 1) / r.split_len, 1);
       if (r.flags & kFlagValid) {
         if (r.flags & kFlagRowPath) cnt[0] = (long long)Hk * r.q_len * r.nsplit;
         else cnt[1] = (long long)Hk * ceil_div_ll((long long)r.q_len * G, kTileRows) * r.nsplit;
@@ -379,128 +399,197 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
 }
 
 // ---------------------------------------------------------------------------
-// merge: one warp per (token, query head)
+// merge
 // ---------------------------------------------------------------------------
+// A row is one (token, query head); out = sum_i w_i O_i with
+// w_i = 2^(lse_i - M) / (sum_j 2^(lse_j - M) + 2^(sink - M)) over the row's
+// prefix partials, then its own.  Eight lanes hold a row's head_dim values and
+// walk its partials with a running maximum, four at a time (their loads are
+// independent); W such groups share a row's partials and meet in shared memory.
+// Bound by the latency of a few dependent loads when rows are few, by reading
+// the partials from L2 when they are many.
+constexpr int kMergeGroups = kMergeThreads / 8;
 
 template <typename T>
-__device__ inline void store_vec(T *dst, const float (&v)[4], int n);
+__device__ inline void store4(T *dst, float a, float b, float c, float d);
 template <>
-__device__ inline void store_vec<float>(float *dst, const float (&v)[4], int n) {
-  for (int x = 0; x < n; ++x) dst[x] = v[x];
+__device__ inline void store4<float>(float *dst, float a, float b, float c, float d) {
+  *reinterpret_cast<float4 *>(dst) = make_float4(a, b, c, d);
 }
 template <>
-__device__ inline void store_vec<__nv_bfloat16>(__nv_bfloat16 *dst, const float (&v)[4], int n) {
+__device__ inline void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float a, float b, float c, float d) {
   // one rounding to nearest even, of the finished output
-  for (int x = 0; x < n; x += 2)
-    *reinterpret_cast<__nv_bfloat162 *>(dst + x) = __floats2bfloat162_rn(v[x], v[x + 1]);
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&x),
+                                               *reinterpret_cast<const uint32_t *>(&y));
 }
 
-// out = sum_i w_i O_i with w_i = 2^(lse_i - M) / (sum_j 2^(lse_j - M) + 2^(sink - M)):
-// the row's prefix partials, then its own.
-template <typename T>
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const PrefixParams p) {
+  constexpr int V = D / 32;                   // float4 values a lane holds
+  constexpr int ROWS = kMergeGroups / W;      // rows a block works on at a time
+  constexpr int SPLIT = W > 1 ? W : 1;
   __shared__ int s_qsl[kMergeCache];
+  __shared__ float4 s_o[W > 1 ? kMergeGroups : 1][W > 1 ? 8 * V : 1];
+  __shared__ float s_m[kMergeGroups], s_l[kMergeGroups];
   const FwdParams &f = p.f;
-  const int S = f.num_seqs, H = f.num_heads, D = f.head_dim, G = H / f.num_kv_heads;
-  const int tid = threadIdx.x, lane = tid & 31, dpl = D / 32;
+  const int S = f.num_seqs, H = f.num_heads, G = H / f.num_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 7, grp = tid >> 3, part = grp % SPLIT;
   pdl_trigger();
   pdl_wait();
   T *out = static_cast<T *>(f.out);
   const long long rows = (long long)f.num_tokens * H;
-  const long long gw = ((long long)blockIdx.x * kMergeThreads + tid) >> 5;
-  const long long nw = ((long long)gridDim.x * kMergeThreads) >> 5;
   const bool all_bad = p.plan->all_bad != 0;
   const bool cached = S <= kMergeCache;
   if (cached) {
     for (int s = tid; s < S; s += kMergeThreads) s_qsl[s] = f.qsl[s];
     __syncthreads();
   }
-  for (long long row = gw; row < rows; row += nw) {
-    const int tok = (int)(row / H), h = (int)(row % H);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    T *dst = out + row * D + lane * dpl;
-    if (all_bad) {
-      store_vec<T>(dst, acc, dpl);
-      continue;
-    }
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {  // the last request that starts at or before tok: its own
-      const int mid = (lo + hi + 1) >> 1;
-      if ((cached ? s_qsl[mid] : f.qsl[mid]) <= tok) lo = mid; else hi = mid - 1;
-    }
-    const ReqInfo r = f.req[lo];
-    if (!(r.flags & kFlagValid)) {
-      store_vec<T>(dst, acc, dpl);
-      continue;
-    }
-    const PrefixGroup g = p.grp[p.req_grp[lo]];
-    const int np = g.nsplit, i = tok - r.q_start, pos = r.ctx - r.q_len + i;
-    const int n = np + (pos - r.kv_base) / r.split_len + 1;
-    const long long own0 = r.partial_base + ((long long)i * H + h) * r.nsplit;
-    // row of the prefix part's blocks, and the step between its splits
-    const long long pr = (long long)(tok - g.q_start) * G + h % G;
-    const long long step = (long long)g.nrp * kPrefixRows;
-    const long long pre0 =
-        (g.item0 + (long long)(h / G) * np * g.nrp + pr / kPrefixRows) * kPrefixRows + pr % kPrefixRows;
-    auto lse_of = [&](int e) {
-      return e < np ? __ldg(p.part_lse + pre0 + e * step) : __ldg(f.part_lse + own0 + e - np);
-    };
-    float M = -INFINITY;
-    int bad = 0;
-    for (int e = lane; e < n; e += 32) {
-      const float v = lse_of(e);
-      if (isnan(v)) bad = 1; else M = fmaxf(M, v);
-    }
+  for (long long row0 = (long long)blockIdx.x * ROWS; row0 < rows; row0 += (long long)gridDim.x * ROWS) {
+    const long long row = row0 + grp / SPLIT;
+    float4 acc[V];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-    }
-    const float sink2 = f.sinks ? __ldg(f.sinks + h) * kLog2eF : -INFINITY;
-    M = fmaxf(M, sink2);
-    if (bad || M == -INFINITY) {
-      store_vec<T>(dst, acc, dpl);
-      continue;
-    }
-    float L = 0.f;
-    for (int e0 = 0; e0 < n; e0 += 32) {
-      const float w_own = e0 + lane < n ? fast_exp2(lse_of(e0 + lane) - M) : 0.f;
-      L += w_own;
-      const int cnt = min(32, n - e0);
-      for (int u0 = 0; u0 < cnt; u0 += 8) {
-        float v[8][4];
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    int h = 0;
+    if (row < rows && !all_bad) {
+      const int tok = (int)(row / H);
+      h = (int)(row % H);
+      int lo = 0, hi = S - 1;
+      while (lo < hi) {  // the last request that starts at or before tok: its own
+        const int mid = (lo + hi + 1) >> 1;
+        if ((cached ? s_qsl[mid] : f.qsl[mid]) <= tok) lo = mid; else hi = mid - 1;
+      }
+      const ReqInfo r = f.req[lo];
+      const PrefixGroup g = p.grp[p.req_grp[lo]];
+      if (r.flags & kFlagValid) {
+        const int np = g.nsplit, i = tok - r.q_start, pos = r.ctx - r.q_len + i;
+        const int n = np + (pos - r.kv_base) / r.split_len + 1;
+        const long long own0 = r.partial_base + ((long long)i * H + h) * r.nsplit - np;
+        // row of the prefix part's blocks, and the step between its splits
+        const int pr = (tok - g.q_start) * G + h % G;
+        const long long step = (long long)g.nrp * kPrefixRows;
+        const long long pre0 =
+            (g.item0 + (long long)(h / G) * np * g.nrp + pr / kPrefixRows) * kPrefixRows +
+            pr % kPrefixRows;
+        for (int e0 = part; e0 < n; e0 += 4 * SPLIT) {
+          float lse[4];
+          float4 x[4][V];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int e = e0 + u0 + u;
-          const float *src = (e < np ? p.part_o + (pre0 + e * step) * D
-                                     : f.part_o + (own0 + e - np) * D) + lane * dpl;
-          if (u0 + u < cnt) {
-            if (dpl == 4) {
-              const float4 x = __ldg(reinterpret_cast<const float4 *>(src));
-              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
-            } else {
-              const float2 x = __ldg(reinterpret_cast<const float2 *>(src));
-              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = v[u][3] = 0.f;
+          for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * SPLIT;
+            const long long at = e < np ? pre0 + e * step : own0 + e;
+            const float *src = (e < np ? p.part_o : f.part_o) + at * D + lane * 4;
+            lse[u] = -INFINITY;
+            if (e < n) {
+              lse[u] = __ldg((e < np ? p.part_lse : f.part_lse) + at);
+#pragma unroll
+              for (int v = 0; v < V; ++v) x[u][v] = __ldg(reinterpret_cast<const float4 *>(src + v * 32));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (e0 + u * SPLIT >= n) break;
+            // (a bad split's NaN makes m NaN from here on; a split with no
+            // weight adds 0 O, which keeps the NaN of a NaN input)
+            const float top = lse[u] > m || isnan(lse[u]) ? lse[u] : m;
+            const float a = m == -INFINITY ? 0.f : fast_exp2(m - top);
+            const float w = lse[u] == -INFINITY ? 0.f : fast_exp2(lse[u] - top);
+            m = top;
+            l = fmaf(l, a, w);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              acc[v].x = fmaf(acc[v].x, a, w * x[u][v].x);
+              acc[v].y = fmaf(acc[v].y, a, w * x[u][v].y);
+              acc[v].z = fmaf(acc[v].z, a, w * x[u][v].z);
+              acc[v].w = fmaf(acc[v].w, a, w * x[u][v].w);
             }
           }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (u0 + u >= cnt) break;
-          const float w = __shfl_sync(0xffffffffu, w_own, u0 + u);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) acc[x] = fmaf(w, v[u][x], acc[x]);
-        }
       }
     }
+    if constexpr (W > 1) {
+      // the row's groups: (m, l, O) to shared memory, joined by the first one
+      __syncthreads();  // the rows before are read
+      if (lane == 0) {
+        s_m[grp] = m;
+        s_l[grp] = l;
+      }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (f.sinks) L += fast_exp2(sink2 - M);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+      for (int v = 0; v < V; ++v) s_o[grp][v * 8 + lane] = acc[v];
+      __syncthreads();
+      if (part == 0) {
+        float top = m;
+#pragma unroll 4
+        for (int k = 1; k < W; ++k) {
+          const float v = s_m[grp + k];
+          if (isnan(v) || v > top) top = v;
+          if (isnan(top)) break;
+        }
+        const float a = m == -INFINITY ? 0.f : fast_exp2(m - top);
+        l *= a;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x] *= inv;
-    store_vec<T>(dst, acc, dpl);
+        for (int v = 0; v < V; ++v) {
+          acc[v].x *= a;
+          acc[v].y *= a;
+          acc[v].z *= a;
+          acc[v].w *= a;
+        }
+#pragma unroll 4
+        for (int k = 1; k < W; ++k) {
+          const float mk = s_m[grp + k], b = mk == -INFINITY ? 0.f : fast_exp2(mk - top);
+          l = fmaf(s_l[grp + k], b, l);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float4 o = s_o[grp + k][v * 8 + lane];
+            acc[v].x = fmaf(o.x, b, acc[v].x);
+            acc[v].y = fmaf(o.y, b, acc[v].y);
+            acc[v].z = fmaf(o.z, b, acc[v].z);
+            acc[v].w = fmaf(o.w, b, acc[v].w);
+          }
+        }
+        m = top;
+      }
+    }
+    if (row < rows && part == 0) {
+      // the sink joins the denominator once, with no value; a row with no
+      // weight is 0 O, one with a bad page zero
+      float inv = 0.f;
+      if (m != -INFINITY && !isnan(m)) {
+        float k = 1.f;
+        if (f.sinks) {
+          const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = fmaxf(m, sink2);
+          k = fast_exp2(m - top);
+          l = l * k + fast_exp2(sink2 - top);
+        }
+        inv = l > 0.f ? k / l : 0.f;
+      }
+      const bool zero = isnan(m);
+      T *dst = out + row * D + lane * 4;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (zero) store4<T>(dst + v * 32, 0.f, 0.f, 0.f, 0.f);
+        else store4<T>(dst + v * 32, acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+      }
+    }
   }
+}
+
+template <typename T, int D>
+cudaError_t launch_merge_d(const PrefixParams &p, cudaStream_t st) {
+  // Groups a row: enough of them to give every SM work.  Few rows (a small
+  // decode batch) have many partials each, many rows few.
+  const long long rows = (long long)p.f.num_tokens * p.f.num_heads, sms = p.num_sms;
+  const int W = rows <= 4 * sms ? 16 : rows <= 64 * sms ? 4 : 1;
+  auto kern = W == 16 ? prefix_merge_kernel<T, D, 16>
+              : W == 4 ? prefix_merge_kernel<T, D, 4> : prefix_merge_kernel<T, D, 1>;
+  const long long blocks = std::min(ceil_div_ll(rows * W, kMergeGroups), sms * 8);
+  return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p);
+}
+
+template <typename T>
+cudaError_t launch_merge(const PrefixParams &p, cudaStream_t st) {
+  return p.f.head_dim == 128 ? launch_merge_d<T, 128>(p, st) : launch_merge_d<T, 64>(p, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -682,13 +771,7 @@ pa_status pa_forward_shared_prefix(
   s = launch_rows_and_tiles(c, f, num_sms, st, true);
   if (s != PA_OK) return s;
   slot = prof_begin(PA_K_MERGE, st);
-  const long long warps = (long long)num_tokens * num_heads;
-  const int blocks = (int)std::min(ceil_div_ll(warps, kMergeThreads / 32), (long long)num_sms * 8);
-  err = dtype == PA_BF16
-            ? launch_dependent(prefix_merge_kernel<__nv_bfloat16>, dim3(blocks),
-                               dim3(kMergeThreads), 0, st, p)
-            : launch_dependent(prefix_merge_kernel<float>, dim3(blocks), dim3(kMergeThreads), 0,
-                               st, p);
+  err = dtype == PA_BF16 ? launch_merge<__nv_bfloat16>(p, st) : launch_merge<float>(p, st);
   prof_end(slot, st);
   return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -5,21 +5,22 @@
 // head, twice) and the positions [kv_lo, kv_hi) of its split,
 //   S = Q K^T,  P = 2^(scale log2e S - ref),  l = sum P,  O = sum P V,
 // tile by tile of 128 positions, one pass over K and V, with a reference ref for
-// each row that moves (O and l rescaled) only when weights outgrow it.  Every position is
-// visible to every row: no causal mask; only the last tile of a prefix may be
-// short, its missing positions masked by select.
+// each row that moves (O and l rescaled) only when weights outgrow it.  Every
+// position is visible to every row: no causal mask; only the last tile of a
+// prefix may be short, its missing positions masked by select.
 //
 // One CTA per SM (224 KB of shared memory, all 512 TMEM columns), 16 warps:
 //   warps 0-3, 4-7  softmax of the two 128-row tiles, thread = row (TMEM lane):
-//                   P stored as bf16 over the
-//                   tile's own S.  The sum of a tile's weights tells whether
-//                   the reference still holds: the maximum of 128 scores and
-//                   its latency leave the loop
+//                   P stored as bf16 over the tile's own S.  The sum of half a
+//                   tile's weights tells whether the reference still holds: the
+//                   maximum of the scores and its latency leave the loop
 //   warps 8, 9      each issues one row tile's S = Q K^T (M = 128, N = 128) and
 //                   O += P V (P from TMEM, N = head_dim), taking turns
 //   warps 10-13     TMA: K boxes (10, 11) and V boxes (12, 13) into rings that
 //                   both row tiles read
-// While one row tile's softmax runs, the other's products do.  K and V are
+// The turns keep the row tiles half a period apart: while one's softmax runs,
+// the other's products do.  (Without them both row tiles' products went side by
+// side, and so did their softmaxes while the tensor pipe idled.)  K and V are
 // loaded once for 256 rows, so the loads stay below what HBM or L2 give as
 // long as the products bound the tile; with few rows HBM does.
 // A box that lies past the split, or on a bad page, is loaded from a page
@@ -52,7 +53,7 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
   // barriers
   static constexpr int Q_FULL = 0, Q_FREE = 1, S_FULL = 2, O_HALF = 4, O_DONE = 6, P_HALF = 8,
-                       P_FULL = 10, O_FREE = 12, TURN = 14, K_FULL = 16, V_FULL = K_FULL + KST, K_FREE = V_FULL + VST,
+                       P_FULL = 10, O_FREE = 12, TURN = 14, END = 16, K_FULL = 17, V_FULL = K_FULL + KST, K_FREE = V_FULL + VST,
                        V_FREE = K_FREE + KST, NBAR = V_FREE + VST;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 32;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P and O: the row tile's four warps; a ring stage: two loading warps,
       // two issuing ones
       const bool softmax = b >= C::P_HALF && b < C::TURN, ring = b >= C::K_FULL;
-      mbar_init(&bar[b], softmax ? 4 : ring || b == C::Q_FREE ? 2 : 1);
+      mbar_init(&bar[b], softmax ? 4 : ring || b == C::Q_FREE || b == C::END ? 2 : 1);
     }
     fence_mbar_init();
   }
@@ -282,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(tm_s, a + off, b + off, C::IDESC_S, kk > 0);
         }
       };
-      auto scores_done = [&]() {
+      auto scores_done = [&](bool last) {  // last: of the item, which is then done with Q
         commit(&bar[C::S_FULL + x]);
         commit(&bar[C::K_FREE + ks]);
+        if (last) commit(&bar[C::Q_FREE]);
         if (++ks == C::KST) ks = 0, ++kr;
       };
       for (long long item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two) take_turn();
         scores();
         if (two) pass_turn();
-        scores_done();
+        scores_done(it.kv_lo + kBN >= it.kv_hi);
         for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN, ++n) {
           const bool more = lo + kBN < it.kv_hi;
           mbar_wait(&bar[C::V_FULL + vs], vr & 1, dead, f.status);
@@ -341,13 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(&bar[C::O_DONE + x], n & 1, dead, f.status);
           if (more) scores();
           if (two) pass_turn();
-          if (more) scores_done();
+          if (more) scores_done(lo + 2 * kBN >= it.kv_hi);
         }
         ++mine;
-        commit(&bar[C::Q_FREE]);
       }
       // no commit may land after the CTA is gone
-      if (items > 0) mbar_wait(&bar[C::Q_FREE], (items - 1) & 1, dead, f.status);
+      commit(&bar[C::END]);
+      mbar_wait(&bar[C::END], 0, dead, f.status);
     }
     __syncwarp();
   } else {
@@ -386,23 +388,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&bar[C::S_FULL + x], n & 1, dead, f.status);
         tc_fence_after();
         if (warp_active) {
-          // 64 columns from h0 on: scaled where the scale does not fold, masked
-          // past the split.
-          auto finish = [&](uint32_t(&u)[2][32], int h0) {
+          uint32_t ua[2][32], ub[2][32], pw[32];
+          // The 64 scores of columns c0 on, to be completed by take(): awaited,
+          // scaled where the scale does not fold, masked past the split.
+          auto load = [&](uint32_t(&u)[2][32], int c0) {
+            tc_ld32(tm_s + c0, u[0]);
+            tc_ld32(tm_s + c0 + 32, u[1]);
+          };
+          auto take = [&](uint32_t(&u)[2][32], int c0) {
+            wait_ld(u[0], u[1]);
             if (!fold) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
                 u[c / 32][c % 32] = __float_as_uint(__uint_as_float(u[c / 32][c % 32]) * c2);
             }
-            if (lo + h0 + 64 > it.kv_hi) {
+            if (lo + c0 + 64 > it.kv_hi) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
-                if (lo + h0 + c >= it.kv_hi) u[c / 32][c % 32] = 0xff800000u;  // -inf
+                if (lo + c0 + c >= it.kv_hi) u[c / 32][c % 32] = 0xff800000u;  // -inf
             }
           };
           // Their weights as bf16 pairs (the tensor core's operand); the sum,
           // of the weights before that rounding, stays fp32.
-          auto weights = [&](const uint32_t(&u)[2][32], uint32_t(&pw)[32]) {
+          auto weights = [&](const uint32_t(&u)[2][32]) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < 32; ++w) {
@@ -416,84 +424,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return (acc[0] + acc[1]) + (acc[2] + acc[3]);
           };
-          // The reference stands until weights outgrow it (or there is none
-          // yet, or a score is not finite).  Then it becomes the maximum of the
-          // columns from h0 on, O and l are rescaled, and the caller makes the
-          // weights again.  O is whole: these scores were issued after the last
-          // tile's product, and for h0 > 0 this tile's first half is awaited.
-          auto rebase = [&](bool redo, int h0) {
-            float mx = -INFINITY;
+          auto store = [&](int at) {  // (two halves: each leaves as soon as it is made)
+            tc_st16(tm_s + at, *reinterpret_cast<const uint32_t(*)[16]>(pw));
+            tc_st16(tm_s + at + 16, *reinterpret_cast<const uint32_t(*)[16]>(pw + 16));
+          };
+          // The maximum of columns [c0, c1), scaled.
+          auto max_of = [&](int c0, int c1) {
+            float a = -INFINITY, b = -INFINITY;
 #pragma unroll 1
-            for (int h = h0; h < kBN; h += 64) {
-              uint32_t u[2][32];
-              tc_ld32(tm_s + h, u[0]);
-              tc_ld32(tm_s + h + 32, u[1]);
-              wait_ld(u[0], u[1]);
-              finish(u, h);
+            for (; c0 < c1; c0 += 64) {
+              load(ua, c0);
+              take(ua, c0);
 #pragma unroll
-              for (int c = 0; c < 64; c += 2)
-                mx = fmax3(mx, __uint_as_float(u[c / 32][c % 32]), __uint_as_float(u[c / 32][c % 32 + 1]));
+              for (int c = 0; c < 64; c += 4) {
+                a = fmax3(a, __uint_as_float(ua[c / 32][c % 32]), __uint_as_float(ua[c / 32][c % 32 + 1]));
+                b = fmax3(b, __uint_as_float(ua[c / 32][c % 32 + 2]), __uint_as_float(ua[c / 32][c % 32 + 3]));
+              }
             }
-            if (fold && mx != -INFINITY) mx *= c2;
+            return fmaxf(a, b) * cs;
+          };
+          // The row's reference becomes mx, the maximum of scores to come (or
+          // stays: redo false, or nothing but -inf there); O and l follow.
+          auto rebase = [&](float mx, bool redo) {
             float a = 1.f;
             if (redo && mx != -INFINITY) {
               if (l != 0.f) a = fast_exp2(ref - mx);
               l *= a;
               ref = mx;
             }
-            if (h0 > 0) {
-              mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
-              tc_fence_after();
-            }
-            if (lo > it.kv_lo || h0 > 0) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t raw[16];
+              tc_ld16(tm_o + c0, raw);
+              tc_wait_ld();
 #pragma unroll
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                uint32_t raw[16];
-                tc_ld16(tm_o + c0, raw);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
-                tc_st16(tm_o + c0, raw);
-              }
-              tc_wait_st();
+              for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
+              tc_st16(tm_o + c0, raw);
             }
+            tc_wait_st();
           };
-          uint32_t ua[2][32], ub[2][32], pw[32];
-          tc_ld32(tm_s, ua[0]);
-          tc_ld32(tm_s + 32, ua[1]);
-          wait_ld(ua[0], ua[1]);
-          tc_ld32(tm_s + 64, ub[0]);
-          tc_ld32(tm_s + 96, ub[1]);
-          finish(ua, 0);
-          float sum = weights(ua, pw);
-          bool redo = !(sum <= kMostSum) || l == 0.f;
-          if (__any_sync(0xffffffffu, redo)) {
-            rebase(redo, 0);
-            tc_ld32(tm_s, ua[0]);
-            tc_ld32(tm_s + 32, ua[1]);
-            wait_ld(ua[0], ua[1]);
-            finish(ua, 0);
-            sum = weights(ua, pw);
+          // The first tile sets the references.  They stand until some row's
+          // weights outgrow them (or all weights so far are zero, or a score is
+          // not finite): then they move, and the weights are made again.
+          const bool first = lo == it.kv_lo;
+          if (first) {
+            const float mx = max_of(0, kBN);
+            if (mx != -INFINITY) ref = mx;
           }
-          wait_ld(ub[0], ub[1]);
-          tc_st32(tm_s, pw);  // over columns 0 - 31, read
+          load(ua, 0);
+          load(ub, 64);
+          take(ua, 0);
+          float sum = weights(ua);
+          bool redo = !first && (!(sum <= kMostSum) || l == 0.f);
+          if (__any_sync(0xffffffffu, redo)) {
+            // (these scores were issued after the last product on O was done)
+            wait_ld(ub[0], ub[1]);
+            rebase(max_of(0, kBN), redo);
+            load(ua, 0);
+            take(ua, 0);
+            sum = weights(ua);
+          }
+          take(ub, 64);
+          store(0);  // over columns 0 - 31, read
           l += sum;
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[C::P_HALF + x]);
-          finish(ub, 64);
-          sum = weights(ub, pw);
-          redo = !(sum <= kMostSum) || l == 0.f;
+          sum = weights(ub);
+          redo = !first && (!(sum <= kMostSum) || l == 0.f);
           if (__any_sync(0xffffffffu, redo)) {
-            rebase(redo, 64);
-            tc_ld32(tm_s + 64, ub[0]);
-            tc_ld32(tm_s + 96, ub[1]);
-            wait_ld(ub[0], ub[1]);
-            finish(ub, 64);
-            sum = weights(ub, pw);
+            // (the product on the first half's weights is on its way)
+            mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
+            tc_fence_after();
+            rebase(max_of(64, kBN), redo);
+            load(ub, 64);
+            take(ub, 64);
+            sum = weights(ub);
           }
-          tc_st32(tm_s + 32, pw);
+          store(32);
           l += sum;
           tc_wait_st();
         } else if (lane == 0) {
