@@ -31,8 +31,10 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeCache = 1024;       // requests whose starts the merge keeps in shared memory
 constexpr int kModelGroups = 128;       // groups up to which the split model is evaluated
 // The own part's decode rows are cut into about this many items a resident
-// block of the row kernel, and kRowItemTarget at most (it bounds the partials).
-constexpr int kRowItems = 4;
+// block of the row kernel, and kRowItemTarget in all at most (it bounds the
+// partials).  2, 3, 4, 8 items: 90 requests at G = 16 take 38, 40, 42, 57 us of
+// row kernel, 64 at G = 4 take 51.5, 51.4, 51.5, 55.
+constexpr int kRowItems = 2;
 constexpr int kRowItemTarget = 2560;
 // What an item costs beside its tiles (query loads, the first scores' and the
 // last products' latency, storing and merging 256 partial rows), in tiles.
@@ -46,93 +48,93 @@ constexpr int kItemOverhead = 2;
 // prefix: its length L gives every group ceil(n_g / L) splits, the items run in
 // ceil(items / SMs) waves, and a wave lasts L + kItemOverhead tiles.
 __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const int *s_w, int nmax,
-                                  long long tiles) {
-  __shared__ long long s_cost[kPlanThreads / 32];
+                                  unsigned long long tiles) {
+  __shared__ unsigned long long s_cost[kPlanThreads / 32];
   const int NG = p.num_groups, tid = threadIdx.x;
   if (nmax <= 0) return 1;
   if (NG > kModelGroups) {
     // enough units to fill the SMs in most batches: about two items per SM
-    const long long L = ceil_div_ll(tiles, 2ll * p.num_sms);
-    return (int)(L < 1 ? 1 : L > nmax ? nmax : L);
+    const unsigned long long L = (tiles + 2 * p.num_sms - 1) / (2 * p.num_sms);
+    return (int)(L < 1 ? 1 : L > (unsigned long long)nmax ? nmax : L);
   }
-  const int s = tid + 1, L = (nmax + s - 1) / s;
-  long long cost = 0x7fffffffffffll;
-  if (s <= nmax) {
-    long long items = 0;
-    for (int g = 0; g < NG; ++g) items += (long long)s_w[g] * ((s_n[g] + L - 1) / L);
-    if (s == 1 || items <= p.item_cap)
-      cost = ceil_div_ll(items, p.num_sms) * (L + kItemOverhead);
+  const unsigned s = tid + 1, L = ((unsigned)nmax + s - 1) / s;
+  unsigned long long cost = 0x3fffffffffffffull;
+  if (s <= (unsigned)nmax) {
+    unsigned long long items = 0;
+    for (int g = 0; g < NG; ++g) items += (unsigned long long)s_w[g] * (((unsigned)s_n[g] + L - 1) / L);
+    if (s == 1 || items <= (unsigned long long)p.item_cap) {
+      const unsigned waves = ((unsigned)min(items, 0x7fffffffull) + p.num_sms - 1) / p.num_sms;
+      cost = (unsigned long long)waves * (L + kItemOverhead);
+    }
   }
-  long long best = cost << 10 | tid;  // ties: the fewest splits
+  unsigned long long best = cost << 9 | tid;  // ties: the fewest splits
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
   if ((tid & 31) == 0) s_cost[tid >> 5] = best;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) best = min(best, s_cost[w]);
-  const int ns = (int)(best & 1023) + 1;
-  return (nmax + ns - 1) / ns;
+  const unsigned ns = (unsigned)(best & 511) + 1;
+  return (int)(((unsigned)nmax + ns - 1) / ns);
 }
 
 // A chain of short steps: what it takes is the latency of each.  The metadata
-// is read once, into shared memory, and every step after that works from there
-// (batches beyond kPlanCache read it again from L2).
+// is read once, into shared memory, every step after that works from there
+// (batches beyond kPlanCache read it again from L2), and the groups' items and
+// the requests' lists share one scan.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
-  __shared__ long long scratch[3 * 33];
+  __shared__ long long scratch[4 * 33];
   __shared__ int s_qsl[kPlanCache + 1], s_len[kPlanCache], s_gsl[kPlanCache + 1], s_pre[kPlanCache];
   __shared__ int s_n[kModelGroups], s_w[kModelGroups];
   __shared__ int s_nmax;
   __shared__ unsigned long long s_tiles, s_work;
   const FwdParams &f = p.f;
   const int S = f.num_seqs, NG = p.num_groups, T = f.num_tokens, tid = threadIdx.x;
-  const int Hk = f.num_kv_heads, G = f.num_heads / Hk, H = f.num_heads, bs = f.block_size;
+  const int Hk = f.num_kv_heads, G = f.num_heads / Hk, H = f.num_heads;
+  const unsigned bs = f.block_size;
   const bool cached = S <= kPlanCache && NG <= kPlanCache;
-  pdl_trigger();
-  pdl_wait();
-  if (cached) {
-    for (int s = tid; s <= S; s += kPlanThreads) {
-      s_qsl[s] = f.qsl[s];
-      if (s < S) s_len[s] = f.seq_lens[s];
-    }
-    for (int g = tid; g <= NG; g += kPlanThreads) {
-      s_gsl[g] = p.group_start[g];
-      if (g < NG) s_pre[g] = p.prefix_lens[g];
-    }
-  }
   if (tid == 0) {
     s_nmax = 0;
     s_tiles = s_work = 0;
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (cached) {
+    for (int i = tid; i <= max(S, NG); i += kPlanThreads) {
+      if (i <= S) s_qsl[i] = f.qsl[i];
+      if (i < S) s_len[i] = f.seq_lens[i];
+      if (i <= NG) s_gsl[i] = p.group_start[i];
+      if (i < NG) s_pre[i] = p.prefix_lens[i];
+    }
   }
   __syncthreads();
   auto qsl = [&](int s) { return cached ? s_qsl[s] : f.qsl[s]; };
   auto gsl = [&](int g) { return cached ? s_gsl[g] : p.group_start[g]; };
 
-  // -- starts: query_start_loc over the tokens, group_start_loc over the requests
-  int bad = 0;
-  if (tid == 0) bad = qsl(0) != 0 || qsl(S) != T || gsl(0) != 0 || gsl(NG) != S;
-  for (int s = tid; s < S; s += kPlanThreads)
-    if (qsl(s + 1) < qsl(s)) bad = 1;
-  for (int g = tid; g < NG; g += kPlanThreads)
-    if (gsl(g + 1) < gsl(g)) bad = 1;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) {
-      atomicOr(f.status, PA_DEV_BAD_QSL);
-      p.plan->n_items = 0;
-      p.plan->all_bad = 1;
-      for (int x = 0; x < kNumLists; ++x) f.plan->n[x] = 0;
-      for (int x = 0; x < 8; ++x) f.plan->counter[x] = 0;
-      f.plan->qsl_bad = 1;
-    }
-    return;
-  }
-
-  auto group_prefix = [&](int g) {  // -1: bad
+  // a group's prefix, -1 when it is bad
+  auto group_prefix = [&](int g) {
     const int P = cached ? s_pre[g] : p.prefix_lens[g];
-    const bool ok = P >= 0 && P <= p.max_prefix_len && P % bs == 0 &&
-                    P / bs <= f.max_blocks_per_seq;
+    const bool ok = P >= 0 && P <= p.max_prefix_len && (unsigned)P % bs == 0 &&
+                    (unsigned)P / bs <= (unsigned)f.max_blocks_per_seq;
     return ok ? P : -1;
   };
-  auto classify = [&](int s, int &g, ReqInfo &r) {  // returns the status bits
+  unsigned flags = 0;
+  auto group_of = [&](int g) {
+    // (clamped: the starts may not have been found good yet)
+    const int r0 = min(max(gsl(g), 0), S), r1 = min(max(gsl(g + 1), 0), S);
+    const int q0 = qsl(r0), nq = qsl(r1) - q0;
+    int P = group_prefix(g);
+    if (P < 0) {
+      if (r1 > r0) flags |= PA_DEV_BAD_SEQLEN;
+      P = 0;
+    }
+    const int nrp = nq > 0 ? (int)(((long long)nq * G + kPrefixRows - 1) / kPrefixRows) : 0;
+    return PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0, 0};
+  };
+  auto tiles_of = [&](const PrefixGroup &g) {
+    return g.q_len > 0 ? (int)(((unsigned)g.prefix + kPrefixTile - 1) / kPrefixTile) : 0;
+  };
+  auto classify = [&](int s, int &g, ReqInfo &r) {
     int lo = 0, hi = NG - 1;
     while (lo < hi) {  // the last group that starts at or before s
       const int mid = (lo + hi + 1) >> 1;
@@ -145,126 +147,119 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     r.ctx = cached ? s_len[s] : f.seq_lens[s];
     r.kv_base = P < 0 ? 0 : P;
     const bool len_ok = r.ctx >= 0 && r.ctx <= f.max_seq_len &&
-                        ceil_div_ll(r.ctx, bs) <= (long long)f.max_blocks_per_seq;
+                        ((unsigned)r.ctx + bs - 1) / bs <= (unsigned)f.max_blocks_per_seq;
     const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen);
     const bool own_ok = P >= 0 && r.ctx - r.q_len >= P;
     const bool valid = r.q_len > 0 && len_ok && q_ok && own_ok;
     r.flags = (r.q_len == 1 ? kDecode : kExtend) | (valid ? kFlagValid : 0) |
               (!f.tile_ok || r.q_len == 1 ? kFlagRowPath : 0);
-    if (r.q_len == 0) return 0u;
-    return (len_ok && own_ok ? 0u : PA_DEV_BAD_SEQLEN) | (q_ok ? 0u : PA_DEV_BAD_QLEN);
+    if (r.q_len != 0)
+      flags |= (len_ok && own_ok ? 0u : PA_DEV_BAD_SEQLEN) | (q_ok ? 0u : PA_DEV_BAD_QLEN);
   };
 
-  // -- groups: rows and prefix tiles; requests: the decode rows' own work
-  unsigned flags = 0;
-  auto group_of = [&](int g) {
-    const int r0 = gsl(g), r1 = gsl(g + 1), q0 = qsl(r0), nq = qsl(r1) - q0;
-    int P = group_prefix(g);
-    if (P < 0) {
-      if (r1 > r0) flags |= PA_DEV_BAD_SEQLEN;
-      P = 0;
-    }
-    const int nrp = nq > 0 ? (int)ceil_div_ll((long long)nq * G, kPrefixRows) : 0;
-    return PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0, 0};
-  };
-  auto tiles_of = [&](const PrefixGroup &g) {
-    return g.q_len > 0 ? (g.prefix + kPrefixTile - 1) / kPrefixTile : 0;
-  };
+  // -- the starts' checks; the groups' tiles; the decode rows' own work
+  int bad = 0;
+  if (tid == 0) bad = qsl(0) != 0 || qsl(S) != T || gsl(0) != 0 || gsl(NG) != S;
   for (int g = tid; g < NG; g += kPlanThreads) {
+    if (gsl(g + 1) < gsl(g)) bad = 1;
     const PrefixGroup gr = group_of(g);
     const int n = tiles_of(gr);
     if (NG <= kModelGroups) {
       s_n[g] = n;
       s_w[g] = n > 0 ? Hk * gr.nrp : 0;
     }
-    atomicMax(&s_nmax, n);
-    atomicAdd(&s_tiles, (unsigned long long)n * Hk * gr.nrp);
+    if (n > 0) {
+      atomicMax(&s_nmax, n);
+      atomicAdd(&s_tiles, (unsigned long long)n * Hk * gr.nrp);
+    }
   }
   unsigned long long work = 0;
   for (int s = tid; s < S; s += kPlanThreads) {
+    if (qsl(s + 1) < qsl(s)) bad = 1;
     int g;
     ReqInfo r{};
-    flags |= classify(s, g, r);
+    classify(s, g, r);
     if ((r.flags & kFlagValid) && r.q_len == 1) work += r.ctx - r.kv_base;
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
   if ((tid & 31) == 0 && work) atomicAdd(&s_work, work);
-  __syncthreads();
-  const int L = plan_splits(p, s_n, s_w, s_nmax, (long long)s_tiles);
-  long long n_items = 0;
-  for (int base = 0; base < NG; base += kPlanThreads) {
-    const int g = base + tid;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      atomicOr(f.status, PA_DEV_BAD_QSL);
+      p.plan->n_items = 0;
+      p.plan->all_bad = 1;
+      for (int x = 0; x < kNumLists; ++x) f.plan->n[x] = 0;
+      for (int x = 0; x < 8; ++x) f.plan->counter[x] = 0;
+      f.plan->qsl_bad = 1;
+    }
+    return;
+  }
+  if (flags) atomicOr(f.status, flags);
+  const int L = plan_splits(p, s_n, s_w, s_nmax, s_tiles);
+  // The own part's decode rows: about kRowItems items a resident block, down to
+  // one 64-position stage of the row kernel.
+  const unsigned target = min(kRowItems * max(f.row_ctas, 1), kRowItemTarget);
+  const unsigned long long Lw = (s_work * Hk + target - 1) / target;
+  const int Ld = (int)min(max((Lw + 63) / 64 * 64, (unsigned long long)kFastMinSplit),
+                          (unsigned long long)kRowMaxSplit);
+  // rows of longer requests on the row path (fp32): at most about 4 splits
+  const int Lr = min(max(Ld, (f.max_seq_len / 4 + 16) / 16 * 16), kRowMaxSplit);
+
+  // -- the groups' items, and the requests' lists: row items, tile items, partial rows
+  long long sum[4] = {0, 0, 0, 0};
+  for (int base = 0; base < max(S, NG); base += kPlanThreads) {
+    const int i = base + tid;
+    long long cnt[4] = {0, 0, 0, 0}, tot[4];
     PrefixGroup gr{};
-    long long v[1] = {0}, tot[1];
-    if (g < NG) {
-      gr = group_of(g);
+    ReqInfo r{};
+    int g = 0;
+    if (i < NG) {
+      gr = group_of(i);
       const int n = tiles_of(gr), ns = (n + L - 1) / L;
       // equal splits; as many as have tiles
       const int len = ns > 0 ? (n + ns - 1) / ns : 1;
       gr.nsplit = (n + len - 1) / len;
       gr.split_len = len * kPrefixTile;
-      v[0] = (long long)Hk * gr.nrp * gr.nsplit;
+      cnt[0] = (long long)Hk * gr.nrp * gr.nsplit;
     }
-    const long long items = v[0];
-    block_scan_multi<1>(v, scratch, tot);
-    if (g < NG) {
-      gr.item0 = n_items + v[0] - items;
-      p.grp[g] = gr;
-      p.grp_end[g] = n_items + v[0];
-    }
-    n_items += tot[0];
-  }
-  if (flags) atomicOr(f.status, flags);
-
-  // -- requests: the own part's lists.  Decode rows: splits as the one-launch
-  // decode sizes them, about kRowItems items a resident block, down to one
-  // 64-position stage.
-  const long long target = min((long long)kRowItems * max(f.row_ctas, 1), (long long)kRowItemTarget);
-  const long long Lw = ceil_div_ll(ceil_div_ll((long long)s_work * Hk, target), 64) * 64;
-  const int Ld = (int)min(max(Lw, (long long)kFastMinSplit), (long long)kRowMaxSplit);
-  // rows of longer requests on the row path (fp32): at most about 4 splits
-  const int Lr = (int)min(max((long long)Ld, ceil_div_ll(ceil_div_ll(f.max_seq_len, 4), 16) * 16),
-                          (long long)kRowMaxSplit);
-  long long sum[3] = {0, 0, 0};  // row items, tile items, partial rows
-  for (int base = 0; base < S; base += kPlanThreads) {
-    const int s = base + tid;
-    long long cnt[3] = {0, 0, 0};
-    ReqInfo r{};
-    int g = 0;
-    if (s < S) {
-      classify(s, g, r);
+    if (i < S) {
+      classify(i, g, r);
       const int own = r.ctx - r.kv_base;
       r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : max(own, 1);
       r.nsplit = max((own + r.split_len - 1) / r.split_len, 1);
       if (r.flags & kFlagValid) {
-        if (r.flags & kFlagRowPath) cnt[0] = (long long)Hk * r.q_len * r.nsplit;
-        else cnt[1] = (long long)Hk * ceil_div_ll((long long)r.q_len * G, kTileRows) * r.nsplit;
-        cnt[2] = (long long)r.q_len * H * r.nsplit;
+        if (r.flags & kFlagRowPath) cnt[1] = (long long)Hk * r.q_len * r.nsplit;
+        else cnt[2] = (long long)Hk * (((long long)r.q_len * G + kTileRows - 1) / kTileRows) * r.nsplit;
+        cnt[3] = (long long)r.q_len * H * r.nsplit;
       }
     }
-    const long long part = cnt[2];
-    long long tot[3];
-    block_scan_multi<3>(cnt, scratch, tot);
-    if (s < S) {
-      r.partial_base = cnt[2] + sum[2] - part;
-      f.list_end[(size_t)kListRow * S + s] = cnt[0] + sum[0];
-      f.list_end[(size_t)kListTile * S + s] = cnt[1] + sum[1];
-      f.ord[s] = s;
-      f.req[s] = r;
-      p.req_grp[s] = g;
+    const long long items = cnt[0], part = cnt[3];
+    block_scan_multi<4>(cnt, scratch, tot);
+    if (i < NG) {
+      gr.item0 = cnt[0] + sum[0] - items;
+      p.grp[i] = gr;
+      p.grp_end[i] = cnt[0] + sum[0];
+    }
+    if (i < S) {
+      r.partial_base = cnt[3] + sum[3] - part;
+      f.list_end[(size_t)kListRow * S + i] = cnt[1] + sum[1];
+      f.list_end[(size_t)kListTile * S + i] = cnt[2] + sum[2];
+      f.ord[i] = i;
+      f.req[i] = r;
+      p.req_grp[i] = g;
     }
 #pragma unroll
-    for (int x = 0; x < 3; ++x) sum[x] += tot[x];
+    for (int x = 0; x < 4; ++x) sum[x] += tot[x];
   }
   if (tid == 0) {
-    const bool overflow = sum[2] > f.part_cap || n_items > p.item_cap;
+    const bool overflow = sum[3] > f.part_cap || sum[0] > p.item_cap;
     if (overflow) atomicOr(f.status, PA_DEV_OVERFLOW);
-    p.plan->n_items = overflow ? 0 : n_items;
+    p.plan->n_items = overflow ? 0 : sum[0];
     p.plan->all_bad = overflow ? 1 : 0;
     for (int x = 0; x < kNumLists; ++x) f.plan->n[x] = 0;
-    f.plan->n[kListRow] = overflow ? 0 : sum[0];
-    f.plan->n[kListTile] = overflow ? 0 : sum[1];
+    f.plan->n[kListRow] = overflow ? 0 : sum[1];
+    f.plan->n[kListTile] = overflow ? 0 : sum[2];
     for (int x = 0; x < 8; ++x) f.plan->counter[x] = 0;
     f.plan->qsl_bad = overflow ? 1 : 0;
   }
@@ -440,7 +435,9 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
   T *out = static_cast<T *>(f.out);
   const long long rows = (long long)f.num_tokens * H;
   const bool all_bad = p.plan->all_bad != 0;
-  const bool cached = S <= kMergeCache;
+  // a decode batch: token tok is most likely request tok's, no search
+  const bool one = f.max_qlen == 1 && S == f.num_tokens;
+  const bool cached = !one && S <= kMergeCache;
   if (cached) {
     for (int s = tid; s < S; s += kMergeThreads) s_qsl[s] = f.qsl[s];
     __syncthreads();
@@ -456,12 +453,13 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
       const int tok = (int)(row / H);
       h = (int)(row % H);
       int lo = 0, hi = S - 1;
+      if (one && f.req[tok].q_start == tok && f.req[tok].q_len == 1) lo = hi = tok;
       while (lo < hi) {  // the last request that starts at or before tok: its own
         const int mid = (lo + hi + 1) >> 1;
         if ((cached ? s_qsl[mid] : f.qsl[mid]) <= tok) lo = mid; else hi = mid - 1;
       }
       const ReqInfo r = f.req[lo];
-      const PrefixGroup g = p.grp[p.req_grp[lo]];
+      const PrefixGroup g = p.grp[p.num_groups == 1 ? 0 : p.req_grp[lo]];
       if (r.flags & kFlagValid) {
         const int np = g.nsplit, i = tok - r.q_start, pos = r.ctx - r.q_len + i;
         const int n = np + (pos - r.kv_base) / r.split_len + 1;
@@ -580,8 +578,9 @@ cudaError_t launch_merge_d(const PrefixParams &p, cudaStream_t st) {
   // Groups a row: enough of them to give every SM work.  Few rows (a small
   // decode batch) have many partials each, many rows few.
   const long long rows = (long long)p.f.num_tokens * p.f.num_heads, sms = p.num_sms;
-  const int W = rows <= 4 * sms ? 16 : rows <= 64 * sms ? 4 : 1;
+  const int W = rows <= 4 * sms ? 16 : rows <= 16 * sms ? 8 : rows <= 64 * sms ? 4 : 1;
   auto kern = W == 16 ? prefix_merge_kernel<T, D, 16>
+              : W == 8 ? prefix_merge_kernel<T, D, 8>
               : W == 4 ? prefix_merge_kernel<T, D, 4> : prefix_merge_kernel<T, D, 1>;
   const long long blocks = std::min(ceil_div_ll(rows * W, kMergeGroups), sms * 8);
   return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p);
