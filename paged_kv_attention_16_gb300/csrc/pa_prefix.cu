@@ -29,6 +29,7 @@ constexpr int kPlanThreads = 256;
 constexpr int kPlanCache = 1024;        // requests, and groups, planned from shared memory
 constexpr int kMergeThreads = 256;
 constexpr int kMergeCache = 1024;       // requests whose starts the merge keeps in shared memory
+constexpr int kPrefetchGroups = 64;     // groups whose page lists the planner prefetches
 constexpr int kModelGroups = 128;       // groups up to which the split model is evaluated
 // The own part's decode rows are cut into about this many items a resident
 // block of the row kernel, and kRowItemTarget in all at most (it bounds the
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       P = 0;
     }
     const int nrp = nq > 0 ? (int)(((long long)nq * G + kPrefixRows - 1) / kPrefixRows) : 0;
-    return PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0, 0};
+    return PrefixGroup{q0, nq, r0, P, nrp, 0, 0, 0};
   };
   auto tiles_of = [&](const PrefixGroup &g) {
     return g.q_len > 0 ? (int)(((unsigned)g.prefix + kPrefixTile - 1) / kPrefixTile) : 0;
@@ -196,6 +197,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     return;
   }
   if (flags) atomicOr(f.status, flags);
+  // the prefixes' page lists on their way to L2: the next kernel's first loads
+  for (int g = tid >> 5; g < min(NG, kPrefetchGroups); g += kPlanThreads / 32) {
+    const PrefixGroup gr = group_of(g);
+    const char *row = reinterpret_cast<const char *>(f.block_table + (size_t)gr.req0 * f.max_blocks_per_seq);
+    for (unsigned at = (tid & 31) * 128; gr.q_len > 0 && at < (unsigned)gr.prefix / bs * 4; at += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+  }
   const int L = plan_splits(p, s_n, s_w, s_nmax, s_tiles);
   // The own part's decode rows: about kRowItems items a resident block, down to
   // one 64-position stage of the row kernel.
@@ -237,9 +245,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     const long long items = cnt[0], part = cnt[3];
     block_scan_multi<4>(cnt, scratch, tot);
     if (i < NG) {
-      gr.item0 = cnt[0] + sum[0] - items;
+      gr.item0 = (int)(cnt[0] + sum[0] - items);
       p.grp[i] = gr;
-      p.grp_end[i] = cnt[0] + sum[0];
+      p.grp_end[i] = (int)(cnt[0] + sum[0]);
     }
     if (i < S) {
       r.partial_base = cnt[3] + sum[3] - part;
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   if (tid == 0) {
     const bool overflow = sum[3] > f.part_cap || sum[0] > p.item_cap;
     if (overflow) atomicOr(f.status, PA_DEV_OVERFLOW);
-    p.plan->n_items = overflow ? 0 : sum[0];
+    p.plan->n_items = overflow ? 0 : (int)sum[0];
     p.plan->all_bad = overflow ? 1 : 0;
     for (int x = 0; x < kNumLists; ++x) f.plan->n[x] = 0;
     f.plan->n[kListRow] = overflow ? 0 : sum[1];
@@ -284,11 +292,12 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
   const int Hk = f.num_kv_heads;
   pdl_trigger();
   pdl_wait();
-  const long long n_items = p.plan->n_items;
+  const int n_items = p.plan->n_items;
+  const PrefixGroup g0 = p.grp[0];
   const float *kc = static_cast<const float *>(p.k_cache);
   const float *vc = static_cast<const float *>(p.v_cache);
-  for (long long item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const PrefixItem it = prefix_item(p, item, G);
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    const PrefixItem it = prefix_item(p, g0, item, G);
     const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
     const int rows = min(kPrefixRows, (it.q_len - it.t0) * G);
     for (int pass = 0; pass * 64 < rows; ++pass) {
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
         }
       }
       if (in) {
-        const long long prow = item * kPrefixRows + r;
+        const long long prow = (long long)item * kPrefixRows + r;
         const float inv = l > 0.f && !bad ? 1.f / l : 0.f;
 #pragma unroll
         for (int i = 0; i < D / 4; i += 4)
@@ -468,8 +477,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
         const int pr = (tok - g.q_start) * G + h % G;
         const long long step = (long long)g.nrp * kPrefixRows;
         const long long pre0 =
-            (g.item0 + (long long)(h / G) * np * g.nrp + pr / kPrefixRows) * kPrefixRows +
-            pr % kPrefixRows;
+            (long long)(g.item0 + h / G * np * g.nrp + pr / kPrefixRows) * kPrefixRows + pr % kPrefixRows;
         for (int e0 = part; e0 < n; e0 += 4 * SPLIT) {
           float lse[4];
           float4 x[4][V];
@@ -638,7 +646,7 @@ PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_toke
   l.list_end = take(S * kNumLists * sizeof(long long));
   l.pplan = take(sizeof(PrefixPlan));
   l.grp = take(NG * sizeof(PrefixGroup));
-  l.grp_end = take(NG * sizeof(long long));
+  l.grp_end = take(NG * sizeof(int));
   l.req_grp = take(S * sizeof(int));
   l.pre_o = take((size_t)l.item_cap * kPrefixRows * head_dim * sizeof(float));
   l.pre_lse = take((size_t)l.item_cap * kPrefixRows * sizeof(float));
@@ -701,6 +709,7 @@ pa_status pa_forward_shared_prefix(
     return PA_ERR_INVALID_ARG;
   const PrefixLayout lay = prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads,
                                          num_kv_heads, head_dim, max_seq_len);
+  if (lay.item_cap > 0x7fffffffll / 2) return PA_ERR_UNSUPPORTED;  // items are counted in ints
   if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return PA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -752,7 +761,7 @@ pa_status pa_forward_shared_prefix(
   p.num_sms = num_sms;
   p.plan = reinterpret_cast<PrefixPlan *>(ws + lay.pplan);
   p.grp = reinterpret_cast<PrefixGroup *>(ws + lay.grp);
-  p.grp_end = reinterpret_cast<long long *>(ws + lay.grp_end);
+  p.grp_end = reinterpret_cast<int *>(ws + lay.grp_end);
   p.req_grp = reinterpret_cast<int *>(ws + lay.req_grp);
   p.part_o = reinterpret_cast<float *>(ws + lay.pre_o);
   p.part_lse = reinterpret_cast<float *>(ws + lay.pre_lse);

@@ -23,12 +23,11 @@ struct PrefixGroup {
   int nrp;          // 256-row blocks of a KV head: ceil(q_len * G / 256)
   int nsplit;       // splits of the prefix
   int split_len;    // positions per split, a multiple of kPrefixTile
-  int pad;
-  long long item0;  // first item; item = item0 + (kv head * nsplit + split) * nrp + block
+  int item0;        // first item; item = item0 + (kv head * nsplit + split) * nrp + block
 };
 
 struct PrefixPlan {
-  long long n_items;
+  int n_items;
   int all_bad;  // bad query_start_loc or group_start_loc, or no room: every row is zero
 };
 
@@ -42,7 +41,7 @@ struct PrefixParams {
   int num_groups, max_prefix_len, num_sms;
   PrefixPlan *plan;
   PrefixGroup *grp;     // [num_groups]
-  long long *grp_end;   // [num_groups] inclusive prefix sum of the items
+  int *grp_end;         // [num_groups] inclusive prefix sum of the items
   int *req_grp;         // [num_seqs] group of each request
   float *part_o, *part_lse;
   long long item_cap;
@@ -54,17 +53,24 @@ struct PrefixItem {
   int kv_lo, kv_hi;          // positions of its split
 };
 
-__device__ inline PrefixItem prefix_item(const PrefixParams &p, long long item, int G) {
-  const PrefixGroup g = p.grp[p.num_groups == 1 ? 0 : list_find(p.grp_end, p.num_groups, item)];
-  const long long local = item - g.item0;
+// g0: group 0, loaded beside the number of items (most batches have one group).
+__device__ inline PrefixItem prefix_item(const PrefixParams &p, const PrefixGroup &g0, int item,
+                                         int G) {
+  int lo = 0, hi = p.num_groups - 1;
+  while (lo < hi) {  // the first group that ends behind the item
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.grp_end + mid) > item) hi = mid; else lo = mid + 1;
+  }
+  PrefixGroup g = g0;
+  if (lo) g = p.grp[lo];
+  const unsigned local = item - g.item0, rest = local / (unsigned)g.nrp;
   PrefixItem it;
   it.q_start = g.q_start;
   it.q_len = g.q_len;
   it.req0 = g.req0;
-  it.t0 = (int)(local % g.nrp) * (kPrefixRows / G);
-  const long long rest = local / g.nrp;
-  it.kvh = (int)(rest / g.nsplit);
-  it.kv_lo = (int)(rest % g.nsplit) * g.split_len;
+  it.t0 = (int)(local - rest * g.nrp) * (kPrefixRows / G);
+  it.kvh = (int)(rest / (unsigned)g.nsplit);
+  it.kv_lo = (int)(rest % (unsigned)g.nsplit) * g.split_len;
   it.kv_hi = min(it.kv_lo + g.split_len, g.prefix);
   return it;
 }

@@ -185,12 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  pdl_wait();  // the plan
-  const long long n_items = p.plan->n_items;
   bool dead = false;
 
   if (warp >= kIssueWarp) {
     reg_dec<kOtherRegs>();
+    pdl_wait();  // the plan
+    const int n_items = p.plan->n_items;
+    const PrefixGroup g0 = p.grp[0];
     if (warp >= kLoad0 && warp < kLoadEnd) {
       // ------------------------------------------------------------- loads
       // Two warps for K and two for V, each half of a tile's boxes, one box a
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *full = &bar[is_v ? C::V_FULL : C::K_FULL], *free = &bar[is_v ? C::V_FREE : C::K_FREE];
       uint8_t *ring = smem + (is_v ? C::OFF_V : C::OFF_K) + at;
       uint32_t st = 0, round = 0, items = 0;
-      for (long long item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
-        const PrefixItem it = prefix_item(p, item, G);
+      for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
+        const PrefixItem it = prefix_item(p, g0, item, G);
         const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
         auto page_of = [&](int pos) {
           int page = f.num_blocks;  // past the pool: zeros
@@ -289,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) commit(&bar[C::Q_FREE]);
         if (++ks == C::KST) ks = 0, ++kr;
       };
-      for (long long item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
-        const PrefixItem it = prefix_item(p, item, G);
+      for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
+        const PrefixItem it = prefix_item(p, g0, item, G);
         const int rows = (it.q_len - it.t0) * G;
         const bool two = rows > 128;
         mbar_wait(&bar[C::Q_FULL], items & 1, dead, f.status);
@@ -309,7 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
-        // (the weights of the item before have been read: O_DONE was awaited)
+        // (the weights of the item before have been read: O_DONE was awaited;
+        // and the dry round is over)
+        if (mine == 0) mbar_wait(&bar[C::O_FREE + x], 0, dead, f.status);
         if (two) take_turn();
         scores();
         if (two) pass_turn();
@@ -318,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = lo + kBN < it.kv_hi;
           mbar_wait(&bar[C::V_FULL + vs], vr & 1, dead, f.status);
           if (more) mbar_wait(&bar[C::K_FULL + ks], kr & 1, dead, f.status);
-          if (lo == it.kv_lo && mine > 0)
-            mbar_wait(&bar[C::O_FREE + x], (mine - 1) & 1, dead, f.status);
+          // O of the item before has been stored (phase 0 is the dry round's)
+          if (lo == it.kv_lo) mbar_wait(&bar[C::O_FREE + x], mine & 1, dead, f.status);
           // the leading offset steps to the next 64-wide chunk of the box
           const uint32_t b = desc_lo(sv + vs * C::KV_BYTES, box * 128);
           mbar_wait(&bar[C::P_HALF + x], n & 1, dead, f.status);
@@ -363,12 +366,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool fold = c2 > 0.f;
     const float cs = fold ? c2 : 1.f;
     uint32_t n = 0;
-    for (long long item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const PrefixItem it = prefix_item(p, item, G);
-      const int rows = min(128, (it.q_len - it.t0) * G - x * 128);
+    // The first round is dry: two tiles of whatever TMEM holds, no barrier
+    // touched and nothing stored, run before the plan is awaited.  It brings this
+    // code into the instruction cache, which costs the first tile 3 to 6 us
+    // when a call's own keys have just swept L2.
+    int n_items = 0;
+    PrefixGroup g0{};
+    for (int item = -1; item < n_items; item = item < 0 ? (int)blockIdx.x : item + (int)gridDim.x) {
+      const bool dry = item < 0;
+      PrefixItem it;
+      if (dry) it.q_start = it.q_len = it.req0 = it.kvh = it.t0 = it.kv_lo = 0, it.kv_hi = 2 * kBN;
+      else it = prefix_item(p, g0, item, G);
+      const int rows = dry ? 128 : min(128, (it.q_len - it.t0) * G - x * 128);
       if (rows <= 0) continue;
       // a bad page in the split marks all of the item's rows
-      {
+      if (!dry) {
         const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
         int bad = 0;
         for (int lp = it.kv_lo / bs + r; lp <= (it.kv_hi - 1) / bs; lp += 128) {
@@ -381,11 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad) atomicOr(&s_bad[x], 1);
         named_sync(1 + x, 128);
       }
-      const bool item_bad = s_bad[x] != 0;
+      const bool item_bad = !dry && s_bad[x] != 0;
       const bool warp_active = (warp & 3) * 32 < rows;  // its other rows are padding
       float ref = 0.f, l = 0.f;  // the weights' reference exponent and their sum
-      for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN, ++n) {
-        mbar_wait(&bar[C::S_FULL + x], n & 1, dead, f.status);
+      for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN, n += !dry) {
+        if (!dry) mbar_wait(&bar[C::S_FULL + x], n & 1, dead, f.status);
         tc_fence_after();
         if (warp_active) {
           uint32_t ua[2][32], ub[2][32], pw[32];
@@ -424,101 +436,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return (acc[0] + acc[1]) + (acc[2] + acc[3]);
           };
-          auto store = [&](int at) {  // (two halves: each leaves as soon as it is made)
-            tc_st16(tm_s + at, *reinterpret_cast<const uint32_t(*)[16]>(pw));
-            tc_st16(tm_s + at + 16, *reinterpret_cast<const uint32_t(*)[16]>(pw + 16));
+          // Half a tile's weights over columns 0 - 31 or 32 - 63, which are read.
+          auto store = [&](int c0, float sum) {
+            tc_st16(tm_s + c0 / 2, *reinterpret_cast<const uint32_t(*)[16]>(pw));
+            tc_st16(tm_s + c0 / 2 + 16, *reinterpret_cast<const uint32_t(*)[16]>(pw + 16));
+            l += sum;
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && !dry) mbar_arrive(&bar[(c0 ? C::P_FULL : C::P_HALF) + x]);
           };
-          // The maximum of columns [c0, c1), scaled.
-          auto max_of = [&](int c0, int c1) {
-            float a = -INFINITY, b = -INFINITY;
+          // The first tile sets the references.  They stand until some row's
+          // weights outgrow them (or all weights so far are zero, or a score is
+          // not finite).
+          const bool first = lo == it.kv_lo;
+          int done = 0;      // columns whose weights are stored
+          bool redo = true;  // this row's reference has to move
+          if (!first) {
+            load(ua, 0);
+            load(ub, 64);
+            take(ua, 0);
+            float sum = weights(ua);
+            redo = !(sum <= kMostSum) || l == 0.f;
+            if (!__any_sync(0xffffffffu, redo)) {
+              take(ub, 64);
+              store(0, sum);
+              done = 64;
+              sum = weights(ub);
+              redo = !(sum <= kMostSum) || l == 0.f;
+              if (!__any_sync(0xffffffffu, redo)) {
+                store(64, sum);
+                done = kBN;
+              }
+            } else {
+              wait_ld(ub[0], ub[1]);
+            }
+          }
+          if (done < kBN) {
+            // The reference becomes the maximum of the scores to come (or stays:
+            // not redo, or nothing but -inf there); O and l follow.
+            float mx = -INFINITY;
 #pragma unroll 1
-            for (; c0 < c1; c0 += 64) {
+            for (int c0 = done; c0 < kBN; c0 += 64) {
               load(ua, c0);
               take(ua, c0);
+              float other = -INFINITY;
 #pragma unroll
               for (int c = 0; c < 64; c += 4) {
-                a = fmax3(a, __uint_as_float(ua[c / 32][c % 32]), __uint_as_float(ua[c / 32][c % 32 + 1]));
-                b = fmax3(b, __uint_as_float(ua[c / 32][c % 32 + 2]), __uint_as_float(ua[c / 32][c % 32 + 3]));
+                mx = fmax3(mx, __uint_as_float(ua[c / 32][c % 32]), __uint_as_float(ua[c / 32][c % 32 + 1]));
+                other = fmax3(other, __uint_as_float(ua[c / 32][c % 32 + 2]),
+                              __uint_as_float(ua[c / 32][c % 32 + 3]));
               }
+              mx = fmaxf(mx, other);
             }
-            return fmaxf(a, b) * cs;
-          };
-          // The row's reference becomes mx, the maximum of scores to come (or
-          // stays: redo false, or nothing but -inf there); O and l follow.
-          auto rebase = [&](float mx, bool redo) {
+            mx *= cs;
             float a = 1.f;
             if (redo && mx != -INFINITY) {
               if (l != 0.f) a = fast_exp2(ref - mx);
               l *= a;
               ref = mx;
             }
+            if (!first) {
+              // (these scores were issued after the last product on O was done;
+              // that on this tile's first half is on its way)
+              if (done > 0 && !dry) {
+                mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
+                tc_fence_after();
+              }
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              uint32_t raw[16];
-              tc_ld16(tm_o + c0, raw);
-              tc_wait_ld();
+              for (int o = 0; o < D; o += 16) {
+                uint32_t raw[16];
+                tc_ld16(tm_o + o, raw);
+                tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
-              tc_st16(tm_o + c0, raw);
+                for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
+                tc_st16(tm_o + o, raw);
+              }
+              tc_wait_st();
             }
-            tc_wait_st();
-          };
-          // The first tile sets the references.  They stand until some row's
-          // weights outgrow them (or all weights so far are zero, or a score is
-          // not finite): then they move, and the weights are made again.
-          const bool first = lo == it.kv_lo;
-          if (first) {
-            const float mx = max_of(0, kBN);
-            if (mx != -INFINITY) ref = mx;
+#pragma unroll 1
+            for (; done < kBN; done += 64) {
+              load(ua, done);
+              take(ua, done);
+              store(done, weights(ua));
+            }
           }
-          load(ua, 0);
-          load(ub, 64);
-          take(ua, 0);
-          float sum = weights(ua);
-          bool redo = !first && (!(sum <= kMostSum) || l == 0.f);
-          if (__any_sync(0xffffffffu, redo)) {
-            // (these scores were issued after the last product on O was done)
-            wait_ld(ub[0], ub[1]);
-            rebase(max_of(0, kBN), redo);
-            load(ua, 0);
-            take(ua, 0);
-            sum = weights(ua);
-          }
-          take(ub, 64);
-          store(0);  // over columns 0 - 31, read
-          l += sum;
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[C::P_HALF + x]);
-          sum = weights(ub);
-          redo = !first && (!(sum <= kMostSum) || l == 0.f);
-          if (__any_sync(0xffffffffu, redo)) {
-            // (the product on the first half's weights is on its way)
-            mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
-            tc_fence_after();
-            rebase(max_of(64, kBN), redo);
-            load(ub, 64);
-            take(ub, 64);
-            sum = weights(ub);
-          }
-          store(32);
-          l += sum;
-          tc_wait_st();
         } else if (lane == 0) {
           mbar_arrive(&bar[C::P_HALF + x]);
+          mbar_arrive(&bar[C::P_FULL + x]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[C::P_FULL + x]);
       }
       // ---- O / l and the log-sum-exp of the rows
-      mbar_wait(&bar[C::O_DONE + x], (n - 1) & 1, dead, f.status);
+      if (!dry) mbar_wait(&bar[C::O_DONE + x], (n - 1) & 1, dead, f.status);
       tc_fence_after();
       if (warp_active) {
         const float inv = l > 0.f && !item_bad ? 1.f / l : 0.f;
         const uint32_t keep = item_bad ? 0u : 0xffffffffu;
-        const long long prow = item * kPrefixRows + x * 128 + r;
+        const long long prow = (long long)item * kPrefixRows + x * 128 + r;
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t raw[32];
@@ -526,17 +540,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) raw[i] &= keep;
-          if (r < rows) {
+          if (r < rows && !dry) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) store32(p.part_o + prow * D + c0 + i, raw, i, inv);
           }
         }
-        if (r < rows)
+        if (r < rows && !dry)
           p.part_lse[prow] = item_bad ? __int_as_float(0x7fc00000) : l > 0.f ? ref + log2f(l) : -INFINITY;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[C::O_FREE + x]);
+      if (dry) {
+        pdl_wait();  // the plan
+        n_items = p.plan->n_items;
+        g0 = p.grp[0];
+      }
     }
   }
   tc_fence_before();
