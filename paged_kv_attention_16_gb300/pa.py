@@ -317,23 +317,35 @@ def pa_cache_write(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_
     return st
 
 
-def _on_device(device, **tensors):
-    """Every tensor given lies on CUDA device `device`, the current one."""
-    if device < 0 or device != torch.cuda.current_device():
-        raise ValueError("the tensors must lie on the current CUDA device")
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"{name} lies on another device")
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _contiguous(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is None:
-            continue
+def _check_tensors(device, *groups):
+    """groups: (dtype, {name: tensor}).  Every tensor given is contiguous, of its
+    group's dtype, and lies on CUDA device `device`, the current one.  Called to
+    name what _fits found amiss."""
+    named = [(name, t, dtype) for dtype, ts in groups for name, t in ts.items() if t is not None]
+    for name, t, dtype in named:
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    for name, t, _ in named:
+        if device < 0 or t.get_device() != device or device != _get_device():
+            raise ValueError(f"{name} does not lie on the current CUDA device with the others")
+
+
+def _fits(device, dtype, *tensors):
+    """Whether _check_tensors would pass (a plain loop: it runs on every call)."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != device
+                              or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _current(device):
+    return device >= 0 and device == _get_device()
 
 
 def pa_block_tables(seq_lens, query_start_loc, block_table, slot_mapping, block_size, stream=None,
@@ -344,41 +356,51 @@ def pa_block_tables(seq_lens, query_start_loc, block_table, slot_mapping, block_
     are written; with free_pages [num_free], free_start [1] and free_end [1]
     (int32) the pages the requests lack are taken from free_pages[free_start:]
     and written into block_table [S, max_blocks] in place."""
-    S, T = int(seq_lens.shape[0]), int(slot_mapping.shape[0])
-    _contiguous(torch.int32, seq_lens=seq_lens, query_start_loc=query_start_loc,
-                block_table=block_table, free_pages=free_pages, free_start=free_start,
-                free_end=free_end, positions=positions)
-    _contiguous(torch.int64, slot_mapping=slot_mapping)
-    if query_start_loc.numel() != S + 1 or block_table.dim() != 2 or block_table.shape[0] != S:
+    S, T, num_free = seq_lens.numel(), slot_mapping.numel(), 0
+    rows, width = block_table.shape
+    if query_start_loc.numel() != S + 1 or rows != S:
         raise ValueError("query_start_loc [S + 1] and block_table [S, max_blocks] go with seq_lens [S]")
-    if positions is not None and positions.numel() != T:
-        raise ValueError("positions must have slot_mapping's length")
-    if (free_start is None) != (free_end is None) or (free_start is None and free_pages is not None):
-        raise ValueError("free_pages, free_start and free_end go together")
-    for t in (free_start, free_end):
-        if t is not None and t.numel() != 1:
-            raise ValueError("free_start and free_end are one int32 each")
     device = slot_mapping.get_device()
-    _on_device(device, seq_lens=seq_lens, query_start_loc=query_start_loc, block_table=block_table,
-               free_pages=free_pages, free_start=free_start, free_end=free_end,
-               positions=positions)
-    st = lib().pa_block_tables(
-        _ptr(seq_lens), _ptr(query_start_loc), _ptr(free_pages), _ptr(free_start), _ptr(free_end),
-        _ptr(block_table), _ptr(slot_mapping), _ptr(positions), int(block_size),
-        _stream_ptr(stream, device), S, T, int(block_table.shape[1]), int(num_blocks),
-        0 if free_pages is None else int(free_pages.numel()))
-    if check:
+    fits = (_current(device) and _fits(device, torch.int64, slot_mapping)
+            and _fits(device, torch.int32, seq_lens, query_start_loc, block_table))
+    pages = start = end = pos = None
+    if positions is not None:
+        if positions.numel() != T:
+            raise ValueError("positions must have slot_mapping's length")
+        fits = fits and _fits(device, torch.int32, positions)
+        pos = positions.data_ptr()
+    if free_start is not None:
+        if free_pages is None or free_end is None:
+            raise ValueError("free_pages, free_start and free_end go together")
+        if free_start.numel() != 1 or free_end.numel() != 1:
+            raise ValueError("free_start and free_end are one int32 each")
+        fits = fits and _fits(device, torch.int32, free_pages, free_start, free_end)
+        pages, num_free = free_pages.data_ptr(), free_pages.numel()
+        start, end = free_start.data_ptr(), free_end.data_ptr()
+    elif free_pages is not None or free_end is not None:
+        raise ValueError("free_pages, free_start and free_end go together")
+    if not fits:
+        _check_tensors(device, (torch.int64, dict(slot_mapping=slot_mapping)),
+                       (torch.int32, dict(seq_lens=seq_lens, query_start_loc=query_start_loc,
+                                          block_table=block_table, free_pages=free_pages,
+                                          free_start=free_start, free_end=free_end,
+                                          positions=positions)))
+    st = (_lib or lib()).pa_block_tables(
+        seq_lens.data_ptr(), query_start_loc.data_ptr(), pages, start, end, block_table.data_ptr(),
+        slot_mapping.data_ptr(), pos, int(block_size), _stream_ptr(stream, device), S, T, width,
+        int(num_blocks), num_free)
+    if check and st:
         _check(st, "pa_block_tables")
     return st
 
 
-def _token_stride(t, name):
+def _token_stride(t, T, Hk, D, name):
     """Elements from one token's [heads, dim] row to the next; the row itself
     must be contiguous."""
-    T, Hk, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (Hk > 1 and t.stride(1) != D):
+    token, head, elem = t.stride()
+    if (elem != 1 and D > 1) or (head != D and Hk > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return int(t.stride(0)) if T > 1 else Hk * D
+    return token if T > 1 else Hk * D
 
 
 def pa_cache_write_slots(k_new, v_new, k_cache, v_cache, slot_mapping, block_size, stream=None,
@@ -387,22 +409,27 @@ def pa_cache_write_slots(k_new, v_new, k_cache, v_cache, slot_mapping, block_siz
     [T, Hk, D], each token's row contiguous and any number of elements from the
     next (slices of a fused projection); slot_mapping [T] int64, negative slots
     skipped."""
-    T, Hk, D = (int(x) for x in k_new.shape)
+    T, Hk, D = shape = k_new.shape
+    dtype, device = k_new.dtype, k_new.get_device()
     dt, layout = _dtype_code(k_new), layout_code(kv_layout)
-    _contiguous(torch.int64, slot_mapping=slot_mapping)
-    _contiguous(k_new.dtype, k_cache=k_cache, v_cache=v_cache)
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or slot_mapping.numel() != T:
-        raise ValueError("k_new and v_new [T, Hk, D] of one type go with slot_mapping [T]")
-    page = (block_size, Hk, D) if layout != PA_KV_HND else (Hk, block_size, D)
-    if tuple(k_cache.shape[1:]) != page or k_cache.shape != v_cache.shape:
+    if (v_new.shape != shape or v_new.dtype is not dtype or v_new.get_device() != device
+            or slot_mapping.numel() != T):
+        raise ValueError("k_new and v_new [T, Hk, D] of one type and device go with slot_mapping [T]")
+    blocks, x, y, z = shape = k_cache.shape
+    if (z != D or (x, y) != ((Hk, block_size) if layout == PA_KV_HND else (block_size, Hk))
+            or v_cache.shape != shape):
         raise ValueError("the caches' shape does not fit the rows, block_size and kv_layout")
-    device = k_new.get_device()
-    _on_device(device, v_new=v_new, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
-    st = lib().pa_cache_write_slots(
-        _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), Hk, D,
-        int(block_size), _stream_ptr(stream, device), dt, T, _token_stride(k_new, "k_new"),
-        _token_stride(v_new, "v_new"), int(k_cache.shape[0]), layout)
-    if check:
+    if not (_current(device) and _fits(device, torch.int64, slot_mapping)
+            and _fits(device, dtype, k_cache, v_cache)):
+        _check_tensors(device, (torch.int64, dict(slot_mapping=slot_mapping)),
+                       (dtype, dict(k_cache=k_cache, v_cache=v_cache)))
+        raise ValueError("k_new does not lie on the current CUDA device")
+    st = (_lib or lib()).pa_cache_write_slots(
+        k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_mapping.data_ptr(), Hk, D, int(block_size), _stream_ptr(stream, device), dt, T,
+        _token_stride(k_new, T, Hk, D, "k_new"), _token_stride(v_new, T, Hk, D, "v_new"), blocks,
+        layout)
+    if check and st:
         _check(st, "pa_cache_write_slots")
     return st
 
@@ -426,58 +453,57 @@ def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_s
     run; None takes one from torch's allocator for this call, so calls on
     several streams and captured graphs each have their own."""
     dt, layout = _dtype_code(q), layout_code(kv_layout)
-    _contiguous(q.dtype, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
-    _contiguous(torch.int32, block_table=block_table, seq_lens=seq_lens,
-                query_start_loc=query_start_loc, group_start_loc=group_start_loc,
-                prefix_lens=prefix_lens)
-    S, NG, T = int(seq_lens.numel()), int(prefix_lens.numel()), int(q.shape[0])
-    page = (block_size, num_kv_heads, head_dim)
-    if layout == PA_KV_HND:
-        page = (num_kv_heads, block_size, head_dim)
-    if tuple(q.shape[1:]) != (num_heads, head_dim) or out.shape != q.shape:
+    S, NG = seq_lens.numel(), prefix_lens.numel()
+    T, H, D = shape = q.shape
+    if H != num_heads or D != head_dim or out.shape != shape:
         raise ValueError("q and out must be [T, num_heads, head_dim]")
-    if tuple(k_cache.shape[1:]) != page or v_cache.shape[1:] != k_cache.shape[1:]:
+    blocks, x, y, z = k_cache.shape
+    page = (num_kv_heads, block_size) if layout == PA_KV_HND else (block_size, num_kv_heads)
+    if z != D or (x, y) != page or v_cache.shape != k_cache.shape:
         raise ValueError("the caches' shape does not fit the heads, block_size and kv_layout")
-    if (query_start_loc.numel() != S + 1 or group_start_loc.numel() != NG + 1
-            or block_table.dim() != 2 or block_table.shape[0] != S):
+    rows, width = block_table.shape
+    if query_start_loc.numel() != S + 1 or group_start_loc.numel() != NG + 1 or rows != S:
         raise ValueError("query_start_loc [S + 1], block_table [S, max_blocks] and "
                          "group_start_loc [groups + 1] go with seq_lens [S] and prefix_lens [groups]")
-    for name, t in (("sinks", sinks), ("alibi_slopes", alibi_slopes)):
-        if isinstance(t, torch.Tensor):
-            _contiguous(torch.float32, **{name: t})
-            if t.numel() != num_heads:
-                raise TypeError(f"{name} must be a float32 tensor of num_heads elements")
-    blocks = min(int(k_cache.shape[0]), int(v_cache.shape[0]))
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != num_heads):
+        raise TypeError("sinks must be a float32 tensor of num_heads elements")
     if num_blocks is not None:
         if num_blocks > blocks:
             raise ValueError("num_blocks exceeds the caches")
         blocks = int(num_blocks)
     device = q.get_device()
-    _on_device(device, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-               seq_lens=seq_lens, query_start_loc=query_start_loc,
-               group_start_loc=group_start_loc, prefix_lens=prefix_lens, out=out,
-               workspace=workspace)
+    if not (_current(device) and _fits(device, q.dtype, q, k_cache, v_cache, out)
+            and _fits(device, torch.int32, block_table, seq_lens, query_start_loc,
+                      group_start_loc, prefix_lens)
+            and _fits(device, torch.float32, sinks)):
+        _check_tensors(device, (q.dtype, dict(q=q, k_cache=k_cache, v_cache=v_cache, out=out)),
+                       (torch.int32, dict(block_table=block_table, seq_lens=seq_lens,
+                                          query_start_loc=query_start_loc,
+                                          group_start_loc=group_start_loc,
+                                          prefix_lens=prefix_lens)),
+                       (torch.float32, dict(sinks=sinks)))
     raw = _stream_ptr(stream, device)
-    need = pa_forward_shared_prefix_workspace_bytes(dt, S, NG, T, num_heads, num_kv_heads,
-                                                    head_dim, max_seq_len)
+    L = _lib or lib()
     if workspace is None:
-        if raw == _stream_ptr(None, device):
+        need = L.pa_forward_shared_prefix_workspace_bytes(
+            dt, S, NG, T, int(num_heads), int(num_kv_heads), int(head_dim), int(max_seq_len))
+        if stream is None or raw == _stream_ptr(None, device):
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:  # allocated for the stream that uses it, so that its reuse is ordered there
             owner = (torch.cuda.ExternalStream(raw, device=q.device) if raw
                      else torch.cuda.default_stream(q.device))
             with torch.cuda.stream(owner):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        _contiguous(torch.uint8, workspace=workspace)
+    elif not _fits(device, torch.uint8, workspace):
+        _check_tensors(device, (torch.uint8, dict(workspace=workspace)))
     opts = _forward_options(sinks, layout, sliding_window, alibi_slopes, alibi_sqrt, max_query_len)
-    st = lib().pa_forward_shared_prefix(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-        _ptr(query_start_loc), _ptr(group_start_loc), _ptr(prefix_lens), int(num_heads),
-        int(num_kv_heads), int(head_dim), int(block_size), float(scale), _ptr(out), raw, dt, S,
-        NG, T, int(block_table.shape[1]), blocks, int(max_seq_len), int(max_prefix_len),
-        ctypes.byref(opts), _ptr(workspace), int(workspace.numel()))
-    if check:
+    st = L.pa_forward_shared_prefix(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), query_start_loc.data_ptr(), group_start_loc.data_ptr(),
+        prefix_lens.data_ptr(), int(num_heads), int(num_kv_heads), int(head_dim), int(block_size),
+        float(scale), out.data_ptr(), raw, dt, S, NG, T, width, blocks, int(max_seq_len),
+        int(max_prefix_len), ctypes.byref(opts), workspace.data_ptr(), workspace.numel())
+    if check and st:
         _check(st, "pa_forward_shared_prefix")
     return st
 
