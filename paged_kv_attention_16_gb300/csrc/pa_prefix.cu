@@ -771,13 +771,13 @@ pa_status pa_forward_shared_prefix(
   cudaError_t err = launch_dependent(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p);
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
-  s = launch_rows_and_tiles(c, f, num_sms, st, true);
-  if (s != PA_OK) return s;
   slot = prof_begin(PA_K_PREFIX, st);
   err = dtype == PA_BF16 ? launch_prefix_mma(p, c.kv_layout, num_sms, st)
                          : launch_simt(p, c.kv_layout == PA_KV_HND, num_sms, st);
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
+  s = launch_rows_and_tiles(c, f, num_sms, st, true);
+  if (s != PA_OK) return s;
   slot = prof_begin(PA_K_MERGE, st);
   err = dtype == PA_BF16 ? launch_merge<__nv_bfloat16>(p, st) : launch_merge<float>(p, st);
   prof_end(slot, st);

@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool fold = c2 > 0.f;
     const float cs = fold ? c2 : 1.f;
     uint32_t n = 0;
-    // The first round is dry: two tiles of whatever TMEM holds, no barrier
-    // touched and nothing stored, run before the plan is awaited.  It brings this
+    // The first round is dry: a tile of whatever TMEM holds, no barrier touched
+    // and nothing stored, run before the plan is awaited.  It brings this
     // code into the instruction cache, which costs the first tile 3 to 6 us
     // when a call's own keys have just swept L2.
     int n_items = 0;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int item = -1; item < n_items; item = item < 0 ? (int)blockIdx.x : item + (int)gridDim.x) {
       const bool dry = item < 0;
       PrefixItem it;
-      if (dry) it.q_start = it.q_len = it.req0 = it.kvh = it.t0 = it.kv_lo = 0, it.kv_hi = 2 * kBN;
+      if (dry) it.q_start = it.q_len = it.req0 = it.kvh = it.t0 = it.kv_lo = 0, it.kv_hi = kBN;
       else it = prefix_item(p, g0, item, G);
       const int rows = dry ? 128 : min(128, (it.q_len - it.t0) * G - x * 128);
       if (rows <= 0) continue;
@@ -446,74 +446,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0 && !dry) mbar_arrive(&bar[(c0 ? C::P_FULL : C::P_HALF) + x]);
           };
+          // The maximum of columns [c0, 128), scaled.
+          auto max_from = [&](int c0) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+            for (; c0 < kBN; c0 += 64) {
+              load(ua, c0);
+              take(ua, c0);
+#pragma unroll
+              for (int c = 0; c < 64; c += 4) {
+                m0 = fmax3(m0, __uint_as_float(ua[c / 32][c % 32]), __uint_as_float(ua[c / 32][c % 32 + 1]));
+                m1 = fmax3(m1, __uint_as_float(ua[c / 32][c % 32 + 2]), __uint_as_float(ua[c / 32][c % 32 + 3]));
+              }
+            }
+            return fmaxf(m0, m1) * cs;
+          };
           // The first tile sets the references.  They stand until some row's
           // weights outgrow them (or all weights so far are zero, or a score is
           // not finite).
           const bool first = lo == it.kv_lo;
-          int done = 0;      // columns whose weights are stored
-          bool redo = true;  // this row's reference has to move
-          if (!first) {
-            load(ua, 0);
-            load(ub, 64);
-            take(ua, 0);
-            float sum = weights(ua);
-            redo = !(sum <= kMostSum) || l == 0.f;
+          if (first) {
+            const float mx = max_from(0);
+            ref = mx == -INFINITY ? 0.f : mx;
+          }
+          load(ua, 0);
+          load(ub, 64);
+          take(ua, 0);
+          float sum = weights(ua);
+          int done = 0;  // columns whose weights are stored
+          bool redo = !first && (!(sum <= kMostSum) || l == 0.f);
+          if (!__any_sync(0xffffffffu, redo)) {
+            take(ub, 64);
+            store(0, sum);
+            done = 64;
+            sum = weights(ub);
+            redo = !first && (!(sum <= kMostSum) || l == 0.f);
             if (!__any_sync(0xffffffffu, redo)) {
-              take(ub, 64);
-              store(0, sum);
-              done = 64;
-              sum = weights(ub);
-              redo = !(sum <= kMostSum) || l == 0.f;
-              if (!__any_sync(0xffffffffu, redo)) {
-                store(64, sum);
-                done = kBN;
-              }
-            } else {
-              wait_ld(ub[0], ub[1]);
+              store(64, sum);
+              done = kBN;
             }
+          } else {
+            wait_ld(ub[0], ub[1]);
           }
           if (done < kBN) {
-            // The reference becomes the maximum of the scores to come (or stays:
-            // not redo, or nothing but -inf there); O and l follow.
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c0 = done; c0 < kBN; c0 += 64) {
-              load(ua, c0);
-              take(ua, c0);
-              float other = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                mx = fmax3(mx, __uint_as_float(ua[c / 32][c % 32]), __uint_as_float(ua[c / 32][c % 32 + 1]));
-                other = fmax3(other, __uint_as_float(ua[c / 32][c % 32 + 2]),
-                              __uint_as_float(ua[c / 32][c % 32 + 3]));
-              }
-              mx = fmaxf(mx, other);
-            }
-            mx *= cs;
+            // The reference of a row that asked for it becomes the maximum of the
+            // scores to come (unless they are all -inf); O and l follow.
+            const float mx = max_from(done);
             float a = 1.f;
             if (redo && mx != -INFINITY) {
               if (l != 0.f) a = fast_exp2(ref - mx);
               l *= a;
               ref = mx;
             }
-            if (!first) {
-              // (these scores were issued after the last product on O was done;
-              // that on this tile's first half is on its way)
-              if (done > 0 && !dry) {
-                mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
-                tc_fence_after();
-              }
-#pragma unroll 1
-              for (int o = 0; o < D; o += 16) {
-                uint32_t raw[16];
-                tc_ld16(tm_o + o, raw);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
-                tc_st16(tm_o + o, raw);
-              }
-              tc_wait_st();
+            // (these scores were issued after the last product on O was done;
+            // that on this tile's first half is on its way)
+            if (done > 0) {
+              mbar_wait(&bar[C::O_HALF + x], n & 1, dead, f.status);
+              tc_fence_after();
             }
+#pragma unroll 1
+            for (int o = 0; o < D; o += 16) {
+              uint32_t raw[16];
+              tc_ld16(tm_o + o, raw);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * a);
+              tc_st16(tm_o + o, raw);
+            }
+            tc_wait_st();
 #pragma unroll 1
             for (; done < kBN; done += 64) {
               load(ua, done);
