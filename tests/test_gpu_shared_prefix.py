@@ -170,6 +170,97 @@ def test_largest_values_and_masked_garbage():
     check(b, run(b))
 
 
+def _scores(prefix, own, profile, D=128, G=4, dtype="bf16"):
+    """A batch whose scores are `profile`(position) exactly, for every row: q is
+    the first unit vector, keys carry the score in that column (profile values
+    are whole numbers that bf16 holds), scale is 1."""
+    b = make([(prefix, [(1, own), (1, own)])], G, 1, D, 16, dtype, seed=70, scale=1.0)
+    b.q.zero_()
+    b.q[..., 0] = 1.0
+    n = prefix + own
+    for s in range(2):
+        for p in range(n):
+            page, at = int(b.full_table[s, p // 16]), p % 16
+            b.k_cache[page, at] = 0.0
+            b.k_cache[page, at, 0, 0] = float(profile(p))
+    return b
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", ["rising", "falling", "steps", "sawtooth"])
+def test_scores_that_leave_the_reference_behind(shape, dtype):
+    """The running reference has to follow scores that grow by hundreds within a
+    tile of positions and from tile to tile, and to hold when they fall."""
+    profile = {"rising": lambda p: p // 4, "falling": lambda p: 200 - p // 4,
+               "steps": lambda p: 100 * (p // 96), "sawtooth": lambda p: 64 * ((p // 32) % 3)}[shape]
+    b = _scores(640, 9, lambda p: min(max(profile(p), 0), 255), dtype=dtype)
+    check(b, run(b), what=shape)
+
+
+@pytest.mark.parametrize("at", [0, 1, 63, 64, 65, 127, 128, 191, 192, 255, 256, 383, 500, 639, 645])
+def test_one_key_takes_the_weight(at):
+    """One score 200 above the others, in either half of the first, a middle or
+    the last tile, or behind the prefix: the row is that key's value."""
+    b = _scores(640, 9, lambda p: 200 if p == at else 0)
+    out = run(b).float().cpu()
+    for s in range(2):
+        want = b.v_cache[int(b.full_table[s, at // 16]), at % 16, 0].float()
+        assert torch.equal(out[s], want.expand(4, -1))
+
+
+@pytest.mark.parametrize("hidden", [16, 64, 128, 129, 192, 300, 640])
+def test_leading_scores_of_minus_infinity(hidden):
+    """The first keys have a score of -inf (an overflowed product): no weight,
+    and the reference is set by the first finite score."""
+    b = _scores(640, 9, lambda p: 0)
+    b.q[..., 1] = 2e38
+    for s in range(2):
+        for p in range(hidden):
+            b.k_cache[int(b.full_table[s, p // 16]), p % 16, 0, 1] = -2e38
+    out = run(b).float().cpu().double()
+    for s in range(2):
+        v = torch.stack([b.v_cache[int(b.full_table[s, p // 16]), p % 16, 0].double()
+                         for p in range(hidden, 649)])
+        # equal weights: their mean, one rounding of each weight and of the output
+        tol = 2.0 ** -8 * (v.abs().mean(0) + v.mean(0).abs()) + 1e-6
+        assert ((out[s] - v.mean(0)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("where", ["q", "prefix_k", "prefix_v", "own_v"])
+def test_nan_stays_visible(where):
+    """A NaN in a visible input reaches the rows that see it, and no others."""
+    b = make([(160, [(1, 9), (1, 20)]), (32, [(1, 5)])], 4, 2, 64, 16, seed=71)
+    rows = [0, 1]
+    if where == "q":
+        b.q[1] = float("nan")
+        rows = [1]
+    elif where == "own_v":
+        b.v_cache[int(b.full_table[1, 10]), 3] = float("nan")
+        rows = [1]
+    else:
+        cache = b.k_cache if where == "prefix_k" else b.v_cache
+        cache[int(b.full_table[0, 4]), 7] = float("nan")
+    out = run(b).float().cpu()
+    for t in range(3):
+        assert torch.isnan(out[t]).all() if t in rows else torch.isfinite(out[t]).all()
+
+
+def test_cache_offsets_past_32_bits():
+    """Pages beyond 2^32 bytes into the caches."""
+    b = make([(1024, decodes(5, 1, 60, 1))], 8, 8, 128, 16, seed=72, poison=False)
+    pages = (1 << 32) // (16 * 8 * 128 * 2) + b.num_blocks
+    big = [torch.empty((pages, 16, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for dst, src in zip(big, (b.k_cache, b.v_cache)):
+        dst[-b.num_blocks:] = src.cuda()
+    d = pa.to_device(b)
+    want = pa.forward_shared_prefix(d).clone()
+    d.k_cache, d.v_cache = big
+    d.block_table = torch.where(d.block_table >= 0, d.block_table + (pages - b.num_blocks), d.block_table)
+    assert torch.equal(pa.forward_shared_prefix(d), want)
+    check(b, want)
+    assert pa.pa_get_device_status() == 0
+
+
 def test_rows_with_no_finite_score_are_zero():
     """Every key -inf away from every query: no weight is left."""
     b = make([(64, [(1, 3), (4, 9)])], 4, 2, 64, 16, seed=13, poison=False)
