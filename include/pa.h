@@ -448,8 +448,9 @@ pa_status pa_cache_write(const void *k_new, const void *v_new, void *k_cache,
  * Bad device metadata: as for pa_forward; besides,
  *   PA_DEV_BAD_QSL     also for a bad group_start_loc: every row is 0
  *   PA_DEV_BAD_SEQLEN  also for a prefix_len that is negative, above
- *                      max_prefix_len, no multiple of block_size or longer
- *                      than a block-table row (the group's rows are 0), and
+ *                      max_prefix_len or max_seq_len, no multiple of
+ *                      block_size or longer than a block-table row (the
+ *                      group's rows are 0), and
  *                      for a request whose new tokens begin inside its
  *                      group's prefix (its rows are 0)
  * Errors: as for pa_forward; PA_ERR_INVALID_ARG also for num_tokens > 0 with
@@ -469,7 +470,7 @@ pa_status pa_forward_shared_prefix(
     size_t workspace_bytes);
 
 /* Workspace bytes pa_forward_shared_prefix needs for these host-known extents
- * (0 for extents it refuses as PA_ERR_INVALID_ARG). */
+ * (0 for extents it refuses as PA_ERR_INVALID_ARG or as too large). */
 size_t pa_forward_shared_prefix_workspace_bytes(pa_dtype dtype, int num_seqs,
                                                 int num_groups, int num_tokens,
                                                 int num_heads, int num_kv_heads,

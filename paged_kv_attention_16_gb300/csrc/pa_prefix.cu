@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   // a group's prefix, -1 when it is bad
   auto group_prefix = [&](int g) {
     const int P = cached ? s_pre[g] : p.prefix_lens[g];
-    const bool ok = P >= 0 && P <= p.max_prefix_len && (unsigned)P % bs == 0 &&
+    const bool ok = P >= 0 && P <= p.max_prefix_len && P <= f.max_seq_len && (unsigned)P % bs == 0 &&
                     (unsigned)P / bs <= (unsigned)f.max_blocks_per_seq;
     return ok ? P : -1;
   };
@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
 // prefix part on CUDA cores (fp32)
 // ---------------------------------------------------------------------------
 // Four threads share a row (each every fourth 16-byte group of its head_dim
-// values), 64 rows a pass; 32 keys and values at a time in shared memory.  A row's scores of 8 keys are reduced over its four threads, then
-// join the running maximum and sum.  Every key costs 4 D fp32 operations a
-// row: the FMA units bound it.
+// values), 64 rows a pass; 32 keys and values at a time in shared memory.  A
+// row's scores of 8 keys are reduced over its four threads, then join the
+// running maximum and sum.  Every key costs 4 D fp32 operations a row: the FMA
+// units bound it.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 32;
 
@@ -603,6 +604,8 @@ cudaError_t launch_merge(const PrefixParams &p, cudaStream_t st) {
 // host
 // ---------------------------------------------------------------------------
 
+constexpr long long kMaxItems = 1ll << 30;  // items are counted in ints
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefixLayout {
@@ -621,7 +624,9 @@ PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_toke
   // one item per (KV head, 256-row block, group) unsplit, and what splitting
   // adds, but no more than one a tile
   const long long units = Hk * (ceil_div_ll(T * G, kPrefixRows) + NG);
-  l.item_cap = std::min(units + kPrefixSplitItems, units * ceil_div_ll(msl, kPrefixTile));
+  const long long splits = ceil_div_ll(msl, kPrefixTile);
+  l.item_cap = units + (splits == 1 ? 0 : units >= kPrefixSplitItems ? kPrefixSplitItems
+                                        : std::min((long long)kPrefixSplitItems, units * (splits - 1)));
   // own part: decode rows ceil(len / Ld) splits each, Ld sized to the item
   // target; longer rows one split (tile kernel) or about four (fp32)
   const long long dec = std::min(S, T);
@@ -672,11 +677,12 @@ size_t pa_forward_shared_prefix_workspace_bytes(pa_dtype dtype, int num_seqs, in
                                                 int num_tokens, int num_heads, int num_kv_heads,
                                                 int head_dim, int max_seq_len) {
   if (num_seqs < 0 || num_groups < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-      num_heads % num_kv_heads || head_dim <= 0 || max_seq_len < 0)
+      num_heads % num_kv_heads || head_dim <= 0 || max_seq_len < 0 ||
+      (long long)num_tokens * num_heads > (1ll << 40) / head_dim)
     return 0;
-  return prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads, num_kv_heads, head_dim,
-                       max_seq_len)
-      .total;
+  const PrefixLayout lay = prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads,
+                                         num_kv_heads, head_dim, max_seq_len);
+  return lay.item_cap > kMaxItems ? 0 : lay.total;
 }
 
 pa_status pa_forward_shared_prefix(
@@ -709,7 +715,7 @@ pa_status pa_forward_shared_prefix(
     return PA_ERR_INVALID_ARG;
   const PrefixLayout lay = prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads,
                                          num_kv_heads, head_dim, max_seq_len);
-  if (lay.item_cap > 0x7fffffffll / 2) return PA_ERR_UNSUPPORTED;  // items are counted in ints
+  if (lay.item_cap > kMaxItems) return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return PA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

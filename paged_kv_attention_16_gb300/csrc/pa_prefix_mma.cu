@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stages = is_v ? C::VST : C::KST;
       uint64_t *full = &bar[is_v ? C::V_FULL : C::K_FULL], *free = &bar[is_v ? C::V_FREE : C::K_FREE];
       uint8_t *ring = smem + (is_v ? C::OFF_V : C::OFF_K) + at;
-      uint32_t st = 0, round = 0, items = 0;
-      for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++items) {
+      uint32_t st = 0, round = 0, items = 0, queries = 0;
+      for (int item = blockIdx.x; item < n_items && !dead; item += gridDim.x, ++items) {
         const PrefixItem it = prefix_item(p, g0, item, G);
         const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
         auto page_of = [&](int pos) {
@@ -223,8 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoad0 && lane == 0) {
           const int tiles = (it.q_len - it.t0) * G > 128 ? 2 : 1;
           if (items > 0) mbar_wait(&bar[C::Q_FREE], (items - 1) & 1, dead, f.status);
-          mbar_arrive_expect_tx(&bar[C::Q_FULL], tiles * C::Q_TILE);
-          for (int x = 0; x < tiles; ++x)
+          if (!dead) {
+            mbar_arrive_expect_tx(&bar[C::Q_FULL], tiles * C::Q_TILE);
+            ++queries;
+          }
+          for (int x = 0; x < tiles && !dead; ++x)
             for (int h = 0; h < C::NH; ++h)
               tma_load_3d(smem + x * C::Q_TILE + h * 128 * 128, &tm_q, h * 64, it.kvh * G,
                           it.q_start + it.t0 + x * TQ, &bar[C::Q_FULL]);
@@ -235,9 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int next = page_of(pos + kBN);  // its latency passes during the wait
           if (lane == 0) {
             if (round > 0) mbar_wait(&free[st], (round - 1) & 1, dead, f.status);
-            mbar_arrive_expect_tx(&full[st], bytes);
+            if (!dead) mbar_arrive_expect_tx(&full[st], bytes);
           }
-          __syncwarp();
+          dead = __any_sync(0xffffffffu, dead);
+          if (dead) break;  // timed out: the stage is not free
           if (lane < nb) {
             uint8_t *dst = ring + st * C::KV_BYTES;
             if (is_v) tma_load_5d(dst, &tm_v, 0, pos % bs, 0, it.kvh, page, &full[st]);
@@ -251,6 +255,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++round;
           }
         }
+      }
+      // No copy may land after the CTA is gone, not even if its readers timed out.
+      if (lane == 0) {
+        bool late = false;
+        for (uint32_t s = 0; s < (uint32_t)stages; ++s) {
+          const uint32_t fills = round + (s < st);
+          if (fills > 0) mbar_wait(&full[s], (fills - 1) & 1, late, f.status);
+        }
+        if (queries > 0) mbar_wait(&bar[C::Q_FULL], (queries - 1) & 1, late, f.status);
       }
     } else if (warp < kLoad0) {
       // ------------------------------------------------------------- products
@@ -350,9 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++mine;
       }
-      // no commit may land after the CTA is gone
+      // nor may a product's commit
+      bool late = false;
       commit(&bar[C::END]);
-      mbar_wait(&bar[C::END], 0, dead, f.status);
+      mbar_wait(&bar[C::END], 0, late, f.status);
     }
     __syncwarp();
   } else {

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kTablesThreads) block_tables_kernel(const Tabl
     bool ok = false;
     if (s < S) {
       const int q0 = a.qsl[s], q1 = a.qsl[s + 1], len = a.seq_lens[s], q = q1 - q0;
-      if (q < 0 || (s == 0 && q0 != 0) || (s == S - 1 && q1 > T)) bad = 1;
+      if (q1 < q0 || (s == 0 && q0 != 0) || (s == S - 1 && q1 > T)) bad = 1;
       s_qsl[s] = q0;
       s_len[s] = len;
       if (s == S - 1) s_qsl[S] = q1;

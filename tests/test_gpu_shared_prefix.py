@@ -127,6 +127,17 @@ def test_long_prefix_is_split_over_the_grid(D, bs, layout):
     check(b, run(b, max_query_len=1), rows=np.sort(rows).astype(np.int64))
 
 
+@pytest.mark.parametrize("D,G,layout", [(128, 4, "nhd"), (64, 8, "hnd"), (128, 1, "hnd"), (64, 16, "nhd")])
+def test_more_items_than_sms(D, G, layout):
+    """A block goes through several items, of one and of two row tiles, with
+    tiles that wrap the rings of both."""
+    rng = np.random.default_rng(D + G)
+    groups = [(16 * int(rng.integers(1, 90)), decodes(int(rng.integers(1, 600 // G)), 1, 40, i))
+              for i in range(30)]
+    b = make(groups, 8 * G, 8, D, 16, layout=layout, seed=D + G)
+    check(b, run(b), rows=np.sort(rng.choice(b.num_tokens * 8 * G, 500, replace=False)).astype(np.int64))
+
+
 def test_many_groups():
     """More groups than the split model looks at, more requests than the merge caches."""
     rng = np.random.default_rng(8)
@@ -226,10 +237,11 @@ def test_leading_scores_of_minus_infinity(hidden):
         assert ((out[s] - v.mean(0)).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("where", ["q", "prefix_k", "prefix_v", "own_v"])
-def test_nan_stays_visible(where):
+def test_nan_stays_visible(where, dtype):
     """A NaN in a visible input reaches the rows that see it, and no others."""
-    b = make([(160, [(1, 9), (1, 20)]), (32, [(1, 5)])], 4, 2, 64, 16, seed=71)
+    b = make([(160, [(1, 9), (1, 20)]), (32, [(1, 5)])], 4, 2, 64, 16, dtype, seed=71)
     rows = [0, 1]
     if where == "q":
         b.q[1] = float("nan")
@@ -331,6 +343,16 @@ def test_lengths_beyond_the_bound_do_not_leave_the_workspace():
     b = _bad("bf16")
     b.max_seq_len = 100  # the last request alone is shorter
     _zero_and_right(_bad("bf16"), run(b, status=pa.PA_DEV_BAD_SEQLEN), [0, 1, 2, 3, 4], "bound")
+
+
+def test_a_prefix_beyond_the_bound_of_the_lengths():
+    """max_prefix_len may be set above max_seq_len; no request can have such a prefix."""
+    def batch():
+        return make([(96, [(1, 5)]), (4096, [(1, 5), (9, 9)]), (48, [(3, 40)])], 8, 2, 64, 16, seed=22)
+    b = batch()
+    b.max_seq_len = 200
+    assert b.max_prefix_len == 4096
+    _zero_and_right(batch(), run(b, status=pa.PA_DEV_BAD_SEQLEN), [1, 2], "prefix")
 
 
 # ---------------------------------------------------------------------------

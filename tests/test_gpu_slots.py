@@ -120,6 +120,14 @@ def test_bad_metadata(what):
     assert want[4] != 0
 
 
+def test_starts_whose_difference_wraps():
+    """Decreasing starts that a 32-bit difference would call a length."""
+    lens, qsl, table, nb, free = batch(7, 3, 40, 100, 16)
+    top = 2 ** 31 - 1
+    want = check(np.array([top, top, 40]), np.array([0, top, -5, 3]), table, 16, nb, 3, free, 0)
+    assert want[4] == pa.PA_DEV_BAD_QSL
+
+
 def test_no_requests_and_no_tokens():
     e = np.zeros(0, int)
     got = step(e, [0], np.zeros((0, 4), int), 16, 8, 5, [3, 4], 1)

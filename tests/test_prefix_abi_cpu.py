@@ -61,6 +61,13 @@ def test_prefix_workspace_bytes(lib):
     # part: at least one per KV head and group, and 152 where the prefix has tiles for them
     assert base >= 152 * 256 * (128 + 1) * 4
     assert f(pa.PA_BF16, 1, 1, 1, 32, 8, 128, 100) < base / 10
+    # one tile of positions cannot be split: an item for each KV head and group, their partials alone
+    one = f(pa.PA_BF16, 64, 64, 64, 32, 8, 128, 128)
+    assert 8 * 64 * 256 * 129 * 4 < one < 8 * 66 * 256 * 129 * 4 * 2
+    # sizes whose products pass what a call takes
+    top = 2 ** 31 - 1
+    assert f(pa.PA_BF16, top, top, top, top, top, 128, top) == 0
+    assert f(pa.PA_BF16, 1, top, 1, 64, 64, 64, top) == 0
     assert f(pa.PA_BF16, -1, 1, 1, 32, 8, 128, 64) == 0 and f(1, 1, 1, 1, 32, 5, 128, 64) == 0
 
 
