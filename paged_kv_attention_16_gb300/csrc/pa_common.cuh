@@ -593,6 +593,18 @@ __device__ inline void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligne
 __device__ inline void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ inline void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The start of a row or tile kernel.  In a pa_forward call: the kernels before
+// it, the planner among them, are done.  With partial_only it is launched from
+// the trigger of a kernel that has awaited the planner itself, so the plan and
+// all that the planner awaited are there already (the fence keeps what an
+// earlier kernel left in this SM's L1 out of the way); of the kernels in
+// between it reads nothing, and runs beside them.  It then calls pdl_wait()
+// before it ends, so that whatever waits for it waits for them too.
+__device__ inline void plan_wait(const FwdParams &p) {
+  if (p.partial_only) __threadfence();
+  else pdl_wait();
+}
+
 __device__ inline void named_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }

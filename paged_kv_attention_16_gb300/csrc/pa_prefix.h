@@ -59,7 +59,7 @@ __device__ inline PrefixItem prefix_item(const PrefixParams &p, const PrefixGrou
   int lo = 0, hi = p.num_groups - 1;
   while (lo < hi) {  // the first group that ends behind the item
     const int mid = (lo + hi) >> 1;
-    if (__ldg(p.grp_end + mid) > item) hi = mid; else lo = mid + 1;
+    if (p.grp_end[mid] > item) hi = mid; else lo = mid + 1;
   }
   PrefixGroup g = g0;
   if (lo) g = p.grp[lo];

@@ -163,9 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const FwdParams &f = p.f;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = f.num_heads / f.num_kv_heads, TQ = 128 / G, bs = f.block_size;
-  pdl_trigger();
   if (smem_u32(smem) & 1023) {  // the same for every thread: all leave together
     if (tid == 0) atomicOr(f.status, PA_DEV_INTERNAL);
+    pdl_wait();  // (the own part's kernels count on the plan being done)
     return;
   }
   if (tid == 0) {
@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kIssueWarp) {
     reg_dec<kOtherRegs>();
-    pdl_wait();  // the plan
+    pdl_wait();     // the plan
+    pdl_trigger();  // the own part's kernels count on it being done
     const int n_items = p.plan->n_items;
     const PrefixGroup g0 = p.grp[0];
     if (warp >= kLoad0 && warp < kLoadEnd) {

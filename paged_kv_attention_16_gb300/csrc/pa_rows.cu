@@ -177,7 +177,7 @@ __global__ void __maxnreg__(168) row_kernel(const __grid_constant__ CUtensorMap 
   }
   __syncthreads();
   pdl_trigger();
-  pdl_wait();  // the plan
+  plan_wait(p);
   bool dead = false;
 
   if (warp == C::NWARP) {
@@ -240,7 +240,10 @@ __global__ void __maxnreg__(168) row_kernel(const __grid_constant__ CUtensorMap 
         mbar_arrive(&item_full[slot]);
       }
       ++seq;
-      if (d.done) break;
+      if (d.done) {
+        if (p.partial_only) pdl_wait();
+        break;
+      }
       if (d.bad) continue;
       // stream the split's K/V stages
       const int nst = (d.kv_hi - d.kv_lo + C::ST - 1) / C::ST;

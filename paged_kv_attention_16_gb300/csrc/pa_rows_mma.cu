@@ -185,7 +185,7 @@ __global__ void __maxnreg__(168) row_mma_kernel(const __grid_constant__ CUtensor
   }
   __syncthreads();
   pdl_trigger();
-  pdl_wait();  // the plan
+  plan_wait(p);
   bool dead = false;
 
   if (warp == C::NWARP) {
@@ -386,6 +386,7 @@ __global__ void __maxnreg__(168) row_mma_kernel(const __grid_constant__ CUtensor
         }
       }
     }
+    if (p.partial_only) pdl_wait();
     return;
   }
 

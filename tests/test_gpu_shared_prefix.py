@@ -364,6 +364,63 @@ def test_two_calls_give_the_same_bits():
     assert torch.equal(run(b).view(torch.int16), run(b).view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype,max_query_len", [("bf16", 0), ("bf16", 1), ("f32", 0)])
+def test_a_run_of_calls_on_one_workspace_with_other_metadata_each(dtype, max_query_len):
+    """Back to back calls whose metadata is written by the kernel before each of
+    them: every kernel of a call goes by that call's plan, none by the last one's."""
+    def batch(i):
+        def reqs(n, lo, hi, j):
+            one = decodes(n, lo, hi, 10 * i + j)
+            return one if max_query_len == 1 else one[:-2] + [(9 + 3 * i, 40), (23 - 3 * i, 60 + i)]
+        return make([(16 * (30 - 9 * i), reqs(9 + i, 1, 300, 1)), (16 * (5 + 20 * i), reqs(12 - i, 1, 200, 2))],
+                    8, 2, 128, 16, dtype, seed=33)
+    names = ("q", "block_table", "seq_lens", "query_start_loc", "group_start_loc", "prefix_lens")
+    bs = [batch(i) for i in range(3)]
+    T, NB, M = bs[0].num_tokens, max(b.num_blocks for b in bs), max(b.block_table.shape[1] for b in bs)
+    for b in bs:
+        assert b.num_tokens == T and b.num_seqs == bs[0].num_seqs
+        b.block_table = torch.nn.functional.pad(b.block_table, (0, M - b.block_table.shape[1]), value=-1)
+        b.max_seq_len = max(x.max_seq_len for x in bs)
+        b.max_prefix_len = max(x.max_prefix_len for x in bs)
+        for name in ("k_cache", "v_cache"):
+            c = getattr(b, name)
+            setattr(b, name, torch.cat([c, c.new_zeros((NB - c.shape[0], *c.shape[1:]))]))
+    ds = [pa.to_device(b) for b in bs]
+    want = [pa.forward_shared_prefix(d, max_query_len=max_query_len).clone() for d in ds]
+    for b, w in zip(bs, want):
+        check(b, w, rows=np.arange(0, T * 8, 7))
+    live = [[getattr(d, n).clone() for n in names] for d in ds]
+    kv = [torch.cat([getattr(d, n) for d in ds]) for n in ("k_cache", "v_cache")]
+    for i, x in enumerate(live):  # one pool, the batches' pages one behind the other
+        x[1] = torch.where(x[1] >= 0, x[1] + i * NB, x[1])
+    d = pa.to_device(bs[0])
+    d.k_cache, d.v_cache = kv
+    outs = torch.full((60, *d.q.shape), 7.0, dtype=d.q.dtype, device="cuda")
+    ws = torch.empty(pa.pa_forward_shared_prefix_workspace_bytes(
+        pa.PA_BF16 if dtype == "bf16" else pa.PA_F32, d.num_seqs, 2, T, 8, 2, 128, d.max_seq_len),
+        dtype=torch.uint8, device="cuda")
+
+    def steps():
+        for i in range(len(outs)):
+            for name, x in zip(names, live[(i + i // 4) % 3]):
+                getattr(d, name).copy_(x)
+            pa.forward_shared_prefix(d, out=outs[i], max_query_len=max_query_len, workspace=ws)
+    steps()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    eager = outs.clone()
+    outs.fill_(7.0)
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in (eager, outs):
+        for i in range(len(outs)):
+            assert torch.equal(got[i], want[(i + i // 4) % 3]), i
+    assert pa.pa_get_device_status() == 0
+
+
 def test_calls_on_two_streams_at_once():
     made = [make([(4096, decodes(24, 1, 300, i))], 16, 4, 128, 16, seed=40 + i) for i in range(2)]
     d = [pa.to_device(b) for b in made]
