@@ -39,17 +39,23 @@ constexpr int kRowItems = 2;
 constexpr int kRowItemTarget = 2560;
 // What an item costs beside its tiles (query loads, the first scores' and the
 // last products' latency, storing and merging 256 partial rows), in tiles.
-constexpr int kItemOverhead = 2;
+constexpr int kItemOverhead = 3;
 
 // ---------------------------------------------------------------------------
 // planner: one block
 // ---------------------------------------------------------------------------
 
 // Tiles per split.  Each thread tries one number of splits of the longest
-// prefix: its length L gives every group ceil(n_g / L) splits, the items run in
-// ceil(items / SMs) waves, and a wave lasts L + kItemOverhead tiles.
+// prefix: its length L gives every group ceil(n_g / L) splits.  The prefix part
+// is done after ceil(items / SMs) waves of L + kItemOverhead tiles; the SMs are
+// done with it and with the own part, which takes the SMs that it leaves
+// (`own` tiles of one SM), after (tiles + items kItemOverhead + own) / SMs; and
+// what is left of the own part when the last prefix item ends should be a round
+// of its items, own / (kRowItems SMs).  So a batch with much of its own gets few,
+// long items, on some of the SMs: 64 requests behind 8192 positions 76 -> 67 us,
+// 256 behind 32768 310 -> 288 us against the prefix part sized for itself.
 __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const int *s_w, int nmax,
-                                  unsigned long long tiles) {
+                                  unsigned long long tiles, unsigned long long own) {
   __shared__ unsigned long long s_cost[kPlanThreads / 32];
   const int NG = p.num_groups, tid = threadIdx.x;
   if (nmax <= 0) return 1;
@@ -65,7 +71,8 @@ __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const i
     for (int g = 0; g < NG; ++g) items += (unsigned long long)s_w[g] * (((unsigned)s_n[g] + L - 1) / L);
     if (s == 1 || items <= (unsigned long long)p.item_cap) {
       const unsigned waves = ((unsigned)min(items, 0x7fffffffull) + p.num_sms - 1) / p.num_sms;
-      cost = (unsigned long long)waves * (L + kItemOverhead);
+      cost = max((unsigned long long)waves * (L + kItemOverhead) * p.num_sms + own / kRowItems,
+                 tiles + items * kItemOverhead + own);
     }
   }
   unsigned long long best = cost << 9 | tid;  // ties: the fewest splits
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   __shared__ int s_qsl[kPlanCache + 1], s_len[kPlanCache], s_gsl[kPlanCache + 1], s_pre[kPlanCache];
   __shared__ int s_n[kModelGroups], s_w[kModelGroups];
   __shared__ int s_nmax;
-  __shared__ unsigned long long s_tiles, s_work;
+  __shared__ unsigned long long s_tiles, s_work, s_ext;
   const FwdParams &f = p.f;
   const int S = f.num_seqs, NG = p.num_groups, T = f.num_tokens, tid = threadIdx.x;
   const int Hk = f.num_kv_heads, G = f.num_heads / Hk, H = f.num_heads;
@@ -96,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   const bool cached = S <= kPlanCache && NG <= kPlanCache;
   if (tid == 0) {
     s_nmax = 0;
-    s_tiles = s_work = 0;
+    s_tiles = s_work = s_ext = 0;
   }
   pdl_trigger();
   pdl_wait();
@@ -174,17 +181,25 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       atomicAdd(&s_tiles, (unsigned long long)n * Hk * gr.nrp);
     }
   }
-  unsigned long long work = 0;
+  unsigned long long work = 0, ext = 0;  // positions of decode rows; tiles of longer requests
   for (int s = tid; s < S; s += kPlanThreads) {
     if (qsl(s + 1) < qsl(s)) bad = 1;
     int g;
     ReqInfo r{};
     classify(s, g, r);
-    if ((r.flags & kFlagValid) && r.q_len == 1) work += r.ctx - r.kv_base;
+    if (r.flags & kFlagValid) {
+      const unsigned len = r.ctx - r.kv_base;
+      if (r.q_len == 1) work += len;
+      else ext += (((unsigned long long)r.q_len * G + 127) / 128) * ((len + 127) / 128);
+    }
   }
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  for (int o = 16; o >= 1; o >>= 1) {
+    work += __shfl_xor_sync(0xffffffffu, work, o);
+    ext += __shfl_xor_sync(0xffffffffu, ext, o);
+  }
   if ((tid & 31) == 0 && work) atomicAdd(&s_work, work);
+  if ((tid & 31) == 0 && ext) atomicAdd(&s_ext, ext);
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       atomicOr(f.status, PA_DEV_BAD_QSL);
@@ -204,7 +219,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     for (unsigned at = (tid & 31) * 128; gr.q_len > 0 && at < (unsigned)gr.prefix / bs * 4; at += 32 * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
   }
-  const int L = plan_splits(p, s_n, s_w, s_nmax, s_tiles);
+  // (fp32: both parts run on CUDA cores, and the prefix part is sized alone)
+  const unsigned long long own =
+      f.dtype == PA_BF16 ? s_work * Hk / 128 * (f.head_dim == 128 ? 18 : 10) / 16 + s_ext * Hk * 14 / 16 : 0;
+  const int L = plan_splits(p, s_n, s_w, s_nmax, s_tiles, own);
   // The own part's decode rows: about kRowItems items a resident block, down to
   // one 64-position stage of the row kernel.
   const unsigned target = min(kRowItems * max(f.row_ctas, 1), kRowItemTarget);
