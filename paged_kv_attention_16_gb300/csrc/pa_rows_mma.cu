@@ -59,7 +59,11 @@ struct MmaRowCfg {
   static constexpr int KS = D / 16;                  // k-steps of S = Q K^T
   static constexpr int NT = D / 8;                   // n-tiles of O
   static constexpr int NSLOT = 2;                    // merge scratch slots
-  static constexpr int SCR_BYTES = NSLOT * G * D * 4;
+  // columns of O merged at a time: half of them where all would cost a third
+  // ring stage (256 decode rows of 1024 positions at G = 16: 107 us, 123 with two
+  // stages)
+  static constexpr int SCRD = G * D > 8 * 128 ? D / 2 : D;
+  static constexpr int SCR_BYTES = NSLOT * G * SCRD * 4;
   static constexpr int MAX_PAGES = kRowMaxSplit / BOX + 2;
   static constexpr int FPREF_BYTES = (kFastMaxSeqs + 1) * 4;  // decode-only item prefix
   // everything but the ring and the scratch (barriers for up to 6 stages)
@@ -78,9 +82,16 @@ struct MmaRowCfg {
   static constexpr int NBAR = 2 * NSTAGE + 4;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
   static_assert(2 * (SMEM + 64 + 1024) <= 233472, "two CTAs per SM");
-  static constexpr int OPT = (G * D + 127) / 128;         // merge outputs per thread
+  static constexpr int OPT = (G * SCRD + 127) / 128;      // merge outputs per thread,
+  static constexpr int VEC = OPT < 4 ? OPT : 4;           // this many side by side
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static_assert(G >= 1 && G <= 16, "at most 16 query heads per KV head");
+};
+
+// N values side by side, moved in one access.
+template <typename T, int N>
+struct __align__(sizeof(T) * N) RowVec {
+  T v[N];
 };
 
 struct MmaRowDesc {
@@ -675,13 +686,14 @@ __global__ void __maxnreg__(168) row_mma_kernel(const __grid_constant__ CUtensor
     // which fold them in (log-sum-exp) and hand the result on; the output
     // stage then merges two slots.  (Four slots would cost a ring stage at
     // G = 8.)
-    auto put = [&](int slot) {
+    constexpr int NTP = C::SCRD / 8;  // n-tiles of O a pass
+    auto put = [&](int slot, int n0) {
       if (gq < G) {
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
-          *reinterpret_cast<float2 *>(&s_o[(slot * G + gq) * D + n * 8 + 2 * tq]) =
-              make_float2(o[n][0], o[n][1]);
-        if (tq == 0) {
+        for (int n = 0; n < NTP; ++n)
+          *reinterpret_cast<float2 *>(&s_o[(slot * G + gq) * C::SCRD + n * 8 + 2 * tq]) =
+              make_float2(o[n0 + n][0], o[n0 + n][1]);
+        if (tq == 0 && n0 == 0) {
           s_m[slot * G + gq] = m_lo;
           s_l[slot * G + gq] = l_lo;
         }
@@ -689,74 +701,90 @@ __global__ void __maxnreg__(168) row_mma_kernel(const __grid_constant__ CUtensor
       if constexpr (G > 8) {
         if (gq + 8 < G) {
 #pragma unroll
-          for (int n = 0; n < C::NT; ++n)
-            *reinterpret_cast<float2 *>(&s_o[(slot * G + gq + 8) * D + n * 8 + 2 * tq]) =
-                make_float2(o[n][2], o[n][3]);
-          if (tq == 0) {
+          for (int n = 0; n < NTP; ++n)
+            *reinterpret_cast<float2 *>(&s_o[(slot * G + gq + 8) * C::SCRD + n * 8 + 2 * tq]) =
+                make_float2(o[n0 + n][2], o[n0 + n][3]);
+          if (tq == 0 && n0 == 0) {
             s_m[slot * G + gq + 8] = m_hi;
             s_l[slot * G + gq + 8] = l_hi;
           }
         }
       }
     };
-    // fold slot `slot`'s row `row` (fragment columns c0, c0 + 1 of o) into m, l, o
-    auto fold = [&](int slot, int row, float &m, float &l, int c0) {
-      const float mp = s_m[slot * G + row], lp = s_l[slot * G + row];
-      const float mn = fmaxf(m, mp);
-      const float a = m == -INFINITY ? 0.f : fast_exp2(m - mn);
-      const float b = mp == -INFINITY ? 0.f : fast_exp2(mp - mn);
-      l = l * a + lp * b;
-      m = mn;
+    // fold slot `slot`'s row `row` (fragment columns c0, c0 + 1 of o) into m,
+    // l (the first pass, which sets the weights a and b) and o
+    auto fold = [&](int slot, int row, float &m, float &l, float &a, float &b, int c0, int n0) {
+      if (n0 == 0) {
+        const float mp = s_m[slot * G + row], lp = s_l[slot * G + row];
+        const float mn = fmaxf(m, mp);
+        a = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+        b = mp == -INFINITY ? 0.f : fast_exp2(mp - mn);
+        l = l * a + lp * b;
+        m = mn;
+      }
 #pragma unroll
-      for (int n = 0; n < C::NT; ++n) {
-        const float2 po = *reinterpret_cast<const float2 *>(&s_o[(slot * G + row) * D + n * 8 + 2 * tq]);
-        o[n][c0] = o[n][c0] * a + po.x * b;
-        o[n][c0 + 1] = o[n][c0 + 1] * a + po.y * b;
+      for (int n = 0; n < NTP; ++n) {
+        const float2 po =
+            *reinterpret_cast<const float2 *>(&s_o[(slot * G + row) * C::SCRD + n * 8 + 2 * tq]);
+        o[n0 + n][c0] = o[n0 + n][c0] * a + po.x * b;
+        o[n0 + n][c0 + 1] = o[n0 + n][c0 + 1] * a + po.y * b;
       }
     };
-    named_sync(1, 128);  // the scratch of the previous item has been read
-    if (warp >= 2) put(warp - 2);
-    named_sync(1, 128);
-    if (warp < 2) {
-      if (gq < G) fold(warp, gq, m_lo, l_lo, 0);
-      if constexpr (G > 8) {
-        if (gq + 8 < G) fold(warp, gq + 8, m_hi, l_hi, 2);
+    float a_lo = 0.f, b_lo = 0.f, a_hi = 0.f, b_hi = 0.f;
+#pragma unroll
+    for (int n0 = 0; n0 < C::NT; n0 += NTP) {
+      named_sync(1, 128);  // the scratch of the previous item or pass has been read
+      if (warp >= 2) put(warp - 2, n0);
+      named_sync(1, 128);
+      if (warp < 2) {
+        if (gq < G) fold(warp, gq, m_lo, l_lo, a_lo, b_lo, 0, n0);
+        if constexpr (G > 8) {
+          if (gq + 8 < G) fold(warp, gq + 8, m_hi, l_hi, a_hi, b_hi, 2, n0);
+        }
       }
-    }
-    named_sync(1, 128);  // slots read
-    if (warp < 2) put(warp);
-    named_sync(1, 128);
-    // ---- log-sum-exp merge of the two slots, then output or partial
-    const int e0 = tid * C::OPT;
-    if (e0 < G * D) {
-      const int h = e0 / D, d0 = e0 % D;
-      float M = -INFINITY;
+      named_sync(1, 128);  // slots read
+      if (warp < 2) put(warp, n0);
+      named_sync(1, 128);
+      // ---- log-sum-exp merge of the two slots, then output or partial
 #pragma unroll
-      for (int w = 0; w < C::NSLOT; ++w) M = fmaxf(M, s_m[w * G + h]);
-      float L = 0.f, acc[C::OPT];
+      for (int v = 0; v < C::OPT; v += C::VEC) {
+        const int e0 = v * 128 + tid * C::VEC;
+        if (e0 >= G * C::SCRD) continue;
+        const int h = e0 / C::SCRD, d0 = e0 % C::SCRD;
+        float M = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < C::OPT; ++x) acc[x] = 0.f;
+        for (int w = 0; w < C::NSLOT; ++w) M = fmaxf(M, s_m[w * G + h]);
+        float L = 0.f, acc[C::VEC];
 #pragma unroll
-      for (int w = 0; w < C::NSLOT; ++w) {
-        const float ms = s_m[w * G + h];
-        if (ms == -INFINITY) continue;
-        const float wt = fast_exp2(ms - M);
-        L = fmaf(s_l[w * G + h], wt, L);
+        for (int x = 0; x < C::VEC; ++x) acc[x] = 0.f;
 #pragma unroll
-        for (int x = 0; x < C::OPT; ++x) acc[x] = fmaf(s_o[(w * G + h) * D + d0 + x], wt, acc[x]);
-      }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      if (d.direct) {
-        const float dinv = sink_inv(p.sinks, kvh * G + h, M, L);  // the row's own output
-        __nv_bfloat16 *dst =
-            reinterpret_cast<__nv_bfloat16 *>(p.out) + ((size_t)d.tok * H + kvh * G + h) * D + d0;
+        for (int w = 0; w < C::NSLOT; ++w) {
+          const float ms = s_m[w * G + h];
+          if (ms == -INFINITY) continue;
+          const float wt = fast_exp2(ms - M);
+          L = fmaf(s_l[w * G + h], wt, L);
+          const RowVec<float, C::VEC> ov =
+              *reinterpret_cast<const RowVec<float, C::VEC> *>(&s_o[(w * G + h) * C::SCRD + d0]);
 #pragma unroll
-        for (int x = 0; x < C::OPT; ++x) dst[x] = __float2bfloat16_rn(acc[x] * dinv);
-      } else {
-        const long long prow = d.prow0 + (long long)h * d.nsplit;
+          for (int x = 0; x < C::VEC; ++x) acc[x] = fmaf(ov.v[x], wt, acc[x]);
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int col = n0 * 8 + d0;
+        if (d.direct) {
+          const float dinv = sink_inv(p.sinks, kvh * G + h, M, L);  // the row's own output
+          RowVec<__nv_bfloat16, C::VEC> y;
 #pragma unroll
-        for (int x = 0; x < C::OPT; ++x) p.part_o[prow * D + d0 + x] = acc[x] * inv;
-        if (d0 == 0) p.part_lse[prow] = L > 0.f ? M + log2f(L) : -INFINITY;
+          for (int x = 0; x < C::VEC; ++x) y.v[x] = __float2bfloat16_rn(acc[x] * dinv);
+          *reinterpret_cast<RowVec<__nv_bfloat16, C::VEC> *>(
+              reinterpret_cast<__nv_bfloat16 *>(p.out) + ((size_t)d.tok * H + kvh * G + h) * D + col) = y;
+        } else {
+          const long long prow = d.prow0 + (long long)h * d.nsplit;
+          RowVec<float, C::VEC> y;
+#pragma unroll
+          for (int x = 0; x < C::VEC; ++x) y.v[x] = acc[x] * inv;
+          *reinterpret_cast<RowVec<float, C::VEC> *>(p.part_o + prow * D + col) = y;
+          if (col == 0) p.part_lse[prow] = L > 0.f ? M + log2f(L) : -INFINITY;
+        }
       }
     }
     if (p.fast && !d.direct) fast_finish(d);
