@@ -609,10 +609,15 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
 
 template <typename T, int D>
 cudaError_t launch_merge_d(const PrefixParams &p, cudaStream_t st) {
-  // Groups a row: enough of them to give every SM work.  Few rows (a small
-  // decode batch) have many partials each, many rows few.
+  // Groups a row: as many as the SMs hold at once (two blocks each): 2048 rows
+  // take 64 us of a call with 4, 67 with 8; 5760 rows 66 with one, 70 with 4; 384
+  // rows of 75 partials 52 with 16, 54 with 8, 78 with one.  And no more than a
+  // row's partials fill, four at a time: 128 rows of 11 take 18.6 with 4, 19.3
+  // with 16.
   const long long rows = (long long)p.f.num_tokens * p.f.num_heads, sms = p.num_sms;
-  const int W = rows <= 4 * sms ? 16 : rows <= 16 * sms ? 8 : rows <= 64 * sms ? 4 : 1;
+  const long long most = ceil_div_ll(p.f.max_seq_len, kPrefixTile) + 4;
+  const int fit = rows <= 4 * sms ? 16 : rows <= 8 * sms ? 8 : rows <= 16 * sms ? 4 : 1;
+  const int W = std::min(fit, most <= 16 ? 4 : most <= 32 ? 8 : 16);
   auto kern = W == 16 ? prefix_merge_kernel<T, D, 16>
               : W == 8 ? prefix_merge_kernel<T, D, 8>
               : W == 4 ? prefix_merge_kernel<T, D, 4> : prefix_merge_kernel<T, D, 1>;

@@ -7,6 +7,7 @@ integer addresses.  There is no fallback: if libpa.so is missing or fails to
 load, every call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -441,6 +442,10 @@ def pa_forward_shared_prefix_workspace_bytes(dtype, num_seqs, num_groups, num_to
         int(num_kv_heads), int(head_dim), int(max_seq_len))
 
 
+# A call's workspace size from its extents alone, asked of the library once for each.
+_prefix_workspace_bytes = functools.lru_cache(maxsize=1024)(pa_forward_shared_prefix_workspace_bytes)
+
+
 def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                              group_start_loc, prefix_lens, num_heads, num_kv_heads, head_dim,
                              block_size, scale, out, stream=None, *, max_seq_len, max_prefix_len,
@@ -485,8 +490,7 @@ def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_s
     raw = _stream_ptr(stream, device)
     L = _lib or lib()
     if workspace is None:
-        need = L.pa_forward_shared_prefix_workspace_bytes(
-            dt, S, NG, T, int(num_heads), int(num_kv_heads), int(head_dim), int(max_seq_len))
+        need = _prefix_workspace_bytes(dt, S, NG, T, num_heads, num_kv_heads, head_dim, max_seq_len)
         if stream is None or raw == _stream_ptr(None, device):
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:  # allocated for the stream that uses it, so that its reuse is ordered there
