@@ -1009,57 +1009,49 @@ pa_status launch_rows_and_tiles(const FwdCall &c, FwdParams &p, int num_sms, cud
     if (!encode_tiled(&tm_vt, c.v_cache, c.dtype, 5, dims, strides, box, true))
       return PA_ERR_CUDA;
   }
-  auto rows = [&]() -> pa_status {
-    if (c.all_tile) return PA_OK;  // no row items
-    cudaError_t row_err = cudaSuccess;
-    int slot = timed ? prof_begin(PA_K_ROW, st) : -1;
-    if (mma_rows) {
-      row_err = launch_row_mma_kernel(p, tm_kr, tm_vr, row_ctas, st);
-    } else {
-      // fp32: whole rows of head_dim elements, no swizzle (CUDA-core kernel)
-      CUtensorMap tm_k, tm_v;
-      if (!encode_cache_map(&tm_k, c.k_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
-                            c.num_kv_heads, c.head_dim, c.head_dim, 16,
-                            CU_TENSOR_MAP_SWIZZLE_NONE) ||
-          !encode_cache_map(&tm_v, c.v_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
-                            c.num_kv_heads, c.head_dim, c.head_dim, 16,
-                            CU_TENSOR_MAP_SWIZZLE_NONE))
-        return PA_ERR_CUDA;
-      row_err = launch_row_kernel(p, tm_k, tm_v, row_ctas, st);
-    }
+  cudaError_t row_err = cudaSuccess;
+  int slot = timed ? prof_begin(PA_K_ROW, st) : -1;
+  if (c.all_tile) {
+    // no row items: the row kernel is not launched
+  } else if (mma_rows) {
+    row_err = launch_row_mma_kernel(p, tm_kr, tm_vr, row_ctas, st);
+  } else {
+    // fp32: whole rows of head_dim elements, no swizzle (CUDA-core kernel)
+    CUtensorMap tm_k, tm_v;
+    if (!encode_cache_map(&tm_k, c.k_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
+                          c.num_kv_heads, c.head_dim, c.head_dim, 16,
+                          CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_cache_map(&tm_v, c.v_cache, c.dtype, c.kv_layout, c.num_blocks, c.block_size,
+                          c.num_kv_heads, c.head_dim, c.head_dim, 16,
+                          CU_TENSOR_MAP_SWIZZLE_NONE))
+      return PA_ERR_CUDA;
+    row_err = launch_row_kernel(p, tm_k, tm_v, row_ctas, st);
+  }
+  prof_end(slot, st);
+  if (row_err != cudaSuccess) return PA_ERR_CUDA;
+  // A decode-only batch (the caller's bound max_query_len == 1; a request
+  // above it is zeroed as bad metadata) has no tile items: no launch.
+  if (tile_ok && c.max_query_len != 1) {
+    // Q as [tokens, heads, dim] with 64-element (128-byte) swizzled boxes of
+    // G heads x (128 / G) tokens.
+    CUtensorMap tm_q;
+    EncodeTiledFn fn = encode_fn();
+    cuuint64_t qd[3] = {(cuuint64_t)dqk, (cuuint64_t)c.num_heads, (cuuint64_t)c.num_tokens};
+    cuuint64_t qs[2] = {(cuuint64_t)dqk * 2, (cuuint64_t)c.num_heads * dqk * 2};
+    cuuint32_t qb[3] = {64, (cuuint32_t)group, (cuuint32_t)(kTileRows / group)};
+    cuuint32_t qe[3] = {1, 1, 1};
+    if (!fn ||
+        fn(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(c.q), qd, qs, qb, qe,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return PA_ERR_CUDA;
+    slot = timed ? prof_begin(PA_K_TILE, st) : -1;
+    const cudaError_t tile_err =
+        launch_tile_kernel(p, tm_q, tm_kt, page_boxes ? tm_vt : tm_vr, tm_krope, num_sms, st);
     prof_end(slot, st);
-    return row_err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-  };
-  auto tiles = [&]() -> pa_status {
-    // A decode-only batch (the caller's bound max_query_len == 1; a request
-    // above it is zeroed as bad metadata) has no tile items: no launch.
-    if (tile_ok && c.max_query_len != 1) {
-      // Q as [tokens, heads, dim] with 64-element (128-byte) swizzled boxes of
-      // G heads x (128 / G) tokens.
-      CUtensorMap tm_q;
-      EncodeTiledFn fn = encode_fn();
-      cuuint64_t qd[3] = {(cuuint64_t)dqk, (cuuint64_t)c.num_heads, (cuuint64_t)c.num_tokens};
-      cuuint64_t qs[2] = {(cuuint64_t)dqk * 2, (cuuint64_t)c.num_heads * dqk * 2};
-      cuuint32_t qb[3] = {64, (cuuint32_t)group, (cuuint32_t)(kTileRows / group)};
-      cuuint32_t qe[3] = {1, 1, 1};
-      if (!fn ||
-          fn(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(c.q), qd, qs, qb, qe,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return PA_ERR_CUDA;
-      const int slot = timed ? prof_begin(PA_K_TILE, st) : -1;
-      const cudaError_t tile_err =
-          launch_tile_kernel(p, tm_q, tm_kt, page_boxes ? tm_vt : tm_vr, tm_krope, num_sms, st);
-      prof_end(slot, st);
-      if (tile_err != cudaSuccess) return PA_ERR_CUDA;
-    }
-    return PA_OK;
-  };
-  // Beside the prefix part (partial_only) the longer items go first: a kernel
-  // starts when all blocks of the one before are in place.
-  const pa_status s = p.partial_only ? tiles() : rows();
-  if (s != PA_OK) return s;
-  return p.partial_only ? rows() : tiles();
+    if (tile_err != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }
 
 pa_status fwd_launch(const FwdCall &c, void *workspace, unsigned int *status, int num_sms,

@@ -598,11 +598,17 @@ __device__ inline void pdl_trigger() { asm volatile("griddepcontrol.launch_depen
 // the trigger of a kernel that has awaited the planner itself, so the plan and
 // all that the planner awaited are there already (the fence keeps what an
 // earlier kernel left in this SM's L1 out of the way); of the kernels in
-// between it reads nothing, and runs beside them.  It then calls pdl_wait()
-// before it ends, so that whatever waits for it waits for them too.
+// between it reads nothing, and runs beside them.
 __device__ inline void plan_wait(const FwdParams &p) {
   if (p.partial_only) __threadfence();
   else pdl_wait();
+}
+// The end of such a kernel: with partial_only its first block stays until the
+// kernels before it are done, so that whatever waits for it waits for them too.
+// (One block is enough.  With all of them staying, the next kernel's found no
+// room: 24 requests of 1 to 512 new tokens 118 us, 111 so.)
+__device__ inline void plan_pass(const FwdParams &p) {
+  if (p.partial_only && blockIdx.x == 0) pdl_wait();
 }
 
 __device__ inline void named_sync(int id, int count) {

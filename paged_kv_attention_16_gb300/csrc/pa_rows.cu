@@ -241,7 +241,7 @@ __global__ void __maxnreg__(168) row_kernel(const __grid_constant__ CUtensorMap 
       }
       ++seq;
       if (d.done) {
-        if (p.partial_only) pdl_wait();
+        plan_pass(p);
         break;
       }
       if (d.bad) continue;

@@ -397,7 +397,7 @@ __global__ void __maxnreg__(168) row_mma_kernel(const __grid_constant__ CUtensor
         }
       }
     }
-    if (p.partial_only) pdl_wait();
+    plan_pass(p);
     return;
   }
 

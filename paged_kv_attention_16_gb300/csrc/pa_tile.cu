@@ -208,12 +208,12 @@ __global__ void __launch_bounds__((TileCfg<DQK, DV>::THREADS), 2)
   plan_wait(p);  // and, but for partial_only, the row kernel before us in the stream
   const long long n_items = p.plan->n[kListTile];
   if (n_items == 0) {  // no extend / prefill rows in this batch
-    if (p.partial_only) pdl_wait();
+    plan_pass(p);
     return;
   }
   if (smem_u32(smem_raw) & 1023) {  // the same for every thread: all leave together
     if (tid == 0) atomicOr(p.status, PA_DEV_INTERNAL);
-    if (p.partial_only) pdl_wait();
+    plan_pass(p);
     return;
   }
 
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__((TileCfg<DQK, DV>::THREADS), 2)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
-  if (p.partial_only) pdl_wait();
+  plan_pass(p);
 }
 
 template <int DQK, int DV, bool PB64>
