@@ -18,7 +18,13 @@
 // Splits are whole 128-position tiles of equal length, sized by a cost model
 // over the whole grid (see plan_splits).  Items that read the same keys are
 // neighbours, so that they run at the same time and share them through L2.
+//
+// Launches: plan, prefix part, rows, tiles (unless declared decode-only), merge.
+// The rows and tiles need the plan alone: they start as the prefix part's blocks
+// end (programmatic launches, see plan_wait), so the SMs that the prefix part
+// leaves are theirs.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_prefix.h"
 
@@ -38,7 +44,8 @@ constexpr int kModelGroups = 128;       // groups up to which the split model is
 constexpr int kRowItems = 2;
 constexpr int kRowItemTarget = 2560;
 // What an item costs beside its tiles (query loads, the first scores' and the
-// last products' latency, storing and merging 256 partial rows), in tiles.
+// last products' latency, storing and merging 256 partial rows), in tiles.  (1 to
+// 4 measure alike, 5 and more slower on batches of many row blocks.)
 constexpr int kItemOverhead = 3;
 
 // ---------------------------------------------------------------------------
@@ -89,7 +96,9 @@ __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const i
 // A chain of short steps: what it takes is the latency of each.  The metadata
 // is read once, into shared memory, every step after that works from there
 // (batches beyond kPlanCache read it again from L2), and the groups' items and
-// the requests' lists share one scan.
+// the requests' lists share one scan.  4 to 64 requests take 5 us from the end of
+// the kernel before it (checks 1.3, splits 1.1, lists 2.3), mostly the first
+// passes of its code through the instruction cache.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   __shared__ long long scratch[4 * 33];
   __shared__ int s_qsl[kPlanCache + 1], s_len[kPlanCache], s_gsl[kPlanCache + 1], s_pre[kPlanCache];
@@ -294,20 +303,39 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
 // ---------------------------------------------------------------------------
 // prefix part on CUDA cores (fp32)
 // ---------------------------------------------------------------------------
-// Four threads share a row (each every fourth 16-byte group of its head_dim
-// values), 64 rows a pass; 32 keys and values at a time in shared memory.  A
-// row's scores of 8 keys are reduced over its four threads, then join the
-// running maximum and sum.  Every key costs 4 D fp32 operations a row: the FMA
-// units bound it.
+// Eight threads share four rows (each every eighth 16-byte group of their
+// head_dim values), 128 rows a pass; 32 keys and values at a time in shared
+// memory, each load of them used for the four rows.  The scores of 8 keys are
+// reduced over the eight threads so that each ends up with one key's (7
+// shuffles a row), join the running maximum and sum there, and the weights are
+// handed round again.  256 rows x 128 positions take 71 us of an SM at head_dim
+// 128 (36 TFLOP/s over the GPU) and 47 at 64, against 143 and 80 with one row in
+// four threads: what bounds it is the latency of the FMA chains and the shuffles
+// with two warps a scheduler, all that four rows' registers leave room for.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 32;
+constexpr int kSimtRows = 4;  // rows of a thread, 32 apart
 
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixParams p, int hnd) {
-  __shared__ __align__(16) float s_k[kSimtKeys][D], s_v[kSimtKeys][D];
-  __shared__ int s_page[kSimtKeys];
+struct SimtTile {  // two of them: one is loaded while the other is used
+  float k[kSimtKeys][D], v[kSimtKeys][D];
+};
+
+// 16 bytes from global to shared memory, or zeros.
+__device__ inline void copy16(float *dst, const float *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSimtThreads, 1) prefix_simt_kernel(const PrefixParams p, int hnd) {
+  constexpr int N = D / 8;  // values of a row that a thread holds
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  SimtTile<D> *s_tile = reinterpret_cast<SimtTile<D> *>(s_raw);
   const FwdParams &f = p.f;
-  const int tid = threadIdx.x, c = tid & 3, G = f.num_heads / f.num_kv_heads, bs = f.block_size;
+  const int tid = threadIdx.x, lane = tid & 31, c = tid & 7;
+  const int G = f.num_heads / f.num_kv_heads, bs = f.block_size;
   const int Hk = f.num_kv_heads;
   pdl_wait();     // the plan
   pdl_trigger();  // the own part's kernels count on the plan being done
@@ -319,104 +347,142 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
     const PrefixItem it = prefix_item(p, g0, item, G);
     const int32_t *bt = f.block_table + (size_t)it.req0 * f.max_blocks_per_seq;
     const int rows = min(kPrefixRows, (it.q_len - it.t0) * G);
-    for (int pass = 0; pass * 64 < rows; ++pass) {
-      const int r = pass * 64 + (tid >> 2);  // row of the item
-      const bool in = r < rows;
-      const int tok = it.q_start + it.t0 + (in ? r / G : 0), head = it.kvh * G + (in ? r % G : 0);
-      const float *q = static_cast<const float *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
-      float qv[D / 4], o[D / 4];
+    // (a pass of fewer rows than threads' rows holds one or two a thread)
+    auto pass = [&](int row0, auto rows_c) {
+      constexpr int R = decltype(rows_c)::value;
+      float qv[R][N], o[R][N], m[R], l[R];
 #pragma unroll
-      for (int i = 0; i < D / 4; i += 4) {
+      for (int r = 0; r < R; ++r) {
+        const int row = min(row0 + r * 32 + (tid >> 3), rows - 1);
+        const int tok = it.q_start + it.t0 + row / G, head = it.kvh * G + row % G;
+        const float *q = static_cast<const float *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          qv[i + e] = q[i * 4 + c * 4 + e] * f.scale_log2;
-          o[i + e] = 0.f;
+        for (int i = 0; i < N; i += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(q + i * 8 + c * 4);
+          qv[r][i] = x.x * f.scale_log2;
+          qv[r][i + 1] = x.y * f.scale_log2;
+          qv[r][i + 2] = x.z * f.scale_log2;
+          qv[r][i + 3] = x.w * f.scale_log2;
+          o[r][i] = o[r][i + 1] = o[r][i + 2] = o[r][i + 3] = 0.f;
         }
       }
-      float m = -INFINITY, l = 0.f;
       int bad = 0;
-      for (int lo = it.kv_lo; lo < it.kv_hi; lo += kSimtKeys) {
-        __syncthreads();  // the tile before is read
-        if (tid < kSimtKeys) {
-          const int pos = lo + tid;
-          int page = -1;
-          if (pos < it.kv_hi) {
-            page = __ldg(bt + pos / bs);
-            if (page < 0 || page >= f.num_blocks) {
-              atomicOr(f.status, PA_DEV_BAD_BLOCK);
-              page = -2;
-            }
-          }
-          s_page[tid] = page;
-        }
-        __syncthreads();
+      auto load = [&](SimtTile<D> &t, int lo) {
+#pragma unroll 4
         for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
-          const int j = e / (D / 4), x = e % (D / 4) * 4, page = s_page[j];
-          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
-          if (page >= 0) {
-            const int slot = (lo + j) % bs;
-            const size_t row = hnd ? ((size_t)page * Hk + it.kvh) * bs + slot
-                                   : ((size_t)page * bs + slot) * Hk + it.kvh;
-            k4 = *reinterpret_cast<const float4 *>(kc + row * D + x);
-            v4 = *reinterpret_cast<const float4 *>(vc + row * D + x);
+          const int j = e / (D / 4), x = e % (D / 4) * 4, pos = lo + j;
+          bool in = pos < it.kv_hi;
+          size_t row = 0;
+          if (in) {
+            const int page = __ldg(bt + pos / bs), slot = pos % bs;
+            if (page < 0 || page >= f.num_blocks) {
+              bad = 1;
+              in = false;
+            } else {
+              row = hnd ? ((size_t)page * Hk + it.kvh) * bs + slot : ((size_t)page * bs + slot) * Hk + it.kvh;
+            }
           }
-          *reinterpret_cast<float4 *>(&s_k[j][x]) = k4;
-          *reinterpret_cast<float4 *>(&s_v[j][x]) = v4;
+          copy16(&t.k[j][x], kc + row * D + x, in);
+          copy16(&t.v[j][x], vc + row * D + x, in);
         }
-        __syncthreads();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      int buf = 0;
+      load(s_tile[0], it.kv_lo);
+      for (int lo = it.kv_lo; lo < it.kv_hi; lo += kSimtKeys, buf ^= 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the tile is there, and the other one has been read
+        const SimtTile<D> &t = s_tile[buf];
+        if (lo + kSimtKeys < it.kv_hi) load(s_tile[buf ^ 1], lo + kSimtKeys);
         for (int j0 = 0; j0 < kSimtKeys && lo + j0 < it.kv_hi; j0 += 8) {
-          float sc[8];
-          float mx = -INFINITY;
+          float w[R][8];  // the thread's shares of 8 scores, then its key's weight in [0]
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float acc = 0.f;
+            float4 k4[N / 4];
 #pragma unroll
-            for (int i = 0; i < D / 4; i += 4) {
-              const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[j0 + j][i * 4 + c * 4]);
-              acc = fmaf(qv[i], k4.x, acc);
-              acc = fmaf(qv[i + 1], k4.y, acc);
-              acc = fmaf(qv[i + 2], k4.z, acc);
-              acc = fmaf(qv[i + 3], k4.w, acc);
+            for (int i = 0; i < N / 4; ++i)
+              k4[i] = *reinterpret_cast<const float4 *>(&t.k[j0 + j][i * 32 + c * 4]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+              for (int i = 0; i < N / 4; ++i) {
+                ffma2(a0, a1, qv[r][4 * i], qv[r][4 * i + 1], k4[i].x, k4[i].y);
+                ffma2(b0, b1, qv[r][4 * i + 2], qv[r][4 * i + 3], k4[i].z, k4[i].w);
+              }
+              w[r][j] = (a0 + a1) + (b0 + b1);
             }
-            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-            if (s_page[j0 + j] == -2) bad = 1;
-            sc[j] = lo + j0 + j < it.kv_hi ? acc : -INFINITY;
-            mx = fmaxf(mx, sc[j]);
           }
-          if (mx > m) {
-            const float a = m == -INFINITY ? 0.f : exp2f(m - mx);
-            l *= a;
+          const bool seen = lo + j0 + c < it.kv_hi;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) o[i] *= a;
-            m = mx;
+          for (int r = 0; r < R; ++r) {
+            // sum over the eight threads, half of the keys going to each half
+#pragma unroll
+            for (int h = 4; h >= 1; h >>= 1) {
+#pragma unroll
+              for (int j = 0; j < h; ++j) {
+                const float keep = c & h ? w[r][j + h] : w[r][j], send = c & h ? w[r][j] : w[r][j + h];
+                w[r][j] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+              }
+            }
+            const float sc = seen ? w[r][0] : -INFINITY;
+            float mx = sc;
+#pragma unroll
+            for (int h = 4; h >= 1; h >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, h));
+            if (mx > m[r]) {
+              const float a = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mx);
+              l[r] *= a;
+#pragma unroll
+              for (int i = 0; i < N; ++i) o[r][i] *= a;
+              m[r] = mx;
+            }
+            w[r][0] = exp2f(sc - (m[r] == -INFINITY ? 0.f : m[r]));
+            l[r] += w[r][0];
           }
-          const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float w = exp2f(sc[j] - mu);
-            l += w;
+            float4 v4[N / 4];
 #pragma unroll
-            for (int i = 0; i < D / 4; i += 4) {
-              const float4 v4 = *reinterpret_cast<const float4 *>(&s_v[j0 + j][i * 4 + c * 4]);
-              o[i] = fmaf(w, v4.x, o[i]);
-              o[i + 1] = fmaf(w, v4.y, o[i + 1]);
-              o[i + 2] = fmaf(w, v4.z, o[i + 2]);
-              o[i + 3] = fmaf(w, v4.w, o[i + 3]);
+            for (int i = 0; i < N / 4; ++i)
+              v4[i] = *reinterpret_cast<const float4 *>(&t.v[j0 + j][i * 32 + c * 4]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float wj = __shfl_sync(0xffffffffu, w[r][0], (lane & 24) | j);
+#pragma unroll
+              for (int i = 0; i < N / 4; ++i) {
+                ffma2(o[r][4 * i], o[r][4 * i + 1], v4[i].x, v4[i].y, wj, wj);
+                ffma2(o[r][4 * i + 2], o[r][4 * i + 3], v4[i].z, v4[i].w, wj, wj);
+              }
             }
           }
         }
       }
-      if (in) {
-        const long long prow = (long long)item * kPrefixRows + r;
-        const float inv = l > 0.f && !bad ? 1.f / l : 0.f;
+      bad = __syncthreads_or(bad);  // (and both tiles have been read)
+      if (bad && tid == 0) atomicOr(f.status, PA_DEV_BAD_BLOCK);
 #pragma unroll
-        for (int i = 0; i < D / 4; i += 4)
-          *reinterpret_cast<float4 *>(p.part_o + prow * D + i * 4 + c * 4) =
-              make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-        if (c == 0)
-          p.part_lse[prow] = bad ? __int_as_float(0x7fc00000) : l > 0.f ? m + log2f(l) : -INFINITY;
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int h = 4; h >= 1; h >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], h);
+        const int row = row0 + r * 32 + (tid >> 3);
+        if (row < rows) {
+          const long long prow = (long long)item * kPrefixRows + row;
+          const float inv = l[r] > 0.f && !bad ? 1.f / l[r] : 0.f;
+#pragma unroll
+          for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(p.part_o + prow * D + i * 8 + c * 4) =
+                make_float4(o[r][i] * inv, o[r][i + 1] * inv, o[r][i + 2] * inv, o[r][i + 3] * inv);
+          if (c == 0)
+            p.part_lse[prow] =
+                bad ? __int_as_float(0x7fc00000) : l[r] > 0.f ? m[r] + log2f(l[r]) : -INFINITY;
+        }
       }
+    };
+    for (int row0 = 0; row0 < rows; row0 += 32 * kSimtRows) {
+      if (rows - row0 <= 32) pass(row0, std::integral_constant<int, 1>());
+      else if (rows - row0 <= 64) pass(row0, std::integral_constant<int, 2>());
+      else pass(row0, std::integral_constant<int, kSimtRows>());
     }
   }
 }
@@ -429,8 +495,9 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixP
 // prefix partials, then its own.  Eight lanes hold a row's head_dim values and
 // walk its partials with a running maximum, four at a time (their loads are
 // independent); W such groups share a row's partials and meet in shared memory.
-// Bound by the latency of a few dependent loads when rows are few, by reading
-// the partials from L2 when they are many.
+// Bound by the latency of a few dependent loads when rows are few (2048 rows of 7
+// partials: 8 us alone), by reading the partials from L2 when they are many
+// (38,700 rows of 256 bytes x 2 to 6: 16 us).
 constexpr int kMergeGroups = kMergeThreads / 8;
 
 template <typename T>
@@ -691,9 +758,18 @@ PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_toke
   return l;
 }
 
+template <int D>
+cudaError_t launch_simt_d(const PrefixParams &p, int hnd, int num_sms, cudaStream_t st) {
+  constexpr int kSmem = 2 * (int)sizeof(SimtTile<D>);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = set_smem_attrs_once(prefix_simt_kernel<D>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(prefix_simt_kernel<D>, dim3(num_sms), dim3(kSimtThreads), kSmem, st, p, hnd);
+}
+
 cudaError_t launch_simt(const PrefixParams &p, int hnd, int num_sms, cudaStream_t st) {
-  auto kern = p.f.head_dim == 128 ? prefix_simt_kernel<128> : prefix_simt_kernel<64>;
-  return launch_dependent(kern, dim3(num_sms * 2), dim3(kSimtThreads), 0, st, p, hnd);
+  return p.f.head_dim == 128 ? launch_simt_d<128>(p, hnd, num_sms, st)
+                             : launch_simt_d<64>(p, hnd, num_sms, st);
 }
 
 }  // namespace

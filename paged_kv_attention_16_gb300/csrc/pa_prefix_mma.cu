@@ -18,6 +18,12 @@
 //                   O += P V (P from TMEM, N = head_dim), taking turns
 //   warps 10-13     TMA: K boxes (10, 11) and V boxes (12, 13) into rings that
 //                   both row tiles read
+// What it takes: 1.4 to 1.45 us of an SM for 256 rows x 128 positions at head_dim
+// 128 (92 % of the measured bf16 peak while it runs; products 1.32), 1.28 at 64
+// (52 %: there the softmax, some 1400 clocks of two warps a scheduler, and the
+// chain S, softmax, P V of each row tile bound it).  128 rows or fewer take 1.33
+// with K and V in L2 and 1.53 from HBM, which is 6.5 TB/s over the SMs.  An item
+// adds about 4 us: its first tile, and 2 us of storing 256 rows of partials.
 // The turns keep the row tiles half a period apart: while one's softmax runs,
 // the other's products do.  (Without them both row tiles' products went side by
 // side, and so did their softmaxes while the tensor pipe idled.)  K and V are

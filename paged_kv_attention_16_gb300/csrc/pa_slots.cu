@@ -22,7 +22,8 @@ namespace {
 // then takes a share of the tokens (request by binary search).  The token at
 // the start of a fresh page writes that page's table entry: pages held before
 // are only read, fresh ones only written, so no entry is both.  What bounds it
-// is the chain of its loads: the lengths, then the pages.
+// is the chain of its loads: the lengths, then the pages (64 requests of one new
+// token 5 us, 512 of up to 2048 10 us).
 constexpr int kTablesThreads = 512;
 constexpr int kTablesMaxSeqs = 16384;  // 12 bytes of shared memory a request
 constexpr int kTokensPerThread = 4;    // tokens a thread takes at a time, side by side
@@ -159,8 +160,9 @@ __global__ void __launch_bounds__(kTablesThreads) block_tables_kernel(const Tabl
 // A copy: 4 x the row bytes of a token move (K and V, read and written), so
 // HBM bounds it.  One warp takes one token's K and V rows, 32 (or 16) bytes a
 // lane at a time, two pieces of each row loaded before the first is stored.
-// 32,730 tokens of 2 KB rows take 40 us (ncu): 6.7 TB/s, 98.6 % of the
-// measured copy bandwidth.
+// 32,730 tokens of 2 KB rows take 38 us (ncu, serialised): 7.1 TB/s where a plain
+// copy reads and writes 6.8, part of the writes being in L2 still.  A decode
+// step's 64 tokens take 4 us, the latency of the slot, then of its rows.
 constexpr int kWriteThreads = 256;
 
 struct SlotWriteArgs {
