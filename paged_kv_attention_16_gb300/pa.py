@@ -47,12 +47,15 @@ class ForwardOptions(ctypes.Structure):
                 ("alibi_sqrt", ctypes.c_int), ("max_query_len", ctypes.c_int)]
 
 
+_LAYOUTS = {"nhd": PA_KV_NHD, "hnd": PA_KV_HND}
+
+
 def layout_code(kv_layout):
     """pa_kv_layout of "nhd" ([num_blocks, block_size, Hk, D]) or "hnd"
     ([num_blocks, Hk, block_size, D]); ints pass through."""
     if isinstance(kv_layout, int):
         return kv_layout
-    return {"nhd": PA_KV_NHD, "hnd": PA_KV_HND}[kv_layout]
+    return _LAYOUTS[kv_layout]
 
 
 class PaError(RuntimeError):
@@ -361,26 +364,23 @@ def pa_block_tables(seq_lens, query_start_loc, block_table, slot_mapping, block_
     rows, width = block_table.shape
     if query_start_loc.numel() != S + 1 or rows != S:
         raise ValueError("query_start_loc [S + 1] and block_table [S, max_blocks] go with seq_lens [S]")
-    device = slot_mapping.get_device()
-    fits = (_current(device) and _fits(device, torch.int64, slot_mapping)
-            and _fits(device, torch.int32, seq_lens, query_start_loc, block_table))
+    grow = free_start is not None
+    if (free_pages is not None) != grow or (free_end is not None) != grow:
+        raise ValueError("free_pages, free_start and free_end go together")
     pages = start = end = pos = None
+    if grow:
+        if free_start.numel() != 1 or free_end.numel() != 1:
+            raise ValueError("free_start and free_end are one int32 each")
+        pages, num_free = free_pages.data_ptr(), free_pages.numel()
+        start, end = free_start.data_ptr(), free_end.data_ptr()
     if positions is not None:
         if positions.numel() != T:
             raise ValueError("positions must have slot_mapping's length")
-        fits = fits and _fits(device, torch.int32, positions)
         pos = positions.data_ptr()
-    if free_start is not None:
-        if free_pages is None or free_end is None:
-            raise ValueError("free_pages, free_start and free_end go together")
-        if free_start.numel() != 1 or free_end.numel() != 1:
-            raise ValueError("free_start and free_end are one int32 each")
-        fits = fits and _fits(device, torch.int32, free_pages, free_start, free_end)
-        pages, num_free = free_pages.data_ptr(), free_pages.numel()
-        start, end = free_start.data_ptr(), free_end.data_ptr()
-    elif free_pages is not None or free_end is not None:
-        raise ValueError("free_pages, free_start and free_end go together")
-    if not fits:
+    device = slot_mapping.get_device()
+    if not (_current(device) and _fits(device, torch.int64, slot_mapping)
+            and _fits(device, torch.int32, seq_lens, query_start_loc, block_table, free_pages,
+                      free_start, free_end, positions)):
         _check_tensors(device, (torch.int64, dict(slot_mapping=slot_mapping)),
                        (torch.int32, dict(seq_lens=seq_lens, query_start_loc=query_start_loc,
                                           block_table=block_table, free_pages=free_pages,
