@@ -148,6 +148,22 @@ def test_many_groups():
     check(b, run(b), rows=np.sort(rng.choice(b.num_tokens * 4, 600, replace=False)).astype(np.int64))
 
 
+def test_more_groups_than_the_planner_keeps():
+    rng = np.random.default_rng(9)
+    b = make([(16 * int(rng.integers(0, 12)), [(1, int(rng.integers(1, 20)))]) for _ in range(1100)],
+             2, 1, 64, 16, seed=9)
+    check(b, run(b, max_query_len=1), rows=np.sort(rng.choice(2200, 500, replace=False)).astype(np.int64))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_group_shares_anything(dtype):
+    b = make([(0, [(1, 40), (7, 90)]), (0, [(3, 3)])], 8, 2, 128, 16, dtype, seed=10)
+    assert b.max_prefix_len == 0
+    check(b, run(b))
+    b = make([(0, [(0, 17), (1, 1)])], 4, 4, 64, 16, dtype, seed=11)
+    check(b, run(b, max_query_len=1))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_sinks(dtype):
     b = make(BATCHES["extend"](16), 8, 2, 128, 16, dtype, seed=3)
