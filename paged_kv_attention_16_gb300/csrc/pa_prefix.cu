@@ -177,9 +177,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   // -- the starts' checks; the groups' tiles; the decode rows' own work
   int bad = 0;
   if (tid == 0) bad = qsl(0) != 0 || qsl(S) != T || gsl(0) != 0 || gsl(NG) != S;
+  // (this thread's first group and request stay in registers for the lists:
+  // the planner's time is that of its code, so what runs once runs once)
+  PrefixGroup gr0{};
+  ReqInfo r0{};
+  int group0 = 0;
   for (int g = tid; g < NG; g += kPlanThreads) {
     if (gsl(g + 1) < gsl(g)) bad = 1;
     const PrefixGroup gr = group_of(g);
+    if (g == tid) gr0 = gr;
     const int n = tiles_of(gr);
     if (NG <= kModelGroups) {
       s_n[g] = n;
@@ -196,6 +202,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     int g;
     ReqInfo r{};
     classify(s, g, r);
+    if (s == tid) r0 = r, group0 = g;
     if (r.flags & kFlagValid) {
       const unsigned len = r.ctx - r.kv_base;
       if (r.q_len == 1) work += len;
@@ -222,11 +229,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   }
   if (flags) atomicOr(f.status, flags);
   // the prefixes' page lists on their way to L2: the next kernel's first loads
-  for (int g = tid >> 5; g < min(NG, kPrefetchGroups); g += kPlanThreads / 32) {
-    const PrefixGroup gr = group_of(g);
-    const char *row = reinterpret_cast<const char *>(f.block_table + (size_t)gr.req0 * f.max_blocks_per_seq);
-    for (unsigned at = (tid & 31) * 128; gr.q_len > 0 && at < (unsigned)gr.prefix / bs * 4; at += 32 * 128)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+  if (cached) {
+    for (int g = tid >> 5; g < min(NG, kPrefetchGroups); g += kPlanThreads / 32) {
+      const char *row = reinterpret_cast<const char *>(f.block_table + (size_t)s_gsl[g] * f.max_blocks_per_seq);
+      const unsigned pages = s_gsl[g + 1] > s_gsl[g] ? (unsigned)min(max(s_pre[g], 0), p.max_prefix_len) / bs : 0;
+      const unsigned bytes = min(pages, (unsigned)f.max_blocks_per_seq) * 4;
+      for (unsigned at = (tid & 31) * 128; at < bytes; at += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+    }
   }
   // (fp32: both parts run on CUDA cores, and the prefix part is sized alone)
   const unsigned long long own =
@@ -249,8 +259,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     PrefixGroup gr{};
     ReqInfo r{};
     int g = 0;
+    if (base == 0) {
+      gr = gr0;
+      r = r0;
+      g = group0;
+    } else {
+      if (i < NG) gr = group_of(i);
+      if (i < S) classify(i, g, r);
+    }
     if (i < NG) {
-      gr = group_of(i);
       const int n = tiles_of(gr), ns = (n + L - 1) / L;
       // equal splits; as many as have tiles
       const int len = ns > 0 ? (n + ns - 1) / ns : 1;
@@ -259,7 +276,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       cnt[0] = (long long)Hk * gr.nrp * gr.nsplit;
     }
     if (i < S) {
-      classify(i, g, r);
       const int own = r.ctx - r.kv_base;
       r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : max(own, 1);
       r.nsplit = max((own + r.split_len - 1) / r.split_len, 1);
