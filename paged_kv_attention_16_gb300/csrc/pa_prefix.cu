@@ -96,9 +96,10 @@ __device__ inline int plan_splits(const PrefixParams &p, const int *s_n, const i
 // A chain of short steps: what it takes is the latency of each.  The metadata
 // is read once, into shared memory, every step after that works from there
 // (batches beyond kPlanCache read it again from L2), and the groups' items and
-// the requests' lists share one scan.  4 to 64 requests take 5 us from the end of
-// the kernel before it (checks 1.3, splits 1.1, lists 2.3), mostly the first
-// passes of its code through the instruction cache.
+// the requests' lists share one scan.  4 to 64 requests take 4.6 us from the end
+// of the kernel before it (metadata 0.6, checks 1.1, splits 1.1, lists 1.8), mostly
+// its code's way into the instruction cache: each element is worked out once, and
+// divisions are few and of 32 bits (5.5 us before).
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   __shared__ long long scratch[4 * 33];
   __shared__ int s_qsl[kPlanCache + 1], s_len[kPlanCache], s_gsl[kPlanCache + 1], s_pre[kPlanCache];
@@ -128,11 +129,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   auto qsl = [&](int s) { return cached ? s_qsl[s] : f.qsl[s]; };
   auto gsl = [&](int g) { return cached ? s_gsl[g] : p.group_start[g]; };
 
+  // positions that a request may have: the caller's bound, and a block-table row's
+  const int longest = (int)min((unsigned long long)f.max_seq_len, (unsigned long long)f.max_blocks_per_seq * bs);
   // a group's prefix, -1 when it is bad
   auto group_prefix = [&](int g) {
     const int P = cached ? s_pre[g] : p.prefix_lens[g];
-    const bool ok = P >= 0 && P <= p.max_prefix_len && P <= f.max_seq_len && (unsigned)P % bs == 0 &&
-                    (unsigned)P / bs <= (unsigned)f.max_blocks_per_seq;
+    const bool ok = P >= 0 && P <= longest && P <= p.max_prefix_len && (unsigned)P % bs == 0;
     return ok ? P : -1;
   };
   unsigned flags = 0;
@@ -163,8 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     r.q_len = qsl(s + 1) - r.q_start;
     r.ctx = cached ? s_len[s] : f.seq_lens[s];
     r.kv_base = P < 0 ? 0 : P;
-    const bool len_ok = r.ctx >= 0 && r.ctx <= f.max_seq_len &&
-                        ((unsigned)r.ctx + bs - 1) / bs <= (unsigned)f.max_blocks_per_seq;
+    const bool len_ok = r.ctx >= 0 && r.ctx <= longest;
     const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen);
     const bool own_ok = P >= 0 && r.ctx - r.q_len >= P;
     const bool valid = r.q_len > 0 && len_ok && q_ok && own_ok;
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   if (cached) {
     for (int g = tid >> 5; g < min(NG, kPrefetchGroups); g += kPlanThreads / 32) {
       const char *row = reinterpret_cast<const char *>(f.block_table + (size_t)s_gsl[g] * f.max_blocks_per_seq);
-      const unsigned pages = s_gsl[g + 1] > s_gsl[g] ? (unsigned)min(max(s_pre[g], 0), p.max_prefix_len) / bs : 0;
+      // (pages have 16 positions or more; a prefix found bad is only held to the row)
+      const unsigned pages = s_gsl[g + 1] > s_gsl[g] ? (unsigned)min(max(s_pre[g], 0), longest) / 16 : 0;
       const unsigned bytes = min(pages, (unsigned)f.max_blocks_per_seq) * 4;
       for (unsigned at = (tid & 31) * 128; at < bytes; at += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
@@ -245,9 +247,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   // The own part's decode rows: about kRowItems items a resident block, down to
   // one 64-position stage of the row kernel.
   const unsigned target = min(kRowItems * max(f.row_ctas, 1), kRowItemTarget);
-  const unsigned long long Lw = (s_work * Hk + target - 1) / target;
-  const int Ld = (int)min(max((Lw + 63) / 64 * 64, (unsigned long long)kFastMinSplit),
-                          (unsigned long long)kRowMaxSplit);
+  // (in floats, whose rounding the bound on the partials has room for)
+  const float Lw = fminf((float)s_work * Hk / target, (float)kRowMaxSplit);
+  const int Ld = min(max(((int)Lw + 64) / 64 * 64, kFastMinSplit), kRowMaxSplit);
   // rows of longer requests on the row path (fp32): at most about 4 splits
   const int Lr = min(max(Ld, (f.max_seq_len / 4 + 16) / 16 * 16), kRowMaxSplit);
 
@@ -268,9 +270,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       if (i < S) classify(i, g, r);
     }
     if (i < NG) {
-      const int n = tiles_of(gr), ns = (n + L - 1) / L;
+      const unsigned n = tiles_of(gr), ns = (n + L - 1) / (unsigned)L;
       // equal splits; as many as have tiles
-      const int len = ns > 0 ? (n + ns - 1) / ns : 1;
+      const unsigned len = ns > 0 ? (n + ns - 1) / ns : 1;
       gr.nsplit = (n + len - 1) / len;
       gr.split_len = len * kPrefixTile;
       cnt[0] = (long long)Hk * gr.nrp * gr.nsplit;
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     if (i < S) {
       const int own = r.ctx - r.kv_base;
       r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : max(own, 1);
-      r.nsplit = max((own + r.split_len - 1) / r.split_len, 1);
+      r.nsplit = max(((unsigned)max(own, 0) + r.split_len - 1) / (unsigned)r.split_len, 1u);
       if (r.flags & kFlagValid) {
         if (r.flags & kFlagRowPath) cnt[1] = (long long)Hk * r.q_len * r.nsplit;
         else cnt[2] = (long long)Hk * (((long long)r.q_len * G + kTileRows - 1) / kTileRows) * r.nsplit;
