@@ -43,6 +43,14 @@ constexpr int kModelGroups = 128;       // groups up to which the split model is
 // row kernel, 64 at G = 4 take 51.5, 51.4, 51.5, 55.
 constexpr int kRowItems = 2;
 constexpr int kRowItemTarget = 2560;
+// Longer requests' rows (128-row tiles of the tile kernel): when they are fewer
+// tiles than this, about two blocks an SM, they are cut into about this many items
+// of kTileMinSplit positions or more (17 requests of up to 15 tokens and 1368
+// positions at G = 16: 70 -> 49 us; 9 of up to 236 and 751 at G = 1: 42 -> 34, 36
+// with 256 positions).  More tiles stay whole: cutting them too costs 4 to 14 us of
+// 111 for 24 requests of up to 512 tokens.
+constexpr int kTileItems = 304;
+constexpr int kTileMinSplit = 128;
 // What an item costs beside its tiles (query loads, the first scores' and the
 // last products' latency, storing and merging 256 partial rows), in tiles.  (1 to
 // 4 measure alike, 5 and more slower on batches of many row blocks.)
@@ -105,6 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   __shared__ int s_qsl[kPlanCache + 1], s_len[kPlanCache], s_gsl[kPlanCache + 1], s_pre[kPlanCache];
   __shared__ int s_n[kModelGroups], s_w[kModelGroups];
   __shared__ int s_nmax;
+  __shared__ unsigned s_units;
   __shared__ unsigned long long s_tiles, s_work, s_ext;
   const FwdParams &f = p.f;
   const int S = f.num_seqs, NG = p.num_groups, T = f.num_tokens, tid = threadIdx.x;
@@ -113,6 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   const bool cached = S <= kPlanCache && NG <= kPlanCache;
   if (tid == 0) {
     s_nmax = 0;
+    s_units = 0;
     s_tiles = s_work = s_ext = 0;
   }
   pdl_trigger();
@@ -197,7 +207,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       atomicAdd(&s_tiles, (unsigned long long)n * Hk * gr.nrp);
     }
   }
-  unsigned long long work = 0, ext = 0;  // positions of decode rows; tiles of longer requests
+  unsigned long long work = 0, ext = 0;  // positions of decode rows; 128 x 64 tiles of longer requests
+  unsigned units = 0;                    // and their 128-row tiles, of a KV head
   for (int s = tid; s < S; s += kPlanThreads) {
     if (qsl(s + 1) < qsl(s)) bad = 1;
     int g;
@@ -207,7 +218,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     if (r.flags & kFlagValid) {
       const unsigned len = r.ctx - r.kv_base;
       if (r.q_len == 1) work += len;
-      else ext += (((unsigned long long)r.q_len * G + 127) / 128) * ((len + 127) / 128);
+      else {
+        const unsigned t = (unsigned)(((unsigned long long)r.q_len * G + kTileRows - 1) / kTileRows);
+        units += t;
+        ext += (unsigned long long)t * ((len + 63) / 64);
+      }
     }
   }
 #pragma unroll
@@ -216,7 +231,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     ext += __shfl_xor_sync(0xffffffffu, ext, o);
   }
   if ((tid & 31) == 0 && work) atomicAdd(&s_work, work);
-  if ((tid & 31) == 0 && ext) atomicAdd(&s_ext, ext);
+  units = __reduce_add_sync(0xffffffffu, units);
+  if ((tid & 31) == 0 && ext) {
+    atomicAdd(&s_ext, ext);
+    atomicAdd(&s_units, units);
+  }
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       atomicOr(f.status, PA_DEV_BAD_QSL);
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   }
   // (fp32: both parts run on CUDA cores, and the prefix part is sized alone)
   const unsigned long long own =
-      f.dtype == PA_BF16 ? s_work * Hk / 128 * (f.head_dim == 128 ? 18 : 10) / 16 + s_ext * Hk * 14 / 16 : 0;
+      f.dtype == PA_BF16 ? s_work * Hk / 128 * (f.head_dim == 128 ? 18 : 10) / 16 + s_ext * Hk * 7 / 16 : 0;
   const int L = plan_splits(p, s_n, s_w, s_nmax, s_tiles, own);
   // The own part's decode rows: about kRowItems items a resident block, down to
   // one 64-position stage of the row kernel.
@@ -250,7 +269,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   // (in floats, whose rounding the bound on the partials has room for)
   const float Lw = fminf((float)s_work * Hk / target, (float)kRowMaxSplit);
   const int Ld = min(max(((int)Lw + 64) / 64 * 64, kFastMinSplit), kRowMaxSplit);
-  // rows of longer requests on the row path (fp32): at most about 4 splits
+  // rows of longer requests: tiles (0: whole), or (fp32) row items of at most
+  // about 4 splits
+  const int Lt = s_units >= (unsigned)kTileItems / Hk
+                     ? 0
+                     : max((int)((float)s_ext * Hk / kTileItems) + 1, kTileMinSplit / 64) * 64;
   const int Lr = min(max(Ld, (f.max_seq_len / 4 + 16) / 16 * 16), kRowMaxSplit);
 
   // -- the groups' items, and the requests' lists: row items, tile items, partial rows
@@ -279,7 +302,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     }
     if (i < S) {
       const int own = r.ctx - r.kv_base;
-      r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : max(own, 1);
+      r.split_len = r.q_len == 1 ? Ld : (r.flags & kFlagRowPath) ? Lr : Lt > 0 ? Lt : max(own, 1);
       r.nsplit = max(((unsigned)max(own, 0) + r.split_len - 1) / (unsigned)r.split_len, 1u);
       if (r.flags & kFlagValid) {
         if (r.flags & kFlagRowPath) cnt[1] = (long long)Hk * r.q_len * r.nsplit;
@@ -743,7 +766,8 @@ PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_toke
   l.item_cap = units + (splits == 1 ? 0 : units >= kPrefixSplitItems ? kPrefixSplitItems
                                         : std::min((long long)kPrefixSplitItems, units * (splits - 1)));
   // own part: decode rows ceil(len / Ld) splits each, Ld sized to the item
-  // target; longer rows one split (tile kernel) or about four (fp32)
+  // target; longer rows one split and what kTileItems adds (tile kernel), or
+  // about four (fp32)
   const long long dec = std::min(S, T);
   long long cap = H * dec * (1 + ceil_div_ll(msl, kRowMaxSplit)) + G * kRowItemTarget;
   long long per_row = 1;
@@ -751,6 +775,8 @@ PrefixLayout prefix_layout(int dtype, int num_seqs, int num_groups, int num_toke
     long long lr = ceil_div_ll(ceil_div_ll(msl, 4), 16) * 16;
     lr = std::min(std::max(lr, (long long)kFastMinSplit), (long long)kRowMaxSplit);
     per_row = ceil_div_ll(msl, lr);
+  } else {
+    cap += std::min((long long)kTileItems * kTileRows, T * H * (ceil_div_ll(msl, kTileMinSplit) - 1));
   }
   cap += T * H * per_row;
   l.part_cap = cap;

@@ -148,6 +148,18 @@ def test_many_groups():
     check(b, run(b), rows=np.sort(rng.choice(b.num_tokens * 4, 600, replace=False)).astype(np.int64))
 
 
+@pytest.mark.parametrize("H,Hk,D,bs,layout", [(64, 4, 128, 16, "nhd"), (4, 2, 64, 64, "hnd"),
+                                              (8, 8, 128, 128, "nhd"), (16, 1, 64, 48, "nhd")])
+def test_few_long_rows_are_cut_over_their_own_positions(H, Hk, D, bs, layout):
+    """Requests of more than one token whose own parts are many positions: several
+    splits a row, the last tokens' rows seeing more of them than the first's."""
+    b = make([(4 * bs, [(15, 1368), (3, 700), (1, 50), (130, 131)]), (0, [(40, 901), (2, 2)])],
+             H, Hk, D, bs, layout=layout, seed=12)
+    sinks = np.linspace(-3, 3, H).astype(np.float32)
+    check(b, run(b, sinks=sinks), sinks=sinks)
+    assert torch.equal(run(b).view(torch.int16), run(b).view(torch.int16))
+
+
 def test_more_groups_than_the_planner_keeps():
     rng = np.random.default_rng(9)
     b = make([(16 * int(rng.integers(0, 12)), [(1, int(rng.integers(1, 20)))]) for _ in range(1100)],
