@@ -42,6 +42,7 @@ constexpr int kBN = kPrefixTile;
 // maximum: far from overflow in bf16 and in the fp32 sums, so a row's reference
 // is mostly its first tile's maximum, and no maximum is taken of the others.
 constexpr float kMostSum = 1048576.f;
+constexpr float kMostLead = 14.f;  // 64 weights of 2^14 sum to that much
 constexpr int kThreads = 512;
 constexpr int kIssueWarp = 8, kLoad0 = 10, kLoadEnd = 14;  // 14, 15 idle
 // launch registers 512 x 128; the softmax warpgroups take 176, the others keep 80
@@ -511,10 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (done < kBN) {
             // The reference of a row that asked for it becomes the maximum of the
-            // scores to come (unless they are all -inf); O and l follow.
+            // scores to come (unless they are all -inf); O and l follow.  So does
+            // that of a row whose scores to come outgrow it: with another row's
+            // first half rejected, nobody has looked at its second one yet.
             const float mx = max_from(done);
             float a = 1.f;
-            if (redo && mx != -INFINITY) {
+            if (mx != -INFINITY && (redo || mx - ref > kMostLead)) {
               if (l != 0.f) a = fast_exp2(ref - mx);
               l *= a;
               ref = mx;

@@ -247,6 +247,89 @@ def test_one_key_takes_the_weight(at):
         assert torch.equal(out[s], want.expand(4, -1))
 
 
+# Scores of one query row by position, the first of them that holds; a score of None is -inf.
+# A row's reference is its maximum over positions 0 .. 127, the first tile of its item.
+PROFILES = [
+    lambda p: 0,
+    lambda p: 30 if p == 130 else 0,                        # grows in the first half of a tile
+    lambda p: 200 if p == 200 else 0,                       # in the second half of the same tile
+    lambda p: None if p < 128 else 90 if p == 200 else 0,   # nothing to see in the first tile
+    lambda p: None if p < 192 else 0,
+    lambda p: 100 if p == 140 else 250 if p == 220 else 0,  # in both halves
+    lambda p: 250 if p == 140 else 100 if p == 220 else 0,
+    lambda p: 255 - p // 4,
+    lambda p: p // 4,
+    lambda p: 150 if p == 330 else 0,                       # the next tile's second half
+    lambda p: 40 if p == 260 else 0,                        # and its first
+    lambda p: 13 if 192 <= p < 256 else 0,                  # just below what moves a reference,
+    lambda p: 16 if 192 <= p < 256 else 0,                  # and just above
+    lambda p: 64 * (p // 32 % 4),
+    lambda p: 120 if p in (191, 447) else 255 if p == 639 else 0,
+    lambda p: None if p < 640 else 0,
+    lambda p: None,
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,layout", [(128, "nhd"), (64, "hnd")])
+def test_rows_of_one_warp_with_other_scores_each(D, layout, dtype):
+    """32 rows side by side (8 requests x 4 heads) whose scores leave their
+    references behind at different places, if at all: what one row needs, the
+    rows beside it neither get in its place nor miss.  Twenty groups of 8 KV
+    heads on the same pages: more row blocks than SMs, so that no prefix is
+    split and an item goes through all five tiles."""
+    n, NG, Hk, own, none = len(PROFILES), 20, 8, 9, 32
+    N = 640 + own
+    b = make([(640, [(1, own)] * 8)] * NG, 4 * Hk, Hk, D, 16, dtype, seed=73, scale=1.0)
+    for t in (b.block_table, b.full_table):
+        for g in range(1, NG):
+            t[8 * g:8 * g + 8] = t[:8]
+    x = np.array([[-np.inf if f(p) is None else f(p) for p in range(N)] for f in PROFILES])
+    keys = torch.zeros((N, D))
+    keys[:, :n] = torch.from_numpy(np.where(np.isinf(x), 0.0, x)).T
+    keys[:, none:none + n] = torch.from_numpy(np.where(np.isinf(x), -2e38, 0.0)).T
+    pages = b.full_table[0, :40].long()
+    b.k_cache[pages] = keys[:640].view(40, 16, 1, D).to(b.k_cache.dtype)
+    tails = b.full_table[:8, 40].long()
+    b.k_cache[tails, :own] = keys[640:].view(1, own, 1, D).to(b.k_cache.dtype)
+    rng = np.random.default_rng(74)
+    of = torch.from_numpy(rng.integers(0, n, (8 * NG, 4 * Hk)))
+    of[:8, :4] = 1  # and warps whose rows have but two profiles
+    of[3, 2] = 2
+    of[8:16, 4:8] = 5
+    of[9, 7] = 4
+    b.q.zero_()
+    b.q.scatter_(2, of[..., None], 1.0)
+    b.q.scatter_(2, none + of[..., None], 2e38)  # times -2e38: an fp32 product of -inf
+    top = x.max(axis=1, keepdims=True)
+    w = np.where(np.isinf(x), 0.0, np.exp(x - np.where(np.isinf(top), 0.0, top)))
+    w = torch.from_numpy(w / np.maximum(w.sum(axis=1, keepdims=True), 1.0))  # (all -inf: no weight)
+    vp = b.v_cache[pages].double().reshape(640, Hk, D)
+    vo = b.v_cache[tails, :own].double()  # [8, own, Hk, D]
+
+    def rows(v_pre, v_own):
+        all_ = (torch.einsum("fp,pkd->fkd", w[:, :640], v_pre)[:, None]
+                + torch.einsum("fp,spkd->fskd", w[:, 640:], v_own))  # [profile, request, head, D]
+        s = torch.arange(8 * NG)[:, None] % 8
+        return all_[of, s, torch.arange(4 * Hk)[None, :] // 4]
+
+    want, absolute = rows(vp, vo), rows(vp.abs(), vo.abs())
+    # The scores are exact (one product of whole numbers).  A weight's exponent takes roundings
+    # of log2 e, the product, the reference, its moves (two at most: a difference of near
+    # references is exact, and what a far one leaves behind has no weight) and the log-sum-exp,
+    # each of 2^-24 x 255 log2 e, and counts twice (weight and denominator); then as in
+    # tolerance().
+    tol = 2.0 ** -24 * (2 * 6 * 255 + 2 * N + 64) * absolute
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (absolute + want.abs())
+    b = inputs.as_hnd(b) if layout == "hnd" else b
+    got = run(b, max_query_len=1).double().cpu()
+    bad = ~torch.isfinite(got).all(-1)
+    assert not bad.any(), f"profiles of rows that are not finite: {sorted(set(of[bad].tolist()))}"
+    over = ((got - want).abs() > tol).any(-1)
+    assert not over.any(), f"profiles of rows that are off: {sorted(set(of[over].tolist()))}"
+
+
 @pytest.mark.parametrize("hidden", [16, 64, 128, 129, 192, 300, 640])
 def test_leading_scores_of_minus_infinity(hidden):
     """The first keys have a score of -inf (an overflowed product): no weight,
