@@ -423,7 +423,9 @@ pa_status pa_cache_write(const void *k_new, const void *v_new, void *k_cache,
  *
  *  q, k_cache, v_cache, seq_lens, query_start_loc, num_heads, num_kv_heads,
  *  head_dim, block_size, scale, out, dtype, max_seq_len: as for pa_forward.
- *  seq_lens count the shared positions too.
+ *  seq_lens count the shared positions too.  query_start_loc may end before
+ *  num_tokens: the rows of q and out behind the last request (a batch padded
+ *  to a captured size) belong to no one, and those of out are left as they were
  *  group_start_loc [num_groups + 1] int32: group g is the requests
  *                  group_start_loc[g] .. group_start_loc[g + 1] - 1;
  *                  group_start_loc[0] = 0, non-decreasing, ends at num_seqs
@@ -446,7 +448,8 @@ pa_status pa_cache_write(const void *k_new, const void *v_new, void *k_cache,
  *                  may overlap need one each.  Its contents need not be set
  *
  * Bad device metadata: as for pa_forward; besides,
- *   PA_DEV_BAD_QSL     also for a bad group_start_loc: every row is 0
+ *   PA_DEV_BAD_QSL     not for qsl[num_seqs] < num_tokens, but also for a bad
+ *                      group_start_loc: every row is 0
  *   PA_DEV_BAD_SEQLEN  also for a prefix_len that is negative, above
  *                      max_prefix_len or max_seq_len, no multiple of
  *                      block_size or longer than a block-table row (the

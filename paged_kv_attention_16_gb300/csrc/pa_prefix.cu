@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
 
   // -- the starts' checks; the groups' tiles; the decode rows' own work
   int bad = 0;
-  if (tid == 0) bad = qsl(0) != 0 || qsl(S) != T || gsl(0) != 0 || gsl(NG) != S;
+  if (tid == 0) bad = qsl(0) != 0 || qsl(S) > T || gsl(0) != 0 || gsl(NG) != S;
   // (this thread's first group and request stay in registers for the lists:
   // the planner's time is that of its code, so what runs once runs once)
   PrefixGroup gr0{};
@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
     for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
     int h = 0, np = 0, n = 0;  // the row's prefix partials, and all of them
+    bool mine = row < rows;    // (not a row behind the last request)
     long long pre0 = 0, own0 = 0, step = 0;
     if (row < rows && !all_bad) {
       const int tok = (int)(row / H);
@@ -602,7 +603,8 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
       }
       const ReqInfo r = f.req[lo];
       const PrefixGroup g = p.grp[p.num_groups == 1 ? 0 : p.req_grp[lo]];
-      if (r.flags & kFlagValid) {
+      mine = tok - r.q_start < r.q_len;
+      if (mine && (r.flags & kFlagValid)) {
         const int i = tok - r.q_start, pos = r.ctx - r.q_len + i;
         np = g.nsplit;
         n = np + (pos - r.kv_base) / r.split_len + 1;
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
         m = top;
       }
     }
-    if (row < rows && part == 0) {
+    if (mine && part == 0) {
       // the sink joins the denominator once, with no value; a row with no
       // weight is 0 O, one with a bad page zero
       float inv = 0.f;

@@ -453,7 +453,8 @@ def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_s
                              alibi_slopes=None, alibi_sqrt=False, max_query_len=0,
                              workspace=None, check=True):
     """Attention for a batch whose requests share prefixes group by group (see
-    include/pa.h).  workspace: a uint8 tensor of at least
+    include/pa.h).  Rows of `out` behind the last request (a padded batch) are
+    left as they were.  workspace: a uint8 tensor of at least
     pa_forward_shared_prefix_workspace_bytes, for this call alone until it has
     run; None takes one from torch's allocator for this call, so calls on
     several streams and captured graphs each have their own."""

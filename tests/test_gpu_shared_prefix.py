@@ -467,6 +467,114 @@ def test_a_prefix_beyond_the_bound_of_the_lengths():
 
 
 # ---------------------------------------------------------------------------
+# rows behind the last request: a batch padded to a captured size
+# ---------------------------------------------------------------------------
+
+def _padded(b, pad):
+    """b with `pad` token rows behind its requests, holding NaN."""
+    b.q = torch.cat([b.q, torch.full((pad, *b.q.shape[1:]), float("nan"), dtype=b.q.dtype)])
+    return b
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,max_query_len,groups", [
+    # few rows and many (another merge), decodes declared and not, more rows than real ones
+    (3, 0, [(96, [(1, 5), (6, 20)]), (0, [(1, 9)])]),
+    (1, 1, [(320, [(1, 5)] * 7), (64, [(1, 30)])]),
+    (200, 1, [(320, [(1, 5), (1, 17)])]),
+    (77, 0, [(640, [(1, 40)] * 500), (16, [(40, 77)])]),
+    # as many tokens as requests, two of which have none; and no token at all
+    (2, 1, [(160, [(1, 5), (0, 9), (1, 3), (0, 0)])]),
+    (4, 0, [(160, [(0, 9), (0, 3)])]),
+])
+def test_rows_behind_the_last_request_are_left_as_they_were(pad, max_query_len, groups, dtype):
+    H, D = 8, 64
+    b = make(groups, H, 2, D, 16, dtype, seed=23)
+    T = b.num_tokens
+    d = pa.to_device(_padded(make(groups, H, 2, D, 16, dtype, seed=23), pad))
+    out = torch.full_like(d.q, 7.0)
+    pa.forward_shared_prefix(d, out=out, max_query_len=max_query_len)
+    assert pa.pa_get_device_status() == 0
+    assert (out[T:] == 7.0).all()
+    if T:
+        check(b, out[:T], rows=np.arange(0, T * H, max(1, T // 40)))
+
+
+def test_starts_beyond_the_tokens_are_refused():
+    b = make([(96, [(1, 5), (6, 20)]), (0, [(1, 9)])], 8, 2, 64, 16, seed=24)
+    b.q = b.q[:-1].contiguous()
+    assert (run(b, status=pa.PA_DEV_BAD_QSL).float() == 0).all()
+
+
+@pytest.mark.parametrize("layout,block_size", [("nhd", 16), ("hnd", 64)])
+def test_a_captured_step_of_changing_size(layout, block_size):
+    """One graph of tables, cache write and attention for up to 24 tokens of up
+    to 6 requests, replayed for steps of fewer: each against the oracle."""
+    H, Hk, D, bs, S, T = 8, 2, 64, block_size, 6, 24
+    prefix, nb, width = [4 * bs, 2 * bs], 64, 12
+    g = torch.Generator().manual_seed(78)
+    shape = (nb, bs, Hk, D) if layout == "nhd" else (nb, Hk, bs, D)
+    kc, vc = (torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    free = torch.randperm(nb, generator=g).to(torch.int32)
+    table = torch.full((S, width), -1, dtype=torch.int32)
+    at = 0
+    for s, p in ((0, prefix[0]), (3, prefix[1])):  # the shared pages, filled beforehand
+        for j in range(p // bs):
+            table[s, j] = free[at]
+            at += 1
+    pages = free[:at].long().cuda()
+    for c in (kc, vc):
+        c[pages] = torch.randn((at, *shape[1:]), generator=g).to(torch.bfloat16).cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    seq, qsl, table, free = i32([0] * S), i32([0] * (S + 1)), table.cuda(), free.cuda()
+    words = [i32([at]), i32([0])]
+    rows = torch.zeros((T, H + 2 * Hk, D), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(T, dtype=torch.int64, device="cuda")
+    out = torch.empty_like(q)
+    starts, plens = i32([0, 3, S]), i32(prefix)
+
+    def step():
+        pa.pa_block_tables(seq, qsl, table, slots, bs, num_blocks=nb, free_pages=free,
+                           free_start=words[0], free_end=words[1])
+        pa.pa_cache_write_slots(rows[:, H:H + Hk], rows[:, H + Hk:], kc, vc, slots, bs, kv_layout=layout)
+        pa.pa_forward_shared_prefix(q, kc, vc, table, seq, qsl, starts, plens, H, Hk, D, bs, 0.125,
+                                    out, max_seq_len=width * bs, max_prefix_len=max(prefix),
+                                    kv_layout=layout)
+        words[0].copy_(words[1])
+    step()  # (no tokens yet; the first call on a device cannot be captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    lens = [prefix[0]] * 3 + [prefix[1]] * 3
+    for q_lens in ([9, 1, 0, 5, 7, 2], [1] * 6, [0, 3, 0, 0, 1, 0], [0] * 6, [1, 0, 20, 0, 0, 3]):
+        n = sum(q_lens)
+        lens = [a + b for a, b in zip(lens, q_lens)]
+        seq.copy_(i32(lens))
+        qsl.copy_(i32(np.cumsum([0] + q_lens).tolist()))
+        rows.copy_(torch.randn((T, H + 2 * Hk, D), generator=g).to(torch.bfloat16))
+        q.copy_(rows[:, :H])
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert pa.pa_get_device_status() == 0
+        assert (slots[n:] == -1).all() and (slots[:n] >= 0).all() and (out[n:] == 7.0).all()
+        if n == 0:
+            continue
+        full = table.cpu().clone()
+        for s in range(S):
+            p = prefix[s // 3] // bs
+            full[s, :p] = full[s // 3 * 3, :p]
+        b = inputs.SharedPrefixBatch(
+            q=q[:n].cpu(), k_cache=kc.cpu(), v_cache=vc.cpu(), block_table=table.cpu(),
+            seq_lens=seq.cpu(), query_start_loc=qsl.cpu(), num_heads=H, num_kv_heads=Hk, head_dim=D,
+            block_size=bs, scale=0.125, dtype="bf16", max_seq_len=width * bs, full_table=full)
+        b.kv_layout = layout
+        check(b, out[:n], what=str(q_lens))
+
+
+# ---------------------------------------------------------------------------
 # streams, graphs, repeated calls
 # ---------------------------------------------------------------------------
 
