@@ -457,7 +457,8 @@ pa_status pa_cache_write(const void *k_new, const void *v_new, void *k_cache,
  *                      for a request whose new tokens begin inside its
  *                      group's prefix (its rows are 0)
  * Errors: as for pa_forward; PA_ERR_INVALID_ARG also for num_tokens > 0 with
- * no group, or a workspace that is not 256-byte aligned; PA_ERR_WORKSPACE when
+ * no group, int32 arrays that are not 4-byte aligned, or a workspace that is
+ * not 256-byte aligned; PA_ERR_WORKSPACE when
  * the workspace is NULL or too small, or when the first call on a device is
  * made during capture.  num_tokens == 0 launches nothing.
  */

@@ -865,6 +865,8 @@ pa_status pa_forward_shared_prefix(
   if (s != PA_OK || num_tokens == 0) return s;
   if (num_groups == 0 || num_seqs == 0 || !group_start_loc || !prefix_lens)
     return PA_ERR_INVALID_ARG;
+  for (const int32_t *x : {block_table, seq_lens, query_start_loc, group_start_loc, prefix_lens})
+    if (reinterpret_cast<uintptr_t>(x) & 3) return PA_ERR_INVALID_ARG;
   const PrefixLayout lay = prefix_layout(dtype, num_seqs, num_groups, num_tokens, num_heads,
                                          num_kv_heads, head_dim, max_seq_len);
   if (lay.item_cap > kMaxItems) return PA_ERR_UNSUPPORTED;

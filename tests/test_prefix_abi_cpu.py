@@ -43,6 +43,12 @@ def test_prefix_argument_checks(lib, kw, want):
     assert _prefix(lib, **kw) == want
 
 
+@pytest.mark.parametrize("name", ["bt", "sl", "qsl", "gsl", "pl"])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_prefix_metadata_alignment(lib, name, off):
+    assert _prefix(lib, **{name: P + off}) == 1
+
+
 @pytest.mark.parametrize("opts,want", [
     ((None, 0, 0, None, 0, 0), 0), ((None, 1, 0, None, 0, 1), 0), ((P + 2, 0, 0, None, 0, 0), 1),
     ((None, 2, 0, None, 0, 0), 1), ((None, 0, -1, None, 0, 0), 1), ((None, 0, 16, None, 0, 0), 2),
