@@ -368,6 +368,28 @@ def test_nan_stays_visible(where, dtype):
         assert torch.isnan(out[t]).all() if t in rows else torch.isfinite(out[t]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_and_a_bad_page_behind_the_first_tile_of_an_item(dtype):
+    """More row blocks than SMs, so that an item goes through all five tiles of
+    its prefix: what one group's later tiles hold reaches that group alone."""
+    groups = [(640, [(1, 5 + s) for s in range(4)])] * 20
+    b, good = (make(groups, 32, 8, 64, 16, dtype, seed=75) for _ in range(2))
+    b.q[2, 7] = float("nan")
+    b.k_cache[int(b.full_table[12, 17]), 3] = float("nan")  # group 3, position 275
+    b.v_cache[int(b.full_table[20, 39]), 15] = float("nan")  # group 5, position 639
+    b.block_table[28, 20] = b.num_blocks  # group 7, position 320
+    out = run(b, status=pa.PA_DEV_BAD_BLOCK, max_query_len=1)
+    nan, zero = torch.isnan(out.float()).all(-1).cpu(), (out == 0).all(-1).cpu()
+    want = torch.zeros((80, 32), dtype=torch.bool)
+    want[2, 7] = want[12:16] = want[20:24] = True
+    assert torch.equal(nan, want)
+    dead = torch.zeros((80, 32), dtype=torch.bool)
+    dead[28:32] = True
+    assert torch.equal(zero, dead)
+    rows = (~(want | dead)).flatten().nonzero().flatten()[::7].numpy()
+    check(good, out, rows=rows)
+
+
 def test_cache_offsets_past_32_bits():
     """Pages beyond 2^32 bytes into the caches."""
     b = make([(1024, decodes(5, 1, 60, 1))], 8, 8, 128, 16, seed=72, poison=False)
