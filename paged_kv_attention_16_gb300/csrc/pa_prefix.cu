@@ -44,7 +44,8 @@ constexpr int kModelGroups = 128;       // groups up to which the split model is
 constexpr int kRowItems = 2;
 constexpr int kRowItemTarget = 2560;
 // Longer requests' rows (128-row tiles of the tile kernel): when they are fewer
-// tiles than this, about two blocks an SM, they are cut into about this many items
+// tiles than this, two blocks on each of 152 SMs (a constant, since the host
+// bounds the partials by it), they are cut into about this many items
 // of kTileMinSplit positions or more (17 requests of up to 15 tokens and 1368
 // positions at G = 16: 70 -> 49 us; 9 of up to 236 and 751 at G = 1: 42 -> 34, 36
 // with 256 positions).  More tiles stay whole: cutting them too costs 4 to 14 us of
@@ -259,6 +260,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
         asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
     }
   }
+  // The own part's work in the prefix part's tiles, of 1.4 us of an SM at head_dim
+  // 128 and 1.28 at 64: 128 positions of a decode row's KV head are 64 or 32 KB, at
+  // an SM's share of the row kernel's 6.3 TB/s 1.57 or 0.79 us, so 18/16 or 10/16 of
+  // a tile; a 128-row x 64-position tile of longer requests takes about 0.6 us, 7/16.
+  // (Without the own part's weight 64 requests behind 8192 positions take 76 us, 67
+  // with it; 256 behind 32768 310 and 288.)
   // (fp32: both parts run on CUDA cores, and the prefix part is sized alone)
   const unsigned long long own =
       f.dtype == PA_BF16 ? s_work * Hk / 128 * (f.head_dim == 128 ? 18 : 10) / 16 + s_ext * Hk * 7 / 16 : 0;
