@@ -575,9 +575,10 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
   const int tid = threadIdx.x, lane = tid & 7, grp = tid >> 3, part = grp % SPLIT;
   pdl_trigger();
   // The plan is done (see plan_wait): with few rows, everything up to the first
-  // partials is read while the kernels that make them run (19.3 us for 4
-  // requests, 19.8 without; 75 for 64, 78).  With many it only costs (the loop
-  // over rows waits anew: merge of 98,000 rows 16.4 us, 14.2 without).
+  // partials is read while the kernels that make them run (64 requests behind
+  // 8192 positions 65 us, 67 without; 48 behind 131072 55, 57).  With many it
+  // only costs (the loop over rows waits anew: merge of 98,000 rows 16.4 us, 14.2
+  // without).
   if (W > 1) __threadfence();
   else pdl_wait();
   T *out = static_cast<T *>(f.out);
