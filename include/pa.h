@@ -43,6 +43,9 @@
  *      PA_DEV_TIMEOUT     a bounded wait inside a kernel gave up (never expected)
  *      PA_DEV_NO_PAGES    pa_block_tables ran out of free pages; the requests
  *                         that got none have no slots
+ *      PA_DEV_BAD_TREE    pa_tree_masks: a parent that is not an earlier new token;
+ *                         pa_cache_accept: a path that does not rise within the
+ *                         request's new tokens
  *      PA_DEV_INTERNAL    a kernel found its launch set-up unusable (its shared
  *                         memory window not 1024-byte aligned) and wrote
  *                         nothing (never expected)
@@ -89,6 +92,7 @@ typedef enum {
 #define PA_DEV_TIMEOUT 0x20u
 #define PA_DEV_INTERNAL 0x40u
 #define PA_DEV_NO_PAGES 0x80u
+#define PA_DEV_BAD_TREE 0x100u
 
 /*
  * pa_forward -- unified paged attention over a mixed batch.
@@ -575,6 +579,235 @@ pa_status pa_cache_write_slots(const void *k_new, const void *v_new,
                                pa_kv_layout kv_layout);
 
 /*
+ * Speculative decoding with a tree of drafted tokens: the new tokens of a request
+ * are the nodes of a tree (or several) below its last cached token, in an order in
+ * which every node comes behind its parent; their K and V rows are in the cache at
+ * positions seq_len - q_len + i, node by node (pa_block_tables and
+ * pa_cache_write_slots put them there).  A step is pa_tree_masks, the model with
+ * pa_forward_tree as its attention, the choice of the accepted path (the
+ * caller's), then pa_cache_accept.
+ *
+ * pa_tree_masks -- each new token's mask over its request's new tokens and its
+ * rotary position, from the tokens' parents:
+ *   bit j of token i's mask: j is i or an ancestor of i
+ *   position of token i:     seq_len - q_len + (number of its ancestors)
+ *
+ *  parents         [num_tokens] int32: the parent's index among the request's new
+ *                  tokens (below the token's own), -1 for a child of the last
+ *                  cached token.  Those behind the last request are not read
+ *  query_start_loc [num_seqs + 1] int32; may end before num_tokens (a batch
+ *                  padded to a captured size)
+ *  seq_lens        [num_seqs] int32, the new tokens included; may be NULL without
+ *                  positions
+ *  tree_mask       [num_tokens, mask_words] uint64, fully written: bit j % 64 of
+ *                  word j / 64 of a token's row; 0 in rows behind the last request
+ *  positions       [num_tokens] int32, fully written (0 behind the last request),
+ *                  or NULL
+ *  mask_words      64-bit words of a row, at least 1
+ * Bad device metadata (the rows concerned get mask 0 and position 0):
+ *   PA_DEV_BAD_QSL     bad query_start_loc: every row
+ *   PA_DEV_BAD_QLEN    more than 64 * mask_words new tokens, or more than seq_len
+ *   PA_DEV_BAD_SEQLEN  a negative seq_len
+ *   PA_DEV_BAD_TREE    a parent that is not an earlier token of the request (or
+ *                      below -1): that token and those below it
+ * Asynchronous on `stream`, one launch, no workspace; capturable after the first
+ * call on a device.  Errors: PA_ERR_INVALID_ARG for null pointers with nonzero
+ * sizes, negative sizes, mask_words < 1 or pointers not aligned to their element.
+ */
+pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_start_loc,
+                        const int32_t *seq_lens, uint64_t *tree_mask,
+                        int32_t *positions, void *stream, int num_seqs,
+                        int num_tokens, int mask_words);
+
+/*
+ * pa_forward_tree -- attention of drafted tokens: new token i of request s (P =
+ * seq_len - q_len cached positions before its new tokens) sees positions j < P and
+ * those new tokens n, at position P + n, whose bit is set in its row of tree_mask:
+ *   out[r][h][:] = sum_j softmax_j(scale * <q[r][h], K_j>) * V_j  over these j.
+ * A row that sees nothing (P = 0 and no bit set) is written as zeros.  Any mask is
+ * taken, a causal one or one that sees later tokens as well; bits from q_len on
+ * mean nothing.  What a row does not see has no influence on it, whatever its K and
+ * V hold (NaN and infinities included).
+ *
+ *  q, k_cache, v_cache, block_table, seq_lens, num_heads, num_kv_heads, head_dim,
+ *  block_size, scale, out, dtype, max_seq_len: as for pa_forward
+ *  query_start_loc as for pa_forward, but it may end before num_tokens: the rows of
+ *                  out behind the last request are left as they were
+ *  tree_mask       [num_tokens, mask_words] uint64, 8-byte aligned (pa_tree_masks)
+ *  options         sinks, kv_layout and max_query_len (a bound on the new tokens of
+ *                  a request) as for pa_forward_ex; a sliding window or ALiBi is
+ *                  PA_ERR_UNSUPPORTED.  NULL: none
+ *  workspace       device memory of the caller, 256-byte aligned, at least
+ *                  pa_forward_tree_workspace_bytes() for the same extents, for this
+ *                  call alone until its kernels have run (calls on several streams,
+ *                  or several captured graphs, that may overlap need one each).  Its
+ *                  contents need not be set
+ * Bad device metadata: as for pa_forward (PA_DEV_BAD_QSL not for a
+ * query_start_loc that ends early); PA_DEV_BAD_QLEN also for a request of more than
+ * 64 * mask_words new tokens.  PA_DEV_BAD_BLOCK zeroes all rows of the 256-row
+ * blocks (tokens x query heads of a KV head) that meet the bad page.
+ * Errors: as for pa_forward; PA_ERR_INVALID_ARG also for no request with
+ * num_tokens > 0, a NULL or misaligned mask or mask_words < 1, int32 arrays that are
+ * not 4-byte aligned, or a workspace that is not 256-byte aligned;
+ * PA_ERR_WORKSPACE when the workspace is NULL or too small, or when the first call
+ * on a device is made during capture; PA_ERR_UNSUPPORTED for extents whose units of
+ * work pass 2^31.  num_tokens == 0 launches nothing.
+ */
+pa_status pa_forward_tree(const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *block_table, const int32_t *seq_lens,
+                          const int32_t *query_start_loc,
+                          const uint64_t *tree_mask, int num_heads,
+                          int num_kv_heads, int head_dim, int block_size,
+                          float scale, void *out, void *stream, pa_dtype dtype,
+                          int num_seqs, int num_tokens, int mask_words,
+                          int max_blocks_per_seq, int num_blocks, int max_seq_len,
+                          const pa_forward_options *options, void *workspace,
+                          size_t workspace_bytes);
+
+/* Workspace bytes pa_forward_tree needs (0 for extents it refuses).  max_query_len
+ * as in the call's options (0: unknown, which takes more). */
+size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tokens,
+                                       int num_heads, int num_kv_heads,
+                                       int head_dim, int max_seq_len,
+                                       int max_query_len);
+
+/*
+ * pa_cache_accept -- behind the verification of drafted tokens: the K and V rows of
+ * the accepted ones, path[s][0 .. path_lens[s]) among request s's new tokens, move
+ * to positions P, P + 1, ... (P = seq_len - q_len), in place, bit for bit; the
+ * request is then P + path_lens[s] positions long, and the pages behind those are
+ * free again.
+ *
+ *  k_cache, v_cache as for pa_cache_write, in place.  A request's pages from P on
+ *                   must not be another request's too
+ *  block_table      [num_seqs, max_blocks_per_seq], read only: the entries of the
+ *                   freed pages stay, and are not read any more
+ *  seq_lens, query_start_loc: those of the verified step
+ *  path             [num_seqs, max_path] int32, strictly rising; entries from
+ *                   path_lens[s] on are not read
+ *  path_lens        [num_seqs] int32, 0 .. min(q_len, max_path)
+ *  seq_lens_out     [num_seqs] int32, written; another array than seq_lens
+ *  freed_pages      [freed_capacity] int32: the ids of the pages from
+ *                   ceil(new length / block_size) to ceil(seq_len / block_size) of
+ *                   each request, in request order (a list that pa_block_tables
+ *                   takes pages from); num_freed: device pointer to one int32, their
+ *                   number.  Both NULL: not wanted
+ *  head_dim x element size a multiple of 16 bytes, at most 16384; any block_size
+ * Bad device metadata: PA_DEV_BAD_QSL (a decreasing pair of starts),
+ * PA_DEV_BAD_SEQLEN, PA_DEV_BAD_QLEN, PA_DEV_BAD_TREE (a path_len or path out of its
+ * range): that request is left as it is, its length too.  PA_DEV_BAD_BLOCK: a row
+ * from or to a bad page is not moved; a bad id in the list of freed pages is
+ * written as -1.  PA_DEV_OVERFLOW: more freed pages than freed_capacity; the first
+ * ones are listed.
+ * Asynchronous on `stream`, one launch, no workspace; capturable after the first
+ * call on a device.  Errors as for pa_cache_write.
+ */
+pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_table,
+                          const int32_t *seq_lens, const int32_t *query_start_loc,
+                          const int32_t *path, const int32_t *path_lens,
+                          int32_t *seq_lens_out, int32_t *freed_pages,
+                          int32_t *num_freed, int num_kv_heads, int head_dim,
+                          int block_size, void *stream, pa_dtype dtype,
+                          int num_seqs, int max_path, int max_blocks_per_seq,
+                          int num_blocks, int freed_capacity,
+                          pa_kv_layout kv_layout);
+
+/*
+ * A cache held to a budget: pa_forward_weights adds up the softmax weight that each
+ * cached position gets, pa_cache_evict drops the positions that got least.
+ *
+ * pa_forward_weights -- pa_forward (causal), and for every KV head k and position j
+ *   W[k][j] = sum over the request's rows i and the query heads h of k of
+ *             softmax_j(scale * <q[i][h], K_j>)
+ * in fp32.  The rows given are those that vote: one token a request in decoding, or
+ * the last tokens of a prompt whose output another call has made.
+ *
+ *  q, k_cache, block_table, seq_lens, num_heads, num_kv_heads, head_dim, block_size,
+ *  scale, dtype, max_seq_len: as for pa_forward
+ *  query_start_loc as for pa_forward; it may end before num_tokens (rows of out
+ *                  behind the last request are left as they were)
+ *  v_cache, out    as for pa_forward.  out may be NULL: the weights alone, v_cache
+ *                  is then not read and may be NULL
+ *  weights         [num_blocks, num_kv_heads, block_size] fp32, 16-byte aligned: the
+ *                  accumulated weight of each cache slot.  A slot that two requests
+ *                  of the call share (a common page) ends up with either one's sum
+ *  accumulate      1: W is added to the slots of the positions before the new tokens,
+ *                  and set in those of the new tokens (whose weight begins here);
+ *                  0: set in all of the request's slots.  Other slots are left as
+ *                  they were
+ *  options         sinks (in the denominators), kv_layout, max_query_len as for
+ *                  pa_forward_ex; a sliding window or ALiBi is PA_ERR_UNSUPPORTED
+ *  workspace       as for pa_forward_tree, pa_forward_weights_workspace_bytes()
+ * Bad device metadata: as for pa_forward_tree; the weights of a request with bad
+ * metadata or a bad page are left as they were.  Errors as for pa_forward_tree;
+ * PA_ERR_INVALID_ARG also for NULL or misaligned weights, or accumulate not 0 or 1.
+ */
+pa_status pa_forward_weights(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_table, const int32_t *seq_lens,
+                             const int32_t *query_start_loc, int num_heads,
+                             int num_kv_heads, int head_dim, int block_size,
+                             float scale, void *out, float *weights, int accumulate,
+                             void *stream, pa_dtype dtype, int num_seqs,
+                             int num_tokens, int max_blocks_per_seq, int num_blocks,
+                             int max_seq_len, const pa_forward_options *options,
+                             void *workspace, size_t workspace_bytes);
+
+/* Workspace bytes pa_forward_weights needs, with or without an output (0 for extents
+ * it refuses).  max_query_len as in the call's options (0: unknown). */
+size_t pa_forward_weights_workspace_bytes(pa_dtype dtype, int num_seqs,
+                                          int num_tokens, int num_heads,
+                                          int num_kv_heads, int head_dim,
+                                          int max_seq_len, int max_query_len);
+
+/*
+ * pa_cache_evict -- a request longer than keep_lens[s] keeps that many positions,
+ * KV head by KV head: its first num_first, its last num_recent, and of the others
+ * those of largest weight (equal ones: the lower positions; -0 equals 0; NaN is
+ * below everything).  Where keep_lens[s] holds fewer, the first ones come before the
+ * recent ones.  The kept K and V rows move to positions 0, 1, ... in their order, in
+ * place and bit for bit, and their weights with them.  The rows keep the rotary
+ * angle they were written with; the caller goes on counting positions by itself.
+ *
+ *  k_cache, v_cache as for pa_cache_write, in place.  A request's pages must not be
+ *                   another request's too
+ *  weights, weights_out  [num_blocks, num_kv_heads, block_size] fp32: the slots of a
+ *                   request's kept positions are written in weights_out (requests
+ *                   that stay as they are included), the others are left as they
+ *                   were.  The same array for both, or two that do not overlap
+ *  block_table      read only, as for pa_cache_accept
+ *  seq_lens         [num_seqs] int32, at most max_seq_len
+ *  keep_lens        [num_seqs] int32, the most positions each may keep (0 and more)
+ *  seq_lens_out     [num_seqs] int32, written: min(seq_len, keep_len); another array
+ *                   than seq_lens and keep_lens
+ *  freed_pages, num_freed, freed_capacity: as for pa_cache_accept
+ *  max_seq_len      host-known bound on seq_lens (sizes the workspace)
+ *  workspace        as for pa_forward_tree, pa_cache_evict_workspace_bytes()
+ *  head_dim x element size a multiple of 16 bytes, at most 16384; any block_size
+ * Bad device metadata: PA_DEV_BAD_SEQLEN (a seq_len or keep_len out of range): that
+ * request is left as it is, seq_lens_out its seq_len, weights_out unwritten.
+ * PA_DEV_BAD_BLOCK: a position on a bad page counts as a NaN weight, rows and
+ * weights from or to it are not moved; in the list of freed pages it is -1.
+ * PA_DEV_OVERFLOW as for pa_cache_accept.
+ * Asynchronous on `stream`, two launches; capturable after the first call on a
+ * device.  Errors as for pa_cache_write; PA_ERR_WORKSPACE as for pa_forward_tree;
+ * PA_ERR_UNSUPPORTED also for extents beyond 2^31 moved runs.
+ */
+pa_status pa_cache_evict(void *k_cache, void *v_cache, const float *weights,
+                         float *weights_out, const int32_t *block_table,
+                         const int32_t *seq_lens, const int32_t *keep_lens,
+                         int32_t *seq_lens_out, int32_t *freed_pages,
+                         int32_t *num_freed, int num_first, int num_recent,
+                         int num_kv_heads, int head_dim, int block_size,
+                         void *stream, pa_dtype dtype, int num_seqs,
+                         int max_blocks_per_seq, int num_blocks, int freed_capacity,
+                         int max_seq_len, pa_kv_layout kv_layout, void *workspace,
+                         size_t workspace_bytes);
+
+/* Workspace bytes pa_cache_evict needs for these extents (0 for ones it refuses). */
+size_t pa_cache_evict_workspace_bytes(pa_dtype dtype, int num_seqs, int num_kv_heads,
+                                      int head_dim, int max_seq_len);
+
+/*
  * pa_debug_gather -- the page-gather indexing alone (PA_KV_NHD), for
  * bit-exact tests:
  *   dense_out[s][j][:] = k_cache[block_table[s][j / bs]][j % bs][0:row_elems]
@@ -605,8 +838,8 @@ pa_status pa_debug_wait_timeout(uint64_t limit_ns, int *done, void *stream);
 
 /*
  * Kernel timing.  While enabled, every kernel that pa_forward, pa_mla_decode,
- * pa_forward_shared_prefix and pa_debug_gather launch is bracketed by a pair of CUDA events recorded
- * on the caller's stream (nothing is recorded for a stream that is being
+ * pa_forward_shared_prefix, pa_forward_tree, pa_forward_weights and pa_debug_gather launch is
+ * bracketed by a pair of CUDA events recorded on the caller's stream (nothing is recorded for a stream that is being
  * captured).  pa_profile_read synchronises on those events, writes for each
  * kernel id below the summed milliseconds and the launch count (arrays of
  * PA_K_COUNT entries), and clears the record.  Recording costs two event
@@ -623,7 +856,9 @@ enum {
   PA_K_UPPROJ = 7,    /* MLA prefill up-projection (tensor cores)   */
   PA_K_MLA_ROPE = 8,  /* MLA prefill rotary-key copy                */
   PA_K_PREFIX = 9,    /* prefix part of pa_forward_shared_prefix    */
-  PA_K_COUNT = 10
+  PA_K_SPAN = 10,     /* pa_forward_tree, pa_forward_weights: keys and values  */
+  PA_K_VOTES = 11,    /* pa_forward_weights: the sums over rows                */
+  PA_K_COUNT = 12
 };
 pa_status pa_profile_enable(int on);
 pa_status pa_profile_read(double *total_ms, int *launches);

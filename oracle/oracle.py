@@ -360,6 +360,206 @@ def widen(a):
     raise TypeError(f"oracle inputs must be float32 or uint16 (bf16 bits), got {a.dtype}")
 
 
+DEV_OVERFLOW, DEV_BAD_TREE = 0x10, 0x100
+
+
+def tree_masks(parents, query_start_loc, num_tokens, mask_words, seq_lens=None):
+    """Ancestor masks and positions of drafted tokens, token by token along the
+    chain of its parents.  Returns (mask [T, words] uint64, positions, status)."""
+    mask = np.zeros((num_tokens, mask_words), np.uint64)
+    positions = np.zeros(num_tokens, np.int64)
+    qsl = [int(x) for x in query_start_loc]
+    if len(qsl) > 1 and (qsl[0] != 0 or qsl[-1] > num_tokens
+                         or any(b < a for a, b in zip(qsl, qsl[1:]))):
+        return mask, positions, DEV_BAD_QSL
+    status = 0
+    for s in range(len(qsl) - 1):
+        n = qsl[s + 1] - qsl[s]
+        length = n if seq_lens is None else int(seq_lens[s])
+        if n == 0:
+            continue
+        if length < 0:
+            status |= DEV_BAD_SEQLEN
+            continue
+        if n > length or n > 64 * mask_words:
+            status |= DEV_BAD_QLEN
+            continue
+        for i in range(n):
+            chain, at = [], i
+            while at >= 0:
+                chain.append(at)
+                up = int(parents[qsl[s] + at])
+                if up < -1 or up >= at:
+                    chain = None
+                    status |= DEV_BAD_TREE
+                    break
+                at = up
+            if chain is None:
+                continue
+            for j in chain:
+                mask[qsl[s] + i, j // 64] |= np.uint64(1 << (j % 64))
+            positions[qsl[s] + i] = length - n + len(chain) - 1
+    return mask, positions, status
+
+
+def mask_rows(mask, start, n):
+    """[n, n] truth values: new token i of the request that starts at row `start`
+    sees new token j."""
+    seen = np.zeros((n, n), bool)
+    for i in range(n):
+        for j in range(n):
+            seen[i, j] = bool(int(mask[start + i, j // 64]) >> (j % 64) & 1)
+    return seen
+
+
+def span_attention(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, num_heads,
+                   num_kv_heads, head_dim, block_size, scale, mask=None, sinks=None,
+                   kv_layout="nhd"):
+    """Attention in which a new token sees its request's cached positions and, of
+    the new ones, those of its mask (None: causal).  Returns per request a dict of
+      out     [n, H, D]    sum p v (0 where a row sees nothing)
+      mass    [n, H, D]    sum p |v|: what relative errors of the weights act on
+      weights [Hk, ctx]    sum over rows and the KV head's query heads of p
+      dots    the largest sum |q_d k_d| over visible pairs, and lse [n, H]."""
+    qw = widen(q)
+    kn, vn = nhd_view(k_cache, kv_layout), None if v_cache is None else nhd_view(v_cache, kv_layout)
+    G = num_heads // num_kv_heads
+    out = []
+    for s in range(len(seq_lens)):
+        q0, q1, ctx = int(query_start_loc[s]), int(query_start_loc[s + 1]), int(seq_lens[s])
+        n, prefix = q1 - q0, ctx - (q1 - q0)
+        seen = np.ones((n, ctx), bool)
+        seen[:, prefix:] = np.tril(np.ones((n, n), bool)) if mask is None else mask_rows(mask, q0, n)
+        at = np.arange(ctx)
+        pages = np.asarray(block_table[s])[at // block_size] if ctx else np.zeros(0, np.int64)
+        r = dict(out=np.zeros((n, num_heads, head_dim)), mass=np.zeros((n, num_heads, head_dim)),
+                 weights=np.zeros((num_kv_heads, ctx)), dots=0.0, lse=np.full((n, num_heads), -np.inf))
+        for h in range(num_kv_heads if n else 0):
+            k = widen(kn[pages, at % block_size, h])
+            v = None if vn is None else widen(vn[pages, at % block_size, h])
+            for g in range(h * G, (h + 1) * G):
+                for i in range(n):
+                    see = seen[i]
+                    if not see.any():
+                        continue
+                    x = scale * (k[see] @ qw[q0 + i, g])
+                    r["dots"] = max(r["dots"], float((np.abs(k[see]) @ np.abs(qw[q0 + i, g])).max()))
+                    top = x.max() if sinks is None else max(x.max(), float(sinks[g]))
+                    e = np.exp(x - top)
+                    den = e.sum() + (0.0 if sinks is None else np.exp(float(sinks[g]) - top))
+                    r["lse"][i, g] = top + np.log(den)
+                    r["weights"][h, see] += e / den
+                    if v is not None:
+                        r["out"][i, g] = (e / den) @ v[see]
+                        r["mass"][i, g] = (e / den) @ np.abs(v[see])
+        out.append(r)
+    return out
+
+
+def _freed(seq_lens, after, block_table, block_size, num_blocks, capacity):
+    """The pages behind the new lengths, request by request: (list, status)."""
+    pages, status = [], 0
+    for s, (a, b) in enumerate(zip(seq_lens, after)):
+        for j in range(-(-int(b) // block_size), -(-int(a) // block_size)):
+            page = int(block_table[s][j])
+            if not 0 <= page < num_blocks:
+                page, status = -1, status | DEV_BAD_BLOCK
+            pages.append(page)
+    if len(pages) > capacity:
+        pages, status = pages[:capacity], status | DEV_OVERFLOW
+    return pages, status
+
+
+def cache_accept(k_cache, v_cache, block_table, seq_lens, query_start_loc, path, path_lens,
+                 block_size, num_blocks, capacity, kv_layout="nhd"):
+    """The accepted tokens' rows moved behind the cached ones, one after the other
+    from a copy of the caches.  Returns (k, v, new lengths, freed pages, status)."""
+    k_store, v_store = np.array(k_cache), np.array(v_cache)
+    k_in, v_in = nhd_view(np.asarray(k_cache), kv_layout), nhd_view(np.asarray(v_cache), kv_layout)
+    k_out, v_out = nhd_view(k_store, kv_layout), nhd_view(v_store, kv_layout)
+    after, status = [int(x) for x in seq_lens], 0
+    for s in range(len(seq_lens)):
+        n = int(query_start_loc[s + 1]) - int(query_start_loc[s])
+        length, m = int(seq_lens[s]), int(path_lens[s])
+        prefix = length - n
+        if n < 0 or int(query_start_loc[s]) < 0:
+            status |= DEV_BAD_QSL
+            continue
+        if length < 0 or length > len(block_table[s]) * block_size:
+            status |= DEV_BAD_SEQLEN
+            continue
+        if n > length:
+            status |= DEV_BAD_QLEN
+            continue
+        nodes = [int(x) for x in path[s][:max(m, 0)]]
+        if (m < 0 or m > n or m > len(path[s]) or any(x < 0 or x >= n for x in nodes)
+                or any(b <= a for a, b in zip(nodes, nodes[1:]))):
+            status |= DEV_BAD_TREE
+            continue
+        after[s] = prefix + m
+        for i, node in enumerate(nodes):
+            if node == i:
+                continue
+            a, b = prefix + node, prefix + i
+            pa, pb = int(block_table[s][a // block_size]), int(block_table[s][b // block_size])
+            if not (0 <= pa < num_blocks and 0 <= pb < num_blocks):
+                status |= DEV_BAD_BLOCK
+                continue
+            k_out[pb, b % block_size] = k_in[pa, a % block_size]
+            v_out[pb, b % block_size] = v_in[pa, a % block_size]
+    pages, st = _freed(seq_lens, after, block_table, block_size, num_blocks, capacity)
+    return k_store, v_store, after, pages, status | st
+
+
+def kept_positions(weights, keep, num_first, num_recent):
+    """The positions that a request with these weights keeps, in order."""
+    n = len(weights)
+    if n <= keep:
+        return list(range(n))
+    first = min(num_first, keep)
+    recent = min(num_recent, keep - first)
+    always = list(range(first)) + list(range(n - recent, n))
+
+    def rank(j):  # heaviest first, NaN last, lower positions before equal ones
+        w = float(weights[j])
+        return (1, 0.0, j) if w != w else (0, -w, j)
+
+    rest = sorted(range(first, n - recent), key=rank)[:keep - first - recent]
+    return sorted(always + rest)
+
+
+def cache_evict(k_cache, v_cache, weights, weights_out, block_table, seq_lens, keep_lens,
+                block_size, num_blocks, capacity, max_seq_len, num_first=0, num_recent=0,
+                kv_layout="nhd"):
+    """Requests cut down to their budgets, KV head by KV head, from copies.  Returns
+    (k, v, weights_out, new lengths, freed pages, status)."""
+    k_store, v_store, w_store = np.array(k_cache), np.array(v_cache), np.array(weights_out)
+    k_in, v_in = nhd_view(np.asarray(k_cache), kv_layout), nhd_view(np.asarray(v_cache), kv_layout)
+    k_out, v_out = nhd_view(k_store, kv_layout), nhd_view(v_store, kv_layout)
+    Hk = k_in.shape[2]
+    after, status = [int(x) for x in seq_lens], 0
+    for s in range(len(seq_lens)):
+        length, keep = int(seq_lens[s]), int(keep_lens[s])
+        if length < 0 or length > max_seq_len or length > len(block_table[s]) * block_size or keep < 0:
+            status |= DEV_BAD_SEQLEN
+            continue
+        after[s] = min(length, keep)
+        page = [int(block_table[s][j // block_size]) for j in range(length)]
+        good = [0 <= x < num_blocks for x in page]
+        if not all(good):
+            status |= DEV_BAD_BLOCK
+        for h in range(Hk):
+            w = [weights[page[j], h, j % block_size] if good[j] else np.nan for j in range(length)]
+            for i, j in enumerate(kept_positions(w, keep, num_first, num_recent)):
+                if good[i] and good[j]:
+                    w_store[page[i], h, i % block_size] = w[j]
+                if i != j and good[i] and good[j]:
+                    k_out[page[i], i % block_size, h] = k_in[page[j], j % block_size, h]
+                    v_out[page[i], i % block_size, h] = v_in[page[j], j % block_size, h]
+    pages, st = _freed(seq_lens, after, block_table, block_size, num_blocks, capacity)
+    return k_store, v_store, w_store, after, pages, status | st
+
+
 def mla_prefill(q, kv_cache, w_kv, block_table, seq_lens, query_start_loc, kv_lora_rank,
                 qk_nope_dim, rope_dim, v_head_dim, block_size, scale, rows=None, q_block=64):
     """fp64 non-absorbed MLA prefill / extend ("vLLM AMD ROCm attention backend

@@ -107,6 +107,8 @@ const char *pa_kernel_name(int kernel_id) {
     case PA_K_UPPROJ: return "upproj";
     case PA_K_MLA_ROPE: return "mla_rope";
     case PA_K_PREFIX: return "prefix";
+    case PA_K_SPAN: return "span";
+    case PA_K_VOTES: return "votes";
   }
   return "unknown";
 }

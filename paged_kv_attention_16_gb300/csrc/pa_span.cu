@@ -1,0 +1,800 @@
+// pa_span.cu -- attention of drafted trees (pa_forward_tree) and attention that
+// adds up the weight every cached position gets (pa_forward_weights): argument
+// checks, the planner, the CUDA-core kernel and the merge.
+//
+// Both read a request's context once for all of its rows (a row: one new token
+// x one query head of a KV head), in units of up to 256 rows cut into equal runs
+// of 128-position tiles (pa_span.h).  For row r and visible positions j,
+//   s_j = scale <q_r, k_j>,  out_r = sum_j e^(s_j) v_j / (sum_j e^(s_j) [+ e^sink]),
+// where the new tokens' positions are visible by the bits of a mask (the
+// ancestors of a drafted token) or causally.  pa_forward_weights also forms
+//   W_j = sum_r e^(s_j) / (sum_i e^(s_i) [+ e^sink])
+// over the rows of a KV head, which needs every row's whole sum first: the pass
+// over the keys leaves each row's log-sum-exp and, for few rows, its scores; the
+// kernels of pa_votes.cu then sum over the rows, position by position.
+#include <algorithm>
+#include <type_traits>
+
+#include "pa_span.h"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeGroups = kMergeThreads / 8;
+
+// ---------------------------------------------------------------------------
+// planner: one block
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParams p) {
+  __shared__ long long scratch[3 * 33];
+  const FwdParams &f = p.f;
+  const int S = f.num_seqs, T = f.num_tokens, tid = threadIdx.x;
+  const int Hk = f.num_kv_heads, G = f.num_heads / Hk;
+  pdl_trigger();
+  pdl_wait();
+  const int longest =
+      (int)min((unsigned long long)f.max_seq_len, (unsigned long long)f.max_blocks_per_seq * f.block_size);
+  unsigned flags = 0;
+  int bad = 0;
+  long long sum[3] = {0, 0, 0};
+  for (int base = 0; base < S; base += kPlanThreads) {
+    const int s = base + tid;
+    SpanReq r{};
+    long long cnt[3] = {0, 0, 0}, tot[3];  // units, laid-out work, kept scores
+    long long scores = 0;
+    if (s < S) {
+      const int q0 = f.qsl[s], q1 = f.qsl[s + 1];
+      if (q1 < q0 || (s == 0 && q0 != 0) || (s == S - 1 && q1 > T)) bad = 1;
+      r.q_start = q0;
+      r.q_len = q1 - q0;
+      r.ctx = f.seq_lens[s];
+      const bool len_ok = r.ctx >= 0 && r.ctx <= longest;
+      const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen) &&
+                        (!p.mask || r.q_len <= 64ll * p.mask_words);
+      if (r.q_len != 0) flags |= (len_ok ? 0u : PA_DEV_BAD_SEQLEN) | (q_ok ? 0u : PA_DEV_BAD_QLEN);
+      r.valid = r.q_len > 0 && len_ok && q_ok;
+      if (r.valid) {
+        const long long rows = (long long)r.q_len * G;
+        r.nblk = (int)((rows + kSpanRows - 1) / kSpanRows);
+        r.ntile = (r.ctx + kSpanTile - 1) / kSpanTile;
+        cnt[0] = (long long)Hk * r.nblk;
+        cnt[1] = cnt[0] * (r.ntile + kSpanOverhead);
+        if (p.keep_scores && rows <= kSpanStoredRows) scores = Hk * rows * r.ntile * kSpanTile;
+        cnt[2] = scores;
+      }
+    }
+    const long long units = cnt[0], cost = cnt[1];
+    block_scan_multi<3>(cnt, scratch, tot);
+    if (s < S) {
+      r.unit0 = (int)(sum[0] + cnt[0] - units);
+      r.cost0 = (unsigned)(sum[1] + cnt[1] - cost);
+      r.score0 = scores > 0 ? sum[2] + cnt[2] - scores : -1;
+      p.req[s] = r;
+      p.cost_end[s] = (unsigned)(sum[1] + cnt[1]);
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) sum[x] += tot[x];
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      atomicOr(f.status, PA_DEV_BAD_QSL);
+      *p.plan = SpanPlan{0, 1, 1};
+    }
+    return;
+  }
+  if (flags) atomicOr(f.status, flags);
+  if (tid == 0) {
+    // (the host has bounded the sum by 2^31)
+    const unsigned total = (unsigned)sum[1];
+    *p.plan = SpanPlan{total, max((total + p.grid - 1) / p.grid, 1u + kSpanOverhead), 0};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the pass over keys and values on CUDA cores
+// ---------------------------------------------------------------------------
+// Eight threads share up to four rows (each every eighth 16-byte group of their
+// head_dim values), 128 rows a pass; 32 keys and values at a time in shared
+// memory, the next ones loaded meanwhile, each load of them used for the four
+// rows.  The scores of 8 keys are reduced over the eight threads so that each ends
+// up with one key's, join the running maximum and sum there, and the weights are
+// handed round again.
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 32;
+constexpr int kSimtRows = 4;  // rows of a thread, 32 apart
+constexpr uint32_t kHidden = 0x80000000u;  // -0, the weight of a hidden position
+
+template <int D>
+struct SpanTileBuf {
+  float k[kSimtKeys][D], v[kSimtKeys][D];
+};
+
+// Four values from global to shared memory as fp32, or zeros.
+__device__ inline void copy4(float *dst, const float *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ inline void copy4(float *dst, const __nv_bfloat16 *src, bool take) {
+  uint2 v = make_uint2(0, 0);
+  if (take) v = *reinterpret_cast<const uint2 *>(src);
+  *reinterpret_cast<float4 *>(dst) = make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
+}
+__device__ inline float4 load4(const float *src) { return *reinterpret_cast<const float4 *>(src); }
+__device__ inline float4 load4(const __nv_bfloat16 *src) {
+  const uint2 v = *reinterpret_cast<const uint2 *>(src);
+  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
+}
+
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanParams p) {
+  constexpr int N = D / 8;  // values of a row that a thread holds
+  constexpr bool VALUES = MODE != kSpanVotesOnly, CAUSAL = MODE != kSpanTree;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  SpanTileBuf<D> *s_tile = reinterpret_cast<SpanTileBuf<D> *>(s_raw);
+  const FwdParams &f = p.f;
+  const int tid = threadIdx.x, lane = tid & 31, c = tid & 7;
+  const int Hk = f.num_kv_heads, G = f.num_heads / Hk, bs = f.block_size;
+  pdl_wait();
+  pdl_trigger();
+  const SpanPlan plan = *p.plan;
+  const T *kc = static_cast<const T *>(p.k_cache);
+  const T *vc = static_cast<const T *>(p.v_cache);
+  SpanCursor cur;
+  cur.start(p, plan, blockIdx.x);
+  SpanPiece it;
+  while (cur.next(p, G, CAUSAL, it)) {
+    const int32_t *bt = f.block_table + (size_t)it.req * f.max_blocks_per_seq;
+    const int rows = min(kSpanRows, (it.q_len - it.t0) * G), prefix = it.ctx - it.q_len;
+    // (a pass of fewer rows than threads' rows holds one or two a thread)
+    auto pass = [&](int row0, auto rows_c) {
+      constexpr int R = decltype(rows_c)::value;
+      float qv[R][N], o[R][VALUES ? N : 1], m[R], l[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int row = min(row0 + r * 32 + (tid >> 3), rows - 1);
+        const int tok = it.q_start + it.t0 + row / G, head = it.kvh * G + row % G;
+        const T *q = static_cast<const T *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const float4 x = load4(q + i * 8 + c * 4);
+          qv[r][i] = x.x * f.scale_log2;
+          qv[r][i + 1] = x.y * f.scale_log2;
+          qv[r][i + 2] = x.z * f.scale_log2;
+          qv[r][i + 3] = x.w * f.scale_log2;
+          if constexpr (VALUES) o[r][i] = o[r][i + 1] = o[r][i + 2] = o[r][i + 3] = 0.f;
+        }
+      }
+      int bad = 0;
+      auto load = [&](SpanTileBuf<D> &t, int lo) {
+#pragma unroll 4
+        for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
+          const int j = e / (D / 4), x = e % (D / 4) * 4, pos = lo + j;
+          bool in = pos < it.kv_hi;
+          size_t row = 0;
+          if (in) {
+            const int page = __ldg(bt + pos / bs), slot = pos % bs;
+            if (page < 0 || page >= f.num_blocks) {
+              bad = 1;
+              in = false;
+            } else {
+              row = p.hnd ? ((size_t)page * Hk + it.kvh) * bs + slot
+                          : ((size_t)page * bs + slot) * Hk + it.kvh;
+            }
+          }
+          copy4(&t.k[j][x], kc + row * D + x, in);
+          if constexpr (VALUES) copy4(&t.v[j][x], vc + row * D + x, in);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      int buf = 0;
+      load(s_tile[0], it.kv_lo);
+      for (int lo = it.kv_lo; lo < it.kv_hi; lo += kSimtKeys, buf ^= 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the tile is there, and the other one has been read
+        const SpanTileBuf<D> &t = s_tile[buf];
+        if (lo + kSimtKeys < it.kv_hi) load(s_tile[buf ^ 1], lo + kSimtKeys);
+        for (int j0 = 0; j0 < kSimtKeys && lo + j0 < it.kv_hi; j0 += 8) {
+          float w[R][8];  // the thread's shares of 8 scores, then its key's weight in [0]
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float4 k4[N / 4];
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+              k4[i] = *reinterpret_cast<const float4 *>(&t.k[j0 + j][i * 32 + c * 4]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+              for (int i = 0; i < N / 4; ++i) {
+                ffma2(a0, a1, qv[r][4 * i], qv[r][4 * i + 1], k4[i].x, k4[i].y);
+                ffma2(b0, b1, qv[r][4 * i + 2], qv[r][4 * i + 3], k4[i].z, k4[i].w);
+              }
+              w[r][j] = (a0 + a1) + (b0 + b1);
+            }
+          }
+          const int pos = lo + j0 + c;  // this thread's key
+          const bool in = pos < it.kv_hi;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            // sum over the eight threads, half of the keys going to each half
+#pragma unroll
+            for (int h = 4; h >= 1; h >>= 1) {
+#pragma unroll
+              for (int j = 0; j < h; ++j) {
+                const float keep = c & h ? w[r][j + h] : w[r][j], send = c & h ? w[r][j] : w[r][j + h];
+                w[r][j] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+              }
+            }
+            const int row = row0 + r * 32 + (tid >> 3);
+            const int tl = it.t0 + min(row, rows - 1) / G;
+            bool seen = in;
+            if (in && pos >= prefix) {
+              const int n = pos - prefix;  // as a new token
+              if constexpr (CAUSAL) seen = n <= tl;
+              else seen = (__ldg(p.mask + (size_t)(it.q_start + tl) * p.mask_words + (n >> 6)) >> (n & 63)) & 1;
+            }
+            const float sc = seen ? w[r][0] : -INFINITY;
+            if constexpr (MODE != kSpanTree) {
+              if (it.score0 >= 0 && in && row < rows)
+                p.scores[it.score0 + (long long)row * it.ctx_pad + pos] = sc;
+            }
+            float mx = sc;
+#pragma unroll
+            for (int h = 4; h >= 1; h >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, h));
+            if (mx > m[r]) {
+              const float a = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mx);
+              l[r] *= a;
+              if constexpr (VALUES) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[r][i] *= a;
+              }
+              m[r] = mx;
+            }
+            w[r][0] = seen ? exp2f(sc - (m[r] == -INFINITY ? 0.f : m[r])) : __uint_as_float(kHidden);
+            l[r] += w[r][0];
+          }
+          if constexpr (VALUES) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float4 v4[N / 4];
+#pragma unroll
+              for (int i = 0; i < N / 4; ++i)
+                v4[i] = *reinterpret_cast<const float4 *>(&t.v[j0 + j][i * 32 + c * 4]);
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                const float wj = __shfl_sync(0xffffffffu, w[r][0], (lane & 24) | j);
+                // (a hidden position's value may be anything, NaN too)
+                if (__float_as_uint(wj) != kHidden) {
+#pragma unroll
+                  for (int i = 0; i < N / 4; ++i) {
+                    ffma2(o[r][4 * i], o[r][4 * i + 1], v4[i].x, v4[i].y, wj, wj);
+                    ffma2(o[r][4 * i + 2], o[r][4 * i + 3], v4[i].z, v4[i].w, wj, wj);
+                  }
+                }
+              }
+            }
+          }
+        }
+      }
+      bad = __syncthreads_or(bad);  // (and both tiles have been read)
+      if (bad && tid == 0) atomicOr(f.status, PA_DEV_BAD_BLOCK);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int h = 4; h >= 1; h >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], h);
+        const int row = row0 + r * 32 + (tid >> 3);
+        if (row < rows) {
+          const long long at = span_row(p, it.slot, 0, row);
+          if constexpr (VALUES) {
+            const float inv = l[r] == 0.f || bad ? 0.f : 1.f / l[r];
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+              *reinterpret_cast<float4 *>(p.part_o + at * D + i * 8 + c * 4) =
+                  make_float4(o[r][i] * inv, o[r][i + 1] * inv, o[r][i + 2] * inv, o[r][i + 3] * inv);
+          }
+          if (c == 0)
+            p.part_lse[at] = bad ? INFINITY : l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
+        }
+      }
+    };
+    for (int row0 = 0; row0 < rows; row0 += 32 * kSimtRows) {
+      if (rows - row0 <= 32) pass(row0, std::integral_constant<int, 1>());
+      else if (rows - row0 <= 64) pass(row0, std::integral_constant<int, 2>());
+      else pass(row0, std::integral_constant<int, kSimtRows>());
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// A row is one (token, query head).  Its partials are those of its unit's pieces:
+//   L = log2(sum_i 2^(lse_i) [+ 2^sink]),  out = sum_i 2^(lse_i - L) O_i.
+// Eight lanes hold a row's head_dim values and walk its partials four at a time;
+// W such groups share a row's partials and meet in shared memory.
+
+template <typename T>
+__device__ inline void store4(T *dst, float a, float b, float c, float d);
+template <>
+__device__ inline void store4<float>(float *dst, float a, float b, float c, float d) {
+  *reinterpret_cast<float4 *>(dst) = make_float4(a, b, c, d);
+}
+template <>
+__device__ inline void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float a, float b, float c, float d) {
+  // one rounding to nearest even, of the finished output
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&x),
+                                               *reinterpret_cast<const uint32_t *>(&y));
+}
+
+// The larger one, but a NaN stays.
+__device__ inline float max_nan(float a, float b) { return b > a || b != b ? b : a; }
+
+template <typename T, int D, int W, int MODE>
+__global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanParams p) {
+  constexpr bool VALUES = MODE != kSpanVotesOnly, CAUSAL = MODE != kSpanTree;
+  constexpr int V = VALUES ? D / 32 : 1;  // float4 values a lane holds
+  constexpr int ROWS = kMergeGroups / W;  // rows a block works on at a time
+  __shared__ float4 s_o[W > 1 ? kMergeGroups : 1][W > 1 ? 8 * V : 1];
+  __shared__ float s_m[kMergeGroups], s_l[kMergeGroups];
+  const FwdParams &f = p.f;
+  const int S = f.num_seqs, H = f.num_heads, G = H / f.num_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 7, grp = tid >> 3, part = grp % W;
+  pdl_trigger();
+  pdl_wait();
+  T *out = static_cast<T *>(f.out);
+  const long long rows = (long long)f.num_tokens * H;
+  const SpanPlan plan = *p.plan;
+  for (long long row0 = (long long)blockIdx.x * ROWS; row0 < rows; row0 += (long long)gridDim.x * ROWS) {
+    const long long row = row0 + grp / W;
+    float4 acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    int h = 0, n = 0, c0 = 0, br = 0;
+    unsigned u0 = 0;
+    long long unit = 0;
+    SpanReq r{};
+    int blk_end = 0;
+    bool mine = row < rows;  // (not a row behind the last request)
+    if (mine && !plan.all_bad) {
+      const int tok = (int)(row / H);
+      h = (int)(row % H);
+      int lo = 0, hi = S - 1;
+      while (lo < hi) {  // the last request that starts at or before tok: its own
+        const int mid = (lo + hi + 1) >> 1;
+        if (f.qsl[mid] <= tok) lo = mid; else hi = mid - 1;
+      }
+      r = p.req[lo];
+      const int i = tok - r.q_start;
+      mine = i < r.q_len;
+      if (mine && r.valid) {
+        const int tq = kSpanRows / G, b = i / tq, local = h / G * r.nblk + b;
+        br = (i - b * tq) * G + h % G;
+        unit = (long long)r.unit0 + local;
+        const unsigned len = r.ntile + kSpanOverhead;
+        u0 = r.cost0 + (unsigned)local * len;
+        c0 = (int)(u0 / plan.run);
+        blk_end = span_block_end(r, b * tq, tq, CAUSAL);
+        n = ((int)((u0 + len - 1) / plan.run) - c0 + 1) * (p.halves ? 2 : 1);
+        // a unit of more than 128 rows has one partial a piece, in the row's own place
+        if (p.halves && (r.q_len - b * tq) * G > 128) n /= 2;
+      }
+    }
+    const bool pairs = p.halves && n > 0 && n == 2 * ((int)((u0 + r.ntile + kSpanOverhead - 1) / plan.run) - c0 + 1);
+    for (int e0 = part; e0 < n; e0 += 4 * W) {
+      float lse[4];
+      float4 x[4][V];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u * W;
+        lse[u] = -INFINITY;
+        if (e >= n) continue;
+        const int c = c0 + (pairs ? e >> 1 : e), half = pairs ? e & 1 : 0;
+        // the piece's tiles (it may have none: the overhead alone, or behind the causal end)
+        const unsigned from = max(u0, (unsigned)c * plan.run);
+        const unsigned to = min(u0 + r.ntile + kSpanOverhead, (unsigned)(c + 1) * plan.run);
+        const int t0 = span_tile_at(r, from - u0), t1 = span_tile_at(r, to - u0);
+        if (min(t1 * kSpanTile, blk_end) <= (t0 + half) * kSpanTile) continue;
+        const long long at = span_row(p, unit + c, half, br);
+        lse[u] = __ldcg(p.part_lse + at);
+        if constexpr (VALUES) {
+          const float *src = p.part_o + at * D + lane * 4;
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[u][v] = __ldcg(reinterpret_cast<const float4 *>(src + v * 32));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (lse[u] == -INFINITY) continue;  // no such partial, or one without a visible position
+        const float top = max_nan(m, lse[u]);
+        // (equal infinities: a bad page, which m tells)
+        const float a = m == -INFINITY || m == top ? (m == top ? 1.f : 0.f) : fast_exp2(m - top);
+        const float w = lse[u] == top ? 1.f : fast_exp2(lse[u] - top);
+        m = top;
+        l = fmaf(l, a, w);
+        if constexpr (VALUES) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            acc[v].x = fmaf(acc[v].x, a, w * x[u][v].x);
+            acc[v].y = fmaf(acc[v].y, a, w * x[u][v].y);
+            acc[v].z = fmaf(acc[v].z, a, w * x[u][v].z);
+            acc[v].w = fmaf(acc[v].w, a, w * x[u][v].w);
+          }
+        }
+      }
+    }
+    if constexpr (W > 1) {
+      __syncthreads();  // the rows before are read
+      if (lane == 0) {
+        s_m[grp] = m;
+        s_l[grp] = l;
+      }
+      if constexpr (VALUES) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_o[grp][v * 8 + lane] = acc[v];
+      }
+      __syncthreads();
+      if (part == 0) {
+        float top = m;
+        for (int k = 1; k < W; ++k) top = max_nan(top, s_m[grp + k]);
+        const float a = m == top ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - top);
+        l *= a;
+        if constexpr (VALUES) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            acc[v].x *= a;
+            acc[v].y *= a;
+            acc[v].z *= a;
+            acc[v].w *= a;
+          }
+        }
+        for (int k = 1; k < W; ++k) {
+          const float mk = s_m[grp + k];
+          if (mk == -INFINITY) continue;
+          const float b = mk == top ? 1.f : fast_exp2(mk - top);
+          l = fmaf(s_l[grp + k], b, l);
+          if constexpr (VALUES) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const float4 o = s_o[grp + k][v * 8 + lane];
+              acc[v].x = fmaf(o.x, b, acc[v].x);
+              acc[v].y = fmaf(o.y, b, acc[v].y);
+              acc[v].z = fmaf(o.z, b, acc[v].z);
+              acc[v].w = fmaf(o.w, b, acc[v].w);
+            }
+          }
+        }
+        m = top;
+      }
+    }
+    if (mine && part == 0) {
+      // the sink joins the denominator once, with no value; a row that sees
+      // nothing, or a bad page, is zero
+      const bool bad = m == INFINITY, none = m == -INFINITY;
+      if (!bad && !none && f.sinks) {
+        const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = max_nan(m, sink2);
+        const float k = fast_exp2(m - top);
+        l = l * k + fast_exp2(sink2 - top);
+        m = top;
+        if constexpr (VALUES) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            acc[v].x *= k;
+            acc[v].y *= k;
+            acc[v].z *= k;
+            acc[v].w *= k;
+          }
+        }
+      }
+      if (p.row_lse && lane == 0) p.row_lse[row] = bad || none ? m : m + log2f(l);
+      if constexpr (VALUES) {
+        const float inv = bad || none ? 0.f : 1.f / l;
+        T *dst = out + row * D + lane * 4;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (bad || none) store4<T>(dst + v * 32, 0.f, 0.f, 0.f, 0.f);
+          else store4<T>(dst + v * 32, acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int D, int MODE>
+cudaError_t launch_merge_d(const SpanParams &p, long long most, cudaStream_t st) {
+  // Groups a row: as many as the SMs hold at once (two blocks each), and no more
+  // than a row's partials fill, four at a time.
+  const long long rows = (long long)p.f.num_tokens * p.f.num_heads, sms = p.num_sms;
+  const int fit = rows <= 4 * sms ? 16 : rows <= 8 * sms ? 8 : rows <= 16 * sms ? 4 : 1;
+  const int W = std::min(fit, most <= 4 ? 1 : most <= 16 ? 4 : most <= 32 ? 8 : 16);
+  auto kern = W == 16 ? span_merge_kernel<T, D, 16, MODE>
+              : W == 8 ? span_merge_kernel<T, D, 8, MODE>
+              : W == 4 ? span_merge_kernel<T, D, 4, MODE> : span_merge_kernel<T, D, 1, MODE>;
+  const long long blocks = std::min(ceil_div_ll(rows * W, kMergeGroups), sms * 8);
+  return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p);
+}
+
+template <typename T, int D, int MODE>
+cudaError_t launch_simt_d(const SpanParams &p, cudaStream_t st) {
+  constexpr int kSmem = 2 * (int)sizeof(SpanTileBuf<D>);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = set_smem_attrs_once(span_simt_kernel<T, D, MODE>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(span_simt_kernel<T, D, MODE>, dim3(p.grid), dim3(kSimtThreads), kSmem, st, p);
+}
+
+template <int MODE>
+cudaError_t launch_pass(const SpanParams &p, cudaStream_t st) {
+  const bool bf16 = p.f.dtype == PA_BF16;
+  if (p.f.head_dim == 128)
+    return bf16 ? launch_simt_d<__nv_bfloat16, 128, MODE>(p, st) : launch_simt_d<float, 128, MODE>(p, st);
+  return bf16 ? launch_simt_d<__nv_bfloat16, 64, MODE>(p, st) : launch_simt_d<float, 64, MODE>(p, st);
+}
+
+template <int MODE>
+cudaError_t launch_merge(const SpanParams &p, long long most, cudaStream_t st) {
+  const bool bf16 = p.f.dtype == PA_BF16;
+  if (p.f.head_dim == 128)
+    return bf16 ? launch_merge_d<__nv_bfloat16, 128, MODE>(p, most, st)
+                : launch_merge_d<float, 128, MODE>(p, most, st);
+  return bf16 ? launch_merge_d<__nv_bfloat16, 64, MODE>(p, most, st)
+              : launch_merge_d<float, 64, MODE>(p, most, st);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxGrid = 160;  // blocks that the partials' bound allows for
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct SpanLayout {
+  size_t plan, req, cost_end, part_o, part_lse, row_lse, scores, total;
+  int slot_rows;
+  bool ok;  // the extents are ones that the kernels count in 32 bits
+};
+
+// Host-side bounds of what the planner lays out, from the extents alone.
+SpanLayout span_layout(int dtype, int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                       int head_dim, int max_seq_len, int max_query_len, bool votes, bool values) {
+  SpanLayout l{};
+  const long long S = num_seqs > 0 ? num_seqs : 1, T = num_tokens, H = num_heads, Hk = num_kv_heads,
+                  G = H / Hk, msl = max_seq_len > 0 ? max_seq_len : 1;
+  const long long most = max_query_len > 0 ? std::min<long long>(max_query_len, T) : T;  // new tokens
+  const long long units =
+      Hk * std::min(ceil_div_ll(T * G, kSpanRows) + S, S * ceil_div_ll(most * G, kSpanRows));
+  const long long tiles = ceil_div_ll(msl, kSpanTile) + kSpanOverhead;
+  l.ok = units * tiles < (1ll << 31) - (1 << 20);
+  // two rows of partials for each row of a unit of up to 128
+  l.slot_rows = most * G <= 128 ? (int)(2 * ceil_div_ll(most * G, 4) * 4) : kSpanRows;
+  const long long slots = units + kMaxGrid;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  l.plan = take(sizeof(SpanPlan));
+  l.req = take(S * sizeof(SpanReq));
+  l.cost_end = take(S * sizeof(unsigned));
+  l.part_o = take(values ? (size_t)slots * l.slot_rows * head_dim * sizeof(float) : 0);
+  l.part_lse = take((size_t)slots * l.slot_rows * sizeof(float));
+  if (votes) {
+    l.row_lse = take((size_t)T * H * sizeof(float));
+    const long long kept = std::min(T * G, S * std::min<long long>(most * G, kSpanStoredRows));
+    l.scores = take((size_t)(kept * Hk) * ceil_div_ll(msl, kSpanTile) * kSpanTile * sizeof(float));
+  }
+  l.total = off;
+  (void)dtype;
+  return l;
+}
+
+bool extents_ok(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                int max_seq_len, int max_query_len) {
+  return num_seqs >= 0 && num_tokens >= 0 && num_heads > 0 && num_kv_heads > 0 &&
+         num_heads % num_kv_heads == 0 && head_dim > 0 && max_seq_len >= 0 && max_query_len >= 0 &&
+         (long long)num_tokens * num_heads <= (1ll << 40) / head_dim;
+}
+
+struct SpanCall {
+  FwdCall c;
+  const unsigned long long *mask = nullptr;
+  int mask_words = 0;
+  float *weights = nullptr;
+  int accumulate = 0;
+  void *stream = nullptr;
+  void *workspace = nullptr;
+  size_t workspace_bytes = 0;
+};
+
+// Options of both calls: sinks, layout and max_query_len.
+pa_status take_options(const pa_forward_options *o, FwdCall *c) {
+  if (!o) return PA_OK;
+  if (o->sinks && (reinterpret_cast<uintptr_t>(o->sinks) & 3)) return PA_ERR_INVALID_ARG;
+  if ((o->kv_layout != PA_KV_NHD && o->kv_layout != PA_KV_HND) || o->sliding_window < 0 ||
+      o->max_query_len < 0 || (o->alibi_sqrt != 0 && o->alibi_sqrt != 1))
+    return PA_ERR_INVALID_ARG;
+  // a drafted token's position is its depth's, an evicted cache's not its slot's
+  if (o->sliding_window || o->alibi_slopes) return PA_ERR_UNSUPPORTED;
+  c->sinks = o->sinks;
+  c->kv_layout = o->kv_layout;
+  c->max_query_len = o->max_query_len;
+  return PA_OK;
+}
+
+template <int MODE>
+pa_status span_call(const SpanCall &sc) {
+  const FwdCall &c = sc.c;
+  constexpr bool votes = MODE != kSpanTree, values = MODE != kSpanVotesOnly;
+  for (const int32_t *x : {c.block_table, c.seq_lens, c.qsl})
+    if (reinterpret_cast<uintptr_t>(x) & 3) return PA_ERR_INVALID_ARG;
+  const SpanLayout lay = span_layout(c.dtype, c.num_seqs, c.num_tokens, c.num_heads, c.num_kv_heads,
+                                     c.head_dim, c.max_seq_len, c.max_query_len, votes, values);
+  if (!lay.ok) return PA_ERR_UNSUPPORTED;
+  if (!sc.workspace || sc.workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(sc.workspace) & 255) return PA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(sc.stream);
+  SpanParams p{};
+  void *lib_ws = nullptr;
+  int num_sms = 0;
+  pa_status s = device_resources(st, 0, &lib_ws, &p.f.status, &num_sms);
+  if (s != PA_OK) return s;
+  uint8_t *ws = static_cast<uint8_t *>(sc.workspace);
+  FwdParams &f = p.f;
+  f.q = c.q;
+  f.out = c.out;
+  f.block_table = c.block_table;
+  f.seq_lens = c.seq_lens;
+  f.qsl = c.qsl;
+  f.num_seqs = c.num_seqs;
+  f.num_tokens = c.num_tokens;
+  f.num_heads = c.num_heads;
+  f.num_kv_heads = c.num_kv_heads;
+  f.head_dim = c.head_dim;
+  f.block_size = c.block_size;
+  f.max_blocks_per_seq = c.max_blocks_per_seq;
+  f.num_blocks = c.num_blocks;
+  f.max_seq_len = c.max_seq_len;
+  f.scale = c.scale;
+  f.scale_log2 = c.scale * kLog2eF;
+  f.dtype = c.dtype;
+  f.sinks = c.sinks;
+  f.max_qlen = c.max_query_len;
+  p.k_cache = c.k_cache;
+  p.v_cache = c.v_cache;
+  p.hnd = c.kv_layout == PA_KV_HND;
+  p.mask = sc.mask;
+  p.mask_words = sc.mask_words;
+  p.weights = sc.weights;
+  p.accumulate = sc.accumulate;
+  p.keep_scores = votes;
+  p.num_sms = num_sms;
+  p.grid = std::min(num_sms, kMaxGrid);
+  p.halves = 0;
+  p.slot_rows = lay.slot_rows;
+  p.plan = reinterpret_cast<SpanPlan *>(ws + lay.plan);
+  p.req = reinterpret_cast<SpanReq *>(ws + lay.req);
+  p.cost_end = reinterpret_cast<unsigned *>(ws + lay.cost_end);
+  p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
+  p.part_lse = reinterpret_cast<float *>(ws + lay.part_lse);
+  p.row_lse = votes ? reinterpret_cast<float *>(ws + lay.row_lse) : nullptr;
+  p.scores = votes ? reinterpret_cast<float *>(ws + lay.scores) : nullptr;
+
+  int slot = prof_begin(PA_K_PLAN, st);
+  cudaError_t err = launch_dependent(span_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p);
+  prof_end(slot, st);
+  if (err != cudaSuccess) return PA_ERR_CUDA;
+  slot = prof_begin(PA_K_SPAN, st);
+  err = launch_pass<MODE>(p, st);
+  prof_end(slot, st);
+  if (err != cudaSuccess) return PA_ERR_CUDA;
+  // partials that a row may have: a piece for each block that shares its unit
+  const long long blocks = ceil_div_ll(c.max_seq_len, kSpanTile) + 1;
+  slot = prof_begin(PA_K_MERGE, st);
+  err = launch_merge<MODE>(p, std::min<long long>(blocks, p.grid), st);
+  prof_end(slot, st);
+  if (err != cudaSuccess) return PA_ERR_CUDA;
+  if (votes) {
+    slot = prof_begin(PA_K_VOTES, st);
+    // rows of a KV head that one request may have
+    const long long rows = (c.max_query_len > 0 ? std::min(c.max_query_len, c.num_tokens) : c.num_tokens) *
+                           (long long)(c.num_heads / c.num_kv_heads);
+    err = launch_votes(p, (int)std::min<long long>(rows, 1 << 30), st);
+    prof_end(slot, st);
+    if (err != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tokens, int num_heads,
+                                       int num_kv_heads, int head_dim, int max_seq_len,
+                                       int max_query_len) {
+  if (!extents_ok(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_seq_len, max_query_len))
+    return 0;
+  const SpanLayout l = span_layout(dtype, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                   max_seq_len, max_query_len, false, true);
+  return l.ok ? l.total : 0;
+}
+
+pa_status pa_forward_tree(const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *block_table, const int32_t *seq_lens,
+                          const int32_t *query_start_loc, const uint64_t *tree_mask, int num_heads,
+                          int num_kv_heads, int head_dim, int block_size, float scale, void *out,
+                          void *stream, pa_dtype dtype, int num_seqs, int num_tokens,
+                          int mask_words, int max_blocks_per_seq, int num_blocks, int max_seq_len,
+                          const pa_forward_options *options, void *workspace,
+                          size_t workspace_bytes) {
+  SpanCall sc;
+  sc.c = FwdCall{q, k_cache, v_cache, block_table, seq_lens, query_start_loc, num_heads,
+                 num_kv_heads, head_dim, block_size, scale, out, dtype, num_seqs, num_tokens,
+                 max_blocks_per_seq, num_blocks, max_seq_len, 0};
+  sc.stream = stream;
+  if (mask_words < 0) return PA_ERR_INVALID_ARG;
+  pa_status s = take_options(options, &sc.c);
+  if (s != PA_OK) return s;
+  s = fwd_check(sc.c);
+  if (s != PA_OK || num_tokens == 0) return s;
+  if (num_seqs == 0 || !tree_mask || mask_words == 0 || (reinterpret_cast<uintptr_t>(tree_mask) & 7))
+    return PA_ERR_INVALID_ARG;
+  sc.mask = reinterpret_cast<const unsigned long long *>(tree_mask);
+  sc.mask_words = mask_words;
+  sc.workspace = workspace;
+  sc.workspace_bytes = workspace_bytes;
+  return span_call<kSpanTree>(sc);
+}
+
+size_t pa_forward_weights_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tokens,
+                                          int num_heads, int num_kv_heads, int head_dim,
+                                          int max_seq_len, int max_query_len) {
+  if (!extents_ok(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_seq_len, max_query_len))
+    return 0;
+  const SpanLayout l = span_layout(dtype, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                   max_seq_len, max_query_len, true, true);
+  return l.ok ? l.total : 0;
+}
+
+pa_status pa_forward_weights(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_table, const int32_t *seq_lens,
+                             const int32_t *query_start_loc, int num_heads, int num_kv_heads,
+                             int head_dim, int block_size, float scale, void *out, float *weights,
+                             int accumulate, void *stream, pa_dtype dtype, int num_seqs,
+                             int num_tokens, int max_blocks_per_seq, int num_blocks,
+                             int max_seq_len, const pa_forward_options *options, void *workspace,
+                             size_t workspace_bytes) {
+  SpanCall sc;
+  // (without an output the values are not read: the checks are those of the keys)
+  sc.c = FwdCall{q, k_cache, out ? v_cache : k_cache, block_table, seq_lens, query_start_loc,
+                 num_heads, num_kv_heads, head_dim, block_size, scale,
+                 out ? out : const_cast<void *>(q), dtype, num_seqs, num_tokens,
+                 max_blocks_per_seq, num_blocks, max_seq_len, 0};
+  sc.stream = stream;
+  if (accumulate != 0 && accumulate != 1) return PA_ERR_INVALID_ARG;
+  pa_status s = take_options(options, &sc.c);
+  if (s != PA_OK) return s;
+  s = fwd_check(sc.c);
+  if (s != PA_OK || num_tokens == 0) return s;
+  if (num_seqs == 0 || !weights || (reinterpret_cast<uintptr_t>(weights) & 15)) return PA_ERR_INVALID_ARG;
+  sc.c.out = out;
+  sc.weights = weights;
+  sc.accumulate = accumulate;
+  sc.workspace = workspace;
+  sc.workspace_bytes = workspace_bytes;
+  return out ? span_call<kSpanVotes>(sc) : span_call<kSpanVotesOnly>(sc);
+}
+
+}  // extern "C"

@@ -1,0 +1,182 @@
+// pa_span.h -- what the kernels of pa_forward_tree and pa_forward_weights
+// share: the work cut into spans of KV positions (not part of the public C ABI).
+//
+// A unit is one KV head of one request and up to kSpanRows of its rows (a row:
+// one new token x one query head of the KV head) against the request's whole
+// context, in tiles of kSpanTile positions.  All units' tiles are laid one after
+// the other and cut into equal runs, one for each block of the grid, so every
+// block gets the same work and a unit is split only where a run ends in it.  A
+// block's share of a unit is a piece; its partial results go to slot
+// unit + block, which is a piece's alone (each step from one piece to the next
+// moves on by a unit, by a block, or by both).
+#pragma once
+
+#include "pa_internal.h"
+
+namespace pa {
+
+constexpr int kSpanRows = 256;
+constexpr int kSpanTile = 128;
+// What a piece costs beside its tiles (queries, first scores, partials), in tiles.
+constexpr int kSpanOverhead = 1;
+// Requests with at most this many rows of a KV head have their scores kept for
+// the sums over rows (pa_forward_weights); the others' are computed again.  A
+// position's scores of 32 rows are 128 bytes written and read, its key in bf16
+// 128 or 256 bytes read again and multiplied again.
+constexpr int kSpanStoredRows = 32;
+
+enum SpanMode : int {
+  kSpanTree = 0,   // mask of the new tokens from bits
+  kSpanVotes = 1,  // causal, scores kept, values too
+  kSpanVotesOnly = 2,  // causal, scores kept, no values: the log-sum-exps alone
+};
+
+struct SpanReq {
+  int q_start, q_len;  // its token rows
+  int ctx;             // positions, the new tokens among them
+  int valid;
+  int nblk;            // blocks of kSpanRows rows of a KV head (0: nothing to do)
+  int ntile;           // tiles of its context
+  int unit0;           // first unit; unit = unit0 + kv head * nblk + block
+  unsigned cost0;      // where its first unit begins in the laid-out work
+  long long score0;    // first kept score, -1: not kept
+};
+
+struct SpanPlan {
+  unsigned total;  // laid-out work
+  unsigned run;    // each block's share
+  int all_bad;     // bad query_start_loc: every row is zero
+};
+
+struct SpanParams {
+  FwdParams f;
+  const void *k_cache, *v_cache;
+  int hnd;
+  const unsigned long long *mask;  // [num_tokens][mask_words], or null
+  int mask_words;
+  float *weights;                  // [num_blocks][num_kv_heads][block_size], or null
+  int accumulate;
+  int keep_scores;
+  int num_sms, grid, halves;       // halves: see span_row
+  int slot_rows;
+  SpanPlan *plan;
+  SpanReq *req;          // [num_seqs]
+  unsigned *cost_end;    // [num_seqs] inclusive
+  float *part_o;         // [slots * slot_rows][head_dim], normalised
+  float *part_lse;       // base 2; +inf: a bad page in the piece's range
+  float *row_lse;        // [num_tokens * num_heads], sinks included
+  float *scores;         // kept scores, base 2: [kv head][row][ntile * kSpanTile] a request
+};
+
+// Where row r of a unit lies among the partials of slot `slot`.  The tensor-core
+// kernel gives a unit of up to 128 rows to both of its row tiles, every other tile
+// of positions each: x tells them apart (else x = 0).
+__device__ inline long long span_row(const SpanParams &p, long long slot, int x, int r) {
+  return slot * p.slot_rows + x * (p.slot_rows / 2) + r;
+}
+
+struct SpanPiece {
+  int q_start, q_len, ctx, req;  // the request's rows
+  int kvh, t0;                   // KV head, first token of the row block
+  int kv_lo, kv_hi;              // positions (kv_lo a multiple of kSpanTile)
+  int ctx_pad;                   // the context in whole tiles
+  long long slot;
+  long long score0;              // its kept scores: row r's position j at score0 + r * ctx_pad + j
+};
+
+// Positions that the rows of the block from token t0 on may see: all for bits,
+// up to the block's last token's own position under a causal mask.
+__device__ inline int span_block_end(const SpanReq &r, int t0, int tq, bool causal) {
+  return causal ? r.ctx - r.q_len + min(t0 + tq, r.q_len) : r.ctx;
+}
+// The tile boundary at `cost` of a unit's laid-out work.
+__device__ inline int span_tile_at(const SpanReq &r, unsigned cost) {
+  return min(max((int)cost - kSpanOverhead, 0), r.ntile);
+}
+
+// The pieces of block `cta`, in order.  Every role of a block walks them for itself.
+struct SpanCursor {
+  unsigned pos, end;
+  int s, local, cta;
+  SpanReq r;
+
+  __device__ void start(const SpanParams &p, const SpanPlan &plan, int block) {
+    cta = block;
+    const unsigned long long at = (unsigned long long)block * plan.run;
+    pos = (unsigned)min(at, (unsigned long long)plan.total);
+    end = (unsigned)min(at + plan.run, (unsigned long long)plan.total);
+    s = 0;
+    local = 0;
+    if (pos >= end) return;
+    int lo = 0, hi = p.f.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cost_end[mid] > pos) hi = mid; else lo = mid + 1;
+    }
+    s = lo;
+    r = p.req[s];
+    local = (int)((pos - r.cost0) / (unsigned)(r.ntile + kSpanOverhead));
+  }
+
+  __device__ bool next(const SpanParams &p, int G, bool causal, SpanPiece &it) {
+    const int tq = kSpanRows / G;
+    while (pos < end) {
+      if (r.nblk == 0 || local == p.f.num_kv_heads * r.nblk) {
+        do r = p.req[++s]; while (r.nblk == 0);  // (pos < end: there is one)
+        local = 0;
+      }
+      const unsigned n = r.ntile + kSpanOverhead, u0 = r.cost0 + (unsigned)local * n;
+      const unsigned to = min(end, u0 + n);
+      const int lo = span_tile_at(r, pos - u0), hi = span_tile_at(r, to - u0);
+      const int kvh = local / r.nblk, b = local - kvh * r.nblk;
+      it.q_start = r.q_start;
+      it.q_len = r.q_len;
+      it.ctx = r.ctx;
+      it.req = s;
+      it.kvh = kvh;
+      it.t0 = b * tq;
+      it.kv_lo = lo * kSpanTile;
+      it.kv_hi = min(hi * kSpanTile, span_block_end(r, it.t0, tq, causal));
+      it.ctx_pad = r.ntile * kSpanTile;
+      it.slot = (long long)r.unit0 + local + cta;
+      it.score0 = r.score0 < 0 ? -1 : r.score0 + (long long)kvh * r.q_len * G * it.ctx_pad;
+      pos = to;
+      if (to == u0 + n) ++local;
+      if (it.kv_hi > it.kv_lo) return true;
+    }
+    return false;
+  }
+};
+
+// Bits of 64 positions from `at` on, as the new token in row `tok` of `mask` sees
+// them: bit c stands for position at + c.  Cached positions (below `prefix`) are
+// all seen; beyond ctx there is nothing.
+__device__ inline unsigned long long span_bits(const unsigned long long *mask, int words, int tok,
+                                               int at, int prefix, int ctx) {
+  const unsigned long long *row = mask + (size_t)tok * words;
+  const int n0 = at - prefix;  // as a new token
+  unsigned long long bits;
+  if (n0 <= -64) {
+    bits = ~0ull;
+  } else if (n0 < 0) {
+    bits = (__ldg(row) << -n0) | ((1ull << -n0) - 1);
+  } else {
+    const int w = n0 >> 6, sh = n0 & 63;
+    bits = w < words ? __ldg(row + w) >> sh : 0ull;
+    if (sh && w + 1 < words) bits |= __ldg(row + w + 1) << (64 - sh);
+  }
+  const int left = ctx - at;
+  if (left < 64) bits &= left <= 0 ? 0ull : (1ull << left) - 1;
+  return bits;
+}
+
+// The 64 positions from `at` on that the query at position `own` sees.
+__device__ inline unsigned long long span_causal_bits(int at, int own) {
+  const int n = own - at + 1;
+  return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+}
+
+// The sums over rows of pa_forward_weights, behind the rows' log-sum-exps.
+cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream);
+
+}  // namespace pa

@@ -1,0 +1,230 @@
+// pa_votes.cu -- the sums over rows of pa_forward_weights: with L_r the
+// log-sum-exp of row r (its sink included) and s_rj its score of position j,
+//   W[kv head][slot of j] (+)= sum_r 2^(s_rj - L_r)
+// over the rows of the KV head, position by position, each written by one thread
+// in a fixed order of rows: no atomics, the same bits every time.
+#include <algorithm>
+
+#include "pa_span.h"
+
+namespace pa {
+namespace {
+
+constexpr int kVoteThreads = 256;
+
+// The weight of one score; a row that sees nothing (L = -inf) has none.
+__device__ inline float vote(float score, float lse) {
+  return lse == -INFINITY ? 0.f : fast_exp2(score - lse);
+}
+
+// Adds `sum`, of the four positions from pos on, to their slots.  Positions of the
+// new tokens start at their sum; positions from ctx on have no slot.
+__device__ inline void add_votes(const SpanParams &p, const SpanReq &r, const int32_t *bt, int kvh,
+                                 int pos, const float (&sum)[4]) {
+  const FwdParams &f = p.f;
+  const int bs = f.block_size, page = __ldg(bt + pos / bs);  // (bs % 16 == 0: one page)
+  float *dst = p.weights + ((size_t)page * f.num_kv_heads + kvh) * bs + pos % bs;
+  const int fresh = p.accumulate ? r.ctx - r.q_len : 0;
+  if (pos + 4 <= r.ctx) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pos < fresh) x = *reinterpret_cast<const float4 *>(dst);
+    x.x = pos < fresh ? x.x + sum[0] : sum[0];
+    x.y = pos + 1 < fresh ? x.y + sum[1] : sum[1];
+    x.z = pos + 2 < fresh ? x.z + sum[2] : sum[2];
+    x.w = pos + 3 < fresh ? x.w + sum[3] : sum[3];
+    *reinterpret_cast<float4 *>(dst) = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (pos + i < r.ctx) dst[i] = (pos + i < fresh ? dst[i] : 0.f) + sum[i];
+  }
+}
+
+// Whether the request's last row met a bad page: it sees all of them.
+__device__ inline bool request_bad(const SpanParams &p, const SpanReq &r) {
+  return __ldcg(p.row_lse + (size_t)(r.q_start + r.q_len - 1) * p.f.num_heads) == INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// kept scores (up to kSpanStoredRows rows): read once, four positions a thread
+// ---------------------------------------------------------------------------
+constexpr int kKeptChunk = 4 * kVoteThreads;
+
+__global__ void __launch_bounds__(kVoteThreads) votes_kept_kernel(const SpanParams p, int chunks) {
+  __shared__ float s_lse[kSpanStoredRows];
+  const FwdParams &f = p.f;
+  const int tid = threadIdx.x, H = f.num_heads, Hk = f.num_kv_heads, G = H / Hk;
+  pdl_trigger();
+  pdl_wait();
+  if (p.plan->all_bad) return;
+  const long long n = (long long)chunks * f.num_seqs * Hk;
+  for (long long item = blockIdx.x; item < n; item += gridDim.x) {
+    const int sh = (int)(item % ((long long)f.num_seqs * Hk)), s = sh / Hk, kvh = sh % Hk;
+    const int at = (int)(item / ((long long)f.num_seqs * Hk)) * kKeptChunk;
+    const SpanReq r = p.req[s];
+    if (!r.valid || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
+    const int R = r.q_len * G;
+    __syncthreads();  // s_lse of the item before is read
+    if (tid < R) s_lse[tid] = __ldcg(p.row_lse + (size_t)(r.q_start + tid / G) * H + kvh * G + tid % G);
+    const bool bad = request_bad(p, r);
+    __syncthreads();
+    const int pos = at + tid * 4;
+    if (bad || pos >= r.ctx) continue;
+    const long long pad = (long long)r.ntile * kSpanTile;
+    const float *src = p.scores + r.score0 + (long long)kvh * R * pad + pos;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < R; ++i) {
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + i * pad));
+      const float l = s_lse[i];
+      sum[0] += vote(x.x, l);
+      sum[1] += vote(x.y, l);
+      sum[2] += vote(x.z, l);
+      sum[3] += vote(x.w, l);
+    }
+    add_votes(p, r, f.block_table + (size_t)s * f.max_blocks_per_seq, kvh, pos, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// more rows: the scores are multiplied out again, on CUDA cores
+// ---------------------------------------------------------------------------
+// 64 positions x 32 rows a step, a thread 4 positions x 2 rows; a block's keys
+// stay in shared memory while all rows pass.
+constexpr int kPos = 64, kRows = 32;
+
+template <typename T>
+__device__ inline float4 load4f(const T *src);
+template <>
+__device__ inline float4 load4f<float>(const float *src) {
+  return *reinterpret_cast<const float4 *>(src);
+}
+template <>
+__device__ inline float4 load4f<__nv_bfloat16>(const __nv_bfloat16 *src) {
+  const uint2 v = *reinterpret_cast<const uint2 *>(src);
+  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanParams p, int chunks) {
+  extern __shared__ __align__(16) float s_dyn[];
+  constexpr int LD = D + 4;
+  float *s_k = s_dyn, *s_q = s_dyn + kPos * LD;
+  __shared__ float s_lse[kRows], s_sum[kVoteThreads / 16][kPos];
+  const FwdParams &f = p.f;
+  const int tid = threadIdx.x, H = f.num_heads, Hk = f.num_kv_heads, G = H / Hk, bs = f.block_size;
+  const int tx = tid & 15, ty = tid >> 4;  // positions 4 tx .., rows ty and ty + 16
+  pdl_trigger();
+  pdl_wait();
+  if (p.plan->all_bad) return;
+  const long long n = (long long)chunks * f.num_seqs * Hk;
+  for (long long item = blockIdx.x; item < n; item += gridDim.x) {
+    const int sh = (int)(item % ((long long)f.num_seqs * Hk)), s = sh / Hk, kvh = sh % Hk;
+    const int at = (int)(item / ((long long)f.num_seqs * Hk)) * kPos;
+    const SpanReq r = p.req[s];
+    if (!r.valid || r.score0 >= 0 || at >= r.ctx) continue;
+    if (request_bad(p, r)) continue;
+    const int32_t *bt = f.block_table + (size_t)s * f.max_blocks_per_seq;
+    const int R = r.q_len * G, prefix = r.ctx - r.q_len;
+    __syncthreads();
+    for (int e = tid; e < kPos * (D / 4); e += kVoteThreads) {
+      const int j = e / (D / 4), x = e % (D / 4) * 4, pos = at + j;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (pos < r.ctx) {
+        const int page = __ldg(bt + pos / bs), slot = pos % bs;
+        const size_t row = p.hnd ? ((size_t)page * Hk + kvh) * bs + slot : ((size_t)page * bs + slot) * Hk + kvh;
+        v = load4f(static_cast<const T *>(p.k_cache) + row * D + x);
+      }
+      *reinterpret_cast<float4 *>(&s_k[j * LD + x]) = v;
+    }
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    // rows that see none of these positions are left out
+    const int first = max(0, at - prefix) * G;
+    for (int r0 = first / kRows * kRows; r0 < R; r0 += kRows) {
+      __syncthreads();
+      for (int e = tid; e < kRows * (D / 4); e += kVoteThreads) {
+        const int i = e / (D / 4), x = e % (D / 4) * 4, row = min(r0 + i, R - 1);
+        const size_t at_q = ((size_t)(r.q_start + row / G) * H + kvh * G + row % G) * D + x;
+        float4 v = load4f(static_cast<const T *>(f.q) + at_q);
+        v.x *= f.scale_log2;
+        v.y *= f.scale_log2;
+        v.z *= f.scale_log2;
+        v.w *= f.scale_log2;
+        *reinterpret_cast<float4 *>(&s_q[i * LD + x]) = v;
+      }
+      if (tid < kRows) {
+        const int row = r0 + tid;
+        s_lse[tid] = row < R ? __ldcg(p.row_lse + (size_t)(r.q_start + row / G) * H + kvh * G + row % G)
+                             : -INFINITY;
+      }
+      __syncthreads();
+      float acc[2][4] = {};
+#pragma unroll 4
+      for (int x = 0; x < D; x += 4) {
+        float4 a[2], b[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4 *>(&s_q[(ty + 16 * i) * LD + x]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(&s_k[(tx * 4 + j) * LD + x]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+            acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+            acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+            acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = r0 + ty + 16 * i, own = prefix + min(row, R - 1) / G;
+        const float l = s_lse[ty + 16 * i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (at + tx * 4 + j <= own) sum[j] += vote(acc[i][j], l);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_sum[ty][tx * 4 + j] = sum[j];
+    __syncthreads();
+    if (tid < kPos / 4 && at + tid * 4 < r.ctx) {
+      float tot[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x = 0.f;
+        for (int y = 0; y < kVoteThreads / 16; ++y) x += s_sum[y][tid * 4 + j];
+        tot[j] = x;
+      }
+      add_votes(p, r, bt, kvh, at + tid * 4, tot);
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_simt(const SpanParams &p, cudaStream_t st) {
+  constexpr int kSmem = (kPos + kRows) * (D + 4) * (int)sizeof(float);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = set_smem_attrs_once(votes_simt_kernel<T, D>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  const long long chunks = ceil_div_ll(std::max(p.f.max_seq_len, 1), kPos);
+  const long long n = chunks * p.f.num_seqs * p.f.num_kv_heads;
+  return launch_dependent(votes_simt_kernel<T, D>, dim3((unsigned)std::min<long long>(n, 3ll * p.num_sms)),
+                          dim3(kVoteThreads), kSmem, st, p, (int)chunks);
+}
+
+}  // namespace
+
+cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream) {
+  const long long chunks = ceil_div_ll(std::max(p.f.max_seq_len, 1), kKeptChunk);
+  const long long n = chunks * p.f.num_seqs * p.f.num_kv_heads;
+  cudaError_t e = launch_dependent(votes_kept_kernel, dim3((unsigned)std::min<long long>(n, 8ll * p.num_sms)),
+                                   dim3(kVoteThreads), 0, stream, p, (int)chunks);
+  if (e != cudaSuccess || most_rows <= kSpanStoredRows) return e;
+  const bool bf16 = p.f.dtype == PA_BF16;
+  if (p.f.head_dim == 128)
+    return bf16 ? launch_simt<__nv_bfloat16, 128>(p, stream) : launch_simt<float, 128>(p, stream);
+  return bf16 ? launch_simt<__nv_bfloat16, 64>(p, stream) : launch_simt<float, 64>(p, stream);
+}
+
+}  // namespace pa

@@ -26,6 +26,7 @@ PA_DEV_OVERFLOW = 0x10
 PA_DEV_TIMEOUT = 0x20
 PA_DEV_INTERNAL = 0x40
 PA_DEV_NO_PAGES = 0x80
+PA_DEV_BAD_TREE = 0x100
 PA_KV_NHD, PA_KV_HND = 0, 1  # pa_kv_layout
 
 # Every entry point declared in include/pa.h.
@@ -35,8 +36,10 @@ EXPORTS = ("pa_forward", "pa_forward_workspace_bytes", "pa_mla_decode", "pa_cach
            "pa_profile_read", "pa_kernel_name", "pa_forward_static_scratch", "pa_forward_ex",
            "pa_mla_prefill", "pa_mla_prefill_workspace_bytes", "pa_debug_wait_timeout",
            "pa_forward_shared_prefix", "pa_forward_shared_prefix_workspace_bytes",
-           "pa_block_tables", "pa_cache_write_slots")
-PA_K_COUNT = 10
+           "pa_block_tables", "pa_cache_write_slots", "pa_tree_masks", "pa_forward_tree",
+           "pa_forward_tree_workspace_bytes", "pa_cache_accept", "pa_forward_weights",
+           "pa_forward_weights_workspace_bytes", "pa_cache_evict", "pa_cache_evict_workspace_bytes")
+PA_K_COUNT = 12
 
 
 class ForwardOptions(ctypes.Structure):
@@ -128,6 +131,27 @@ def lib():
         L.pa_cache_write_slots.argtypes = ([vp] * 5 + [c_int] * 3 + [vp, c_int, c_int]
                                            + [ctypes.c_longlong] * 2 + [c_int, c_int])
         L.pa_cache_write_slots.restype = c_int
+        L.pa_tree_masks.argtypes = [vp] * 6 + [c_int] * 3
+        L.pa_tree_masks.restype = c_int
+        L.pa_forward_tree.argtypes = (
+            [vp] * 7 + [c_int] * 4 + [c_float, vp, vp] + [c_int] * 7
+            + [ctypes.POINTER(ForwardOptions), vp, ctypes.c_size_t])
+        L.pa_forward_tree.restype = c_int
+        L.pa_forward_tree_workspace_bytes.argtypes = [c_int] * 8
+        L.pa_forward_tree_workspace_bytes.restype = ctypes.c_size_t
+        L.pa_cache_accept.argtypes = [vp] * 10 + [c_int] * 3 + [vp] + [c_int] * 7
+        L.pa_cache_accept.restype = c_int
+        L.pa_forward_weights.argtypes = (
+            [vp] * 6 + [c_int] * 4 + [c_float, vp, vp, c_int, vp] + [c_int] * 6
+            + [ctypes.POINTER(ForwardOptions), vp, ctypes.c_size_t])
+        L.pa_forward_weights.restype = c_int
+        L.pa_forward_weights_workspace_bytes.argtypes = [c_int] * 8
+        L.pa_forward_weights_workspace_bytes.restype = ctypes.c_size_t
+        L.pa_cache_evict.argtypes = ([vp] * 10 + [c_int] * 5 + [vp] + [c_int] * 7
+                                     + [vp, ctypes.c_size_t])
+        L.pa_cache_evict.restype = c_int
+        L.pa_cache_evict_workspace_bytes.argtypes = [c_int] * 5
+        L.pa_cache_evict_workspace_bytes.restype = ctypes.c_size_t
         L.pa_kernel_name.argtypes = [c_int]
         L.pa_kernel_name.restype = ctypes.c_char_p
         _lib = L
@@ -446,6 +470,17 @@ def pa_forward_shared_prefix_workspace_bytes(dtype, num_seqs, num_groups, num_to
 _prefix_workspace_bytes = functools.lru_cache(maxsize=1024)(pa_forward_shared_prefix_workspace_bytes)
 
 
+def _take_workspace(need, stream, raw, t):
+    """`need` bytes on t's device for one call on the stream `stream`, whose raw handle is raw."""
+    if stream is None or raw == _stream_ptr(None, t.get_device()):
+        return torch.empty(need, dtype=torch.uint8, device=t.device)
+    # allocated for the stream that uses it, so that its reuse is ordered there
+    owner = (torch.cuda.ExternalStream(raw, device=t.device) if raw
+             else torch.cuda.default_stream(t.device))
+    with torch.cuda.stream(owner):
+        return torch.empty(need, dtype=torch.uint8, device=t.device)
+
+
 def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                              group_start_loc, prefix_lens, num_heads, num_kv_heads, head_dim,
                              block_size, scale, out, stream=None, *, max_seq_len, max_prefix_len,
@@ -492,13 +527,7 @@ def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_s
     L = _lib or lib()
     if workspace is None:
         need = _prefix_workspace_bytes(dt, S, NG, T, num_heads, num_kv_heads, head_dim, max_seq_len)
-        if stream is None or raw == _stream_ptr(None, device):
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:  # allocated for the stream that uses it, so that its reuse is ordered there
-            owner = (torch.cuda.ExternalStream(raw, device=q.device) if raw
-                     else torch.cuda.default_stream(q.device))
-            with torch.cuda.stream(owner):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _take_workspace(need, stream, raw, q)
     elif not _fits(device, torch.uint8, workspace):
         _check_tensors(device, (torch.uint8, dict(workspace=workspace)))
     opts = _forward_options(sinks, layout, sliding_window, alibi_slopes, alibi_sqrt, max_query_len)
@@ -510,6 +539,276 @@ def pa_forward_shared_prefix(q, k_cache, v_cache, block_table, seq_lens, query_s
         int(max_prefix_len), ctypes.byref(opts), workspace.data_ptr(), workspace.numel())
     if check and st:
         _check(st, "pa_forward_shared_prefix")
+    return st
+
+
+def pa_tree_masks(parents, query_start_loc, tree_mask, stream=None, *, seq_lens=None,
+                  positions=None, check=True):
+    """Ancestor masks and rotary positions of drafted tokens (see include/pa.h):
+    parents [T] int32; tree_mask [T, words] int64 (the 64-bit words) and, if
+    given, positions [T] int32 are written (with seq_lens [S])."""
+    T, words = tree_mask.shape
+    S = query_start_loc.numel() - 1
+    if parents.numel() != T or S < 0:
+        raise ValueError("parents [T] and query_start_loc [S + 1] go with tree_mask [T, words]")
+    if positions is not None and (positions.numel() != T or seq_lens is None):
+        raise ValueError("positions [T] needs seq_lens and has tree_mask's rows")
+    if seq_lens is not None and seq_lens.numel() != S:
+        raise ValueError("seq_lens [S] goes with query_start_loc [S + 1]")
+    device = tree_mask.get_device()
+    if not (_current(device) and _fits(device, torch.int64, tree_mask)
+            and _fits(device, torch.int32, parents, query_start_loc, seq_lens, positions)):
+        _check_tensors(device, (torch.int64, dict(tree_mask=tree_mask)),
+                       (torch.int32, dict(parents=parents, query_start_loc=query_start_loc,
+                                          seq_lens=seq_lens, positions=positions)))
+    st = (_lib or lib()).pa_tree_masks(
+        parents.data_ptr(), query_start_loc.data_ptr(),
+        None if seq_lens is None else seq_lens.data_ptr(), tree_mask.data_ptr(),
+        None if positions is None else positions.data_ptr(), _stream_ptr(stream, device), S, T, words)
+    if check and st:
+        _check(st, "pa_tree_masks")
+    return st
+
+
+def _span_shapes(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, num_heads,
+                 num_kv_heads, head_dim, block_size, out, layout, num_blocks, sinks):
+    """The checks that pa_forward_tree and pa_forward_weights share; (S, T, table
+    width, pages)."""
+    S = seq_lens.numel()
+    T, H, D = shape = q.shape
+    if H != num_heads or D != head_dim or (out is not None and out.shape != shape):
+        raise ValueError("q and out must be [T, num_heads, head_dim]")
+    blocks, x, y, z = shape = k_cache.shape
+    page = (num_kv_heads, block_size) if layout == PA_KV_HND else (block_size, num_kv_heads)
+    if z != D or (x, y) != page or (v_cache is not None and v_cache.shape != shape):
+        raise ValueError("the caches' shape does not fit the heads, block_size and kv_layout")
+    rows, width = block_table.shape
+    if query_start_loc.numel() != S + 1 or rows != S:
+        raise ValueError("query_start_loc [S + 1] and block_table [S, max_blocks] go with seq_lens [S]")
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != num_heads):
+        raise TypeError("sinks must be a float32 tensor of num_heads elements")
+    if num_blocks is not None:
+        if num_blocks > blocks:
+            raise ValueError("num_blocks exceeds the caches")
+        blocks = int(num_blocks)
+    return S, T, width, blocks
+
+
+def pa_forward_tree_workspace_bytes(dtype, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                    max_seq_len, max_query_len=0):
+    return lib().pa_forward_tree_workspace_bytes(
+        int(dtype), int(num_seqs), int(num_tokens), int(num_heads), int(num_kv_heads),
+        int(head_dim), int(max_seq_len), int(max_query_len))
+
+
+def pa_forward_weights_workspace_bytes(dtype, num_seqs, num_tokens, num_heads, num_kv_heads,
+                                       head_dim, max_seq_len, max_query_len=0):
+    return lib().pa_forward_weights_workspace_bytes(
+        int(dtype), int(num_seqs), int(num_tokens), int(num_heads), int(num_kv_heads),
+        int(head_dim), int(max_seq_len), int(max_query_len))
+
+
+def pa_cache_evict_workspace_bytes(dtype, num_seqs, num_kv_heads, head_dim, max_seq_len):
+    return lib().pa_cache_evict_workspace_bytes(int(dtype), int(num_seqs), int(num_kv_heads),
+                                                int(head_dim), int(max_seq_len))
+
+
+_tree_workspace_bytes = functools.lru_cache(maxsize=1024)(pa_forward_tree_workspace_bytes)
+_weights_workspace_bytes = functools.lru_cache(maxsize=1024)(pa_forward_weights_workspace_bytes)
+_evict_workspace_bytes = functools.lru_cache(maxsize=1024)(pa_cache_evict_workspace_bytes)
+
+
+def pa_forward_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask,
+                    num_heads, num_kv_heads, head_dim, block_size, scale, out, stream=None, *,
+                    max_seq_len, num_blocks=None, sinks=None, kv_layout="nhd", sliding_window=0,
+                    alibi_slopes=None, alibi_sqrt=False, max_query_len=0, workspace=None,
+                    check=True):
+    """Attention of drafted tokens (see include/pa.h): tree_mask [T, words] int64,
+    as pa_tree_masks writes it.  Rows of `out` behind the last request are left as
+    they were.  workspace: as for pa_forward_shared_prefix."""
+    dt, layout = _dtype_code(q), layout_code(kv_layout)
+    S, T, width, blocks = _span_shapes(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                                       num_heads, num_kv_heads, head_dim, block_size, out, layout,
+                                       num_blocks, sinks)
+    mask_rows, words = tree_mask.shape
+    if mask_rows != T:
+        raise ValueError("tree_mask must be [T, words]")
+    device = q.get_device()
+    if not (_current(device) and _fits(device, q.dtype, q, k_cache, v_cache, out)
+            and _fits(device, torch.int32, block_table, seq_lens, query_start_loc)
+            and _fits(device, torch.int64, tree_mask) and _fits(device, torch.float32, sinks)):
+        _check_tensors(device, (q.dtype, dict(q=q, k_cache=k_cache, v_cache=v_cache, out=out)),
+                       (torch.int32, dict(block_table=block_table, seq_lens=seq_lens,
+                                          query_start_loc=query_start_loc)),
+                       (torch.int64, dict(tree_mask=tree_mask)), (torch.float32, dict(sinks=sinks)))
+    raw = _stream_ptr(stream, device)
+    if workspace is None:
+        workspace = _take_workspace(
+            _tree_workspace_bytes(dt, S, T, num_heads, num_kv_heads, head_dim, max_seq_len,
+                                  max_query_len), stream, raw, q)
+    elif not _fits(device, torch.uint8, workspace):
+        _check_tensors(device, (torch.uint8, dict(workspace=workspace)))
+    opts = _forward_options(sinks, layout, sliding_window, alibi_slopes, alibi_sqrt, max_query_len)
+    st = (_lib or lib()).pa_forward_tree(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), query_start_loc.data_ptr(), tree_mask.data_ptr(), int(num_heads),
+        int(num_kv_heads), int(head_dim), int(block_size), float(scale), out.data_ptr(), raw, dt,
+        S, T, words, width, blocks, int(max_seq_len), ctypes.byref(opts), workspace.data_ptr(),
+        workspace.numel())
+    if check and st:
+        _check(st, "pa_forward_tree")
+    return st
+
+
+def pa_forward_weights(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, num_heads,
+                       num_kv_heads, head_dim, block_size, scale, out, weights, stream=None, *,
+                       accumulate, max_seq_len, num_blocks=None, sinks=None, kv_layout="nhd",
+                       sliding_window=0, alibi_slopes=None, alibi_sqrt=False, max_query_len=0,
+                       workspace=None, check=True):
+    """Attention that adds up the weight of every cached position (see
+    include/pa.h): weights [num_blocks, Hk, block_size] float32 in place; out may
+    be None (the weights alone; v_cache is then not read and may be None)."""
+    dt, layout = _dtype_code(q), layout_code(kv_layout)
+    if out is None:
+        v_cache = None
+    elif v_cache is None:
+        raise ValueError("an output needs v_cache")
+    S, T, width, blocks = _span_shapes(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                                       num_heads, num_kv_heads, head_dim, block_size, out, layout,
+                                       num_blocks, sinks)
+    if weights.shape != (k_cache.shape[0], num_kv_heads, block_size):
+        raise ValueError("weights must be [num_blocks, num_kv_heads, block_size]")
+    device = q.get_device()
+    if not (_current(device) and _fits(device, q.dtype, q, k_cache, v_cache, out)
+            and _fits(device, torch.int32, block_table, seq_lens, query_start_loc)
+            and _fits(device, torch.float32, weights, sinks)):
+        _check_tensors(device, (q.dtype, dict(q=q, k_cache=k_cache, v_cache=v_cache, out=out)),
+                       (torch.int32, dict(block_table=block_table, seq_lens=seq_lens,
+                                          query_start_loc=query_start_loc)),
+                       (torch.float32, dict(weights=weights, sinks=sinks)))
+    raw = _stream_ptr(stream, device)
+    if workspace is None:
+        workspace = _take_workspace(
+            _weights_workspace_bytes(dt, S, T, num_heads, num_kv_heads, head_dim, max_seq_len,
+                                     max_query_len), stream, raw, q)
+    elif not _fits(device, torch.uint8, workspace):
+        _check_tensors(device, (torch.uint8, dict(workspace=workspace)))
+    opts = _forward_options(sinks, layout, sliding_window, alibi_slopes, alibi_sqrt, max_query_len)
+    st = (_lib or lib()).pa_forward_weights(
+        q.data_ptr(), k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), int(num_heads),
+        int(num_kv_heads), int(head_dim), int(block_size), float(scale),
+        None if out is None else out.data_ptr(), weights.data_ptr(), int(accumulate), raw, dt, S, T,
+        width, blocks, int(max_seq_len), ctypes.byref(opts), workspace.data_ptr(), workspace.numel())
+    if check and st:
+        _check(st, "pa_forward_weights")
+    return st
+
+
+def _cache_shape(k_cache, v_cache, block_size, layout):
+    """(pages, Hk, D, dtype code) of a pair of caches."""
+    blocks, x, y, D = shape = k_cache.shape
+    Hk, bs = (x, y) if layout == PA_KV_HND else (y, x)
+    if v_cache.shape != shape or bs != block_size:
+        raise ValueError("the caches' shape does not fit block_size and kv_layout")
+    return blocks, Hk, D, _dtype_code(k_cache)
+
+
+def _freed(freed_pages, num_freed):
+    """(pages, count, capacity) of the list of freed pages, or Nones and 0."""
+    if (freed_pages is None) != (num_freed is None):
+        raise ValueError("freed_pages and num_freed go together")
+    if num_freed is None:
+        return None, None, 0
+    if num_freed.numel() != 1:
+        raise ValueError("num_freed is one int32")
+    return freed_pages.data_ptr(), num_freed.data_ptr(), freed_pages.numel()
+
+
+def pa_cache_accept(k_cache, v_cache, block_table, seq_lens, query_start_loc, path, path_lens,
+                    seq_lens_out, block_size, stream=None, *, freed_pages=None, num_freed=None,
+                    num_blocks=None, kv_layout="nhd", check=True):
+    """The accepted tokens' rows moved behind the cached ones, in place (see
+    include/pa.h): path [S, max_path] and path_lens [S] int32; seq_lens_out [S] and,
+    if given, freed_pages [capacity] and num_freed [1] (int32) are written."""
+    layout = layout_code(kv_layout)
+    blocks, Hk, D, dt = _cache_shape(k_cache, v_cache, block_size, layout)
+    S, device = seq_lens.numel(), k_cache.get_device()
+    rows, width = block_table.shape
+    path_rows, max_path = path.shape
+    if not (rows == path_rows == path_lens.numel() == seq_lens_out.numel() == S
+            and query_start_loc.numel() == S + 1):
+        raise ValueError("block_table [S, max_blocks], path [S, max_path], path_lens [S], "
+                         "seq_lens_out [S] and query_start_loc [S + 1] go with seq_lens [S]")
+    if num_blocks is not None:
+        if num_blocks > blocks:
+            raise ValueError("num_blocks exceeds the caches")
+        blocks = int(num_blocks)
+    pages, count, capacity = _freed(freed_pages, num_freed)
+    if not (_current(device) and _fits(device, k_cache.dtype, k_cache, v_cache)
+            and _fits(device, torch.int32, block_table, seq_lens, query_start_loc, path, path_lens,
+                      seq_lens_out, freed_pages, num_freed)):
+        _check_tensors(device, (k_cache.dtype, dict(k_cache=k_cache, v_cache=v_cache)),
+                       (torch.int32, dict(block_table=block_table, seq_lens=seq_lens,
+                                          query_start_loc=query_start_loc, path=path,
+                                          path_lens=path_lens, seq_lens_out=seq_lens_out,
+                                          freed_pages=freed_pages, num_freed=num_freed)))
+    st = (_lib or lib()).pa_cache_accept(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        query_start_loc.data_ptr(), path.data_ptr(), path_lens.data_ptr(), seq_lens_out.data_ptr(),
+        pages, count, Hk, D, int(block_size), _stream_ptr(stream, device), dt, S, max_path, width,
+        blocks, capacity, layout)
+    if check and st:
+        _check(st, "pa_cache_accept")
+    return st
+
+
+def pa_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, keep_lens, seq_lens_out,
+                   block_size, stream=None, *, max_seq_len, weights_out=None, num_first=0,
+                   num_recent=0, freed_pages=None, num_freed=None, num_blocks=None,
+                   kv_layout="nhd", workspace=None, check=True):
+    """Requests longer than keep_lens [S] (int32) cut down to it, KV head by KV head
+    (see include/pa.h): weights [num_blocks, Hk, block_size] float32, moved along into
+    weights_out (None: in place); seq_lens_out [S] and, if given, freed_pages and
+    num_freed [1] (int32) are written.  workspace: as for pa_forward_shared_prefix."""
+    layout = layout_code(kv_layout)
+    blocks, Hk, D, dt = _cache_shape(k_cache, v_cache, block_size, layout)
+    S, device = seq_lens.numel(), k_cache.get_device()
+    rows, width = block_table.shape
+    if not rows == keep_lens.numel() == seq_lens_out.numel() == S:
+        raise ValueError("block_table [S, max_blocks], keep_lens [S] and seq_lens_out [S] go with "
+                         "seq_lens [S]")
+    if weights_out is None:
+        weights_out = weights
+    if not weights.shape == weights_out.shape == (blocks, Hk, block_size):
+        raise ValueError("weights and weights_out must be [num_blocks, num_kv_heads, block_size]")
+    if num_blocks is not None:
+        if num_blocks > blocks:
+            raise ValueError("num_blocks exceeds the caches")
+        blocks = int(num_blocks)
+    pages, count, capacity = _freed(freed_pages, num_freed)
+    if not (_current(device) and _fits(device, k_cache.dtype, k_cache, v_cache)
+            and _fits(device, torch.float32, weights, weights_out)
+            and _fits(device, torch.int32, block_table, seq_lens, keep_lens, seq_lens_out,
+                      freed_pages, num_freed)):
+        _check_tensors(device, (k_cache.dtype, dict(k_cache=k_cache, v_cache=v_cache)),
+                       (torch.float32, dict(weights=weights, weights_out=weights_out)),
+                       (torch.int32, dict(block_table=block_table, seq_lens=seq_lens,
+                                          keep_lens=keep_lens, seq_lens_out=seq_lens_out,
+                                          freed_pages=freed_pages, num_freed=num_freed)))
+    raw = _stream_ptr(stream, device)
+    if workspace is None:
+        workspace = _take_workspace(_evict_workspace_bytes(dt, S, Hk, D, max_seq_len), stream, raw,
+                                    k_cache)
+    elif not _fits(device, torch.uint8, workspace):
+        _check_tensors(device, (torch.uint8, dict(workspace=workspace)))
+    st = (_lib or lib()).pa_cache_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), keep_lens.data_ptr(), seq_lens_out.data_ptr(),
+        pages, count, int(num_first), int(num_recent), Hk, D, int(block_size), raw, dt, S, width,
+        blocks, capacity, int(max_seq_len), layout, workspace.data_ptr(), workspace.numel())
+    if check and st:
+        _check(st, "pa_cache_evict")
     return st
 
 
