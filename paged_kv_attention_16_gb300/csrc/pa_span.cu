@@ -1,6 +1,7 @@
 // pa_span.cu -- attention of drafted trees (pa_forward_tree) and attention that
 // adds up the weight every cached position gets (pa_forward_weights): argument
-// checks, the planner, the CUDA-core kernel and the merge.
+// checks, the planner, the fp32 kernel and the merge
+// (pa_span_mma.cu holds the bf16 kernel).
 //
 // Both read a request's context once for all of its rows (a row: one new token
 // x one query head of a KV head), in units of up to 256 rows cut into equal runs
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
 }
 
 // ---------------------------------------------------------------------------
-// the pass over keys and values on CUDA cores
+// the pass over keys and values on CUDA cores (fp32)
 // ---------------------------------------------------------------------------
 // Eight threads share up to four rows (each every eighth 16-byte group of their
 // head_dim values), 128 rows a pass; 32 keys and values at a time in shared
@@ -112,24 +113,14 @@ struct SpanTileBuf {
   float k[kSimtKeys][D], v[kSimtKeys][D];
 };
 
-// Four values from global to shared memory as fp32, or zeros.
+// Four values from global to shared memory, or zeros.
 __device__ inline void copy4(float *dst, const float *src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(take ? 16 : 0)
                : "memory");
 }
-__device__ inline void copy4(float *dst, const __nv_bfloat16 *src, bool take) {
-  uint2 v = make_uint2(0, 0);
-  if (take) v = *reinterpret_cast<const uint2 *>(src);
-  *reinterpret_cast<float4 *>(dst) = make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
-}
-__device__ inline float4 load4(const float *src) { return *reinterpret_cast<const float4 *>(src); }
-__device__ inline float4 load4(const __nv_bfloat16 *src) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(src);
-  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
-}
 
-template <typename T, int D, int MODE>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanParams p) {
   constexpr int N = D / 8;  // values of a row that a thread holds
   constexpr bool VALUES = MODE != kSpanVotesOnly, CAUSAL = MODE != kSpanTree;
@@ -141,8 +132,8 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
   pdl_wait();
   pdl_trigger();
   const SpanPlan plan = *p.plan;
-  const T *kc = static_cast<const T *>(p.k_cache);
-  const T *vc = static_cast<const T *>(p.v_cache);
+  const float *kc = static_cast<const float *>(p.k_cache);
+  const float *vc = static_cast<const float *>(p.v_cache);
   SpanCursor cur;
   cur.start(p, plan, blockIdx.x);
   SpanPiece it;
@@ -157,12 +148,12 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
       for (int r = 0; r < R; ++r) {
         const int row = min(row0 + r * 32 + (tid >> 3), rows - 1);
         const int tok = it.q_start + it.t0 + row / G, head = it.kvh * G + row % G;
-        const T *q = static_cast<const T *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
+        const float *q = static_cast<const float *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-          const float4 x = load4(q + i * 8 + c * 4);
+          const float4 x = *reinterpret_cast<const float4 *>(q + i * 8 + c * 4);
           qv[r][i] = x.x * f.scale_log2;
           qv[r][i + 1] = x.y * f.scale_log2;
           qv[r][i + 2] = x.z * f.scale_log2;
@@ -521,21 +512,19 @@ cudaError_t launch_merge_d(const SpanParams &p, long long most, cudaStream_t st)
   return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p);
 }
 
-template <typename T, int D, int MODE>
+template <int D, int MODE>
 cudaError_t launch_simt_d(const SpanParams &p, cudaStream_t st) {
   constexpr int kSmem = 2 * (int)sizeof(SpanTileBuf<D>);
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = set_smem_attrs_once(span_simt_kernel<T, D, MODE>, kSmem, done);
+  const cudaError_t e = set_smem_attrs_once(span_simt_kernel<D, MODE>, kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_dependent(span_simt_kernel<T, D, MODE>, dim3(p.grid), dim3(kSimtThreads), kSmem, st, p);
+  return launch_dependent(span_simt_kernel<D, MODE>, dim3(p.grid), dim3(kSimtThreads), kSmem, st, p);
 }
 
 template <int MODE>
 cudaError_t launch_pass(const SpanParams &p, cudaStream_t st) {
-  const bool bf16 = p.f.dtype == PA_BF16;
-  if (p.f.head_dim == 128)
-    return bf16 ? launch_simt_d<__nv_bfloat16, 128, MODE>(p, st) : launch_simt_d<float, 128, MODE>(p, st);
-  return bf16 ? launch_simt_d<__nv_bfloat16, 64, MODE>(p, st) : launch_simt_d<float, 64, MODE>(p, st);
+  if (p.f.dtype == PA_BF16) return launch_span_mma(p, MODE, st);
+  return p.f.head_dim == 128 ? launch_simt_d<128, MODE>(p, st) : launch_simt_d<64, MODE>(p, st);
 }
 
 template <int MODE>
@@ -678,7 +667,7 @@ pa_status span_call(const SpanCall &sc) {
   p.keep_scores = votes;
   p.num_sms = num_sms;
   p.grid = std::min(num_sms, kMaxGrid);
-  p.halves = 0;
+  p.halves = c.dtype == PA_BF16;
   p.slot_rows = lay.slot_rows;
   p.plan = reinterpret_cast<SpanPlan *>(ws + lay.plan);
   p.req = reinterpret_cast<SpanReq *>(ws + lay.req);

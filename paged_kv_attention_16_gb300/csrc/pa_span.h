@@ -176,6 +176,9 @@ __device__ inline unsigned long long span_causal_bits(int at, int own) {
   return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
 }
 
+// The pass over keys and values on the tensor cores (bf16; mode: a SpanMode).
+cudaError_t launch_span_mma(const SpanParams &p, int mode, cudaStream_t stream);
+
 // The sums over rows of pa_forward_weights, behind the rows' log-sum-exps.
 cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream);
 
