@@ -30,7 +30,7 @@ constexpr int kMergeGroups = kMergeThreads / 8;
 // ---------------------------------------------------------------------------
 
 __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParams p) {
-  __shared__ long long scratch[3 * 33];
+  __shared__ long long scratch[4 * 33];
   const FwdParams &f = p.f;
   const int S = f.num_seqs, T = f.num_tokens, tid = threadIdx.x;
   const int Hk = f.num_kv_heads, G = f.num_heads / Hk;
@@ -40,11 +40,11 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
       (int)min((unsigned long long)f.max_seq_len, (unsigned long long)f.max_blocks_per_seq * f.block_size);
   unsigned flags = 0;
   int bad = 0;
-  long long sum[3] = {0, 0, 0};
+  long long sum[4] = {0, 0, 0, 0};
   for (int base = 0; base < S; base += kPlanThreads) {
     const int s = base + tid;
     SpanReq r{};
-    long long cnt[3] = {0, 0, 0}, tot[3];  // units, laid-out work, kept scores
+    long long cnt[4] = {0, 0, 0, 0}, tot[4];  // units, laid-out work, kept scores, voted tiles
     long long scores = 0;
     if (s < S) {
       const int q0 = f.qsl[s], q1 = f.qsl[s + 1];
@@ -65,24 +65,26 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
         cnt[1] = cnt[0] * (r.ntile + kSpanOverhead);
         if (p.keep_scores && rows <= kSpanStoredRows) scores = Hk * rows * r.ntile * kSpanTile;
         cnt[2] = scores;
+        if (p.keep_scores && scores == 0) cnt[3] = (long long)Hk * r.ntile;
       }
     }
     const long long units = cnt[0], cost = cnt[1];
-    block_scan_multi<3>(cnt, scratch, tot);
+    block_scan_multi<4>(cnt, scratch, tot);
     if (s < S) {
       r.unit0 = (int)(sum[0] + cnt[0] - units);
       r.cost0 = (unsigned)(sum[1] + cnt[1] - cost);
       r.score0 = scores > 0 ? sum[2] + cnt[2] - scores : -1;
       p.req[s] = r;
       p.cost_end[s] = (unsigned)(sum[1] + cnt[1]);
+      p.vote_end[s] = (unsigned)(sum[3] + cnt[3]);
     }
 #pragma unroll
-    for (int x = 0; x < 3; ++x) sum[x] += tot[x];
+    for (int x = 0; x < 4; ++x) sum[x] += tot[x];
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       atomicOr(f.status, PA_DEV_BAD_QSL);
-      *p.plan = SpanPlan{0, 1, 1};
+      *p.plan = SpanPlan{0, 1, 0, 1};
     }
     return;
   }
@@ -90,7 +92,8 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
   if (tid == 0) {
     // (the host has bounded the sum by 2^31)
     const unsigned total = (unsigned)sum[1];
-    *p.plan = SpanPlan{total, max((total + p.grid - 1) / p.grid, 1u + kSpanOverhead), 0};
+    *p.plan = SpanPlan{total, max((total + p.grid - 1) / p.grid, 1u + kSpanOverhead),
+                       (unsigned)sum[3], 0};
   }
 }
 
@@ -546,7 +549,7 @@ constexpr int kMaxGrid = 160;  // blocks that the partials' bound allows for
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SpanLayout {
-  size_t plan, req, cost_end, part_o, part_lse, row_lse, scores, total;
+  size_t plan, req, cost_end, vote_end, part_o, part_lse, row_lse, scores, total;
   int slot_rows;
   bool ok;  // the extents are ones that the kernels count in 32 bits
 };
@@ -574,6 +577,7 @@ SpanLayout span_layout(int dtype, int num_seqs, int num_tokens, int num_heads, i
   l.plan = take(sizeof(SpanPlan));
   l.req = take(S * sizeof(SpanReq));
   l.cost_end = take(S * sizeof(unsigned));
+  l.vote_end = take(S * sizeof(unsigned));
   l.part_o = take(values ? (size_t)slots * l.slot_rows * head_dim * sizeof(float) : 0);
   l.part_lse = take((size_t)slots * l.slot_rows * sizeof(float));
   if (votes) {
@@ -672,6 +676,7 @@ pa_status span_call(const SpanCall &sc) {
   p.plan = reinterpret_cast<SpanPlan *>(ws + lay.plan);
   p.req = reinterpret_cast<SpanReq *>(ws + lay.req);
   p.cost_end = reinterpret_cast<unsigned *>(ws + lay.cost_end);
+  p.vote_end = reinterpret_cast<unsigned *>(ws + lay.vote_end);
   p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
   p.part_lse = reinterpret_cast<float *>(ws + lay.part_lse);
   p.row_lse = votes ? reinterpret_cast<float *>(ws + lay.row_lse) : nullptr;

@@ -45,6 +45,7 @@ struct SpanReq {
 struct SpanPlan {
   unsigned total;  // laid-out work
   unsigned run;    // each block's share
+  unsigned vote_tiles;  // (KV head, tile) of the requests whose scores are not kept
   int all_bad;     // bad query_start_loc: every row is zero
 };
 
@@ -62,6 +63,7 @@ struct SpanParams {
   SpanPlan *plan;
   SpanReq *req;          // [num_seqs]
   unsigned *cost_end;    // [num_seqs] inclusive
+  unsigned *vote_end;    // [num_seqs] inclusive sum of Hk * ntile where scores are not kept
   float *part_o;         // [slots * slot_rows][head_dim], normalised
   float *part_lse;       // base 2; +inf: a bad page in the piece's range
   float *row_lse;        // [num_tokens * num_heads], sinks included
@@ -181,5 +183,7 @@ cudaError_t launch_span_mma(const SpanParams &p, int mode, cudaStream_t stream);
 
 // The sums over rows of pa_forward_weights, behind the rows' log-sum-exps.
 cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream);
+// Those of requests whose scores were not kept, on the tensor cores (bf16).
+cudaError_t launch_votes_mma(const SpanParams &p, cudaStream_t stream);
 
 }  // namespace pa

@@ -87,25 +87,15 @@ __global__ void __launch_bounds__(kVoteThreads) votes_kept_kernel(const SpanPara
 }
 
 // ---------------------------------------------------------------------------
-// more rows: the scores are multiplied out again, on CUDA cores
+// more rows: the scores are multiplied out again, on CUDA cores (fp32)
 // ---------------------------------------------------------------------------
 // 64 positions x 32 rows a step, a thread 4 positions x 2 rows; a block's keys
 // stay in shared memory while all rows pass.
 constexpr int kPos = 64, kRows = 32;
 
-template <typename T>
-__device__ inline float4 load4f(const T *src);
-template <>
-__device__ inline float4 load4f<float>(const float *src) {
-  return *reinterpret_cast<const float4 *>(src);
-}
-template <>
-__device__ inline float4 load4f<__nv_bfloat16>(const __nv_bfloat16 *src) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(src);
-  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
-}
+__device__ inline float4 load4f(const float *src) { return *reinterpret_cast<const float4 *>(src); }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanParams p, int chunks) {
   extern __shared__ __align__(16) float s_dyn[];
   constexpr int LD = D + 4;
@@ -133,7 +123,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
       if (pos < r.ctx) {
         const int page = __ldg(bt + pos / bs), slot = pos % bs;
         const size_t row = p.hnd ? ((size_t)page * Hk + kvh) * bs + slot : ((size_t)page * bs + slot) * Hk + kvh;
-        v = load4f(static_cast<const T *>(p.k_cache) + row * D + x);
+        v = load4f(static_cast<const float *>(p.k_cache) + row * D + x);
       }
       *reinterpret_cast<float4 *>(&s_k[j * LD + x]) = v;
     }
@@ -145,7 +135,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
       for (int e = tid; e < kRows * (D / 4); e += kVoteThreads) {
         const int i = e / (D / 4), x = e % (D / 4) * 4, row = min(r0 + i, R - 1);
         const size_t at_q = ((size_t)(r.q_start + row / G) * H + kvh * G + row % G) * D + x;
-        float4 v = load4f(static_cast<const T *>(f.q) + at_q);
+        float4 v = load4f(static_cast<const float *>(f.q) + at_q);
         v.x *= f.scale_log2;
         v.y *= f.scale_log2;
         v.z *= f.scale_log2;
@@ -201,15 +191,15 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt(const SpanParams &p, cudaStream_t st) {
   constexpr int kSmem = (kPos + kRows) * (D + 4) * (int)sizeof(float);
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = set_smem_attrs_once(votes_simt_kernel<T, D>, kSmem, done);
+  const cudaError_t e = set_smem_attrs_once(votes_simt_kernel<D>, kSmem, done);
   if (e != cudaSuccess) return e;
   const long long chunks = ceil_div_ll(std::max(p.f.max_seq_len, 1), kPos);
   const long long n = chunks * p.f.num_seqs * p.f.num_kv_heads;
-  return launch_dependent(votes_simt_kernel<T, D>, dim3((unsigned)std::min<long long>(n, 3ll * p.num_sms)),
+  return launch_dependent(votes_simt_kernel<D>, dim3((unsigned)std::min<long long>(n, 3ll * p.num_sms)),
                           dim3(kVoteThreads), kSmem, st, p, (int)chunks);
 }
 
@@ -221,10 +211,8 @@ cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream
   cudaError_t e = launch_dependent(votes_kept_kernel, dim3((unsigned)std::min<long long>(n, 8ll * p.num_sms)),
                                    dim3(kVoteThreads), 0, stream, p, (int)chunks);
   if (e != cudaSuccess || most_rows <= kSpanStoredRows) return e;
-  const bool bf16 = p.f.dtype == PA_BF16;
-  if (p.f.head_dim == 128)
-    return bf16 ? launch_simt<__nv_bfloat16, 128>(p, stream) : launch_simt<float, 128>(p, stream);
-  return bf16 ? launch_simt<__nv_bfloat16, 64>(p, stream) : launch_simt<float, 64>(p, stream);
+  if (p.f.dtype == PA_BF16) return launch_votes_mma(p, stream);
+  return p.f.head_dim == 128 ? launch_simt<128>(p, stream) : launch_simt<64>(p, stream);
 }
 
 }  // namespace pa
