@@ -22,7 +22,7 @@ bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 constexpr int kSelectThreads = 512;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMoveThreads = 256;
-constexpr int kMovePieces = 4;  // 16-byte pieces of K, and of V, that a thread holds
+constexpr int kMovePieces = 4;  // 16-byte pieces of K, and of V, that a thread copies
 constexpr int kChunkPieces = kMoveThreads * kMovePieces;
 
 struct EvictHeader {
@@ -45,7 +45,9 @@ struct EvictArgs {
   EvictHeader *head;
   unsigned *chunk_end;  // [num_seqs] inclusive sum of the requests' chunks
   unsigned *ready;      // [num_seqs * num_kv_heads][max_chunks] 1: the chunk's rows are read
-  int32_t *kept;        // [num_seqs * num_kv_heads][max_seq_len]
+  int32_t *kept;        // [num_seqs * num_kv_heads][max_seq_len] positions, in order,
+  float *kept_w;        // and their weights
+  int32_t *below;       // [num_seqs * num_kv_heads][max_chunks] kept positions below the chunk's first one
 };
 
 // The request's length behind the eviction; bad metadata: its length, nothing moves.
@@ -69,16 +71,69 @@ __device__ inline uint32_t order_of(float w) {
 // ---------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------
+// A cluster of C blocks for each (request, KV head), each with its share of the
+// positions, whose keys (an integer that orders as the weight does) it reads once
+// into shared memory.  Counts are summed over the cluster through distributed shared
+// memory.  What bounds it is a chain of about ten barriers and the counting's
+// atomics: few positions a block matter more than many blocks.
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ long long scratch[33];
-  __shared__ unsigned s_hist[kBins];
-  __shared__ unsigned s_prefix, s_rank;
+struct SelectShared {
+  alignas(16) unsigned hist[kBins];
+  unsigned count[2];  // of this block's share: kept for sure, equal to the threshold
+  unsigned prefix, rank;
+  unsigned warp_sum[2][kSelectThreads / 32];
+  long long scratch[33];
+};
+
+constexpr int kMostCluster = 8;
+
+__device__ inline unsigned load_cluster(const unsigned *p, unsigned rank) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(smem_u32(p), rank)) : "memory");
+  return v;
+}
+__device__ inline uint4 load_cluster4(const unsigned *p, unsigned rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_map(smem_u32(p), rank))
+               : "memory");
+  return v;
+}
+
+// Inclusive sum over the block's threads, one barrier; `turn` alternates between
+// calls (the sums of the call before may still be read).
+__device__ inline unsigned select_scan(SelectShared &sh, unsigned v, int turn, unsigned &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) sh.warp_sum[turn & 1][warp] = v;
+  __syncthreads();
+  unsigned before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    const unsigned y = sh.warp_sum[turn & 1][w];
+    if (w < warp) before += y;
+    total += y;
+  }
+  return before + v;
+}
+
+// cached: keys that the dynamic shared memory holds (the others are read again)
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a, int C, int cached) {
+  extern __shared__ uint32_t s_key[];
+  __shared__ SelectShared sh;
   const int tid = threadIdx.x, Hk = a.num_kv_heads, bs = a.block_size;
+  const int unit = blockIdx.x / C, part = blockIdx.x - unit * C;
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x == a.num_seqs * Hk) {
-    // -- the last block: chunks, new lengths, the pages that are free again
+  if (unit == a.num_seqs * Hk) {
+    if (part) return;
+    // -- the last cluster: chunks, new lengths, the pages that are free again
     long long sum = 0;
     for (int base = 0; base < a.num_seqs; base += kSelectThreads) {
       const int s = base + tid;
@@ -91,7 +146,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         if (after < len) n = (long long)Hk * ((after + a.chunk_rows - 1) / a.chunk_rows);
         a.seq_lens_out[s] = after;
       }
-      const long long end = block_inclusive_scan(n, scratch, &tot) + sum;
+      const long long end = block_inclusive_scan(n, sh.scratch, &tot) + sum;
       if (s < a.num_seqs) a.chunk_end[s] = (unsigned)end;
       sum += tot;
     }
@@ -106,11 +161,11 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     return;
   }
 
-  const int s = blockIdx.x / Hk, h = blockIdx.x - s * Hk;
+  const int s = unit / Hk, h = unit - s * Hk;
   int len;
   unsigned flags = 0;
   const int after = evicted_len(a, s, len, flags);
-  if (flags) return;  // (the last block reports it)
+  if (flags) return;  // (the last cluster reports it; the same for the whole cluster)
   const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
   auto slot_of = [&](int pos) -> long long {  // of a weight; -1: a bad page
     const int lp = (unsigned)pos / (unsigned)bs, page = __ldg(bt + lp);
@@ -122,7 +177,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   };
   if (after == len) {
     if (a.weights_out != a.weights) {
-      for (int pos = tid; pos < len; pos += kSelectThreads) {
+      for (int pos = part * kSelectThreads + tid; pos < len; pos += C * kSelectThreads) {
         const long long at = slot_of(pos);
         if (at >= 0) a.weights_out[at] = a.weights[at];
       }
@@ -132,8 +187,16 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   }
   const int first = min(a.num_first, after), recent = min(a.num_recent, after - first);
   const int need = after - first - recent, lo = first, hi = len - recent;  // candidates [lo, hi)
-  for (int c = tid; c < (after + a.chunk_rows - 1) / a.chunk_rows; c += kSelectThreads)
-    a.ready[(size_t)blockIdx.x * a.max_chunks + c] = 0;
+  for (int c = part * kSelectThreads + tid; c < (after + a.chunk_rows - 1) / a.chunk_rows; c += C * kSelectThreads)
+    a.ready[(size_t)unit * a.max_chunks + c] = 0;
+  const int share = (len + C - 1) / C, p0 = min(part * share, len), p1 = min(p0 + share, len);
+  auto read_key = [&](int pos) {
+    const long long at = slot_of(pos);
+    return at < 0 ? 0u : order_of(a.weights[at]);
+  };
+  auto key_of = [&](int pos) { return pos - p0 < cached ? s_key[pos - p0] : read_key(pos); };
+#pragma unroll 4
+  for (int i = tid; i < min(p1 - p0, cached); i += kSelectThreads) s_key[i] = read_key(p0 + i);
 
   // -- the candidate of rank `need` from the top: `prefix` its leading bits
   unsigned prefix = 0, rank = need;
@@ -141,73 +204,109 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1 << 10 : kBins;
-      for (int b = tid; b < kBins; b += kSelectThreads) s_hist[b] = 0;
+      for (int b = tid; b < kBins; b += kSelectThreads) sh.hist[b] = 0;
       __syncthreads();
       const unsigned above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
 #pragma unroll 4
-      for (int pos = lo + tid; pos < hi; pos += kSelectThreads) {
-        const long long at = slot_of(pos);
-        const uint32_t key = at < 0 ? 0u : order_of(a.weights[at]);
-        if ((key & above) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
+      for (int pos = max(p0, lo) + tid; pos < min(p1, hi); pos += kSelectThreads) {
+        const uint32_t key = key_of(pos);
+        if ((key & above) == prefix) atomicAdd(&sh.hist[(key >> shift) & (bins - 1)], 1u);
       }
-      __syncthreads();
-      // bins from the top: thread t takes the t-th group of kBins / kSelectThreads
-      constexpr int PER = kBins / kSelectThreads;
-      long long n = 0, tot;
-      const int top = kBins - 1 - tid * PER;
+      if (C > 1) cluster_sync_all();
+      else __syncthreads();
+      // bins from the top: thread t takes the t-th group of four
+      static_assert(kBins == 4 * kSelectThreads, "four bins a thread");
+      const int low = kBins - 4 - tid * 4;
+      unsigned cnt[4] = {0, 0, 0, 0}, tot;  // [0] is the lowest bin
+      if (C > 1) {
+        uint4 v[kMostCluster];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) n += s_hist[top - i];
-      const long long end = block_inclusive_scan(n, scratch, &tot);
-      unsigned before = (unsigned)(end - n);
-      if (before < rank && rank <= (unsigned)end) {  // one thread
-        int b = top;
-        while (before + s_hist[b] < rank) before += s_hist[b--];
-        s_prefix = prefix | (unsigned)b << shift;
-        s_rank = rank - before;
+        for (int k = 0; k < kMostCluster; ++k) v[k] = k < C ? load_cluster4(&sh.hist[low], k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k) cnt[0] += v[k].x, cnt[1] += v[k].y, cnt[2] += v[k].z, cnt[3] += v[k].w;
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(&sh.hist[low]);
+        cnt[0] = v.x, cnt[1] = v.y, cnt[2] = v.z, cnt[3] = v.w;
       }
-      __syncthreads();
-      prefix = s_prefix;
-      rank = s_rank;
+      const unsigned n = cnt[0] + cnt[1] + cnt[2] + cnt[3], end = select_scan(sh, n, pass, tot);
+      unsigned before = end - n;
+      if (before < rank && rank <= end) {  // one thread
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (before < rank && before + cnt[i] >= rank) {
+            sh.prefix = prefix | (unsigned)(low + i) << shift;
+            sh.rank = rank - before;
+          }
+          before += cnt[i];
+        }
+      }
+      if (C > 1) cluster_sync_all();  // (the counts are read)
+      else __syncthreads();
+      prefix = sh.prefix;
+      rank = sh.rank;
     }
   }
+  auto state_of = [&](int pos, uint32_t key) {  // 0 no, 1 kept, 2 equal to the threshold
+    return pos < lo || pos >= hi ? 1 : need == 0 ? 0 : key > prefix ? 1 : key == prefix ? 2 : 0;
+  };
+  // -- how many are kept in the shares before this one
+  unsigned sure_before = 0, equal_before = 0;
+  if (C > 1) {
+    unsigned sure = 0, equal = 0;
+    for (int pos = p0 + tid; pos < p1; pos += kSelectThreads) {
+      const int st = state_of(pos, key_of(pos));
+      sure += st == 1;
+      equal += st == 2;
+    }
+    if (tid < 2) sh.count[tid] = 0;
+    __syncthreads();
+    sure = __reduce_add_sync(0xffffffffu, sure);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if ((tid & 31) == 0) {
+      atomicAdd(&sh.count[0], sure);
+      atomicAdd(&sh.count[1], equal);
+    }
+    cluster_sync_all();
+#pragma unroll
+    for (int k = 0; k < kMostCluster; ++k) {
+      if (k < part) {
+        sure_before += load_cluster(&sh.count[0], k);
+        equal_before += load_cluster(&sh.count[1], k);
+      }
+    }
+    cluster_sync_all();  // (no block leaves while its counts are read)
+  }
   // -- the kept positions in order: the first `rank` of those that equal the threshold
-  int32_t *kept = a.kept + (size_t)blockIdx.x * a.max_seq_len;
-  long long done = 0;  // kept positions so far in the low half, equal ones in the high half
+  int32_t *kept = a.kept + (size_t)unit * a.max_seq_len;
+  float *kept_w = a.kept_w + (size_t)unit * a.max_seq_len;
+  int32_t *below = a.below + (size_t)unit * a.max_chunks;
   constexpr int PER = 4;
-  for (int base = 0; base < len; base += kSelectThreads * PER) {
-    float w[PER];
-    bool there[PER];  // (not on a bad page)
-    int state[PER];   // 0 no, 1 kept, 2 equal to the threshold
-    long long n = 0, tot;
+  int turn = 1;
+  for (int base = p0; base < p1; base += kSelectThreads * PER, ++turn) {
+    int state[PER];
+    unsigned n = 0, tot;  // kept for sure in the low half, equal ones in the high half: 2048 at most
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int pos = base + tid * PER + i;
-      state[i] = 0;
-      w[i] = 0.f;
-      there[i] = false;
-      if (pos >= len) continue;
-      const long long at = slot_of(pos);
-      there[i] = at >= 0;
-      if (there[i]) w[i] = a.weights[at];
-      const uint32_t key = at < 0 ? 0u : order_of(w[i]);
-      state[i] = pos < lo || pos >= hi ? 1 : need == 0 ? 0 : key > prefix ? 1 : key == prefix ? 2 : 0;
-      n += state[i] == 1 ? 1ll : state[i] == 2 ? 1ll << 32 : 0ll;
+      state[i] = pos < p1 ? state_of(pos, key_of(pos)) : 0;
+      n += state[i] == 1 ? 1u : state[i] == 2 ? 1u << 16 : 0u;
     }
-    long long at = block_inclusive_scan(n, scratch, &tot) + done - n;
-    // (every weight of this step is read: the scan is a barrier)
+    unsigned at = select_scan(sh, n, turn, tot) - n;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const unsigned equal = (unsigned)(at >> 32);
-      const bool keep = state[i] == 1 || (state[i] == 2 && equal < rank);
-      if (keep) {
-        const int dst = (int)((unsigned)at + min(equal, rank));
-        kept[dst] = base + tid * PER + i;
-        const long long to = slot_of(dst);
-        if (to >= 0 && there[i]) a.weights_out[to] = w[i];
+      const int pos = base + tid * PER + i;
+      const unsigned equal = equal_before + (at >> 16);
+      const int dst = (int)(sure_before + (at & 0xffff) + min(equal, rank));  // kept ones below pos
+      if (pos < p1 && pos < after && pos % a.chunk_rows == 0) below[pos / a.chunk_rows] = dst;
+      if (state[i] == 1 || (state[i] == 2 && equal < rank)) {
+        const long long from = slot_of(pos);
+        kept[dst] = pos;
+        if (from >= 0) kept_w[dst] = a.weights[from];
       }
-      at += state[i] == 1 ? 1ll : state[i] == 2 ? 1ll << 32 : 0ll;
+      at += state[i] == 1 ? 1u : state[i] == 2 ? 1u << 16 : 0u;
     }
-    done += tot;
+    sure_before += tot & 0xffff;
+    equal_before += tot >> 16;
   }
   if (flags) atomicOr(a.status, flags);
 }
@@ -222,14 +321,20 @@ __device__ inline unsigned load_acquire(const unsigned *p) {
   return v;
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+// 16 bytes from global to shared memory, past L1.
+__device__ inline void copy16(uint4 *dst, const uint8_t *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const EvictArgs a) {
+  __shared__ uint4 s_k[kChunkPieces], s_v[kChunkPieces];
   __shared__ unsigned s_ticket;
   const int tid = threadIdx.x, Hk = a.num_kv_heads, bs = a.block_size, ppr = a.head_bytes / 16;
   pdl_trigger();
   pdl_wait();
   const unsigned chunks = a.head->chunks;
   for (;;) {
-    __syncthreads();  // s_ticket is read
+    __syncthreads();  // s_ticket and the rows of the chunk before are read
     if (tid == 0) s_ticket = atomicAdd(&a.head->ticket, 1u);
     __syncthreads();
     const unsigned t = s_ticket;
@@ -242,51 +347,43 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int s = lo, len = a.seq_lens[s], after = min(len, a.keep_lens[s]);
     const int nc = (after + a.chunk_rows - 1) / a.chunk_rows;
     const int local = (int)(t - (a.chunk_end[s] - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
+    const int unit = s * Hk + h;
     const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
-    const int32_t *kept = a.kept + ((size_t)s * Hk + h) * a.max_seq_len;
-    unsigned *ready = a.ready + ((size_t)s * Hk + h) * a.max_chunks;
+    const int32_t *kept = a.kept + (size_t)unit * a.max_seq_len;
+    unsigned *ready = a.ready + (size_t)unit * a.max_chunks;
     const int i0 = c * a.chunk_rows, rows = min(a.chunk_rows, after - i0);
-    // -- this chunk's rows
-    uint4 k[kMovePieces], v[kMovePieces];
-    long long to[kMovePieces];
+    const int below = __ldg(a.below + (size_t)unit * a.max_chunks + c);
+    // -- this chunk's rows into shared memory
     unsigned flags = 0;
 #pragma unroll
     for (int u = 0; u < kMovePieces; ++u) {
-      const int e = u * kMoveThreads + tid, row = e / ppr, piece = e - row * ppr;
-      to[u] = -1;
+      const int e = u * kMoveThreads + tid, row = (unsigned)e / (unsigned)ppr, piece = e - row * ppr;
       if (row >= rows) continue;
-      const int dst = i0 + row, src = __ldg(kept + dst);
-      if (src == dst) continue;
+      const int src = __ldg(kept + i0 + row);
+      if (src == i0 + row) continue;
       const long long from = row_offset(bt, src, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
-      const long long into = row_offset(bt, dst, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
-      if (from < 0 || into < 0) {
-        flags |= PA_DEV_BAD_BLOCK;
-        continue;
-      }
-      to[u] = into + piece * 16;
-      k[u] = __ldcg(reinterpret_cast<const uint4 *>(a.k_cache + from + piece * 16));
-      v[u] = __ldcg(reinterpret_cast<const uint4 *>(a.v_cache + from + piece * 16));
+      if (from < 0) continue;
+      copy16(s_k + e, a.k_cache + from + piece * 16);
+      copy16(s_v + e, a.v_cache + from + piece * 16);
     }
-    // (the barrier's operand needs every loaded value: the rows are read when it opens)
-    unsigned seen = 0;
-#pragma unroll
-    for (int u = 0; u < kMovePieces; ++u)
-      if (to[u] >= 0) seen ^= k[u].x ^ v[u].x;
-    __syncthreads_or(seen);
+    // -- meanwhile its weights (select has read them all)
+    for (int i = i0 + tid; i < i0 + rows; i += kMoveThreads) {
+      const int from = __ldg(kept + i), page = __ldg(bt + (unsigned)from / (unsigned)bs),
+                lp = (unsigned)i / (unsigned)bs, into = __ldg(bt + lp);
+      if (page >= 0 && page < a.num_blocks && into >= 0 && into < a.num_blocks)
+        a.weights_out[((long long)into * Hk + h) * bs + (i - lp * bs)] = a.kept_w[(size_t)unit * a.max_seq_len + i];
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
     if (tid == 0) {
       __threadfence();
       atomicExch(ready + c, 1u);
     }
     // -- the chunks whose rows lie where this one writes: those that hold the kept
-    // positions of [i0, i0 + rows), from the first one's chunk on; they were handed
-    // out before this one, and mark their rows read without waiting for anything
-    int from = 0, until = after;  // the first kept position that is not below i0
-    while (from < until) {
-      const int mid = (from + until) >> 1;
-      if (__ldg(kept + mid) < i0) from = mid + 1; else until = mid;
-    }
+    // positions from i0 on, from the first one's chunk on; they were handed out
+    // before this one, and mark their rows read without waiting for anything
     bool late = false;
-    for (int w = from / a.chunk_rows + tid; w < c; w += kMoveThreads) {
+    for (int w = below / a.chunk_rows + tid; w < c; w += kMoveThreads) {
       if (load_acquire(ready + w)) continue;
       const uint64_t t0 = global_timer_ns();
       for (uint32_t i = 1; !load_acquire(ready + w); ++i) {
@@ -301,9 +398,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     if (!__syncthreads_or(late)) {
 #pragma unroll
       for (int u = 0; u < kMovePieces; ++u) {
-        if (to[u] < 0) continue;
-        *reinterpret_cast<uint4 *>(a.k_cache + to[u]) = k[u];
-        *reinterpret_cast<uint4 *>(a.v_cache + to[u]) = v[u];
+        const int e = u * kMoveThreads + tid, row = (unsigned)e / (unsigned)ppr, piece = e - row * ppr;
+        if (row >= rows) continue;
+        const int src = __ldg(kept + i0 + row);
+        if (src == i0 + row) continue;
+        const long long from = row_offset(bt, src, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
+        const long long into = row_offset(bt, i0 + row, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
+        if (from < 0 || into < 0) {
+          flags |= PA_DEV_BAD_BLOCK;
+          continue;
+        }
+        *reinterpret_cast<uint4 *>(a.k_cache + into + piece * 16) = s_k[e];
+        *reinterpret_cast<uint4 *>(a.v_cache + into + piece * 16) = s_v[e];
       }
     }
     if (flags) atomicOr(a.status, flags);
@@ -317,7 +423,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct EvictLayout {
-  size_t head, chunk_end, ready, kept, total;
+  size_t head, chunk_end, ready, kept, kept_w, below, total;
   int chunk_rows, max_chunks;
   bool ok;
 };
@@ -338,8 +444,38 @@ EvictLayout evict_layout(int head_bytes, int num_seqs, int num_kv_heads, int max
   l.chunk_end = take(S * sizeof(unsigned));
   l.ready = take((size_t)units * l.max_chunks * sizeof(unsigned));
   l.kept = take((size_t)units * msl * sizeof(int32_t));
+  l.kept_w = take((size_t)units * msl * sizeof(float));
+  l.below = take((size_t)units * l.max_chunks * sizeof(int32_t));
   l.total = off;
   return l;
+}
+
+cudaError_t launch_select(const EvictArgs &a, int num_sms, cudaStream_t st) {
+  const long long units = (long long)a.num_seqs * a.num_kv_heads;
+  // Blocks of a cluster: while the grid leaves SMs and a share has work for its
+  // threads.
+  int C = 1;
+  while (C < kMostCluster && units * C * 2 <= num_sms && a.max_seq_len / (2 * C) >= kSelectThreads) C *= 2;
+  const long long share = ceil_div_ll(std::max(a.max_seq_len, 1), C);
+  // (keys beyond 192 KB are read from memory in every pass)
+  const int cached = (int)std::min<long long>(share, 48 * 1024);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = set_smem_attrs_once(evict_select_kernel, 48 * 1024 * 4, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((units + 1) * C));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = (size_t)cached * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a, C, cached);
 }
 
 }  // namespace
@@ -423,9 +559,9 @@ pa_status pa_cache_evict(void *k_cache, void *v_cache, const float *weights, flo
   a.chunk_end = reinterpret_cast<unsigned *>(ws + lay.chunk_end);
   a.ready = reinterpret_cast<unsigned *>(ws + lay.ready);
   a.kept = reinterpret_cast<int32_t *>(ws + lay.kept);
-  if (launch_dependent(evict_select_kernel, dim3((unsigned)(num_seqs * num_kv_heads + 1)),
-                       dim3(kSelectThreads), 0, st, a) != cudaSuccess)
-    return PA_ERR_CUDA;
+  a.kept_w = reinterpret_cast<float *>(ws + lay.kept_w);
+  a.below = reinterpret_cast<int32_t *>(ws + lay.below);
+  if (launch_select(a, num_sms, st) != cudaSuccess) return PA_ERR_CUDA;
   if (num_seqs == 0) return PA_OK;
   const long long most = (long long)num_seqs * num_kv_heads * lay.max_chunks;
   const long long blocks = std::min<long long>(most, 8ll * num_sms);
