@@ -19,7 +19,7 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 1024;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMoveThreads = 256;
 constexpr int kMovePieces = 4;  // 16-byte pieces of K, and of V, that a thread copies
@@ -41,6 +41,7 @@ struct EvictArgs {
   int num_seqs, num_kv_heads, head_bytes, block_size, max_blocks_per_seq, num_blocks, max_seq_len, hnd;
   int chunk_rows;   // positions of a chunk
   int max_chunks;   // of one (request, KV head)
+  FastDiv by_bs, by_ppr, by_rows;
   unsigned int *status;
   EvictHeader *head;
   unsigned *chunk_end;  // [num_seqs] inclusive sum of the requests' chunks
@@ -68,37 +69,38 @@ __device__ inline uint32_t order_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr uint32_t kZeroKey = 0x80000000u;  // of 0 and of -0
+// The weight of a key, bit for bit, unless it is 0 (a NaN) or kZeroKey.
+__device__ inline float weight_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
 // ---------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------
 // A cluster of C blocks for each (request, KV head), each with its share of the
-// positions, whose keys (an integer that orders as the weight does) it reads once
-// into shared memory.  Counts are summed over the cluster through distributed shared
-// memory.  What bounds it is a chain of about ten barriers and the counting's
-// atomics: few positions a block matter more than many blocks.
+// positions, whose weights it reads once, as keys in shared memory.  Three passes
+// over them count the keys' leading bits, a fourth lists what is kept; counts are summed
+// over the cluster through distributed shared memory.
+
+constexpr int kMostCluster = 8;
 
 struct SelectShared {
   alignas(16) unsigned hist[kBins];
-  unsigned count[2];  // of this block's share: kept for sure, equal to the threshold
+  unsigned count[2 * kMostCluster];  // of each block's share: kept for sure, then equal to the threshold
   unsigned prefix, rank;
-  unsigned warp_sum[2][kSelectThreads / 32];
+  unsigned slice[kMostCluster];
+  unsigned warp_sum[2][32];
   long long scratch[33];
 };
-
-constexpr int kMostCluster = 8;
 
 __device__ inline unsigned load_cluster(const unsigned *p, unsigned rank) {
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(smem_u32(p), rank)) : "memory");
   return v;
 }
-__device__ inline uint4 load_cluster4(const unsigned *p, unsigned rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(cluster_map(smem_u32(p), rank))
-               : "memory");
-  return v;
+__device__ inline void store_cluster(unsigned *p, unsigned rank, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_u32(p), rank)), "r"(v) : "memory");
 }
 
 // Inclusive sum over the block's threads, one barrier; `turn` alternates between
@@ -112,19 +114,24 @@ __device__ inline unsigned select_scan(SelectShared &sh, unsigned v, int turn, u
   }
   if (lane == 31) sh.warp_sum[turn & 1][warp] = v;
   __syncthreads();
-  unsigned before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    const unsigned y = sh.warp_sum[turn & 1][w];
-    if (w < warp) before += y;
-    total += y;
-  }
-  return before + v;
+  static_assert(kSelectThreads == 1024, "a warp's sum for each lane");
+  const unsigned y = sh.warp_sum[turn & 1][lane];
+  total = __reduce_add_sync(0xffffffffu, y);
+  return v + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0u);
 }
 
-// cached: keys that the dynamic shared memory holds (the others are read again)
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a, int C, int cached) {
+// The weight of one position (NaN on a bad page), where it is not in shared memory.
+__device__ __noinline__ float read_weight(const EvictArgs &a, const int32_t *bt, int h, int pos) {
+  const int lp = divide(pos, a.by_bs), page = __ldg(bt + lp);
+  if (page < 0 || page >= a.num_blocks) {
+    atomicOr(a.status, PA_DEV_BAD_BLOCK);
+    return __int_as_float(0x7fc00000);
+  }
+  return __ldg(a.weights + ((long long)page * a.num_kv_heads + h) * a.block_size + (pos - lp * a.block_size));
+}
+
+// cached: keys that the dynamic shared memory holds (the others are made again)
+__global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, int C, int cached) {
   extern __shared__ uint32_t s_key[];
   __shared__ SelectShared sh;
   const int tid = threadIdx.x, Hk = a.num_kv_heads, bs = a.block_size;
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   if (flags) return;  // (the last cluster reports it; the same for the whole cluster)
   const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
   auto slot_of = [&](int pos) -> long long {  // of a weight; -1: a bad page
-    const int lp = (unsigned)pos / (unsigned)bs, page = __ldg(bt + lp);
+    const int lp = divide(pos, a.by_bs), page = __ldg(bt + lp);
     if (page < 0 || page >= a.num_blocks) {
       flags |= PA_DEV_BAD_BLOCK;
       return -1;
@@ -190,123 +197,165 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   for (int c = part * kSelectThreads + tid; c < (after + a.chunk_rows - 1) / a.chunk_rows; c += C * kSelectThreads)
     a.ready[(size_t)unit * a.max_chunks + c] = 0;
   const int share = (len + C - 1) / C, p0 = min(part * share, len), p1 = min(p0 + share, len);
-  auto read_key = [&](int pos) {
-    const long long at = slot_of(pos);
-    return at < 0 ? 0u : order_of(a.weights[at]);
-  };
-  auto key_of = [&](int pos) { return pos - p0 < cached ? s_key[pos - p0] : read_key(pos); };
-#pragma unroll 4
-  for (int i = tid; i < min(p1 - p0, cached); i += kSelectThreads) s_key[i] = read_key(p0 + i);
+  // (a position on a bad page counts as NaN)
+  auto read = [&](int pos) { return read_weight(a, bt, h, pos); };
+  const int c1 = min(p1, p0 + cached);  // positions below it are in shared memory
+  for (int b = tid; b < kBins; b += kSelectThreads) sh.hist[b] = 0;
+  {
+    // two latencies for several of them: the pages, then the weights
+    constexpr int U = 8;
+    for (int base = p0 + tid; base < c1; base += U * kSelectThreads) {
+      int page[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int pos = base + u * kSelectThreads;
+        page[u] = pos < c1 ? __ldg(bt + divide(pos, a.by_bs)) : 0;
+      }
+      float w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int pos = base + u * kSelectThreads;
+        const bool ok = page[u] >= 0 && page[u] < a.num_blocks;
+        w[u] = __int_as_float(0x7fc00000);
+        if (!ok) flags |= PA_DEV_BAD_BLOCK;
+        else if (pos < c1)
+          w[u] = __ldg(a.weights + ((long long)page[u] * Hk + h) * bs + (pos - divide(pos, a.by_bs) * bs));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int pos = base + u * kSelectThreads;
+        if (pos < c1) s_key[pos - p0] = order_of(w[u]);
+      }
+    }
+    __syncthreads();
+  }
+  auto key_of = [&](int pos) { return pos < c1 ? s_key[pos - p0] : order_of(read(pos)); };
 
   // -- the candidate of rank `need` from the top: `prefix` its leading bits
+  // (once a bin is kept as a whole the passes end: prefix is then below all of it, and
+  // no equal ones are wanted)
   unsigned prefix = 0, rank = need;
-  if (need > 0) {
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1 << 10 : kBins;
-      for (int b = tid; b < kBins; b += kSelectThreads) sh.hist[b] = 0;
-      __syncthreads();
-      const unsigned above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
+  for (int pass = 0; rank > 0 && pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1 << 10 : kBins;
+    const unsigned above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
+    auto count = [&](uint32_t key) {
+      if ((key & above) == prefix) atomicAdd(&sh.hist[(key >> shift) & (bins - 1)], 1u);
+    };
+    int pos = max(p0, lo) + tid;
 #pragma unroll 4
-      for (int pos = max(p0, lo) + tid; pos < min(p1, hi); pos += kSelectThreads) {
-        const uint32_t key = key_of(pos);
-        if ((key & above) == prefix) atomicAdd(&sh.hist[(key >> shift) & (bins - 1)], 1u);
-      }
-      if (C > 1) cluster_sync_all();
-      else __syncthreads();
-      // bins from the top: thread t takes the t-th group of four
-      static_assert(kBins == 4 * kSelectThreads, "four bins a thread");
-      const int low = kBins - 4 - tid * 4;
-      unsigned cnt[4] = {0, 0, 0, 0}, tot;  // [0] is the lowest bin
-      if (C > 1) {
-        uint4 v[kMostCluster];
+    for (; pos < min(c1, hi); pos += kSelectThreads) count(s_key[pos - p0]);
+    for (; pos < min(p1, hi); pos += kSelectThreads) count(order_of(read(pos)));
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+    // bins from the top: thread t takes the t-th pair
+    static_assert(kBins == 2 * kSelectThreads, "two bins a thread");
+    const int low = kBins - 2 - tid * 2;
+    const uint2 own = *reinterpret_cast<const uint2 *>(&sh.hist[low]);
+    unsigned tot;
+    if (C > 1) {
+      // block k sums its slice of the bins over the cluster; the slices' sums, given
+      // to all, say in whose slice the rank lies, and that block finds the bin
+      const int width = kBins / C, s0 = kBins - (part + 1) * width;  // slices from the top too
+      unsigned n = 0, v[kMostCluster];
+      const int mine = s0 + width - 1 - tid;  // thread t: the t-th bin from the slice's top
+      if (tid < width) {
 #pragma unroll
-        for (int k = 0; k < kMostCluster; ++k) v[k] = k < C ? load_cluster4(&sh.hist[low], k) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < kMostCluster; ++k) v[k] = k < C ? load_cluster(&sh.hist[mine], k) : 0u;
 #pragma unroll
-        for (int k = 0; k < kMostCluster; ++k) cnt[0] += v[k].x, cnt[1] += v[k].y, cnt[2] += v[k].z, cnt[3] += v[k].w;
-      } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(&sh.hist[low]);
-        cnt[0] = v.x, cnt[1] = v.y, cnt[2] = v.z, cnt[3] = v.w;
+        for (int k = 0; k < kMostCluster; ++k) n += v[k];
       }
-      const unsigned n = cnt[0] + cnt[1] + cnt[2] + cnt[3], end = select_scan(sh, n, pass, tot);
+      const unsigned end = select_scan(sh, n, pass, tot);
+      if (tid < C) store_cluster(&sh.slice[part], tid, tot);
+      cluster_sync_all();
       unsigned before = end - n;
-      if (before < rank && rank <= end) {  // one thread
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          if (before < rank && before + cnt[i] >= rank) {
-            sh.prefix = prefix | (unsigned)(low + i) << shift;
-            sh.rank = rank - before;
-          }
-          before += cnt[i];
+      for (int k = 0; k < part; ++k) before += sh.slice[k];
+      if (tid < width && before < rank && rank <= before + n) {  // one thread of the cluster
+        const unsigned bin = prefix | (unsigned)mine << shift;
+        const bool whole = n == rank - before && bin != 0;
+        for (int k = 0; k < C; ++k) {
+          store_cluster(&sh.prefix, k, bin - whole);
+          store_cluster(&sh.rank, k, whole ? 0u : rank - before);
         }
       }
-      if (C > 1) cluster_sync_all();  // (the counts are read)
-      else __syncthreads();
-      prefix = sh.prefix;
-      rank = sh.rank;
+      cluster_sync_all();
+    } else {
+      const unsigned n = own.x + own.y, end = select_scan(sh, n, pass, tot), before = end - n;
+      if (before < rank && rank <= end) {  // one thread
+        const bool high = before + own.y >= rank;
+        const unsigned bin = prefix | (unsigned)(low + high) << shift;
+        const unsigned left = high ? rank - before : rank - before - own.y;
+        const bool whole = left == (high ? own.y : own.x) && bin != 0;
+        sh.prefix = bin - whole;
+        sh.rank = whole ? 0u : left;
+      }
+      __syncthreads();
     }
+    prefix = sh.prefix;
+    rank = sh.rank;
+    sh.hist[low] = sh.hist[low + 1] = 0;
+    __syncthreads();
   }
   auto state_of = [&](int pos, uint32_t key) {  // 0 no, 1 kept, 2 equal to the threshold
     return pos < lo || pos >= hi ? 1 : need == 0 ? 0 : key > prefix ? 1 : key == prefix ? 2 : 0;
   };
-  // -- how many are kept in the shares before this one
-  unsigned sure_before = 0, equal_before = 0;
+  // -- how many of either kind lie before each warp's stretch of the share
+  const int lane = tid & 31, warp = tid >> 5;
+  const int stretch = (p1 - p0 + kSelectThreads - 1) / kSelectThreads * 32;
+  const int w0 = min(p0 + warp * stretch, p1), w1 = min(w0 + stretch, p1);
+  unsigned sure = 0, equal = 0;
+#pragma unroll 4
+  for (int pos = w0 + lane; pos < w1; pos += 32) {
+    const int st = state_of(pos, key_of(pos));
+    sure += st == 1;
+    equal += st == 2;
+  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    sh.warp_sum[0][warp] = sure;
+    sh.warp_sum[1][warp] = equal;
+  }
+  __syncthreads();
+  const unsigned ws = sh.warp_sum[0][lane], we = sh.warp_sum[1][lane];
+  unsigned sure_before = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0u);
+  unsigned equal_before = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
   if (C > 1) {
-    unsigned sure = 0, equal = 0;
-    for (int pos = p0 + tid; pos < p1; pos += kSelectThreads) {
-      const int st = state_of(pos, key_of(pos));
-      sure += st == 1;
-      equal += st == 2;
-    }
-    if (tid < 2) sh.count[tid] = 0;
-    __syncthreads();
-    sure = __reduce_add_sync(0xffffffffu, sure);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if ((tid & 31) == 0) {
-      atomicAdd(&sh.count[0], sure);
-      atomicAdd(&sh.count[1], equal);
-    }
-    cluster_sync_all();
-#pragma unroll
-    for (int k = 0; k < kMostCluster; ++k) {
-      if (k < part) {
-        sure_before += load_cluster(&sh.count[0], k);
-        equal_before += load_cluster(&sh.count[1], k);
+    if (warp == 0) {
+      const unsigned ts = __reduce_add_sync(0xffffffffu, ws), te = __reduce_add_sync(0xffffffffu, we);
+      if (lane < C) {
+        store_cluster(&sh.count[part], lane, ts);
+        store_cluster(&sh.count[kMostCluster + part], lane, te);
       }
     }
-    cluster_sync_all();  // (no block leaves while its counts are read)
+    cluster_sync_all();
+    for (int k = 0; k < part; ++k) {
+      sure_before += sh.count[k];
+      equal_before += sh.count[kMostCluster + k];
+    }
   }
   // -- the kept positions in order: the first `rank` of those that equal the threshold
   int32_t *kept = a.kept + (size_t)unit * a.max_seq_len;
   float *kept_w = a.kept_w + (size_t)unit * a.max_seq_len;
   int32_t *below = a.below + (size_t)unit * a.max_chunks;
-  constexpr int PER = 4;
-  int turn = 1;
-  for (int base = p0; base < p1; base += kSelectThreads * PER, ++turn) {
-    int state[PER];
-    unsigned n = 0, tot;  // kept for sure in the low half, equal ones in the high half: 2048 at most
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int pos = base + tid * PER + i;
-      state[i] = pos < p1 ? state_of(pos, key_of(pos)) : 0;
-      n += state[i] == 1 ? 1u : state[i] == 2 ? 1u << 16 : 0u;
+  const unsigned under = (1u << lane) - 1;
+  for (int base = w0; base < w1; base += 32) {
+    const int pos = base + lane;
+    const uint32_t key = pos < w1 ? key_of(pos) : 0u;
+    const int st = pos < w1 ? state_of(pos, key) : 0;
+    const unsigned b1 = __ballot_sync(0xffffffffu, st == 1), b2 = __ballot_sync(0xffffffffu, st == 2);
+    const unsigned eq = equal_before + __popc(b2 & under);
+    const int dst = (int)(sure_before + __popc(b1 & under) + min(eq, rank));  // kept ones below pos
+    if (pos < w1 && pos < after) {
+      const int c = divide(pos, a.by_rows);
+      if (c * a.chunk_rows == pos) below[c] = dst;
     }
-    unsigned at = select_scan(sh, n, turn, tot) - n;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int pos = base + tid * PER + i;
-      const unsigned equal = equal_before + (at >> 16);
-      const int dst = (int)(sure_before + (at & 0xffff) + min(equal, rank));  // kept ones below pos
-      if (pos < p1 && pos < after && pos % a.chunk_rows == 0) below[pos / a.chunk_rows] = dst;
-      if (state[i] == 1 || (state[i] == 2 && equal < rank)) {
-        const long long from = slot_of(pos);
-        kept[dst] = pos;
-        if (from >= 0) kept_w[dst] = a.weights[from];
-      }
-      at += state[i] == 1 ? 1u : state[i] == 2 ? 1u << 16 : 0u;
+    if (st == 1 || (st == 2 && eq < rank)) {
+      kept[dst] = pos;
+      kept_w[dst] = key == 0u || key == kZeroKey ? read(pos) : weight_of(key);
     }
-    sure_before += tot & 0xffff;
-    equal_before += tot >> 16;
+    sure_before += __popc(b1);
+    equal_before += __popc(b2);
   }
   if (flags) atomicOr(a.status, flags);
 }
@@ -342,11 +391,11 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     int lo = 0, hi = a.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (a.chunk_end[mid] > t) hi = mid; else lo = mid + 1;
+      if (__ldg(a.chunk_end + mid) > t) hi = mid; else lo = mid + 1;
     }
-    const int s = lo, len = a.seq_lens[s], after = min(len, a.keep_lens[s]);
-    const int nc = (after + a.chunk_rows - 1) / a.chunk_rows;
-    const int local = (int)(t - (a.chunk_end[s] - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
+    const int s = lo, after = min(__ldg(a.seq_lens + s), __ldg(a.keep_lens + s));
+    const int nc = divide(after + a.chunk_rows - 1, a.by_rows);
+    const int local = (int)(t - (__ldg(a.chunk_end + s) - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
     const int unit = s * Hk + h;
     const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
     const int32_t *kept = a.kept + (size_t)unit * a.max_seq_len;
@@ -357,19 +406,19 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     unsigned flags = 0;
 #pragma unroll
     for (int u = 0; u < kMovePieces; ++u) {
-      const int e = u * kMoveThreads + tid, row = (unsigned)e / (unsigned)ppr, piece = e - row * ppr;
+      const int e = u * kMoveThreads + tid, row = divide(e, a.by_ppr), piece = e - row * ppr;
       if (row >= rows) continue;
       const int src = __ldg(kept + i0 + row);
       if (src == i0 + row) continue;
-      const long long from = row_offset(bt, src, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
+      const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
       if (from < 0) continue;
       copy16(s_k + e, a.k_cache + from + piece * 16);
       copy16(s_v + e, a.v_cache + from + piece * 16);
     }
     // -- meanwhile its weights (select has read them all)
     for (int i = i0 + tid; i < i0 + rows; i += kMoveThreads) {
-      const int from = __ldg(kept + i), page = __ldg(bt + (unsigned)from / (unsigned)bs),
-                lp = (unsigned)i / (unsigned)bs, into = __ldg(bt + lp);
+      const int from = __ldg(kept + i), page = __ldg(bt + divide(from, a.by_bs)),
+                lp = divide(i, a.by_bs), into = __ldg(bt + lp);
       if (page >= 0 && page < a.num_blocks && into >= 0 && into < a.num_blocks)
         a.weights_out[((long long)into * Hk + h) * bs + (i - lp * bs)] = a.kept_w[(size_t)unit * a.max_seq_len + i];
     }
@@ -383,7 +432,7 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     // positions from i0 on, from the first one's chunk on; they were handed out
     // before this one, and mark their rows read without waiting for anything
     bool late = false;
-    for (int w = below / a.chunk_rows + tid; w < c; w += kMoveThreads) {
+    for (int w = divide(below, a.by_rows) + tid; w < c; w += kMoveThreads) {
       if (load_acquire(ready + w)) continue;
       const uint64_t t0 = global_timer_ns();
       for (uint32_t i = 1; !load_acquire(ready + w); ++i) {
@@ -398,12 +447,12 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     if (!__syncthreads_or(late)) {
 #pragma unroll
       for (int u = 0; u < kMovePieces; ++u) {
-        const int e = u * kMoveThreads + tid, row = (unsigned)e / (unsigned)ppr, piece = e - row * ppr;
+        const int e = u * kMoveThreads + tid, row = divide(e, a.by_ppr), piece = e - row * ppr;
         if (row >= rows) continue;
         const int src = __ldg(kept + i0 + row);
         if (src == i0 + row) continue;
-        const long long from = row_offset(bt, src, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
-        const long long into = row_offset(bt, i0 + row, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
+        const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
+        const long long into = row_offset(bt, i0 + row, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
         if (from < 0 || into < 0) {
           flags |= PA_DEV_BAD_BLOCK;
           continue;
@@ -553,6 +602,9 @@ pa_status pa_cache_evict(void *k_cache, void *v_cache, const float *weights, flo
   a.num_blocks = num_blocks;
   a.max_seq_len = max_seq_len;
   a.hnd = kv_layout == PA_KV_HND;
+  a.by_bs = fast_div(block_size);
+  a.by_ppr = fast_div(a.head_bytes / 16);
+  a.by_rows = fast_div(lay.chunk_rows);
   a.chunk_rows = lay.chunk_rows;
   a.max_chunks = lay.max_chunks;
   a.head = reinterpret_cast<EvictHeader *>(ws + lay.head);

@@ -100,6 +100,7 @@ struct AcceptArgs {
   FreeList free;
   int num_seqs, num_tokens, max_path, num_kv_heads, head_bytes, block_size, max_blocks_per_seq,
       num_blocks, hnd;
+  FastDiv by_bs, by_ppr;
   unsigned int *status;
 };
 
@@ -141,10 +142,10 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
         const int e = e0 + u * 32 + lane;
         to[u] = -1;
         if (e >= total) continue;
-        const int i = e / ppr, c = e - i * ppr, from = __ldg(path + i);
+        const int i = divide(e, a.by_ppr), c = e - i * ppr, from = __ldg(path + i);
         if (from == i) continue;
-        const long long src = row_offset(bt, prefix + from, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
-        const long long dst = row_offset(bt, prefix + i, h, Hk, bs, a.num_blocks, a.hnd, a.head_bytes);
+        const long long src = row_offset(bt, prefix + from, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
+        const long long dst = row_offset(bt, prefix + i, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
         if (src < 0 || dst < 0) {
           flags |= PA_DEV_BAD_BLOCK;
           continue;
@@ -280,6 +281,8 @@ extern "C" pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.hnd = kv_layout == PA_KV_HND;
+  a.by_bs = fast_div(block_size);
+  a.by_ppr = fast_div(a.head_bytes / 16);
   const long long warps = (long long)num_seqs * num_kv_heads;
   const long long blocks = std::min<long long>(ceil_div_ll(warps, kAcceptThreads / 32) + 1, 8ll * num_sms);
   return launch_dependent(accept_kernel, dim3((unsigned)blocks), dim3(kAcceptThreads), 0, st, a) ==
