@@ -29,23 +29,16 @@ struct FreeList {
   int capacity;
 };
 
+// Index of KV head h's row in slot `slot` of a page.
+__device__ inline long long row_at(int page, int slot, int h, int Hk, int bs, int hnd) {
+  return hnd ? ((long long)page * Hk + h) * bs + slot : ((long long)page * bs + slot) * Hk + h;
+}
 // Byte offset of KV head h's row at position pos; -1 where the page id is bad.
 __device__ inline long long row_offset(const int32_t *bt, int pos, int h, int Hk, int bs, FastDiv by_bs,
                                        int num_blocks, int hnd, int head_bytes) {
   const int lp = divide(pos, by_bs), slot = pos - lp * bs, page = __ldg(bt + lp);
   if (page < 0 || page >= num_blocks) return -1;
-  const long long row = hnd ? ((long long)page * Hk + h) * bs + slot : ((long long)page * bs + slot) * Hk + h;
-  return row * head_bytes;
-}
-
-// Whether path[0 .. n) rises strictly within [0, q_len).  A whole warp calls.
-__device__ inline bool path_ok(const int32_t *path, int n, int q_len, int lane) {
-  bool ok = true;
-  for (int i = lane; i < n; i += 32) {
-    const int x = __ldg(path + i), last = i > 0 ? __ldg(path + i - 1) : -1;
-    ok &= x > last && x < q_len;
-  }
-  return __all_sync(0xffffffffu, ok);
+  return row_at(page, slot, h, Hk, bs, hnd) * head_bytes;
 }
 
 // One block (all THREADS threads of it): lens(s, before, after) for every request,
@@ -56,12 +49,13 @@ __device__ inline void list_free_pages(const FreeList &list, const int32_t *bloc
                                        int max_blocks_per_seq, int bs, int num_blocks, int num_seqs,
                                        unsigned int *status, Lens lens) {
   __shared__ long long scratch[33];
-  __shared__ int s_first[THREADS], s_n[THREADS], s_page[THREADS];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ long long s_end[THREADS];
+  __shared__ int s_n[THREADS], s_page[THREADS];
+  const int tid = threadIdx.x;
   long long sum = 0;
   unsigned flags = 0;
   for (int base = 0; base < num_seqs; base += THREADS) {
-    const int s = base + tid;
+    const int s = base + tid, in = min(THREADS, num_seqs - base);
     int from = 0, n = 0;
     if (s < num_seqs) {
       int before, after;
@@ -73,29 +67,32 @@ __device__ inline void list_free_pages(const FreeList &list, const int32_t *bloc
     }
     if (!list.count) continue;
     long long tot;
-    const long long at = block_inclusive_scan(n, scratch, &tot) + sum - n;
-    // (counts fit 32 bits where they fit the list; beyond it nothing is written)
-    s_first[tid] = (int)min(at, 0x7fffffffll);
+    s_end[tid] = block_inclusive_scan(n, scratch, &tot);
     s_n[tid] = n;
     s_page[tid] = from;
     __syncthreads();
-    for (int k = warp; k < min(THREADS, num_seqs - base); k += THREADS / 32) {
-      const int32_t *bt = block_table + (size_t)(base + k) * max_blocks_per_seq;
-      for (int i = lane; i < s_n[k]; i += 32) {
-        int page = __ldg(bt + s_page[k] + i);
-        if (page < 0 || page >= num_blocks) {
-          page = -1;
-          flags |= PA_DEV_BAD_BLOCK;
-        }
-        const long long to = (long long)s_first[k] + i;
-        if (to < list.capacity) list.pages[to] = page;
-        else flags |= PA_DEV_OVERFLOW;
+    // an entry a thread, all of their loads on their way at once
+    for (long long e = tid; e < min(tot, list.capacity - sum); e += THREADS) {
+      int lo = 0, hi = in - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_end[mid] > e) hi = mid; else lo = mid + 1;
       }
+      const int i = (int)(e - (s_end[lo] - s_n[lo]));
+      int page = __ldg(block_table + (size_t)(base + lo) * max_blocks_per_seq + s_page[lo] + i);
+      if (page < 0 || page >= num_blocks) {
+        page = -1;
+        flags |= PA_DEV_BAD_BLOCK;
+      }
+      list.pages[sum + e] = page;
     }
     sum += tot;
     __syncthreads();  // the shared arrays are read
   }
-  if (list.count && tid == 0) *list.count = (int)min(sum, (long long)list.capacity);
+  if (list.count && tid == 0) {
+    *list.count = (int)min(sum, (long long)list.capacity);
+    if (sum > list.capacity) flags |= PA_DEV_OVERFLOW;
+  }
   if (flags) atomicOr(status, flags);
 }
 

@@ -14,21 +14,36 @@ bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 // pa_tree_masks
 // ---------------------------------------------------------------------------
 // Token i of a request has parent p(i) < i among the request's new tokens, or -1.
-// Its mask is its own bit and those on the chain p(i), p(p(i)), ... to the root,
-// its depth the chain's length.  The chain only goes down, so a thread writes its
-// row's words from the top one to the bottom one as it goes.
-constexpr int kMaskThreads = 128;
+// Its mask is its own bit and those on the chain p(i), p(p(i)), ... to the root, its
+// depth their number.  Chains are followed by doubling: with m(i) the bits of i and
+// its next 2^k - 1 ancestors and u(i) the ancestor behind those,
+//   m(i) |= m(u(i)),  u(i) = u(u(i)),
+// so a chain of 250 takes 8 steps instead of 250 loads one behind the other.  A
+// request of up to 32 tokens is a warp's (shuffles), one of up to kMaskTokens a
+// block's (shared memory); beyond that a thread walks its token's chain, which only
+// goes down, and writes its row's words from the top one to the bottom one.
+constexpr int kMaskThreads = 256, kMaskTokens = 256, kMaskWords = kMaskTokens / 64;
 
 struct MaskArgs {
   const int32_t *parents, *qsl, *seq_lens;
   unsigned long long *mask;
   int32_t *positions;
-  int num_seqs, num_tokens, words;
+  int num_seqs, num_tokens, words, per_block;  // requests of a block
   unsigned int *status;
 };
 
+// What u(i) ends at: the root, or a parent that is none.
+constexpr int kRoot = -1, kBadParent = -2;
+
+__device__ inline int parent_of(const MaskArgs &a, int q0, int i) {
+  const int up = __ldg(a.parents + q0 + i);
+  return up >= i || up < -1 ? kBadParent : up;
+}
+
 __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs a) {
-  const int S = a.num_seqs, T = a.num_tokens, tid = threadIdx.x;
+  __shared__ unsigned long long s_mask[2][kMaskTokens][kMaskWords];
+  __shared__ int s_up[2][kMaskTokens];
+  const int S = a.num_seqs, T = a.num_tokens, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
   int bad = 0;
@@ -38,48 +53,114 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
   }
   bad = __syncthreads_or(bad);
   if (bad && blockIdx.x == 0 && tid == 0) atomicOr(a.status, PA_DEV_BAD_QSL);
-  for (long long t64 = (long long)blockIdx.x * kMaskThreads + tid; t64 < T;
-       t64 += (long long)gridDim.x * kMaskThreads) {
-    const int t = (int)t64;
-    unsigned long long *row = a.mask + (size_t)t * a.words;
-    int w = a.words - 1, position = 0;  // the highest word not yet written
-    unsigned flags = 0;
-    if (!bad && S > 0 && t < a.qsl[S]) {
-      int lo = 0, hi = S - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.qsl[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      const int q0 = a.qsl[lo], q_len = a.qsl[lo + 1] - q0, i = t - q0;
-      const int len = a.seq_lens ? a.seq_lens[lo] : q_len;
-      if (len < 0) flags |= PA_DEV_BAD_SEQLEN;
-      else if (q_len > len || q_len > 64ll * a.words) flags |= PA_DEV_BAD_QLEN;
-      if (!flags) {
-        int depth = 0, node = i;
-        unsigned long long bits = 0;
-        for (;;) {
-          for (; w > node >> 6; --w) {
-            row[w] = bits;
-            bits = 0;
+  // -- rows that belong to no request, or all of them
+  const long long n = bad || S == 0 ? 0 : a.qsl[S];
+  for (long long e = n * a.words + blockIdx.x * kMaskThreads + tid; e < (long long)T * a.words;
+       e += (long long)gridDim.x * kMaskThreads)
+    a.mask[e] = 0;
+  if (a.positions)
+    for (long long t = n + blockIdx.x * kMaskThreads + tid; t < T; t += (long long)gridDim.x * kMaskThreads)
+      a.positions[t] = 0;
+  if (bad) return;
+
+  for (int base = blockIdx.x * a.per_block; base < S; base += gridDim.x * a.per_block) {
+    for (int k = 0; k < min(a.per_block, S - base); ++k) {
+      const int s = base + k, q0 = a.qsl[s], q_len = a.qsl[s + 1] - q0;
+      if (q_len == 0 || (q_len <= 32 && k % (kMaskThreads / 32) != warp)) continue;
+      const int len = a.seq_lens ? a.seq_lens[s] : q_len;
+      unsigned flags = len < 0 ? PA_DEV_BAD_SEQLEN : q_len > len || q_len > 64ll * a.words ? PA_DEV_BAD_QLEN : 0;
+      unsigned long long *rows = a.mask + (size_t)q0 * a.words;
+      auto finish = [&](int i, bool good, int ancestors) {
+        if (a.positions) a.positions[q0 + i] = good ? len - q_len + ancestors : 0;
+      };
+      if (flags) {  // (the same for all that are here)
+        const int from = q_len <= 32 ? lane : tid, step = q_len <= 32 ? 32 : kMaskThreads;
+        for (long long e = from; e < (long long)q_len * a.words; e += step) rows[e] = 0;
+        for (int i = from; i < q_len; i += step) finish(i, false, 0);
+      } else if (q_len <= 32) {
+        const int i = lane;
+        unsigned m = i < q_len ? 1u << i : 0u;
+        int up = i < q_len ? parent_of(a, q0, i) : kRoot;
+        if (up == kBadParent) flags = PA_DEV_BAD_TREE;
+        while (__any_sync(0xffffffffu, up >= 0)) {
+          const unsigned more = __shfl_sync(0xffffffffu, m, max(up, 0));
+          const int above = __shfl_sync(0xffffffffu, up, max(up, 0));
+          if (up >= 0) {
+            m |= more;
+            up = above;
           }
-          bits |= 1ull << (node & 63);
-          const int up = __ldg(a.parents + q0 + node);
-          if (up < -1 || up >= node) flags = PA_DEV_BAD_TREE;
-          if (flags || up < 0) break;
-          node = up;
-          ++depth;
         }
-        if (flags) {
-          w = a.words - 1;  // the whole row again, as zeros
-        } else {
-          row[w--] = bits;
-          position = len - q_len + depth;
+        if (i < q_len) {
+          const bool good = up == kRoot;
+          rows[(size_t)i * a.words] = good ? m : 0u;
+          for (int w = 1; w < a.words; ++w) rows[(size_t)i * a.words + w] = 0;
+          finish(i, good, __popc(m) - 1);
+        }
+      } else if (q_len <= kMaskTokens) {
+        const int W = (q_len + 63) >> 6;
+        __syncthreads();  // the request before is read
+        for (int i = tid; i < q_len; i += kMaskThreads) {
+          const int up = parent_of(a, q0, i);
+          if (up == kBadParent) flags = PA_DEV_BAD_TREE;
+          s_up[0][i] = up;
+#pragma unroll
+          for (int w = 0; w < kMaskWords; ++w) s_mask[0][i][w] = w == i >> 6 ? 1ull << (i & 63) : 0ull;
+        }
+        int cur = 0, more = 1;
+        while (__syncthreads_or(more)) {
+          more = 0;
+          for (int i = tid; i < q_len; i += kMaskThreads) {
+            const int up = s_up[cur][i], from = max(up, 0);
+            const int above = up >= 0 ? s_up[cur][from] : up;
+            s_up[cur ^ 1][i] = above;
+            more |= above >= 0;
+#pragma unroll
+            for (int w = 0; w < kMaskWords; ++w)
+              s_mask[cur ^ 1][i][w] = s_mask[cur][i][w] | (up >= 0 ? s_mask[cur][from][w] : 0ull);
+          }
+          cur ^= 1;
+        }
+        for (int i = tid; i < q_len; i += kMaskThreads) {
+          const bool good = s_up[cur][i] == kRoot;
+          int ancestors = -1;
+          for (int w = 0; w < a.words; ++w) {
+            const unsigned long long m = w < W ? s_mask[cur][i][w] : 0ull;
+            ancestors += __popcll(m);
+            rows[(size_t)i * a.words + w] = good ? m : 0ull;
+          }
+          finish(i, good, ancestors);
+        }
+      } else {
+        for (int i = tid; i < q_len; i += kMaskThreads) {
+          unsigned long long *row = rows + (size_t)i * a.words, bits = 0;
+          int w = a.words - 1, depth = 0, node = i;  // w: the highest word not yet written
+          for (;;) {
+            for (; w > node >> 6; --w) {
+              row[w] = bits;
+              bits = 0;
+            }
+            bits |= 1ull << (node & 63);
+            const int up = parent_of(a, q0, node);
+            if (up < 0) {
+              node = up;
+              break;
+            }
+            node = up;
+            ++depth;
+          }
+          const bool good = node == kRoot;
+          if (good) {
+            row[w--] = bits;
+          } else {
+            flags = PA_DEV_BAD_TREE;
+            w = a.words - 1;  // the whole row again, as zeros
+          }
+          for (; w >= 0; --w) row[w] = 0;
+          finish(i, good, depth);
         }
       }
+      if (flags) atomicOr(a.status, flags);
     }
-    for (; w >= 0; --w) row[w] = 0;
-    if (a.positions) a.positions[t] = position;
-    if (flags) atomicOr(a.status, flags);
   }
 }
 
@@ -87,11 +168,12 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
 // pa_cache_accept
 // ---------------------------------------------------------------------------
 // Row prefix + path[k] of every KV head goes to prefix + k <= prefix + path[k],
-// in place.  A warp takes one KV head of a request and walks its path upwards,
-// some rows at a time, all of them read before the first is written; what a step
-// writes lies below everything that later steps read.  Block 0 lists the pages.
-constexpr int kAcceptThreads = 256;
-constexpr int kAcceptPieces = 4;  // 16-byte pieces of K, and of V, that a lane has in flight
+// in place.  A block takes one KV head of a request and walks its path upwards, some
+// rows at a time, all of them read before the first is written; what a step writes
+// lies below everything that later steps read.  The block of KV head 0 writes the new
+// length; a second launch lists the pages from the lengths.
+constexpr int kAcceptThreads = 128;
+constexpr int kAcceptPieces = 4;  // 16-byte pieces of K, and of V, that a thread has in flight
 
 struct AcceptArgs {
   uint8_t *k_cache, *v_cache;
@@ -117,80 +199,97 @@ __device__ inline int accepted_len(const AcceptArgs &a, int s, int &prefix, int 
   return -1;
 }
 
+// Whether path[0 .. n) rises strictly within [0, q_len): this thread's share of it.
+__device__ inline bool path_rises(const int32_t *path, int n, int q_len, int tid) {
+  bool ok = true;
+  for (int i = tid; i < n; i += kAcceptThreads) {
+    const int x = __ldg(path + i), last = i > 0 ? __ldg(path + i - 1) : -1;
+    ok &= x > last && x < q_len;
+  }
+  return ok;
+}
+
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, bs = a.block_size, Hk = a.num_kv_heads, ppr = a.head_bytes / 16;  // pieces a row
   pdl_trigger();
   pdl_wait();
-  const int warps = gridDim.x * (kAcceptThreads / 32);
-  const int bs = a.block_size, Hk = a.num_kv_heads, ppr = a.head_bytes / 16;  // pieces a row
-  for (long long item = blockIdx.x * (kAcceptThreads / 32) + warp; item < (long long)a.num_seqs * Hk;
-       item += warps) {
+  unsigned bad = 0;
+  for (long long item = blockIdx.x; item < (long long)a.num_seqs * Hk; item += gridDim.x) {
     const int s = (int)(item / Hk), h = (int)(item - (long long)s * Hk);
     int prefix, n;
     unsigned flags = 0;
-    if (accepted_len(a, s, prefix, n, flags) < 0) continue;  // (block 0 reports it)
-    const int q_len = a.seq_lens[s] - prefix;
     const int32_t *path = a.path + (size_t)s * a.max_path;
-    if (!path_ok(path, n, q_len, lane)) continue;
+    int after = accepted_len(a, s, prefix, n, flags);  // (the same for all threads)
+    if (after >= 0 && !__syncthreads_and(path_rises(path, n, a.seq_lens[s] - prefix, tid))) {
+      flags = PA_DEV_BAD_TREE;
+      after = -1;
+    }
+    if (h == 0 && tid == 0) {
+      a.seq_lens_out[s] = after < 0 ? a.seq_lens[s] : after;
+      if (flags) atomicOr(a.status, flags);
+    }
+    if (after < 0) continue;
     const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
     const int total = n * ppr;
-    for (int e0 = 0; e0 < total; e0 += 32 * kAcceptPieces) {
-      uint4 k[kAcceptPieces], v[kAcceptPieces];
-      long long to[kAcceptPieces];
+    for (int e0 = 0; e0 < total; e0 += kAcceptThreads * kAcceptPieces) {
+      // (the pieces' path entries, pages and rows: three latencies for all of them)
+      int row[kAcceptPieces], from[kAcceptPieces], src[kAcceptPieces], dst[kAcceptPieces];
 #pragma unroll
       for (int u = 0; u < kAcceptPieces; ++u) {
-        const int e = e0 + u * 32 + lane;
-        to[u] = -1;
-        if (e >= total) continue;
-        const int i = divide(e, a.by_ppr), c = e - i * ppr, from = __ldg(path + i);
-        if (from == i) continue;
-        const long long src = row_offset(bt, prefix + from, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
-        const long long dst = row_offset(bt, prefix + i, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
-        if (src < 0 || dst < 0) {
-          flags |= PA_DEV_BAD_BLOCK;
+        const int e = e0 + u * kAcceptThreads + tid;
+        row[u] = divide(min(e, total - 1), a.by_ppr);
+        from[u] = __ldg(path + row[u]);
+        if (e >= total) from[u] = row[u];  // (stays where it is)
+      }
+#pragma unroll
+      for (int u = 0; u < kAcceptPieces; ++u) {
+        src[u] = __ldg(bt + divide(prefix + from[u], a.by_bs));
+        dst[u] = __ldg(bt + divide(prefix + row[u], a.by_bs));
+      }
+      uint4 k[kAcceptPieces], v[kAcceptPieces];
+#pragma unroll
+      for (int u = 0; u < kAcceptPieces; ++u) {
+        if (from[u] == row[u]) continue;
+        if (src[u] < 0 || src[u] >= a.num_blocks || dst[u] < 0 || dst[u] >= a.num_blocks) {
+          bad = PA_DEV_BAD_BLOCK;
+          from[u] = row[u];
           continue;
         }
-        to[u] = dst + c * 16;
-        k[u] = *reinterpret_cast<const uint4 *>(a.k_cache + src + c * 16);
-        v[u] = *reinterpret_cast<const uint4 *>(a.v_cache + src + c * 16);
+        const int pos = prefix + from[u], c = e0 + u * kAcceptThreads + tid - row[u] * ppr;
+        const long long at = row_at(src[u], pos - divide(pos, a.by_bs) * bs, h, Hk, bs, a.hnd) * a.head_bytes + c * 16;
+        k[u] = *reinterpret_cast<const uint4 *>(a.k_cache + at);
+        v[u] = *reinterpret_cast<const uint4 *>(a.v_cache + at);
       }
-      __syncwarp();  // all of the step's rows are read
+      // (the barrier's operand needs every loaded value: the rows are read when it opens)
+      unsigned seen = 0;
+#pragma unroll
+      for (int u = 0; u < kAcceptPieces; ++u)
+        if (from[u] != row[u]) seen ^= k[u].x ^ v[u].x;
+      __syncthreads_or(seen);
 #pragma unroll
       for (int u = 0; u < kAcceptPieces; ++u) {
-        if (to[u] < 0) continue;
-        *reinterpret_cast<uint4 *>(a.k_cache + to[u]) = k[u];
-        *reinterpret_cast<uint4 *>(a.v_cache + to[u]) = v[u];
+        if (from[u] == row[u]) continue;
+        const int pos = prefix + row[u], c = e0 + u * kAcceptThreads + tid - row[u] * ppr;
+        const long long at = row_at(dst[u], pos - divide(pos, a.by_bs) * bs, h, Hk, bs, a.hnd) * a.head_bytes + c * 16;
+        *reinterpret_cast<uint4 *>(a.k_cache + at) = k[u];
+        *reinterpret_cast<uint4 *>(a.v_cache + at) = v[u];
       }
     }
-    if (flags) atomicOr(a.status, flags);
   }
-  if (blockIdx.x != gridDim.x - 1) return;
-  // the last block: new lengths and the pages that are free again
+  if (bad) atomicOr(a.status, bad);
+}
+
+// The pages behind the new lengths: one block.
+constexpr int kFreeThreads = 512;
+__global__ void __launch_bounds__(kFreeThreads) free_pages_kernel(const AcceptArgs a) {
+  pdl_trigger();
+  pdl_wait();
   auto lens = [&](int s, int &before, int &after) {
-    int prefix, n;
-    unsigned flags = 0;
     before = a.seq_lens[s];
-    after = accepted_len(a, s, prefix, n, flags);
-    if (after >= 0) {  // (one thread, the whole path)
-      const int32_t *path = a.path + (size_t)s * a.max_path;
-      int last = -1;
-      for (int i = 0; i < n; ++i) {
-        const int x = __ldg(path + i);
-        if (x <= last || x >= before - prefix) {
-          flags |= PA_DEV_BAD_TREE;
-          break;
-        }
-        last = x;
-      }
-    }
-    if (flags) {
-      atomicOr(a.status, flags);
-      after = before;
-    }
-    a.seq_lens_out[s] = after;
+    after = a.seq_lens_out[s];
   };
-  list_free_pages<kAcceptThreads>(a.free, a.block_table, a.max_blocks_per_seq, bs, a.num_blocks,
-                                  a.num_seqs, a.status, lens);
+  list_free_pages<kFreeThreads>(a.free, a.block_table, a.max_blocks_per_seq, a.block_size, a.num_blocks,
+                                a.num_seqs, a.status, lens);
 }
 
 }  // namespace
@@ -224,7 +323,9 @@ extern "C" pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_
   a.num_seqs = num_seqs;
   a.num_tokens = num_tokens;
   a.words = mask_words;
-  const long long blocks = std::min<long long>(ceil_div_ll(num_tokens, kMaskThreads), 8ll * num_sms);
+  // A block a request, or as many as it has warps where there are that many requests.
+  a.per_block = (int)std::min<long long>(std::max<long long>(num_seqs / (4ll * num_sms), 1), kMaskThreads / 32);
+  const long long blocks = std::min<long long>(std::max<long long>(ceil_div_ll(num_seqs, a.per_block), 1), 8ll * num_sms);
   return launch_dependent(tree_masks_kernel, dim3((unsigned)blocks), dim3(kMaskThreads), 0, st, a) ==
                  cudaSuccess
              ? PA_OK
@@ -283,10 +384,12 @@ extern "C" pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t
   a.hnd = kv_layout == PA_KV_HND;
   a.by_bs = fast_div(block_size);
   a.by_ppr = fast_div(a.head_bytes / 16);
-  const long long warps = (long long)num_seqs * num_kv_heads;
-  const long long blocks = std::min<long long>(ceil_div_ll(warps, kAcceptThreads / 32) + 1, 8ll * num_sms);
-  return launch_dependent(accept_kernel, dim3((unsigned)blocks), dim3(kAcceptThreads), 0, st, a) ==
-                 cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
+  const long long blocks = std::min<long long>((long long)num_seqs * num_kv_heads, 16ll * num_sms);
+  if (blocks > 0 && launch_dependent(accept_kernel, dim3((unsigned)blocks), dim3(kAcceptThreads), 0, st, a) !=
+                        cudaSuccess)
+    return PA_ERR_CUDA;
+  if (num_freed &&
+      launch_dependent(free_pages_kernel, dim3(1), dim3(kFreeThreads), 0, st, a) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
 }
