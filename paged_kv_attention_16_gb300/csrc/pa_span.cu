@@ -62,7 +62,12 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
         r.nblk = (int)((rows + kSpanRows - 1) / kSpanRows);
         r.ntile = (r.ctx + kSpanTile - 1) / kSpanTile;
         cnt[0] = (long long)Hk * r.nblk;
-        cnt[1] = cnt[0] * (r.ntile + kSpanOverhead);
+        r.wcost = kSpanWide;
+        r.wlast = rows - (r.nblk - 1ll) * kSpanRows > 128 ? kSpanWide : span_narrow(r.nblk, f.head_dim);
+        r.ulast = r.ntile * r.wlast + kSpanOverhead;
+        r.ucost = r.nblk > 1 ? r.ntile * r.wcost + kSpanOverhead : r.ulast;
+        r.kcost = (r.nblk - 1) * r.ucost + r.ulast;
+        cnt[1] = (long long)Hk * r.kcost;
         if (p.keep_scores && rows <= kSpanStoredRows) scores = Hk * rows * r.ntile * kSpanTile;
         cnt[2] = scores;
         if (p.keep_scores && scores == 0) cnt[3] = (long long)Hk * r.ntile;
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
   SpanTileBuf<D> *s_tile = reinterpret_cast<SpanTileBuf<D> *>(s_raw);
   const FwdParams &f = p.f;
   const int tid = threadIdx.x, lane = tid & 31, c = tid & 7;
-  const int Hk = f.num_kv_heads, G = f.num_heads / Hk, bs = f.block_size;
+  const int Hk = f.num_kv_heads, G = f.num_heads / Hk, bs = f.block_size, lg = __ffs(G) - 1;
   pdl_wait();
   pdl_trigger();
   const SpanPlan plan = *p.plan;
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
   SpanCursor cur;
   cur.start(p, plan, blockIdx.x);
   SpanPiece it;
-  while (cur.next(p, G, CAUSAL, it)) {
+  while (cur.next(p, lg, CAUSAL, it)) {
     const int32_t *bt = f.block_table + (size_t)it.req * f.max_blocks_per_seq;
     const int rows = min(kSpanRows, (it.q_len - it.t0) * G), prefix = it.ctx - it.q_len;
     // (a pass of fewer rows than threads' rows holds one or two a thread)
@@ -351,11 +356,11 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
-    int h = 0, n = 0, c0 = 0, br = 0;
-    unsigned u0 = 0;
+    int h = 0, n = 0, c0 = 0, br = 0, w = 1, blk_end = 0;
+    unsigned u0 = 0, len = 0;
     long long unit = 0;
     SpanReq r{};
-    int blk_end = 0;
+    bool pairs = false;
     bool mine = row < rows;  // (not a row behind the last request)
     if (mine && !plan.all_bad) {
       const int tok = (int)(row / H);
@@ -369,19 +374,30 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
       const int i = tok - r.q_start;
       mine = i < r.q_len;
       if (mine && r.valid) {
-        const int tq = kSpanRows / G, b = i / tq, local = h / G * r.nblk + b;
+        const int tq = kSpanRows / G, b = i / tq, kvh = h / G;
+        const bool last = b == r.nblk - 1;
         br = (i - b * tq) * G + h % G;
-        unit = (long long)r.unit0 + local;
-        const unsigned len = r.ntile + kSpanOverhead;
-        u0 = r.cost0 + (unsigned)local * len;
+        unit = (long long)r.unit0 + kvh * r.nblk + b;
+        u0 = r.cost0 + (unsigned)kvh * r.kcost + (unsigned)b * r.ucost;
+        len = last ? r.ulast : r.ucost;
+        w = last ? r.wlast : r.wcost;
         c0 = (int)(u0 / plan.run);
         blk_end = span_block_end(r, b * tq, tq, CAUSAL);
-        n = ((int)((u0 + len - 1) / plan.run) - c0 + 1) * (p.halves ? 2 : 1);
+        n = (int)((u0 + len - 1) / plan.run) - c0 + 1;
         // a unit of more than 128 rows has one partial a piece, in the row's own place
-        if (p.halves && (r.q_len - b * tq) * G > 128) n /= 2;
+        pairs = p.halves && (r.q_len - b * tq) * G <= 128;
+        if (p.halves && !pairs) {
+          // in one piece it is finished already (pieces before it may have no tile)
+          for (int c = c0; c < c0 + n; ++c) {
+            const int t1 = span_tile_at(r, min(u0 + len, (unsigned)(c + 1) * plan.run) - u0, w);
+            if (t1 == r.ntile) mine = false;
+            if (t1 > 0) break;
+          }
+          if (!mine) n = 0;
+        }
+        if (pairs) n *= 2;
       }
     }
-    const bool pairs = p.halves && n > 0 && n == 2 * ((int)((u0 + r.ntile + kSpanOverhead - 1) / plan.run) - c0 + 1);
     for (int e0 = part; e0 < n; e0 += 4 * W) {
       float lse[4];
       float4 x[4][V];
@@ -392,9 +408,8 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
         if (e >= n) continue;
         const int c = c0 + (pairs ? e >> 1 : e), half = pairs ? e & 1 : 0;
         // the piece's tiles (it may have none: the overhead alone, or behind the causal end)
-        const unsigned from = max(u0, (unsigned)c * plan.run);
-        const unsigned to = min(u0 + r.ntile + kSpanOverhead, (unsigned)(c + 1) * plan.run);
-        const int t0 = span_tile_at(r, from - u0), t1 = span_tile_at(r, to - u0);
+        const unsigned from = max(u0, (unsigned)c * plan.run), to = min(u0 + len, (unsigned)(c + 1) * plan.run);
+        const int t0 = span_tile_at(r, from - u0, w), t1 = span_tile_at(r, to - u0, w);
         if (min(t1 * kSpanTile, blk_end) <= (t0 + half) * kSpanTile) continue;
         const long long at = span_row(p, unit + c, half, br);
         lse[u] = __ldcg(p.part_lse + at);
@@ -410,16 +425,16 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
         const float top = max_nan(m, lse[u]);
         // (equal infinities: a bad page, which m tells)
         const float a = m == -INFINITY || m == top ? (m == top ? 1.f : 0.f) : fast_exp2(m - top);
-        const float w = lse[u] == top ? 1.f : fast_exp2(lse[u] - top);
+        const float wt = lse[u] == top ? 1.f : fast_exp2(lse[u] - top);
         m = top;
-        l = fmaf(l, a, w);
+        l = fmaf(l, a, wt);
         if constexpr (VALUES) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            acc[v].x = fmaf(acc[v].x, a, w * x[u][v].x);
-            acc[v].y = fmaf(acc[v].y, a, w * x[u][v].y);
-            acc[v].z = fmaf(acc[v].z, a, w * x[u][v].z);
-            acc[v].w = fmaf(acc[v].w, a, w * x[u][v].w);
+            acc[v].x = fmaf(acc[v].x, a, wt * x[u][v].x);
+            acc[v].y = fmaf(acc[v].y, a, wt * x[u][v].y);
+            acc[v].z = fmaf(acc[v].z, a, wt * x[u][v].z);
+            acc[v].w = fmaf(acc[v].w, a, wt * x[u][v].w);
           }
         }
       }
@@ -563,7 +578,7 @@ SpanLayout span_layout(int dtype, int num_seqs, int num_tokens, int num_heads, i
   const long long most = max_query_len > 0 ? std::min<long long>(max_query_len, T) : T;  // new tokens
   const long long units =
       Hk * std::min(ceil_div_ll(T * G, kSpanRows) + S, S * ceil_div_ll(most * G, kSpanRows));
-  const long long tiles = ceil_div_ll(msl, kSpanTile) + kSpanOverhead;
+  const long long tiles = ceil_div_ll(msl, kSpanTile) * kSpanWide + kSpanOverhead;
   l.ok = units * tiles < (1ll << 31) - (1 << 20);
   // two rows of partials for each row of a unit of up to 128
   l.slot_rows = most * G <= 128 ? (int)(2 * ceil_div_ll(most * G, 4) * 4) : kSpanRows;
@@ -691,7 +706,7 @@ pa_status span_call(const SpanCall &sc) {
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
   // partials that a row may have: a piece for each block that shares its unit
-  const long long blocks = ceil_div_ll(c.max_seq_len, kSpanTile) + 1;
+  const long long blocks = 2 * (ceil_div_ll(c.max_seq_len, kSpanTile) + 1);
   slot = prof_begin(PA_K_MERGE, st);
   err = launch_merge<MODE>(p, std::min<long long>(blocks, p.grid), st);
   prof_end(slot, st);

@@ -17,8 +17,17 @@ namespace pa {
 
 constexpr int kSpanRows = 256;
 constexpr int kSpanTile = 128;
-// What a piece costs beside its tiles (queries, first scores, partials), in tiles.
-constexpr int kSpanOverhead = 1;
+// Work is laid out in half tiles: a tile of a unit of more than 128 rows, which keeps
+// the tensor cores busy, is two (1.4 us of an SM at head_dim 128, 1.28 at 64); one of
+// a unit of up to 128 rows is one where its keys come from L2, having been read for
+// the request's other rows, or are half as wide (0.7 us), and two where they come
+// from HBM at head_dim 128 (1.45 us).
+constexpr int kSpanWide = 2;
+__host__ __device__ inline int span_narrow(int nblk, int head_dim) {
+  return nblk == 1 && head_dim == 128 ? 2 : 1;
+}
+// What a unit costs beside its tiles (queries, first scores, partials).
+constexpr int kSpanOverhead = 2;
 // Requests with at most this many rows of a KV head have their scores kept for
 // the sums over rows (pa_forward_weights); the others' are computed again.  A
 // position's scores of 32 rows are 128 bytes written and read, its key in bf16
@@ -39,6 +48,9 @@ struct SpanReq {
   int ntile;           // tiles of its context
   int unit0;           // first unit; unit = unit0 + kv head * nblk + block
   unsigned cost0;      // where its first unit begins in the laid-out work
+  int kcost;           // laid-out work of a KV head: its blocks' one after the other,
+  int ucost, ulast;    // a block's, and the last one's
+  int wcost, wlast;    // a tile of a block's, and of the last one's
   long long score0;    // first kept score, -1: not kept
 };
 
@@ -77,11 +89,12 @@ __device__ inline long long span_row(const SpanParams &p, long long slot, int x,
   return slot * p.slot_rows + x * (p.slot_rows / 2) + r;
 }
 
-struct SpanPiece {
+struct alignas(16) SpanPiece {
   int q_start, q_len, ctx, req;  // the request's rows
   int kvh, t0;                   // KV head, first token of the row block
   int kv_lo, kv_hi;              // positions (kv_lo a multiple of kSpanTile)
   int ctx_pad;                   // the context in whole tiles
+  int whole;                     // 1: all of the unit
   long long slot;
   long long score0;              // its kept scores: row r's position j at score0 + r * ctx_pad + j
 };
@@ -91,15 +104,15 @@ struct SpanPiece {
 __device__ inline int span_block_end(const SpanReq &r, int t0, int tq, bool causal) {
   return causal ? r.ctx - r.q_len + min(t0 + tq, r.q_len) : r.ctx;
 }
-// The tile boundary at `cost` of a unit's laid-out work.
-__device__ inline int span_tile_at(const SpanReq &r, unsigned cost) {
-  return min(max((int)cost - kSpanOverhead, 0), r.ntile);
+// The tile boundary at `cost` of a unit's laid-out work; w: of a tile, 1 or 2.
+__device__ inline int span_tile_at(const SpanReq &r, unsigned cost, int w) {
+  return min(max((int)cost - kSpanOverhead, 0) >> (w - 1), r.ntile);
 }
 
-// The pieces of block `cta`, in order.  Every role of a block walks them for itself.
+// The pieces of block `cta`, in order.
 struct SpanCursor {
-  unsigned pos, end;
-  int s, local, cta;
+  unsigned pos, end, u0;  // u0: where the unit begins
+  int s, kvh, blk, cta;
   SpanReq r;
 
   __device__ void start(const SpanParams &p, const SpanPlan &plan, int block) {
@@ -107,8 +120,8 @@ struct SpanCursor {
     const unsigned long long at = (unsigned long long)block * plan.run;
     pos = (unsigned)min(at, (unsigned long long)plan.total);
     end = (unsigned)min(at + plan.run, (unsigned long long)plan.total);
-    s = 0;
-    local = 0;
+    u0 = 0;
+    s = kvh = blk = 0;
     if (pos >= end) return;
     int lo = 0, hi = p.f.num_seqs - 1;
     while (lo < hi) {
@@ -117,33 +130,45 @@ struct SpanCursor {
     }
     s = lo;
     r = p.req[s];
-    local = (int)((pos - r.cost0) / (unsigned)(r.ntile + kSpanOverhead));
+    unsigned rel = pos - r.cost0;
+    kvh = (int)(rel / (unsigned)r.kcost);
+    rel -= (unsigned)kvh * r.kcost;
+    blk = (int)min(rel / (unsigned)r.ucost, (unsigned)(r.nblk - 1));
+    u0 = r.cost0 + (unsigned)kvh * r.kcost + (unsigned)blk * r.ucost;
   }
 
-  __device__ bool next(const SpanParams &p, int G, bool causal, SpanPiece &it) {
-    const int tq = kSpanRows / G;
+  // lg: log2 of the query heads of a KV head
+  __device__ bool next(const SpanParams &p, int lg, bool causal, SpanPiece &it) {
     while (pos < end) {
-      if (r.nblk == 0 || local == p.f.num_kv_heads * r.nblk) {
-        do r = p.req[++s]; while (r.nblk == 0);  // (pos < end: there is one)
-        local = 0;
-      }
-      const unsigned n = r.ntile + kSpanOverhead, u0 = r.cost0 + (unsigned)local * n;
-      const unsigned to = min(end, u0 + n);
-      const int lo = span_tile_at(r, pos - u0), hi = span_tile_at(r, to - u0);
-      const int kvh = local / r.nblk, b = local - kvh * r.nblk;
+      const bool last = blk == r.nblk - 1;
+      const int w = last ? r.wlast : r.wcost;
+      const unsigned n = last ? r.ulast : r.ucost, to = min(end, u0 + n);
+      const int lo = span_tile_at(r, pos - u0, w), hi = span_tile_at(r, to - u0, w);
       it.q_start = r.q_start;
       it.q_len = r.q_len;
       it.ctx = r.ctx;
       it.req = s;
       it.kvh = kvh;
-      it.t0 = b * tq;
+      it.t0 = blk * (kSpanRows >> lg);
       it.kv_lo = lo * kSpanTile;
-      it.kv_hi = min(hi * kSpanTile, span_block_end(r, it.t0, tq, causal));
+      it.kv_hi = min(hi * kSpanTile, span_block_end(r, it.t0, kSpanRows >> lg, causal));
       it.ctx_pad = r.ntile * kSpanTile;
-      it.slot = (long long)r.unit0 + local + cta;
-      it.score0 = r.score0 < 0 ? -1 : r.score0 + (long long)kvh * r.q_len * G * it.ctx_pad;
+      it.whole = lo == 0 && hi == r.ntile;
+      it.slot = (long long)r.unit0 + kvh * r.nblk + blk + cta;
+      it.score0 = r.score0 < 0 ? -1 : r.score0 + ((long long)kvh * r.q_len << lg) * it.ctx_pad;
       pos = to;
-      if (to == u0 + n) ++local;
+      if (to == u0 + n) {
+        u0 = to;
+        if (++blk == r.nblk) {
+          blk = 0;
+          if (++kvh == p.f.num_kv_heads) {
+            kvh = 0;
+            if (pos < end) {  // (then there is another request with work)
+              do r = p.req[++s]; while (r.nblk == 0);
+            }
+          }
+        }
+      }
       if (it.kv_hi > it.kv_lo) return true;
     }
     return false;

@@ -40,24 +40,27 @@ constexpr int kThreads = 512;
 constexpr int kIssueWarp = 8, kLoad0 = 10, kCheck0 = 14;
 // launch registers 512 x 128; the softmax warpgroups take 176, the others keep 80
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+constexpr int kPieces = 8;  // pieces that the first loading warp may be ahead
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S of row tile x at 128 x, O at 256 + 128 x
 
-template <int D>
+// ONE: no piece has more than 128 rows; the second query tile's place holds values
+template <int D, bool ONE>
 struct Cfg {
   static constexpr int NH = D / 64;            // 128-byte chunks of a row
   static constexpr int Q_TILE = NH * 128 * 128;
   static constexpr int KV_BYTES = NH * kBN * 128;
-  static constexpr int KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 5;
-  static constexpr int OFF_K = 2 * Q_TILE;
+  static constexpr int KST = D == 128 ? 3 : 5, VST = D == 128 ? (ONE ? 3 : 2) : 5;
+  static constexpr int OFF_K = (ONE ? 1 : 2) * Q_TILE;
   static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
   // barriers
   static constexpr int Q_FULL = 0, Q_FREE = 1, S_FULL = 2, O_HALF = 4, O_DONE = 6, P_HALF = 8,
                        P_FULL = 10, O_FREE = 12, TURN = 14, END = 16, K_FULL = 17, V_FULL = K_FULL + KST,
                        K_FREE = V_FULL + VST, V_FREE = K_FREE + KST, V_OK = V_FREE + VST,
-                       NBAR = V_OK + VST;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 64;
+                       PIECE = V_OK + VST, PIECE_FREE = PIECE + kPieces, NBAR = PIECE_FREE + kPieces;
+  static constexpr int OFF_PIECE = (OFF_BAR + NBAR * 8 + 15) & ~15;
+  static constexpr int OFF_MISC = OFF_PIECE + kPieces * (int)sizeof(SpanPiece);
+  static constexpr int SMEM = OFF_MISC + 144;
   static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kBN, 0);
   static constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, 1);
   static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -76,10 +79,10 @@ __device__ inline bool not_finite(uint4 v) {  // of eight bf16 values, any
 }
 
 // The values that were zeroed, for one row that may see some of them: added to its
-// partial (normalised by inv) in memory.  Rare and slow.
-template <int D, bool CAUSAL>
+// partial or its finished output (DONE), normalised by inv, in memory.  Rare and slow.
+template <int D, bool CAUSAL, bool DONE>
 __device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it, int row, bool pairs,
-                                        int x, float ref, float inv, float *dst) {
+                                        int x, float ref, float inv, void *out) {
   const FwdParams &f = p.f;
   const int Hk = f.num_kv_heads, G = f.num_heads / Hk, bs = f.block_size, prefix = it.ctx - it.q_len;
   const int tl = it.t0 + row / G, head = it.kvh * G + row % G;
@@ -105,27 +108,36 @@ __device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it,
     float s = 0.f;
     for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
     const float w = fast_exp2(s * f.scale_log2 - ref) * inv;
-    for (int d = 0; d < D; ++d) dst[d] = fmaf(w, __bfloat162float(vv[d]), dst[d]);
+    // (what it adds is not finite where it matters: a finished output's rounding does not)
+    for (int d = 0; d < D; ++d) {
+      const float add = w * __bfloat162float(vv[d]);
+      if (DONE) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(out) + d;
+        *dst = __float2bfloat16_rn(__bfloat162float(*dst) + add);
+      } else {
+        static_cast<float *>(out)[d] += add;
+      }
+    }
   }
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
     span_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ SpanParams p,
                     int box) {
-  using C = Cfg<D>;
+  using C = Cfg<D, ONE>;
   constexpr bool VALUES = MODE != kSpanVotesOnly, CAUSAL = MODE != kSpanTree, VOTES = MODE != kSpanTree;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
-  int *s_bad = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);  // [2]
-  // piece k: s_fix[k % 8] is k + 1 when values of it were zeroed (the rings let the
-  // checking warps be at most VST pieces ahead)
-  volatile int *s_fix = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 16);  // [8]
+  // piece k: s_fix[k % 16] is k + 1 when values of it were zeroed, s_bad[k % 16] when it
+  // met a bad page (the warps that say so are at most 8 pieces ahead)
+  volatile int *s_fix = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);  // [16]
+  volatile int *s_bad = s_fix + 16;                                                // [16]
   const FwdParams &f = p.f;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = f.num_heads / f.num_kv_heads, TQ = 128 / G, bs = f.block_size;
+  const int G = f.num_heads / f.num_kv_heads, TQ = 128 / G, bs = f.block_size, lg = __ffs(G) - 1;
   if (smem_u32(smem) & 1023) {  // the same for every thread: all leave together
     if (tid == 0) atomicOr(f.status, PA_DEV_INTERNAL);
     return;
@@ -138,32 +150,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P and O: the row tile's four warps; a ring stage: two loading warps, two
       // issuing ones, two that look at the values
       const bool softmax = b >= C::P_HALF && b < C::TURN, ring = b >= C::K_FULL;
-      mbar_init(&bar[b], softmax ? 4 : ring || b == C::Q_FREE || b == C::END ? 2 : 1);
+      const int readers = VALUES ? 15 : 11;  // warps that read the pieces
+      mbar_init(&bar[b], b >= C::PIECE_FREE ? readers : b >= C::PIECE ? 1 : softmax ? 4
+                         : ring || b == C::Q_FREE || b == C::END ? 2 : 1);
     }
     fence_mbar_init();
   }
-  if (tid < 8) s_fix[tid] = 0;
+  if (tid < 32) s_fix[tid] = 0;
   if (warp == kIssueWarp) tc_alloc(s_tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   bool dead = false;
-  SpanCursor cur;
+  SpanPiece *const s_piece = reinterpret_cast<SpanPiece *>(smem + C::OFF_PIECE);
   SpanPiece it;
+  uint32_t pieces = 0;  // taken by this warp
+  // The next piece, which the first loading warp has left; false behind the last one.
+  auto next_piece = [&]() {
+    const uint32_t at = pieces % kPieces;
+    mbar_wait(&bar[C::PIECE + at], (pieces / kPieces) & 1, dead, f.status);
+    it = s_piece[at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[C::PIECE_FREE + at]);
+    ++pieces;
+    return it.kv_hi > 0 && !dead;
+  };
 
   if (warp >= kIssueWarp) {
     reg_dec<kOtherRegs>();
     pdl_wait();  // the plan
     pdl_trigger();
-    const SpanPlan plan = *p.plan;
-    cur.start(p, plan, blockIdx.x);
     if (warp >= kCheck0) {
       // -------------------------------------------------- values of hidden positions
       if constexpr (VALUES) {
         const int t = tid - kCheck0 * 32;
         uint32_t vs = 0, vr = 0;
-        for (int k = 0; cur.next(p, G, CAUSAL, it); ++k) {
+        for (int k = 0; next_piece(); ++k) {
           const int hidden = first_hidden<CAUSAL>(it);
           for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN) {
             mbar_wait(&bar[C::V_FULL + vs], vr & 1, dead, f.status);
@@ -189,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               if (zeroed) {
-                s_fix[k & 7] = k + 1;
+                s_fix[k & 15] = k + 1;
                 __threadfence_block();
               }
             }
@@ -216,18 +239,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *full = &bar[is_v ? C::V_FULL : C::K_FULL], *free = &bar[is_v ? C::V_FREE : C::K_FREE];
       uint8_t *ring = smem + (is_v ? C::OFF_V : C::OFF_K) + at;
       uint32_t st = 0, round = 0, items = 0, queries = 0;
-      for (; (VALUES || !is_v) && !dead && cur.next(p, G, CAUSAL, it); ++items) {
+      // The first of them makes the block's pieces and leaves them to the others; one
+      // without positions ends the list.
+      SpanCursor cur;
+      if (warp == kLoad0) cur.start(p, *p.plan, blockIdx.x);
+      auto make_piece = [&]() {
+        if (!cur.next(p, lg, CAUSAL, it)) it.kv_lo = it.kv_hi = 0;
+        const uint32_t at = pieces % kPieces;
+        if (pieces >= kPieces) mbar_wait(&bar[C::PIECE_FREE + at], (pieces / kPieces - 1) & 1, dead, f.status);
+        if (lane == 0) {
+          s_piece[at] = it;
+          mbar_arrive(&bar[C::PIECE + at]);
+        }
+        __syncwarp();
+        ++pieces;
+        return it.kv_hi > 0 && !dead;
+      };
+      for (; (VALUES || !is_v) && !dead && (warp == kLoad0 ? make_piece() : next_piece()); ++items) {
         const int32_t *bt = f.block_table + (size_t)it.req * f.max_blocks_per_seq;
         auto page_of = [&](int pos) {
           int page = f.num_blocks;  // past the pool: zeros
           if (lane < nb && pos < it.kv_hi) {
             const int x = __ldg(bt + pos / bs);
-            if (x >= 0 && x < f.num_blocks) page = x;
+            if (x >= 0 && x < f.num_blocks) {
+              page = x;
+            } else {  // marks all of the piece's rows
+              atomicOr(f.status, PA_DEV_BAD_BLOCK);
+              s_bad[items & 15] = (int)items + 1;
+              __threadfence_block();
+            }
           }
           return page;
         };
         if (warp == kLoad0 && lane == 0) {
-          const int tiles = (it.q_len - it.t0) * G > 128 ? 2 : 1;
+          const int tiles = !ONE && (it.q_len - it.t0) * G > 128 ? 2 : 1;
           if (items > 0) mbar_wait(&bar[C::Q_FREE], (items - 1) & 1, dead, f.status);
           if (!dead) {
             mbar_arrive_expect_tx(&bar[C::Q_FULL], tiles * C::Q_TILE);
@@ -302,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar[C::V_FREE + vs]);
         if (++vs == C::VST) vs = 0, ++vr;
       };
-      while (cur.next(p, G, CAUSAL, it)) {
-        const bool two = (it.q_len - it.t0) * G > 128;
+      while (next_piece()) {
+        const bool two = !ONE && (it.q_len - it.t0) * G > 128;
         const int nt = (it.kv_hi - it.kv_lo + kBN - 1) / kBN;
         const int t0 = two ? 0 : x, dt = two ? 1 : 2;  // own tiles t0, t0 + dt, ..
         const uint32_t sq = smem_u32(smem) + (two ? x * C::Q_TILE : 0);
@@ -422,31 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = -1;  // piece
     it.q_start = it.q_len = it.req = it.kvh = it.t0 = it.kv_lo = it.ctx = it.ctx_pad = 0;
     it.kv_hi = kBN;
-    it.slot = 0;
+    it.slot = it.whole = 0;
     it.score0 = -1;
     for (;;) {
       const bool dry = k < 0;
       const int all = (it.q_len - it.t0) * G;
-      const bool two = all > 128;
+      const bool two = !ONE && all > 128;
       const int row0 = two ? x * 128 : 0, dt = two ? kBN : 2 * kBN;
       const int lo0 = it.kv_lo + (two || dry ? 0 : x * kBN);
       const int rows = dry ? 128 : min(128, all - row0);
       if (rows > 0 && lo0 < it.kv_hi) {
-        // a bad page in the piece marks all of its rows
-        if (!dry) {
-          const int32_t *bt = f.block_table + (size_t)it.req * f.max_blocks_per_seq;
-          int bad = 0;
-          for (int lp = it.kv_lo / bs + r; lp <= (it.kv_hi - 1) / bs; lp += 128) {
-            const int page = __ldg(bt + lp);
-            if (page < 0 || page >= f.num_blocks) bad = 1;
-          }
-          if (bad) atomicOr(f.status, PA_DEV_BAD_BLOCK);
-          if (r == 0) s_bad[x] = 0;
-          named_sync(1 + x, 128);
-          if (bad) atomicOr(&s_bad[x], 1);
-          named_sync(1 + x, 128);
-        }
-        const bool item_bad = !dry && s_bad[x] != 0;
         const bool warp_active = (warp & 3) * 32 < rows;  // its other rows are padding
         const int prefix = it.ctx - it.q_len, hidden = dry ? kBN : first_hidden<CAUSAL>(it);
         const int tl = min(it.t0 + (row0 + r) / G, it.q_len - 1);  // (padding rows: the last token's)
@@ -611,36 +641,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // ---- O / l and the log-sum-exp of the rows
-        const long long prow = span_row(p, it.slot, x, r);
-        const float inv = l == 0.f || item_bad ? 0.f : 1.f / l;
+        // ---- O / l and the log-sum-exp of the rows: finished ones where the piece is
+        // the whole unit and one row tile has all of its positions, else partials
         if constexpr (VALUES) {
           if (!dry) mbar_wait(&bar[C::O_DONE + x], (n - 1) & 1, dead, f.status);
           tc_fence_after();
-          if (warp_active) {
-            const uint32_t keep = item_bad ? 0u : 0xffffffffu;
+        }
+        const bool bad = !dry && s_bad[k & 15] == k + 1, none = l == 0.f;
+        const long long prow = span_row(p, it.slot, x, r);
+        float lse = bad ? INFINITY : none ? -INFINITY : ref + log2f(l), inv = bad || none ? 0.f : 1.f / l;
+        const bool real = r < rows && !dry;
+        if (!ONE && two && it.whole) {
+          const int row = row0 + r, head = it.kvh * G + (row & (G - 1));
+          const long long orow = (long long)(it.q_start + tl) * f.num_heads + head;
+          if (f.sinks && !bad && !none && real) {
+            const float sink2 = __ldg(f.sinks + head) * kLog2eF, top = lse != lse || lse > sink2 ? lse : sink2;
+            const float all_lse = top + log2f(fast_exp2(lse - top) + fast_exp2(sink2 - top));
+            inv *= fast_exp2(lse - all_lse);
+            lse = all_lse;
+          }
+          if constexpr (VALUES) {
+            if (warp_active) {
+              __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(f.out) + orow * D;
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t raw[32], packed[16];
+                tc_ld32(tm_o + c0, raw);
+                tc_wait_ld();
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t raw[32];
-              tc_ld32(tm_o + c0, raw);
-              tc_wait_ld();
+                for (int i = 0; i < 16; ++i) {
+                  // one rounding to nearest even, of the finished output
+                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(raw[2 * i]) * inv,
+                                                                  __uint_as_float(raw[2 * i + 1]) * inv);
+                  packed[i] = bad || none ? 0u : *reinterpret_cast<const uint32_t *>(&h2);
+                }
+                if (real) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) raw[i] &= keep;
-              if (r < rows && !dry) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) store32(p.part_o + prow * D + c0 + i, raw, i, inv);
+                  for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<uint4 *>(dst + c0 + 2 * i) =
+                        make_uint4(packed[i], packed[i + 1], packed[i + 2], packed[i + 3]);
+                }
               }
+              if (real && s_fix[k & 15] == k + 1 && !bad && !none)
+                fix_values<D, CAUSAL, true>(p, it, row, false, x, ref, inv, dst);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-        }
-        if (r < rows && !dry) {
-          p.part_lse[prow] = item_bad ? INFINITY : l == 0.f ? -INFINITY : ref + log2f(l);
+          if (VOTES && real) p.row_lse[orow] = lse;
+        } else {
           if constexpr (VALUES) {
-            if (s_fix[k & 7] == k + 1 && !item_bad && l != 0.f)
-              fix_values<D, CAUSAL>(p, it, row0 + r, !two, x, ref, inv, p.part_o + prow * D);
+            if (warp_active) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t raw[32];
+                tc_ld32(tm_o + c0, raw);
+                tc_wait_ld();
+                if (real) {
+#pragma unroll
+                  for (int i = 0; i < 32; i += 8) store32(p.part_o + prow * D + c0 + i, raw, i, inv);
+                }
+              }
+              if (real && s_fix[k & 15] == k + 1 && !bad && !none)
+                fix_values<D, CAUSAL, false>(p, it, row0 + r, !two, x, ref, inv, p.part_o + prow * D);
+            }
           }
+          if (real) p.part_lse[prow] = lse;
         }
         if (dry || VALUES) {
           tc_fence_before();
@@ -648,11 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bar[C::O_FREE + x]);
         }
       }
-      if (dry) {
-        pdl_wait();  // the plan
-        cur.start(p, *p.plan, blockIdx.x);
-      }
-      if (!cur.next(p, G, CAUSAL, it)) break;
+      if (dry) pdl_wait();  // the plan
+      if (!next_piece()) break;
       ++k;
     }
   }
@@ -662,11 +723,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kIssueWarp) tc_dealloc(tmem, kTmemCols);
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool ONE>
 cudaError_t launch_d(const SpanParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                      const CUtensorMap &tv, int box, cudaStream_t stream) {
-  using C = Cfg<D>;
-  auto kern = span_mma_kernel<D, MODE>;
+  using C = Cfg<D, ONE>;
+  auto kern = span_mma_kernel<D, MODE, ONE>;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_attrs_once(kern, C::SMEM, done);
   if (e != cudaSuccess) return e;
@@ -676,8 +737,13 @@ cudaError_t launch_d(const SpanParams &p, const CUtensorMap &tq, const CUtensorM
 template <int MODE>
 cudaError_t launch_mode(const SpanParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                         const CUtensorMap &tv, int box, cudaStream_t stream) {
-  return p.f.head_dim == 128 ? launch_d<128, MODE>(p, tq, tk, tv, box, stream)
-                             : launch_d<64, MODE>(p, tq, tk, tv, box, stream);
+  // (slots of fewer rows: the caller's bound says that no piece has more than 128)
+  const bool one = p.slot_rows < kSpanRows;
+  if (p.f.head_dim == 128)
+    return one ? launch_d<128, MODE, true>(p, tq, tk, tv, box, stream)
+               : launch_d<128, MODE, false>(p, tq, tk, tv, box, stream);
+  return one ? launch_d<64, MODE, true>(p, tq, tk, tv, box, stream)
+             : launch_d<64, MODE, false>(p, tq, tk, tv, box, stream);
 }
 
 }  // namespace
