@@ -344,6 +344,15 @@ __device__ inline void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, i
                : "memory");
 }
 
+__device__ inline void tma_prefetch_5d(const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                       int c4) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 __device__ inline void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),

@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
         cnt[0] = (long long)Hk * r.nblk;
         r.wcost = kSpanWide;
         r.wlast = rows - (r.nblk - 1ll) * kSpanRows > 128 ? kSpanWide : span_narrow(r.nblk, f.head_dim);
-        r.ulast = r.ntile * r.wlast + kSpanOverhead;
-        r.ucost = r.nblk > 1 ? r.ntile * r.wcost + kSpanOverhead : r.ulast;
+        r.ulast = r.ntile * r.wlast + p.overhead;
+        r.ucost = r.nblk > 1 ? r.ntile * r.wcost + p.overhead : r.ulast;
         r.kcost = (r.nblk - 1) * r.ucost + r.ulast;
         cnt[1] = (long long)Hk * r.kcost;
         if (p.keep_scores && rows <= kSpanStoredRows) scores = Hk * rows * r.ntile * kSpanTile;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
   if (tid == 0) {
     // (the host has bounded the sum by 2^31)
     const unsigned total = (unsigned)sum[1];
-    *p.plan = SpanPlan{total, max((total + p.grid - 1) / p.grid, 1u + kSpanOverhead),
+    *p.plan = SpanPlan{total, max((total + p.grid - 1) / p.grid, (unsigned)kSpanWide),
                        (unsigned)sum[3], 0};
   }
 }
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
         if (p.halves && !pairs) {
           // in one piece it is finished already (pieces before it may have no tile)
           for (int c = c0; c < c0 + n; ++c) {
-            const int t1 = span_tile_at(r, min(u0 + len, (unsigned)(c + 1) * plan.run) - u0, w);
+            const int t1 = span_tile_at(p, r, min(u0 + len, (unsigned)(c + 1) * plan.run) - u0, w);
             if (t1 == r.ntile) mine = false;
             if (t1 > 0) break;
           }
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
         const int c = c0 + (pairs ? e >> 1 : e), half = pairs ? e & 1 : 0;
         // the piece's tiles (it may have none: the overhead alone, or behind the causal end)
         const unsigned from = max(u0, (unsigned)c * plan.run), to = min(u0 + len, (unsigned)(c + 1) * plan.run);
-        const int t0 = span_tile_at(r, from - u0, w), t1 = span_tile_at(r, to - u0, w);
+        const int t0 = span_tile_at(p, r, from - u0, w), t1 = span_tile_at(p, r, to - u0, w);
         if (min(t1 * kSpanTile, blk_end) <= (t0 + half) * kSpanTile) continue;
         const long long at = span_row(p, unit + c, half, br);
         lse[u] = __ldcg(p.part_lse + at);
@@ -687,6 +687,9 @@ pa_status span_call(const SpanCall &sc) {
   p.num_sms = num_sms;
   p.grid = std::min(num_sms, kMaxGrid);
   p.halves = c.dtype == PA_BF16;
+  const long long units = (long long)c.num_kv_heads *
+                          std::max<long long>(c.num_seqs, ceil_div_ll((long long)c.num_tokens * (c.num_heads / c.num_kv_heads), kSpanRows));
+  p.overhead = units >= p.grid ? kSpanOverhead : 0;
   p.slot_rows = lay.slot_rows;
   p.plan = reinterpret_cast<SpanPlan *>(ws + lay.plan);
   p.req = reinterpret_cast<SpanReq *>(ws + lay.req);

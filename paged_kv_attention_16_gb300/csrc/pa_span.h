@@ -26,8 +26,10 @@ constexpr int kSpanWide = 2;
 __host__ __device__ inline int span_narrow(int nblk, int head_dim) {
   return nblk == 1 && head_dim == 128 ? 2 : 1;
 }
-// What a unit costs beside its tiles (queries, first scores, partials).
-constexpr int kSpanOverhead = 2;
+// What a unit costs beside its tiles (queries, first scores, storing the results):
+// 5 us of an SM, where there are units enough for every block; with fewer the tiles
+// alone are cut, so that short contexts spread over the SMs.
+constexpr int kSpanOverhead = 6;
 // Requests with at most this many rows of a KV head have their scores kept for
 // the sums over rows (pa_forward_weights); the others' are computed again.  A
 // position's scores of 32 rows are 128 bytes written and read, its key in bf16
@@ -71,6 +73,7 @@ struct SpanParams {
   int accumulate;
   int keep_scores;
   int num_sms, grid, halves;       // halves: see span_row
+  int overhead;                    // kSpanOverhead, or 0
   int slot_rows;
   SpanPlan *plan;
   SpanReq *req;          // [num_seqs]
@@ -105,15 +108,36 @@ __device__ inline int span_block_end(const SpanReq &r, int t0, int tq, bool caus
   return causal ? r.ctx - r.q_len + min(t0 + tq, r.q_len) : r.ctx;
 }
 // The tile boundary at `cost` of a unit's laid-out work; w: of a tile, 1 or 2.
-__device__ inline int span_tile_at(const SpanReq &r, unsigned cost, int w) {
-  return min(max((int)cost - kSpanOverhead, 0) >> (w - 1), r.ntile);
+__device__ inline int span_tile_at(const SpanParams &p, const SpanReq &r, unsigned cost, int w) {
+  return min(max((int)cost - p.overhead, 0) >> (w - 1), r.ntile);
 }
 
-// The pieces of block `cta`, in order.
+// The pieces of block `cta`: the whole units of its run first, then the end of the
+// unit that its run begins in, then the beginning of the one that it ends in.  So the
+// blocks that share a KV head of a request all begin at its first position, and what
+// one of them has brought from HBM the others find in L2 (12 trees of up to 250 tokens
+// on up to 16384 positions, whose keys and values are 280 MB: 537 us in the order of
+// the run, 487 so).
 struct SpanCursor {
   unsigned pos, end, u0;  // u0: where the unit begins
   int s, kvh, blk, cta;
   SpanReq r;
+  bool put_off;           // the run's first piece is part of a unit
+  unsigned first_pos, first_u0;
+  int first_s, first_kvh, first_blk;
+
+  __device__ unsigned unit_cost(const SpanReq &q, int b) const { return b == q.nblk - 1 ? q.ulast : q.ucost; }
+
+  __device__ void step(const SpanParams &p) {  // to the next unit, where the run goes on
+    u0 = pos;
+    if (++blk < r.nblk) return;
+    blk = 0;
+    if (++kvh < p.f.num_kv_heads) return;
+    kvh = 0;
+    if (pos < end) {  // (then there is another request with work)
+      do r = p.req[++s]; while (r.nblk == 0);
+    }
+  }
 
   __device__ void start(const SpanParams &p, const SpanPlan &plan, int block) {
     cta = block;
@@ -122,6 +146,7 @@ struct SpanCursor {
     end = (unsigned)min(at + plan.run, (unsigned long long)plan.total);
     u0 = 0;
     s = kvh = blk = 0;
+    put_off = false;
     if (pos >= end) return;
     int lo = 0, hi = p.f.num_seqs - 1;
     while (lo < hi) {
@@ -135,43 +160,58 @@ struct SpanCursor {
     rel -= (unsigned)kvh * r.kcost;
     blk = (int)min(rel / (unsigned)r.ucost, (unsigned)(r.nblk - 1));
     u0 = r.cost0 + (unsigned)kvh * r.kcost + (unsigned)blk * r.ucost;
+    const unsigned to = u0 + unit_cost(r, blk);
+    if (pos > u0 && to < end) {
+      put_off = true;
+      first_pos = pos;
+      first_u0 = u0;
+      first_s = s;
+      first_kvh = kvh;
+      first_blk = blk;
+      pos = to;
+      step(p);
+    }
   }
 
-  // lg: log2 of the query heads of a KV head
+  // The piece [from, to) of a unit; whether it has positions.  lg: log2 of the query
+  // heads of a KV head.
+  __device__ bool make(const SpanParams &p, int lg, bool causal, const SpanReq &q, int req, int h, int b,
+                       unsigned begin, unsigned from, unsigned to, SpanPiece &it) const {
+    const int w = b == q.nblk - 1 ? q.wlast : q.wcost;
+    const int lo = span_tile_at(p, q, from - begin, w), hi = span_tile_at(p, q, to - begin, w);
+    it.q_start = q.q_start;
+    it.q_len = q.q_len;
+    it.ctx = q.ctx;
+    it.req = req;
+    it.kvh = h;
+    it.t0 = b * (kSpanRows >> lg);
+    it.kv_lo = lo * kSpanTile;
+    it.kv_hi = min(hi * kSpanTile, span_block_end(q, it.t0, kSpanRows >> lg, causal));
+    it.ctx_pad = q.ntile * kSpanTile;
+    it.whole = lo == 0 && hi == q.ntile;
+    it.slot = (long long)q.unit0 + h * q.nblk + b + cta;
+    it.score0 = q.score0 < 0 ? -1 : q.score0 + ((long long)h * q.q_len << lg) * it.ctx_pad;
+    return it.kv_hi > it.kv_lo;
+  }
+
   __device__ bool next(const SpanParams &p, int lg, bool causal, SpanPiece &it) {
-    while (pos < end) {
-      const bool last = blk == r.nblk - 1;
-      const int w = last ? r.wlast : r.wcost;
-      const unsigned n = last ? r.ulast : r.ucost, to = min(end, u0 + n);
-      const int lo = span_tile_at(r, pos - u0, w), hi = span_tile_at(r, to - u0, w);
-      it.q_start = r.q_start;
-      it.q_len = r.q_len;
-      it.ctx = r.ctx;
-      it.req = s;
-      it.kvh = kvh;
-      it.t0 = blk * (kSpanRows >> lg);
-      it.kv_lo = lo * kSpanTile;
-      it.kv_hi = min(hi * kSpanTile, span_block_end(r, it.t0, kSpanRows >> lg, causal));
-      it.ctx_pad = r.ntile * kSpanTile;
-      it.whole = lo == 0 && hi == r.ntile;
-      it.slot = (long long)r.unit0 + kvh * r.nblk + blk + cta;
-      it.score0 = r.score0 < 0 ? -1 : r.score0 + ((long long)kvh * r.q_len << lg) * it.ctx_pad;
-      pos = to;
-      if (to == u0 + n) {
-        u0 = to;
-        if (++blk == r.nblk) {
-          blk = 0;
-          if (++kvh == p.f.num_kv_heads) {
-            kvh = 0;
-            if (pos < end) {  // (then there is another request with work)
-              do r = p.req[++s]; while (r.nblk == 0);
-            }
-          }
-        }
+    for (;;) {
+      const unsigned n = pos < end ? unit_cost(r, blk) : 0;
+      if (put_off && (pos >= end || u0 + n > end)) {  // no whole unit is left
+        put_off = false;
+        const SpanReq q = p.req[first_s];
+        if (make(p, lg, causal, q, first_s, first_kvh, first_blk, first_u0, first_pos,
+                 first_u0 + unit_cost(q, first_blk), it))
+          return true;
+        continue;
       }
-      if (it.kv_hi > it.kv_lo) return true;
+      if (pos >= end) return false;
+      const unsigned to = min(end, u0 + n);
+      const bool has = make(p, lg, causal, r, s, kvh, blk, u0, pos, to, it);
+      pos = to;
+      if (to == u0 + n) step(p);
+      if (has) return true;
     }
-    return false;
   }
 };
 

@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                           it.q_start + it.t0 + x * TQ, &bar[C::Q_FULL]);
         }
         int pos = it.kv_lo + run * box;
-        int page = page_of(pos);
+        int page = page_of(pos), next = page_of(pos + kBN);
         for (int lo = it.kv_lo; lo < it.kv_hi; lo += kBN) {
-          const int next = page_of(pos + kBN);  // its latency passes during the wait
+          const int after = page_of(pos + 2 * kBN);  // its latency passes during the wait
           if (lane == 0) {
             if (round > 0) mbar_wait(&free[st], (round - 1) & 1, dead, f.status);
             if (!dead) mbar_arrive_expect_tx(&full[st], bytes);
@@ -295,11 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (dead) break;  // timed out: the stage is not free
           if (lane < nb) {
             uint8_t *dst = ring + st * C::KV_BYTES;
-            if (is_v) tma_load_5d(dst, &tm_v, 0, pos % bs, 0, it.kvh, page, &full[st]);
-            else tma_load_4d(dst, &tm_k, chunk * 64, it.kvh, pos % bs, page, &full[st]);
+            if (is_v) {
+              tma_load_5d(dst, &tm_v, 0, pos % bs, 0, it.kvh, page, &full[st]);
+              // with two stages of values (256 rows): the tile behind them to L2 meanwhile
+              if (C::VST == 2 && after < f.num_blocks)
+                tma_prefetch_5d(&tm_v, 0, (pos + 2 * kBN) % bs, 0, it.kvh, after);
+            } else {
+              tma_load_4d(dst, &tm_k, chunk * 64, it.kvh, pos % bs, page, &full[st]);
+            }
           }
           __syncwarp();
           page = next;
+          next = after;
           pos += kBN;
           if (++st == (uint32_t)stages) {
             st = 0;
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = dry ? 128 : min(128, all - row0);
       if (rows > 0 && lo0 < it.kv_hi) {
         const bool warp_active = (warp & 3) * 32 < rows;  // its other rows are padding
-        const int prefix = it.ctx - it.q_len, hidden = dry ? kBN : first_hidden<CAUSAL>(it);
+        const int prefix = it.ctx - it.q_len, seen = dry ? kBN : min(first_hidden<CAUSAL>(it), it.kv_hi);  // by all rows
         const int tl = min(it.t0 + (row0 + r) / G, it.q_len - 1);  // (padding rows: the last token's)
         float ref = 0.f, l = 0.f;  // the weights' reference exponent and their sum
         for (int lo = lo0; lo < it.kv_hi; lo += dt, n += !dry) {
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 64; ++c)
                   u[c / 32][c % 32] = __float_as_uint(__uint_as_float(u[c / 32][c % 32]) * c2);
               }
-              if (lo + c0 + 64 > min(hidden, it.kv_hi)) {
+              if (__builtin_expect(lo + c0 + 64 > seen, 0)) {
                 const unsigned long long bits =
                     CAUSAL ? span_causal_bits(lo + c0, prefix + tl)
                            : span_bits(p.mask, p.mask_words, it.q_start + tl, lo + c0, prefix, it.ctx);
