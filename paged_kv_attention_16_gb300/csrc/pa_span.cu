@@ -24,6 +24,7 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeGroups = kMergeThreads / 8;
+constexpr int kMergeCache = 1024;  // requests whose starts the merge keeps in shared memory
 
 // ---------------------------------------------------------------------------
 // planner: one block
@@ -335,69 +336,197 @@ __device__ inline void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float a, float 
 // The larger one, but a NaN stays.
 __device__ inline float max_nan(float a, float b) { return b > a || b != b ? b : a; }
 
+// Where the partials of one row lie.
+struct SpanRow {
+  unsigned u0, len;     // its unit's laid-out work
+  int c0, n;            // its first block, and the partials that there may be
+  int w, ntile, blk_end, br;
+  long long unit;
+  bool pairs;
+};
+
+// Row of token i and head h of request r.  *done: a unit of more than 128 rows in one
+// piece, which the tensor-core kernel has finished.
+__device__ inline SpanRow span_locate(const SpanParams &p, const SpanPlan &plan, const SpanReq &r, int i, int h,
+                                      int lg, bool causal, bool *done) {
+  SpanRow x;
+  const int tq = kSpanRows >> lg, b = i / tq, kvh = h >> lg;
+  const bool last = b == r.nblk - 1;
+  x.br = ((i - b * tq) << lg) + (h & ((1 << lg) - 1));
+  x.unit = (long long)r.unit0 + kvh * r.nblk + b;
+  x.u0 = r.cost0 + (unsigned)kvh * r.kcost + (unsigned)b * r.ucost;
+  x.len = last ? r.ulast : r.ucost;
+  x.w = last ? r.wlast : r.wcost;
+  x.ntile = r.ntile;
+  x.c0 = (int)(x.u0 / plan.run);
+  x.blk_end = span_block_end(r, b * tq, tq, causal);
+  x.n = (int)((x.u0 + x.len - 1) / plan.run) - x.c0 + 1;
+  // (such a unit has one partial a piece, in the row's own place)
+  x.pairs = p.halves && (r.q_len - b * tq) << lg <= 128;
+  *done = false;
+  if (p.halves && !x.pairs) {
+    for (int c = x.c0; c < x.c0 + x.n; ++c) {  // (pieces before it may have no tile)
+      const int t1 = span_tile_at(p, r, min(x.u0 + x.len, (unsigned)(c + 1) * plan.run) - x.u0, x.w);
+      if (t1 == r.ntile) *done = true;
+      if (t1 > 0) break;
+    }
+  }
+  if (x.pairs) x.n *= 2;
+  return x;
+}
+
+// The e-th of them; -1: the piece has no tiles (its unit's overhead alone, or tiles
+// behind the causal end), or no second one for the second half.
+__device__ inline long long span_partial(const SpanParams &p, const SpanPlan &plan, const SpanRow &x, int e) {
+  const int c = x.c0 + (x.pairs ? e >> 1 : e), half = x.pairs ? e & 1 : 0;
+  const unsigned from = max(x.u0, (unsigned)c * plan.run) - x.u0,
+                 to = min(x.u0 + x.len, (unsigned)(c + 1) * plan.run) - x.u0;
+  const int t0 = min(max((int)from - p.overhead, 0) >> (x.w - 1), x.ntile),
+            t1 = min(max((int)to - p.overhead, 0) >> (x.w - 1), x.ntile);
+  if (min(t1 * kSpanTile, x.blk_end) <= (t0 + half) * kSpanTile) return -1;
+  return span_row(p, x.unit + c, half, x.br);
+}
+
+// ---- the sums over rows of requests whose scores are kept (up to kSpanStoredRows
+// rows): the scores are read once, four positions a thread.  OWN: each block works out
+// the rows' log-sum-exps from their partials, so that this runs beside the merge;
+// else the merge has left them.
+constexpr int kKeptChunk = 4 * kMergeThreads;
+
+template <bool OWN>
+__device__ inline void votes_kept(const SpanParams &p, int block, int blocks, int chunks) {
+  __shared__ float s_lse[kSpanStoredRows];
+  const FwdParams &f = p.f;
+  const int tid = threadIdx.x, Hk = f.num_kv_heads, lg = __ffs(f.num_heads / Hk) - 1, bs = f.block_size;
+  __threadfence();  // (the plan is done: every block of the kernel before awaited it)
+  const SpanPlan plan = *p.plan;
+  bool waited = false;
+  const int units = f.num_seqs * Hk;
+  for (long long item = block; !plan.all_bad && item < (long long)chunks * units; item += blocks) {
+    const int at = (int)(item / units) * kKeptChunk, sh = (int)(item - (long long)at / kKeptChunk * units);
+    const int s = sh / Hk, kvh = sh - s * Hk, pos = at + tid * 4;
+    const SpanReq r = p.req[s];
+    if (!r.valid || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
+    const int R = r.q_len << lg;
+    const bool mine = pos < r.ctx;
+    // (what does not wait for the sums is on its way before them)
+    const int page = mine ? __ldg(f.block_table + (size_t)s * f.max_blocks_per_seq + pos / bs) : 0;
+    if (!waited) pdl_wait();
+    waited = true;
+    const long long pad = (long long)r.ntile * kSpanTile;
+    const float *src = p.scores + r.score0 + (long long)kvh * R * pad + pos;
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (mine && i < R) x[i] = __ldcg(reinterpret_cast<const float4 *>(src + i * pad));
+    __syncthreads();  // s_lse of the item before is read
+    if (!OWN && tid < R)
+      s_lse[tid] = __ldcg(p.row_lse + (size_t)(r.q_start + (tid >> lg)) * f.num_heads + (kvh << lg) +
+                          (tid & ((1 << lg) - 1)));
+    if (OWN && tid < R) {
+      bool done;
+      const int h = (kvh << lg) + (tid & ((1 << lg) - 1));
+      const SpanRow row = span_locate(p, plan, r, tid >> lg, h, lg, true, &done);
+      float m = -INFINITY, l = 0.f;
+      for (int e = 0; e < row.n; ++e) {
+        const long long from = span_partial(p, plan, row, e);
+        const float v = from < 0 ? -INFINITY : __ldcg(p.part_lse + from);
+        if (v == -INFINITY) continue;
+        const float top = max_nan(m, v);
+        l = l * (m == top ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - top)) + (v == top ? 1.f : fast_exp2(v - top));
+        m = top;
+      }
+      if (f.sinks && m != INFINITY && m != -INFINITY) {
+        const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = max_nan(m, sink2);
+        l = l * fast_exp2(m - top) + fast_exp2(sink2 - top);
+        m = top;
+      }
+      s_lse[tid] = m == INFINITY || m == -INFINITY ? m : m + log2f(l);
+    }
+    __syncthreads();
+    // (the last token sees all of the request's pages: a bad one leaves the weights)
+    if (!mine || s_lse[R - 1] == INFINITY) continue;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < R) span_vote(x[i], s_lse[i], sum);
+#pragma unroll 4
+    for (int i = 4; i < R; ++i)
+      span_vote(__ldcg(reinterpret_cast<const float4 *>(src + i * pad)), s_lse[i], sum);
+    span_add_votes(p, r, page, kvh, pos, sum);
+  }
+  // (whatever waits for this kernel waits for the one before it too)
+  if (!waited) pdl_wait();
+}
+
+__global__ void __launch_bounds__(kMergeThreads) votes_kept_kernel(const SpanParams p, int chunks) {
+  pdl_trigger();
+  votes_kept<false>(p, blockIdx.x, gridDim.x, chunks);
+}
+
+// merge_blocks: the blocks that merge; the others sum over rows.
 template <typename T, int D, int W, int MODE>
-__global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanParams p) {
+__global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanParams p, int merge_blocks, int chunks) {
   constexpr bool VALUES = MODE != kSpanVotesOnly, CAUSAL = MODE != kSpanTree;
   constexpr int V = VALUES ? D / 32 : 1;  // float4 values a lane holds
   constexpr int ROWS = kMergeGroups / W;  // rows a block works on at a time
   __shared__ float4 s_o[W > 1 ? kMergeGroups : 1][W > 1 ? 8 * V : 1];
   __shared__ float s_m[kMergeGroups], s_l[kMergeGroups];
+  __shared__ int s_qsl[kMergeCache];
   const FwdParams &f = p.f;
-  const int S = f.num_seqs, H = f.num_heads, G = H / f.num_kv_heads;
+  const int S = f.num_seqs, H = f.num_heads, lg = __ffs(H / f.num_kv_heads) - 1;
   const int tid = threadIdx.x, lane = tid & 7, grp = tid >> 3, part = grp % W;
   pdl_trigger();
-  pdl_wait();
-  T *out = static_cast<T *>(f.out);
+  if constexpr (MODE != kSpanTree) {
+    if ((int)blockIdx.x >= merge_blocks) {
+      votes_kept<true>(p, blockIdx.x - merge_blocks, gridDim.x - merge_blocks, chunks);
+      return;
+    }
+  }
   const long long rows = (long long)f.num_tokens * H;
+  // The plan is done (every block of the kernel before awaited it): a block of one
+  // step works out where its partials lie while they are made.
+  const bool early = (long long)merge_blocks * ROWS >= rows;
+  if (early) __threadfence();
+  else pdl_wait();
+  T *out = static_cast<T *>(f.out);
   const SpanPlan plan = *p.plan;
-  for (long long row0 = (long long)blockIdx.x * ROWS; row0 < rows; row0 += (long long)gridDim.x * ROWS) {
+  // a decode batch: token tok is most likely request tok's, no search
+  const bool one = S == f.num_tokens && f.max_qlen == 1;
+  const bool cached = !one && S <= kMergeCache;
+  if (cached) {
+    for (int s = tid; s < S; s += kMergeThreads) s_qsl[s] = f.qsl[s];
+    __syncthreads();
+  }
+  for (long long row0 = (long long)blockIdx.x * ROWS; row0 < rows; row0 += (long long)merge_blocks * ROWS) {
     const long long row = row0 + grp / W;
     float4 acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
-    int h = 0, n = 0, c0 = 0, br = 0, w = 1, blk_end = 0;
-    unsigned u0 = 0, len = 0;
-    long long unit = 0;
-    SpanReq r{};
-    bool pairs = false;
+    int h = 0, n = 0;
+    SpanRow at{};
     bool mine = row < rows;  // (not a row behind the last request)
     if (mine && !plan.all_bad) {
       const int tok = (int)(row / H);
-      h = (int)(row % H);
+      h = (int)(row - (long long)tok * H);
       int lo = 0, hi = S - 1;
+      if (one && p.req[tok].q_start == tok && p.req[tok].q_len == 1) lo = hi = tok;
       while (lo < hi) {  // the last request that starts at or before tok: its own
         const int mid = (lo + hi + 1) >> 1;
-        if (f.qsl[mid] <= tok) lo = mid; else hi = mid - 1;
+        if ((cached ? s_qsl[mid] : f.qsl[mid]) <= tok) lo = mid; else hi = mid - 1;
       }
-      r = p.req[lo];
+      const SpanReq r = p.req[lo];
       const int i = tok - r.q_start;
       mine = i < r.q_len;
       if (mine && r.valid) {
-        const int tq = kSpanRows / G, b = i / tq, kvh = h / G;
-        const bool last = b == r.nblk - 1;
-        br = (i - b * tq) * G + h % G;
-        unit = (long long)r.unit0 + kvh * r.nblk + b;
-        u0 = r.cost0 + (unsigned)kvh * r.kcost + (unsigned)b * r.ucost;
-        len = last ? r.ulast : r.ucost;
-        w = last ? r.wlast : r.wcost;
-        c0 = (int)(u0 / plan.run);
-        blk_end = span_block_end(r, b * tq, tq, CAUSAL);
-        n = (int)((u0 + len - 1) / plan.run) - c0 + 1;
-        // a unit of more than 128 rows has one partial a piece, in the row's own place
-        pairs = p.halves && (r.q_len - b * tq) * G <= 128;
-        if (p.halves && !pairs) {
-          // in one piece it is finished already (pieces before it may have no tile)
-          for (int c = c0; c < c0 + n; ++c) {
-            const int t1 = span_tile_at(p, r, min(u0 + len, (unsigned)(c + 1) * plan.run) - u0, w);
-            if (t1 == r.ntile) mine = false;
-            if (t1 > 0) break;
-          }
-          if (!mine) n = 0;
-        }
-        if (pairs) n *= 2;
+        bool done;
+        at = span_locate(p, plan, r, i, h, lg, CAUSAL, &done);
+        n = done ? 0 : at.n;
+        if (done) mine = false;
       }
     }
+    if (early) pdl_wait();  // the partials
     for (int e0 = part; e0 < n; e0 += 4 * W) {
       float lse[4];
       float4 x[4][V];
@@ -405,16 +534,11 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
       for (int u = 0; u < 4; ++u) {
         const int e = e0 + u * W;
         lse[u] = -INFINITY;
-        if (e >= n) continue;
-        const int c = c0 + (pairs ? e >> 1 : e), half = pairs ? e & 1 : 0;
-        // the piece's tiles (it may have none: the overhead alone, or behind the causal end)
-        const unsigned from = max(u0, (unsigned)c * plan.run), to = min(u0 + len, (unsigned)(c + 1) * plan.run);
-        const int t0 = span_tile_at(p, r, from - u0, w), t1 = span_tile_at(p, r, to - u0, w);
-        if (min(t1 * kSpanTile, blk_end) <= (t0 + half) * kSpanTile) continue;
-        const long long at = span_row(p, unit + c, half, br);
-        lse[u] = __ldcg(p.part_lse + at);
+        const long long from = e < n ? span_partial(p, plan, at, e) : -1;
+        if (from < 0) continue;
+        lse[u] = __ldcg(p.part_lse + from);
         if constexpr (VALUES) {
-          const float *src = p.part_o + at * D + lane * 4;
+          const float *src = p.part_o + from * D + lane * 4;
 #pragma unroll
           for (int v = 0; v < V; ++v) x[u][v] = __ldcg(reinterpret_cast<const float4 *>(src + v * 32));
         }
@@ -517,7 +641,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
 }
 
 template <typename T, int D, int MODE>
-cudaError_t launch_merge_d(const SpanParams &p, long long most, cudaStream_t st) {
+cudaError_t launch_merge_d(const SpanParams &p, long long most, int most_rows, cudaStream_t st) {
   // Groups a row: as many as the SMs hold at once (two blocks each), and no more
   // than a row's partials fill, four at a time.
   const long long rows = (long long)p.f.num_tokens * p.f.num_heads, sms = p.num_sms;
@@ -526,8 +650,26 @@ cudaError_t launch_merge_d(const SpanParams &p, long long most, cudaStream_t st)
   auto kern = W == 16 ? span_merge_kernel<T, D, 16, MODE>
               : W == 8 ? span_merge_kernel<T, D, 8, MODE>
               : W == 4 ? span_merge_kernel<T, D, 4, MODE> : span_merge_kernel<T, D, 1, MODE>;
-  const long long blocks = std::min(ceil_div_ll(rows * W, kMergeGroups), sms * 8);
-  return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p);
+  long long blocks = std::min(ceil_div_ll(rows * W, kMergeGroups), sms * 8);
+  if (MODE == kSpanTree)
+    return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p, (int)blocks, 0);
+  // The sums over rows of kept scores beside the merge where the two blocks an SM that
+  // its registers leave hold them at once (4 decodes of up to 1000 positions 17.8 us,
+  // 20.5 behind it); else behind it, eight blocks an SM (64 decodes of up to 8192
+  // positions 219 us, 242 beside it).
+  const long long chunks = ceil_div_ll(std::max(p.f.max_seq_len, 1), kKeptChunk);
+  const long long items = chunks * p.f.num_seqs * p.f.num_kv_heads;
+  if (items + blocks <= 2 * sms) {
+    // (without an output the merge is for rows whose scores are not kept)
+    if (MODE == kSpanVotesOnly && most_rows <= kSpanStoredRows) blocks = 0;
+    return launch_dependent(kern, dim3((unsigned)(blocks + items)), dim3(kMergeThreads), 0, st, p, (int)blocks,
+                            (int)chunks);
+  }
+  const cudaError_t e =
+      launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p, (int)blocks, (int)chunks);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(votes_kept_kernel, dim3((unsigned)std::min(items, 8 * sms)), dim3(kMergeThreads), 0, st,
+                          p, (int)chunks);
 }
 
 template <int D, int MODE>
@@ -546,13 +688,13 @@ cudaError_t launch_pass(const SpanParams &p, cudaStream_t st) {
 }
 
 template <int MODE>
-cudaError_t launch_merge(const SpanParams &p, long long most, cudaStream_t st) {
+cudaError_t launch_merge(const SpanParams &p, long long most, int most_rows, cudaStream_t st) {
   const bool bf16 = p.f.dtype == PA_BF16;
   if (p.f.head_dim == 128)
-    return bf16 ? launch_merge_d<__nv_bfloat16, 128, MODE>(p, most, st)
-                : launch_merge_d<float, 128, MODE>(p, most, st);
-  return bf16 ? launch_merge_d<__nv_bfloat16, 64, MODE>(p, most, st)
-              : launch_merge_d<float, 64, MODE>(p, most, st);
+    return bf16 ? launch_merge_d<__nv_bfloat16, 128, MODE>(p, most, most_rows, st)
+                : launch_merge_d<float, 128, MODE>(p, most, most_rows, st);
+  return bf16 ? launch_merge_d<__nv_bfloat16, 64, MODE>(p, most, most_rows, st)
+              : launch_merge_d<float, 64, MODE>(p, most, most_rows, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -708,18 +850,19 @@ pa_status span_call(const SpanCall &sc) {
   err = launch_pass<MODE>(p, st);
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
-  // partials that a row may have: a piece for each block that shares its unit
+  // partials that a row may have: two of each block that shares its unit
   const long long blocks = 2 * (ceil_div_ll(c.max_seq_len, kSpanTile) + 1);
+  // rows of a KV head that one request may have
+  const int most_rows = (int)std::min<long long>(
+      (long long)(c.max_query_len > 0 ? std::min(c.max_query_len, c.num_tokens) : c.num_tokens) *
+          (c.num_heads / c.num_kv_heads), 1 << 30);
   slot = prof_begin(PA_K_MERGE, st);
-  err = launch_merge<MODE>(p, std::min<long long>(blocks, p.grid), st);
+  err = launch_merge<MODE>(p, std::min<long long>(blocks, 2 * p.grid), most_rows, st);
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
-  if (votes) {
+  if (votes && most_rows > kSpanStoredRows) {
     slot = prof_begin(PA_K_VOTES, st);
-    // rows of a KV head that one request may have
-    const long long rows = (c.max_query_len > 0 ? std::min(c.max_query_len, c.num_tokens) : c.num_tokens) *
-                           (long long)(c.num_heads / c.num_kv_heads);
-    err = launch_votes(p, (int)std::min<long long>(rows, 1 << 30), st);
+    err = launch_votes(p, st);
     prof_end(slot, st);
     if (err != cudaSuccess) return PA_ERR_CUDA;
   }

@@ -246,9 +246,40 @@ __device__ inline unsigned long long span_causal_bits(int at, int own) {
 // The pass over keys and values on the tensor cores (bf16; mode: a SpanMode).
 cudaError_t launch_span_mma(const SpanParams &p, int mode, cudaStream_t stream);
 
-// The sums over rows of pa_forward_weights, behind the rows' log-sum-exps.
-cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream);
-// Those of requests whose scores were not kept, on the tensor cores (bf16).
+// The weight of four scores of one row; a row that sees nothing (-inf) has none.
+__device__ inline void span_vote(const float4 x, float lse, float (&sum)[4]) {
+  if (lse == -INFINITY) return;
+  sum[0] += fast_exp2(x.x - lse);
+  sum[1] += fast_exp2(x.y - lse);
+  sum[2] += fast_exp2(x.z - lse);
+  sum[3] += fast_exp2(x.w - lse);
+}
+
+// Adds `sum`, of the four positions from pos on, to their slots of `page`.  Positions
+// of the new tokens start at their sum; positions from ctx on have no slot.
+__device__ inline void span_add_votes(const SpanParams &p, const SpanReq &r, int page, int kvh, int pos,
+                                      const float (&sum)[4]) {
+  const int bs = p.f.block_size;  // (bs % 16 == 0: one page)
+  float *dst = p.weights + ((size_t)page * p.f.num_kv_heads + kvh) * bs + pos % bs;
+  const int fresh = p.accumulate ? r.ctx - r.q_len : 0;
+  if (pos + 4 <= r.ctx) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pos < fresh) x = *reinterpret_cast<const float4 *>(dst);
+    x.x = pos < fresh ? x.x + sum[0] : sum[0];
+    x.y = pos + 1 < fresh ? x.y + sum[1] : sum[1];
+    x.z = pos + 2 < fresh ? x.z + sum[2] : sum[2];
+    x.w = pos + 3 < fresh ? x.w + sum[3] : sum[3];
+    *reinterpret_cast<float4 *>(dst) = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (pos + i < r.ctx) dst[i] = (pos + i < fresh ? dst[i] : 0.f) + sum[i];
+  }
+}
+
+// The sums over rows of requests whose scores were not kept, behind the rows'
+// log-sum-exps: on CUDA cores (fp32) or, for launch_votes_mma, the tensor cores (bf16).
+cudaError_t launch_votes(const SpanParams &p, cudaStream_t stream);
 cudaError_t launch_votes_mma(const SpanParams &p, cudaStream_t stream);
 
 }  // namespace pa

@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = f.num_heads / f.num_kv_heads, TQ = 128 / G, bs = f.block_size, lg = __ffs(G) - 1;
   if (smem_u32(smem) & 1023) {  // the same for every thread: all leave together
     if (tid == 0) atomicOr(f.status, PA_DEV_INTERNAL);
+    pdl_wait();  // (the merge counts on the plan being done)
     return;
   }
   if (tid == 0) {

@@ -17,78 +17,11 @@ __device__ inline float vote(float score, float lse) {
   return lse == -INFINITY ? 0.f : fast_exp2(score - lse);
 }
 
-// Adds `sum`, of the four positions from pos on, to their slots.  Positions of the
-// new tokens start at their sum; positions from ctx on have no slot.
-__device__ inline void add_votes(const SpanParams &p, const SpanReq &r, const int32_t *bt, int kvh,
-                                 int pos, const float (&sum)[4]) {
-  const FwdParams &f = p.f;
-  const int bs = f.block_size, page = __ldg(bt + pos / bs);  // (bs % 16 == 0: one page)
-  float *dst = p.weights + ((size_t)page * f.num_kv_heads + kvh) * bs + pos % bs;
-  const int fresh = p.accumulate ? r.ctx - r.q_len : 0;
-  if (pos + 4 <= r.ctx) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (pos < fresh) x = *reinterpret_cast<const float4 *>(dst);
-    x.x = pos < fresh ? x.x + sum[0] : sum[0];
-    x.y = pos + 1 < fresh ? x.y + sum[1] : sum[1];
-    x.z = pos + 2 < fresh ? x.z + sum[2] : sum[2];
-    x.w = pos + 3 < fresh ? x.w + sum[3] : sum[3];
-    *reinterpret_cast<float4 *>(dst) = x;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (pos + i < r.ctx) dst[i] = (pos + i < fresh ? dst[i] : 0.f) + sum[i];
-  }
-}
-
 // Whether the request's last row met a bad page: it sees all of them.
 __device__ inline bool request_bad(const SpanParams &p, const SpanReq &r) {
   return __ldcg(p.row_lse + (size_t)(r.q_start + r.q_len - 1) * p.f.num_heads) == INFINITY;
 }
 
-// ---------------------------------------------------------------------------
-// kept scores (up to kSpanStoredRows rows): read once, four positions a thread
-// ---------------------------------------------------------------------------
-constexpr int kKeptChunk = 4 * kVoteThreads;
-
-__global__ void __launch_bounds__(kVoteThreads) votes_kept_kernel(const SpanParams p, int chunks) {
-  __shared__ float s_lse[kSpanStoredRows];
-  const FwdParams &f = p.f;
-  const int tid = threadIdx.x, H = f.num_heads, Hk = f.num_kv_heads, G = H / Hk;
-  pdl_trigger();
-  pdl_wait();
-  if (p.plan->all_bad) return;
-  const long long n = (long long)chunks * f.num_seqs * Hk;
-  for (long long item = blockIdx.x; item < n; item += gridDim.x) {
-    const int sh = (int)(item % ((long long)f.num_seqs * Hk)), s = sh / Hk, kvh = sh % Hk;
-    const int at = (int)(item / ((long long)f.num_seqs * Hk)) * kKeptChunk;
-    const SpanReq r = p.req[s];
-    if (!r.valid || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
-    const int R = r.q_len * G;
-    __syncthreads();  // s_lse of the item before is read
-    if (tid < R) s_lse[tid] = __ldcg(p.row_lse + (size_t)(r.q_start + tid / G) * H + kvh * G + tid % G);
-    const bool bad = request_bad(p, r);
-    __syncthreads();
-    const int pos = at + tid * 4;
-    if (bad || pos >= r.ctx) continue;
-    const long long pad = (long long)r.ntile * kSpanTile;
-    const float *src = p.scores + r.score0 + (long long)kvh * R * pad + pos;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < R; ++i) {
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + i * pad));
-      const float l = s_lse[i];
-      sum[0] += vote(x.x, l);
-      sum[1] += vote(x.y, l);
-      sum[2] += vote(x.z, l);
-      sum[3] += vote(x.w, l);
-    }
-    add_votes(p, r, f.block_table + (size_t)s * f.max_blocks_per_seq, kvh, pos, sum);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// more rows: the scores are multiplied out again, on CUDA cores (fp32)
-// ---------------------------------------------------------------------------
 // 64 positions x 32 rows a step, a thread 4 positions x 2 rows; a block's keys
 // stay in shared memory while all rows pass.
 constexpr int kPos = 64, kRows = 32;
@@ -186,7 +119,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
         for (int y = 0; y < kVoteThreads / 16; ++y) x += s_sum[y][tid * 4 + j];
         tot[j] = x;
       }
-      add_votes(p, r, bt, kvh, at + tid * 4, tot);
+      span_add_votes(p, r, __ldg(bt + (at + tid * 4) / bs), kvh, at + tid * 4, tot);
     }
   }
 }
@@ -205,12 +138,7 @@ cudaError_t launch_simt(const SpanParams &p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_votes(const SpanParams &p, int most_rows, cudaStream_t stream) {
-  const long long chunks = ceil_div_ll(std::max(p.f.max_seq_len, 1), kKeptChunk);
-  const long long n = chunks * p.f.num_seqs * p.f.num_kv_heads;
-  cudaError_t e = launch_dependent(votes_kept_kernel, dim3((unsigned)std::min<long long>(n, 8ll * p.num_sms)),
-                                   dim3(kVoteThreads), 0, stream, p, (int)chunks);
-  if (e != cudaSuccess || most_rows <= kSpanStoredRows) return e;
+cudaError_t launch_votes(const SpanParams &p, cudaStream_t stream) {
   if (p.f.dtype == PA_BF16) return launch_votes_mma(p, stream);
   return p.f.head_dim == 128 ? launch_simt<128>(p, stream) : launch_simt<64>(p, stream);
 }
