@@ -83,7 +83,7 @@ __device__ inline float weight_of(uint32_t key) {
 // over them count the keys' leading bits, a fourth lists what is kept; counts are summed
 // over the cluster through distributed shared memory.
 
-constexpr int kMostCluster = 8;
+constexpr int kMostCluster = 16;
 
 struct SelectShared {
   alignas(16) unsigned hist[kBins];
@@ -370,11 +370,6 @@ __device__ inline unsigned load_acquire(const unsigned *p) {
   return v;
 }
 
-// 16 bytes from global to shared memory, past L1.
-__device__ inline void copy16(uint4 *dst, const uint8_t *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
 __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const EvictArgs a) {
   __shared__ uint4 s_k[kChunkPieces], s_v[kChunkPieces];
   __shared__ unsigned s_ticket;
@@ -509,7 +504,14 @@ cudaError_t launch_select(const EvictArgs &a, int num_sms, cudaStream_t st) {
   // (keys beyond 192 KB are read from memory in every pass)
   const int cached = (int)std::min<long long>(share, 48 * 1024);
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = set_smem_attrs_once(evict_select_kernel, 48 * 1024 * 4, done);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  if (dev >= 64 || !(done.load(std::memory_order_acquire) & 1ull << dev)) {  // (16 is beyond the portable 8)
+    const cudaError_t n =
+        cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (n != cudaSuccess) return n;
+  }
+  const cudaError_t e = set_smem_attrs_once(evict_select_kernel, 48 * 1024 * 4, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((units + 1) * C));

@@ -41,6 +41,11 @@ __device__ inline long long row_offset(const int32_t *bt, int pos, int h, int Hk
   return row_at(page, slot, h, Hk, bs, hnd) * head_bytes;
 }
 
+// 16 bytes from global to shared memory, past L1.
+__device__ inline void copy16(uint4 *dst, const uint8_t *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // One block (all THREADS threads of it): lens(s, before, after) for every request,
 // once, and the pages from ceil(after / bs) to ceil(before / bs) of each listed in
 // request order.

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
 // lies below everything that later steps read.  The block of KV head 0 writes the new
 // length; a second launch lists the pages from the lengths.
 constexpr int kAcceptThreads = 128;
-constexpr int kAcceptPieces = 4;  // 16-byte pieces of K, and of V, that a thread has in flight
+constexpr int kAcceptPieces = 4;  // 16-byte pieces of K, and of V, that a thread copies at a time
 
 struct AcceptArgs {
   uint8_t *k_cache, *v_cache;
@@ -210,6 +210,7 @@ __device__ inline bool path_rises(const int32_t *path, int n, int q_len, int tid
 }
 
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs a) {
+  __shared__ uint4 s_k[kAcceptThreads * kAcceptPieces], s_v[kAcceptThreads * kAcceptPieces];
   const int tid = threadIdx.x, bs = a.block_size, Hk = a.num_kv_heads, ppr = a.head_bytes / 16;  // pieces a row
   pdl_trigger();
   pdl_wait();
@@ -232,8 +233,9 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
     const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
     const int total = n * ppr;
     for (int e0 = 0; e0 < total; e0 += kAcceptThreads * kAcceptPieces) {
+      __syncthreads();  // the rows of the step before are written
       // (the pieces' path entries, pages and rows: three latencies for all of them)
-      int row[kAcceptPieces], from[kAcceptPieces], src[kAcceptPieces], dst[kAcceptPieces];
+      int row[kAcceptPieces], from[kAcceptPieces], page[kAcceptPieces];
 #pragma unroll
       for (int u = 0; u < kAcceptPieces; ++u) {
         const int e = e0 + u * kAcceptThreads + tid;
@@ -242,37 +244,35 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
         if (e >= total) from[u] = row[u];  // (stays where it is)
       }
 #pragma unroll
-      for (int u = 0; u < kAcceptPieces; ++u) {
-        src[u] = __ldg(bt + divide(prefix + from[u], a.by_bs));
-        dst[u] = __ldg(bt + divide(prefix + row[u], a.by_bs));
-      }
-      uint4 k[kAcceptPieces], v[kAcceptPieces];
+      for (int u = 0; u < kAcceptPieces; ++u) page[u] = __ldg(bt + divide(prefix + from[u], a.by_bs));
 #pragma unroll
       for (int u = 0; u < kAcceptPieces; ++u) {
         if (from[u] == row[u]) continue;
-        if (src[u] < 0 || src[u] >= a.num_blocks || dst[u] < 0 || dst[u] >= a.num_blocks) {
+        if (page[u] < 0 || page[u] >= a.num_blocks) {
           bad = PA_DEV_BAD_BLOCK;
           from[u] = row[u];
           continue;
         }
-        const int pos = prefix + from[u], c = e0 + u * kAcceptThreads + tid - row[u] * ppr;
-        const long long at = row_at(src[u], pos - divide(pos, a.by_bs) * bs, h, Hk, bs, a.hnd) * a.head_bytes + c * 16;
-        k[u] = *reinterpret_cast<const uint4 *>(a.k_cache + at);
-        v[u] = *reinterpret_cast<const uint4 *>(a.v_cache + at);
+        const int i = u * kAcceptThreads + tid, pos = prefix + from[u], c = e0 + i - row[u] * ppr;
+        const long long at = row_at(page[u], pos - divide(pos, a.by_bs) * bs, h, Hk, bs, a.hnd) * a.head_bytes + c * 16;
+        copy16(s_k + i, a.k_cache + at);
+        copy16(s_v + i, a.v_cache + at);
       }
-      // (the barrier's operand needs every loaded value: the rows are read when it opens)
-      unsigned seen = 0;
 #pragma unroll
-      for (int u = 0; u < kAcceptPieces; ++u)
-        if (from[u] != row[u]) seen ^= k[u].x ^ v[u].x;
-      __syncthreads_or(seen);
+      for (int u = 0; u < kAcceptPieces; ++u) page[u] = __ldg(bt + divide(prefix + row[u], a.by_bs));
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();  // all of the step's rows are read
 #pragma unroll
       for (int u = 0; u < kAcceptPieces; ++u) {
         if (from[u] == row[u]) continue;
-        const int pos = prefix + row[u], c = e0 + u * kAcceptThreads + tid - row[u] * ppr;
-        const long long at = row_at(dst[u], pos - divide(pos, a.by_bs) * bs, h, Hk, bs, a.hnd) * a.head_bytes + c * 16;
-        *reinterpret_cast<uint4 *>(a.k_cache + at) = k[u];
-        *reinterpret_cast<uint4 *>(a.v_cache + at) = v[u];
+        if (page[u] < 0 || page[u] >= a.num_blocks) {
+          bad = PA_DEV_BAD_BLOCK;
+          continue;
+        }
+        const int i = u * kAcceptThreads + tid, pos = prefix + row[u], c = e0 + i - row[u] * ppr;
+        const long long at = row_at(page[u], pos - divide(pos, a.by_bs) * bs, h, Hk, bs, a.hnd) * a.head_bytes + c * 16;
+        *reinterpret_cast<uint4 *>(a.k_cache + at) = s_k[i];
+        *reinterpret_cast<uint4 *>(a.v_cache + at) = s_v[i];
       }
     }
   }
