@@ -122,12 +122,12 @@ __device__ inline unsigned select_scan(SelectShared &sh, unsigned v, int turn, u
 
 // The weight of one position (NaN on a bad page), where it is not in shared memory.
 __device__ __noinline__ float read_weight(const EvictArgs &a, const int32_t *bt, int h, int pos) {
-  const int lp = divide(pos, a.by_bs), page = __ldg(bt + lp);
+  const int lp = divide(pos, a.by_bs), page = bt[lp];
   if (page < 0 || page >= a.num_blocks) {
     atomicOr(a.status, PA_DEV_BAD_BLOCK);
     return __int_as_float(0x7fc00000);
   }
-  return __ldg(a.weights + ((long long)page * a.num_kv_heads + h) * a.block_size + (pos - lp * a.block_size));
+  return a.weights[((long long)page * a.num_kv_heads + h) * a.block_size + (pos - lp * a.block_size)];
 }
 
 // cached: keys that the dynamic shared memory holds (the others are made again)
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
   if (flags) return;  // (the last cluster reports it; the same for the whole cluster)
   const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
   auto slot_of = [&](int pos) -> long long {  // of a weight; -1: a bad page
-    const int lp = divide(pos, a.by_bs), page = __ldg(bt + lp);
+    const int lp = divide(pos, a.by_bs), page = bt[lp];
     if (page < 0 || page >= a.num_blocks) {
       flags |= PA_DEV_BAD_BLOCK;
       return -1;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int pos = base + u * kSelectThreads;
-        page[u] = pos < c1 ? __ldg(bt + divide(pos, a.by_bs)) : 0;
+        page[u] = pos < c1 ? bt[divide(pos, a.by_bs)] : 0;
       }
       float w[U];
 #pragma unroll
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
         w[u] = __int_as_float(0x7fc00000);
         if (!ok) flags |= PA_DEV_BAD_BLOCK;
         else if (pos < c1)
-          w[u] = __ldg(a.weights + ((long long)page[u] * Hk + h) * bs + (pos - divide(pos, a.by_bs) * bs));
+          w[u] = a.weights[((long long)page[u] * Hk + h) * bs + (pos - divide(pos, a.by_bs) * bs)];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -386,24 +386,24 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     int lo = 0, hi = a.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(a.chunk_end + mid) > t) hi = mid; else lo = mid + 1;
+      if (a.chunk_end[mid] > t) hi = mid; else lo = mid + 1;
     }
-    const int s = lo, after = min(__ldg(a.seq_lens + s), __ldg(a.keep_lens + s));
+    const int s = lo, after = min(a.seq_lens[s], a.keep_lens[s]);
     const int nc = divide(after + a.chunk_rows - 1, a.by_rows);
-    const int local = (int)(t - (__ldg(a.chunk_end + s) - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
+    const int local = (int)(t - (a.chunk_end[s] - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
     const int unit = s * Hk + h;
     const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
     const int32_t *kept = a.kept + (size_t)unit * a.max_seq_len;
     unsigned *ready = a.ready + (size_t)unit * a.max_chunks;
     const int i0 = c * a.chunk_rows, rows = min(a.chunk_rows, after - i0);
-    const int below = __ldg(a.below + (size_t)unit * a.max_chunks + c);
+    const int below = a.below[(size_t)unit * a.max_chunks + c];
     // -- this chunk's rows into shared memory
     unsigned flags = 0;
 #pragma unroll
     for (int u = 0; u < kMovePieces; ++u) {
       const int e = u * kMoveThreads + tid, row = divide(e, a.by_ppr), piece = e - row * ppr;
       if (row >= rows) continue;
-      const int src = __ldg(kept + i0 + row);
+      const int src = kept[i0 + row];
       if (src == i0 + row) continue;
       const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
       if (from < 0) continue;
@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     }
     // -- meanwhile its weights (select has read them all)
     for (int i = i0 + tid; i < i0 + rows; i += kMoveThreads) {
-      const int from = __ldg(kept + i), page = __ldg(bt + divide(from, a.by_bs)),
-                lp = divide(i, a.by_bs), into = __ldg(bt + lp);
+      const int from = kept[i], page = bt[divide(from, a.by_bs)],
+                lp = divide(i, a.by_bs), into = bt[lp];
       if (page >= 0 && page < a.num_blocks && into >= 0 && into < a.num_blocks)
         a.weights_out[((long long)into * Hk + h) * bs + (i - lp * bs)] = a.kept_w[(size_t)unit * a.max_seq_len + i];
     }
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
       for (int u = 0; u < kMovePieces; ++u) {
         const int e = u * kMoveThreads + tid, row = divide(e, a.by_ppr), piece = e - row * ppr;
         if (row >= rows) continue;
-        const int src = __ldg(kept + i0 + row);
+        const int src = kept[i0 + row];
         if (src == i0 + row) continue;
         const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
         const long long into = row_offset(bt, i0 + row, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);

@@ -36,7 +36,7 @@ __device__ inline long long row_at(int page, int slot, int h, int Hk, int bs, in
 // Byte offset of KV head h's row at position pos; -1 where the page id is bad.
 __device__ inline long long row_offset(const int32_t *bt, int pos, int h, int Hk, int bs, FastDiv by_bs,
                                        int num_blocks, int hnd, int head_bytes) {
-  const int lp = divide(pos, by_bs), slot = pos - lp * bs, page = __ldg(bt + lp);
+  const int lp = divide(pos, by_bs), slot = pos - lp * bs, page = bt[lp];
   if (page < 0 || page >= num_blocks) return -1;
   return row_at(page, slot, h, Hk, bs, hnd) * head_bytes;
 }
@@ -84,7 +84,7 @@ __device__ inline void list_free_pages(const FreeList &list, const int32_t *bloc
         if (s_end[mid] > e) hi = mid; else lo = mid + 1;
       }
       const int i = (int)(e - (s_end[lo] - s_n[lo]));
-      int page = __ldg(block_table + (size_t)(base + lo) * max_blocks_per_seq + s_page[lo] + i);
+      int page = block_table[(size_t)(base + lo) * max_blocks_per_seq + s_page[lo] + i];
       if (page < 0 || page >= num_blocks) {
         page = -1;
         flags |= PA_DEV_BAD_BLOCK;

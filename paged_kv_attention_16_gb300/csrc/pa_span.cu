@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
           bool in = pos < it.kv_hi;
           size_t row = 0;
           if (in) {
-            const int page = __ldg(bt + pos / bs), slot = pos % bs;
+            const int page = bt[pos / bs], slot = pos % bs;
             if (page < 0 || page >= f.num_blocks) {
               bad = 1;
               in = false;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
             if (in && pos >= prefix) {
               const int n = pos - prefix;  // as a new token
               if constexpr (CAUSAL) seen = n <= tl;
-              else seen = (__ldg(p.mask + (size_t)(it.q_start + tl) * p.mask_words + (n >> 6)) >> (n & 63)) & 1;
+              else seen = (p.mask[(size_t)(it.q_start + tl) * p.mask_words + (n >> 6)] >> (n & 63)) & 1;
             }
             const float sc = seen ? w[r][0] : -INFINITY;
             if constexpr (MODE != kSpanTree) {
@@ -410,7 +410,7 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
     const int R = r.q_len << lg;
     const bool mine = pos < r.ctx;
     // (what does not wait for the sums is on its way before them)
-    const int page = mine ? __ldg(f.block_table + (size_t)s * f.max_blocks_per_seq + pos / bs) : 0;
+    const int page = mine ? f.block_table[(size_t)s * f.max_blocks_per_seq + pos / bs] : 0;
     if (!waited) pdl_wait();
     waited = true;
     const long long pad = (long long)r.ntile * kSpanTile;

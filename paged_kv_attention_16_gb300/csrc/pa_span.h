@@ -115,9 +115,9 @@ __device__ inline int span_tile_at(const SpanParams &p, const SpanReq &r, unsign
 // The pieces of block `cta`: the whole units of its run first, then the end of the
 // unit that its run begins in, then the beginning of the one that it ends in.  So the
 // blocks that share a KV head of a request all begin at its first position, and what
-// one of them has brought from HBM the others find in L2 (12 trees of up to 250 tokens
-// on up to 16384 positions, whose keys and values are 280 MB: 537 us in the order of
-// the run, 487 so).
+// one of them has brought from HBM the others find in L2 more often (12 trees of up to
+// 250 tokens on up to 16384 positions, whose keys and values are 280 MB: 536 us in the
+// order of the run, 527 so; 1.3 GB of 2.7 are then read from HBM).
 struct SpanCursor {
   unsigned pos, end, u0;  // u0: where the unit begins
   int s, kvh, blk, cta;
@@ -226,11 +226,11 @@ __device__ inline unsigned long long span_bits(const unsigned long long *mask, i
   if (n0 <= -64) {
     bits = ~0ull;
   } else if (n0 < 0) {
-    bits = (__ldg(row) << -n0) | ((1ull << -n0) - 1);
+    bits = (row[0] << -n0) | ((1ull << -n0) - 1);
   } else {
     const int w = n0 >> 6, sh = n0 & 63;
-    bits = w < words ? __ldg(row + w) >> sh : 0ull;
-    if (sh && w + 1 < words) bits |= __ldg(row + w + 1) << (64 - sh);
+    bits = w < words ? row[w] >> sh : 0ull;
+    if (sh && w + 1 < words) bits |= row[w + 1] << (64 - sh);
   }
   const int left = ctx - at;
   if (left < 64) bits &= left <= 0 ? 0ull : (1ull << left) - 1;

@@ -94,14 +94,14 @@ __device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it,
     const int n = pos - prefix;
     if (n >= 0) {
       const bool seen = CAUSAL ? n <= tl
-                               : (__ldg(p.mask + (size_t)(it.q_start + tl) * p.mask_words + (n >> 6)) >> (n & 63)) & 1;
+                               : (p.mask[(size_t)(it.q_start + tl) * p.mask_words + (n >> 6)] >> (n & 63)) & 1;
       if (!seen) continue;
     }
-    const int page = __ldg(bt + pos / bs), slot = pos % bs;
+    const int page = bt[pos / bs], slot = pos % bs;
     const size_t at = (p.hnd ? ((size_t)page * Hk + it.kvh) * bs + slot : ((size_t)page * bs + slot) * Hk + it.kvh) * D;
     const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.v_cache) + at);
     bool odd = false;
-    for (int c = 0; c < D / 8; ++c) odd |= not_finite(__ldg(v + c));
+    for (int c = 0; c < D / 8; ++c) odd |= not_finite(v[c]);
     if (!odd) continue;
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(p.k_cache) + at;
     const __nv_bfloat16 *vv = static_cast<const __nv_bfloat16 *>(p.v_cache) + at;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto page_of = [&](int pos) {
           int page = f.num_blocks;  // past the pool: zeros
           if (lane < nb && pos < it.kv_hi) {
-            const int x = __ldg(bt + pos / bs);
+            const int x = bt[pos / bs];
             if (x >= 0 && x < f.num_blocks) {
               page = x;
             } else {  // marks all of the piece's rows

@@ -36,7 +36,7 @@ struct MaskArgs {
 constexpr int kRoot = -1, kBadParent = -2;
 
 __device__ inline int parent_of(const MaskArgs &a, int q0, int i) {
-  const int up = __ldg(a.parents + q0 + i);
+  const int up = a.parents[q0 + i];
   return up >= i || up < -1 ? kBadParent : up;
 }
 
@@ -203,7 +203,7 @@ __device__ inline int accepted_len(const AcceptArgs &a, int s, int &prefix, int 
 __device__ inline bool path_rises(const int32_t *path, int n, int q_len, int tid) {
   bool ok = true;
   for (int i = tid; i < n; i += kAcceptThreads) {
-    const int x = __ldg(path + i), last = i > 0 ? __ldg(path + i - 1) : -1;
+    const int x = path[i], last = i > 0 ? path[i - 1] : -1;
     ok &= x > last && x < q_len;
   }
   return ok;
@@ -240,11 +240,11 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
       for (int u = 0; u < kAcceptPieces; ++u) {
         const int e = e0 + u * kAcceptThreads + tid;
         row[u] = divide(min(e, total - 1), a.by_ppr);
-        from[u] = __ldg(path + row[u]);
+        from[u] = path[row[u]];
         if (e >= total) from[u] = row[u];  // (stays where it is)
       }
 #pragma unroll
-      for (int u = 0; u < kAcceptPieces; ++u) page[u] = __ldg(bt + divide(prefix + from[u], a.by_bs));
+      for (int u = 0; u < kAcceptPieces; ++u) page[u] = bt[divide(prefix + from[u], a.by_bs)];
 #pragma unroll
       for (int u = 0; u < kAcceptPieces; ++u) {
         if (from[u] == row[u]) continue;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
         copy16(s_v + i, a.v_cache + at);
       }
 #pragma unroll
-      for (int u = 0; u < kAcceptPieces; ++u) page[u] = __ldg(bt + divide(prefix + row[u], a.by_bs));
+      for (int u = 0; u < kAcceptPieces; ++u) page[u] = bt[divide(prefix + row[u], a.by_bs)];
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();  // all of the step's rows are read
 #pragma unroll

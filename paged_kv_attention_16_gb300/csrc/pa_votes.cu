@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
       const int j = e / (D / 4), x = e % (D / 4) * 4, pos = at + j;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (pos < r.ctx) {
-        const int page = __ldg(bt + pos / bs), slot = pos % bs;
+        const int page = bt[pos / bs], slot = pos % bs;
         const size_t row = p.hnd ? ((size_t)page * Hk + kvh) * bs + slot : ((size_t)page * bs + slot) * Hk + kvh;
         v = load4f(static_cast<const float *>(p.k_cache) + row * D + x);
       }
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
         for (int y = 0; y < kVoteThreads / 16; ++y) x += s_sum[y][tid * 4 + j];
         tot[j] = x;
       }
-      span_add_votes(p, r, __ldg(bt + (at + tid * 4) / bs), kvh, at + tid * 4, tot);
+      span_add_votes(p, r, bt[(at + tid * 4) / bs], kvh, at + tid * 4, tot);
     }
   }
 }

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     while (!dead && cur.next(p, lg, QR, it)) {
       const int32_t *bt = f.block_table + (size_t)it.s * f.max_blocks_per_seq;
       const int pos = it.at + run * box;
-      const int page = mine && pos < it.r.ctx ? __ldg(bt + pos / bs) : f.num_blocks;  // past the pool: zeros
+      const int page = mine && pos < it.r.ctx ? bt[pos / bs] : f.num_blocks;  // past the pool: zeros
       if (lane == 0) {
         if (kr > 0) mbar_wait(&bar[C::K_FREE + ks], (kr - 1) & 1, dead, f.status);
         if (!dead) mbar_arrive_expect_tx(&bar[C::K_FULL + ks], C::K_BYTES);
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         at_s = it.s;
         at_kvh = it.kvh;
       }
-      const int page = pos < it.r.ctx ? __ldg(f.block_table + (size_t)it.s * f.max_blocks_per_seq + pos / bs) : 0;
+      const int page = pos < it.r.ctx ? f.block_table[(size_t)it.s * f.max_blocks_per_seq + pos / bs] : 0;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int b = it.b0; b < it.nb; ++b, ++n) {
         const float *lse = s_lse + (few ? b : b & 1) * QR;
