@@ -699,8 +699,8 @@ size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tok
  * from or to a bad page is not moved; a bad id in the list of freed pages is
  * written as -1.  PA_DEV_OVERFLOW: more freed pages than freed_capacity; the first
  * ones are listed.
- * Asynchronous on `stream`, one launch, two with a list, no workspace; capturable
- * after the first call on a device.  Errors as for pa_cache_write.
+ * Asynchronous on `stream`, one launch, two for the list of many paths, no
+ * workspace; capturable after the first call on a device.  Errors as for pa_cache_write.
  */
 pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_table,
                           const int32_t *seq_lens, const int32_t *query_start_loc,

@@ -74,10 +74,10 @@ struct SpanParams {
   int keep_scores;
   int num_sms, grid, halves;       // halves: see span_row
   int overhead;                    // kSpanOverhead, or 0
+  int fused;                       // no planner: see span_plan_warp
   int slot_rows;
   SpanPlan *plan;
   SpanReq *req;          // [num_seqs]
-  unsigned *cost_end;    // [num_seqs] inclusive
   unsigned *vote_end;    // [num_seqs] inclusive sum of Hk * ntile where scores are not kept
   float *part_o;         // [slots * slot_rows][head_dim], normalised
   float *part_lse;       // base 2; +inf: a bad page in the piece's range
@@ -90,6 +90,67 @@ struct SpanParams {
 // of positions each: x tells them apart (else x = 0).
 __device__ inline long long span_row(const SpanParams &p, long long slot, int x, int r) {
   return slot * p.slot_rows + x * (p.slot_rows / 2) + r;
+}
+
+// Batches of up to this many requests (bf16) have no planner's launch: every block of
+// the span kernel works the plan out for itself, a request a lane (and as many as its
+// shared memory has room for).
+constexpr int kSpanFusedSeqs = 28;
+
+// Request s as its metadata say, without the sums over the requests before it; cnt:
+// its units, laid-out work, kept scores and tiles of the KV heads that are summed up
+// without them.
+__device__ inline SpanReq span_request(const SpanParams &p, int s, unsigned &flags, int &bad,
+                                       long long (&cnt)[4]) {
+  const FwdParams &f = p.f;
+  const int Hk = f.num_kv_heads, G = f.num_heads / Hk;
+  const int longest =
+      (int)min((unsigned long long)f.max_seq_len, (unsigned long long)f.max_blocks_per_seq * f.block_size);
+  const int q0 = f.qsl[s], q1 = f.qsl[s + 1];
+  if (q1 < q0 || (s == 0 && q0 != 0) || (s == f.num_seqs - 1 && q1 > f.num_tokens)) bad = 1;
+  SpanReq r{};
+  r.q_start = q0;
+  r.q_len = q1 - q0;
+  r.ctx = f.seq_lens[s];
+  const bool len_ok = r.ctx >= 0 && r.ctx <= longest;
+  const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen) &&
+                    (!p.mask || r.q_len <= 64ll * p.mask_words);
+  if (r.q_len != 0) flags |= (len_ok ? 0u : PA_DEV_BAD_SEQLEN) | (q_ok ? 0u : PA_DEV_BAD_QLEN);
+  r.valid = r.q_len > 0 && len_ok && q_ok;
+  r.score0 = -1;
+  cnt[0] = cnt[1] = cnt[2] = cnt[3] = 0;
+  if (r.valid) {
+    const long long rows = (long long)r.q_len * G;
+    r.nblk = (int)((rows + kSpanRows - 1) / kSpanRows);
+    r.ntile = (r.ctx + kSpanTile - 1) / kSpanTile;
+    r.wcost = kSpanWide;
+    r.wlast = rows - (r.nblk - 1ll) * kSpanRows > 128 ? kSpanWide : span_narrow(r.nblk, f.head_dim);
+    r.ulast = r.ntile * r.wlast + p.overhead;
+    r.ucost = r.nblk > 1 ? r.ntile * r.wcost + p.overhead : r.ulast;
+    r.kcost = (r.nblk - 1) * r.ucost + r.ulast;
+    cnt[0] = (long long)Hk * r.nblk;
+    cnt[1] = (long long)Hk * r.kcost;
+    if (p.keep_scores && rows <= kSpanStoredRows) {
+      cnt[2] = Hk * rows * r.ntile * kSpanTile;
+      r.score0 = 0;
+    } else if (p.keep_scores) {
+      cnt[3] = (long long)Hk * r.ntile;
+    }
+  }
+  return r;
+}
+
+// With the sums of cnt over the requests before it.
+__device__ inline void span_place(SpanReq &r, const long long (&before)[4]) {
+  r.unit0 = (int)before[0];
+  r.cost0 = (unsigned)before[1];
+  if (r.score0 >= 0) r.score0 = before[2];
+}
+
+// The plan over all requests' sums (the host has bounded the work by 2^31).
+__device__ inline SpanPlan span_plan_of(const SpanParams &p, const long long (&sum)[4]) {
+  const unsigned total = (unsigned)sum[1];
+  return SpanPlan{total, max((total + p.grid - 1) / p.grid, (unsigned)kSpanWide), (unsigned)sum[3], 0};
 }
 
 struct alignas(16) SpanPiece {
@@ -121,6 +182,7 @@ __device__ inline int span_tile_at(const SpanParams &p, const SpanReq &r, unsign
 struct SpanCursor {
   unsigned pos, end, u0;  // u0: where the unit begins
   int s, kvh, blk, cta;
+  const SpanReq *req;     // [num_seqs]
   SpanReq r;
   bool put_off;           // the run's first piece is part of a unit
   unsigned first_pos, first_u0;
@@ -135,11 +197,12 @@ struct SpanCursor {
     if (++kvh < p.f.num_kv_heads) return;
     kvh = 0;
     if (pos < end) {  // (then there is another request with work)
-      do r = p.req[++s]; while (r.nblk == 0);
+      do r = req[++s]; while (r.nblk == 0);
     }
   }
 
-  __device__ void start(const SpanParams &p, const SpanPlan &plan, int block) {
+  __device__ void start(const SpanParams &p, const SpanReq *requests, const SpanPlan &plan, int block) {
+    req = requests;
     cta = block;
     const unsigned long long at = (unsigned long long)block * plan.run;
     pos = (unsigned)min(at, (unsigned long long)plan.total);
@@ -151,10 +214,10 @@ struct SpanCursor {
     int lo = 0, hi = p.f.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (p.cost_end[mid] > pos) hi = mid; else lo = mid + 1;
+      if (req[mid].cost0 + (unsigned)(p.f.num_kv_heads * req[mid].kcost) > pos) hi = mid; else lo = mid + 1;
     }
     s = lo;
-    r = p.req[s];
+    r = req[s];
     unsigned rel = pos - r.cost0;
     kvh = (int)(rel / (unsigned)r.kcost);
     rel -= (unsigned)kvh * r.kcost;
@@ -199,7 +262,7 @@ struct SpanCursor {
       const unsigned n = pos < end ? unit_cost(r, blk) : 0;
       if (put_off && (pos >= end || u0 + n > end)) {  // no whole unit is left
         put_off = false;
-        const SpanReq q = p.req[first_s];
+        const SpanReq q = req[first_s];
         if (make(p, lg, causal, q, first_s, first_kvh, first_blk, first_u0, first_pos,
                  first_u0 + unit_cost(q, first_blk), it))
           return true;

@@ -60,11 +60,51 @@ struct Cfg {
                        PIECE = V_OK + VST, PIECE_FREE = PIECE + kPieces, NBAR = PIECE_FREE + kPieces;
   static constexpr int OFF_PIECE = (OFF_BAR + NBAR * 8 + 15) & ~15;
   static constexpr int OFF_MISC = OFF_PIECE + kPieces * (int)sizeof(SpanPiece);
-  static constexpr int SMEM = OFF_MISC + 144;
+  static constexpr int OFF_REQ = (OFF_MISC + 144 + 15) & ~15;  // requests, where this kernel plans
+  static constexpr int SMEM = OFF_REQ + kSpanFusedSeqs * (int)sizeof(SpanReq);
   static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kBN, 0);
   static constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, 1);
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
+
+// The plan of up to kSpanFusedSeqs requests by one warp; req: theirs, for this block.
+// `leave`: written to the workspace too, for the kernels behind this one.
+__device__ inline SpanPlan span_plan_warp(const SpanParams &p, SpanReq *req, int lane, bool leave) {
+  unsigned flags = 0;
+  int bad = 0;
+  SpanReq r{};
+  long long cnt[4] = {0, 0, 0, 0}, end[4], sum[4];
+  if (lane < p.f.num_seqs) r = span_request(p, lane, flags, bad, cnt);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    end[x] = cnt[x];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, end[x], o);
+      if (lane >= o) end[x] += y;
+    }
+    sum[x] = __shfl_sync(0xffffffffu, end[x], 31);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  flags = bad ? PA_DEV_BAD_QSL : __reduce_or_sync(0xffffffffu, flags);
+  const SpanPlan plan = bad ? SpanPlan{0, 1, 0, 1} : span_plan_of(p, sum);
+  const long long before[4] = {end[0] - cnt[0], end[1] - cnt[1], end[2] - cnt[2], end[3] - cnt[3]};
+  span_place(r, before);
+  if (lane < p.f.num_seqs) {
+    req[lane] = r;
+    if (leave) {
+      p.req[lane] = r;
+      p.vote_end[lane] = (unsigned)end[3];
+    }
+  }
+  if (leave && lane == 0) {
+    *p.plan = plan;
+    if (flags) atomicOr(p.f.status, flags);
+  }
+  __syncwarp();
+  if (leave) __threadfence();
+  return plan;
+}
 
 // The first position that some row of the piece's block may not see.
 template <bool CAUSAL>
@@ -141,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (smem_u32(smem) & 1023) {  // the same for every thread: all leave together
     if (tid == 0) atomicOr(f.status, PA_DEV_INTERNAL);
     pdl_wait();  // (the merge counts on the plan being done)
+    if (p.fused && blockIdx.x == 0 && tid == 0) *p.plan = SpanPlan{0, 1, 0, 1};
     return;
   }
   if (tid == 0) {
@@ -181,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kIssueWarp) {
     reg_dec<kOtherRegs>();
     pdl_wait();  // the plan
-    pdl_trigger();
     if (warp >= kCheck0) {
       // -------------------------------------------------- values of hidden positions
       if constexpr (VALUES) {
@@ -243,7 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The first of them makes the block's pieces and leaves them to the others; one
       // without positions ends the list.
       SpanCursor cur;
-      if (warp == kLoad0) cur.start(p, *p.plan, blockIdx.x);
+      if (warp == kLoad0) {
+        SpanReq *const s_req = reinterpret_cast<SpanReq *>(smem + C::OFF_REQ);
+        if (p.fused) cur.start(p, s_req, span_plan_warp(p, s_req, lane, blockIdx.x == 0), blockIdx.x);
+        else cur.start(p, p.req, *p.plan, blockIdx.x);
+        pdl_trigger();  // (the merge counts on the plan being done)
+      }
       auto make_piece = [&]() {
         if (!cur.next(p, lg, CAUSAL, it)) it.kv_lo = it.kv_hi = 0;
         const uint32_t at = pieces % kPieces;
