@@ -629,6 +629,10 @@ __device__ inline void plan_pass(const FwdParams &p) {
 __device__ inline void named_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// Counts as one of those that named_sync waits for, and does not wait.
+__device__ inline void named_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 
 }  // namespace pa
 

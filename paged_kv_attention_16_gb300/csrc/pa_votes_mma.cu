@@ -9,10 +9,17 @@
 // its thread sums over the columns in registers: no reduction across threads, no
 // atomics.
 //
-// Two CTAs per SM, each with 4 warps for the sums (thread = position), one issuing
-// warp and one TMA warp.  A CTA walks a run of the (request, KV head, tile of 128
-// positions) list; a tile's keys stay while the rows pass in blocks of QR, scores
-// going to two TMEM buffers in turn.  Bound by the exponentials.
+// Two CTAs per SM, each with two groups of 4 warps for the sums (thread = position),
+// one issuing warp and one TMA warp.  A CTA walks a run of the (request, KV head, tile
+// of 128 positions) list; a tile's keys stay while the rows pass in blocks of QR, whose
+// scores go to two TMEM buffers in turn, a group of warps to each.  The groups' sums
+// meet in shared memory.
+//
+// Bound by the instructions around the exponentials and the waits for the scores:
+// 16 requests of 64 tokens, 4 heads a KV head of 64, 16384 positions: 38 us (268 million
+// exponentials, 2 instructions of the 3.2 issued for each; 56 % of the issue slots, the
+// tensor cores at 22 %, 71 MB from DRAM).  One group a CTA: 42 us, its scores fetched 32
+// columns ahead; with two groups that prefetch costs registers and time (40).
 #include "pa_span.h"
 #include "pa_umma.cuh"
 
@@ -20,9 +27,9 @@ namespace pa {
 namespace {
 
 constexpr int kBN = kSpanTile;
-constexpr int kThreads = 192;
-constexpr int kIssueWarp = 4, kLoadWarp = 5;
-constexpr int kLseRows = 256;  // rows whose log-sum-exps stay while a KV head's tiles pass
+constexpr int kThreads = 320;
+constexpr int kIssueWarp = 8, kLoadWarp = 9;
+constexpr int kLseRows = 512;  // rows whose log-sum-exps stay while a KV head's tiles pass
 
 template <int D>
 struct Cfg {
@@ -35,7 +42,8 @@ struct Cfg {
   static constexpr int K_FULL = 0, K_FREE = K_FULL + KST, Q_FULL = K_FREE + KST, Q_FREE = Q_FULL + QST,
                        S_FULL = Q_FREE + QST, S_FREE = S_FULL + 2, END = S_FREE + 2, NBAR = END + 1;
   static constexpr int OFF_LSE = OFF_BAR + ((NBAR * 8 + 15) & ~15);
-  static constexpr int OFF_MISC = OFF_LSE + kLseRows * 4;
+  static constexpr int OFF_SUM = OFF_LSE + kLseRows * 4;
+  static constexpr int OFF_MISC = OFF_SUM + 2 * kBN * 4;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr uint32_t COLS = 2 * QR;  // two buffers
   static constexpr uint32_t IDESC = umma_idesc_bf16(128, QR, 0);
@@ -109,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   constexpr int QR = C::QR;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-  float *s_lse = reinterpret_cast<float *>(smem + C::OFF_LSE);  // [2][QR]
+  float *s_lse = reinterpret_cast<float *>(smem + C::OFF_LSE);  // [kLseRows] or [2 groups][2][QR]
+  float *s_sum = reinterpret_cast<float *>(smem + C::OFF_SUM);  // [2][kBN]
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   const FwdParams &f = p.f;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -206,58 +215,60 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     mbar_wait(&bar[C::END], 0, late, f.status);
     __syncwarp();
   } else {
-    const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
+    // Two groups of four warps, the one for buffer 0 and the one for buffer 1.
+    const int grp = warp >> 2, th = tid & 127;
+    const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c2 = f.scale_log2;
     // rows behind the last one, and rows without weight, add nothing
-    auto lse_of = [&](const VoteItem &v, int b) {
-      const int row = b * QR + tid;
+    auto lse_of = [&](const VoteItem &v, int row) {
       if (row >= v.r.q_len << lg) return -INFINITY;
       const float l = __ldcg(p.row_lse + (size_t)(v.r.q_start + (row >> lg)) * H + v.kvh * G + (row & (G - 1)));
       return l == -INFINITY ? l : -l;
     };
-    uint32_t n = 0;
+    uint32_t n = 0, own = 0;
     int at_s = -1, at_kvh = -1;  // whose log-sum-exps are in shared memory, all of them
-    while (cur.next(p, lg, QR, it)) {
-      const int pos = it.at + tid, R = it.r.q_len << lg, prefix = it.r.ctx - it.r.q_len;
+    for (uint32_t item = 0; cur.next(p, lg, QR, it); ++item) {
+      const int pos = it.at + th, R = it.r.q_len << lg, prefix = it.r.ctx - it.r.q_len;
       const int first = max(0, pos - prefix) << lg;  // the first row that sees this position
       const bool few = it.nb * QR <= kLseRows;
+      const int mine = it.b0 + ((n ^ grp) & 1);  // the group's first block
       float next = 0.f;
       if (!few) {
-        next = lse_of(it, it.b0);
+        if (mine < it.nb && th < QR) next = lse_of(it, mine * QR + th);
+        if (at_s >= 0) named_sync(1, 256);  // those before are read
         at_s = -1;
       } else if (it.s != at_s || it.kvh != at_kvh) {
-        named_sync(1, 128);  // those before are read
-        for (int b = 0; b < it.nb; ++b)
-          if (tid < QR) s_lse[b * QR + tid] = lse_of(it, b);
-        named_sync(1, 128);
+        named_sync(1, 256);
+        for (int row = tid; row < it.nb * QR; row += 256) s_lse[row] = lse_of(it, row);
+        named_sync(1, 256);
         at_s = it.s;
         at_kvh = it.kvh;
       }
-      const int page = pos < it.r.ctx ? f.block_table[(size_t)it.s * f.max_blocks_per_seq + pos / bs] : 0;
+      const bool store = (item & 1) == grp;  // the groups take turns
+      const int page = store && pos < it.r.ctx ? f.block_table[(size_t)it.s * f.max_blocks_per_seq + pos / bs] : 0;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int b = it.b0; b < it.nb; ++b, ++n) {
-        const float *lse = s_lse + (few ? b : b & 1) * QR;
-        if (!few) {  // (block b - 2's were read before the barrier of b - 1)
-          if (b == it.b0) named_sync(1, 128);
-          if (tid < QR) s_lse[(b & 1) * QR + tid] = next;
-          next = lse_of(it, b + 1);
-          named_sync(1, 128);
+      const uint32_t behind = n + (it.nb - it.b0);
+      n += mine - it.b0;
+      for (int b = mine; b < it.nb; b += 2, n += 2) {
+        const float *lse = s_lse + b * QR;
+        if (!few) {  // (those of two blocks of the group ago were read before the barrier of the last)
+          float *at = s_lse + (grp * 2 + (own++ & 1)) * QR;
+          if (th < QR) at[th] = next;
+          if (b + 2 < it.nb && th < QR) next = lse_of(it, (b + 2) * QR + th);
+          named_sync(2 + grp, 128);
+          lse = at;
         }
         mbar_wait(&bar[C::S_FULL + (n & 1)], (n >> 1) & 1, dead, f.status);
         tc_fence_after();
         const int all_see = max(0, it.at + kBN - 1 - prefix) << lg;  // rows from here on see the whole tile
-        // 32 columns at a time, the next ones on their way from tensor memory
-        uint32_t u[2][32];
-        tc_ld32(tm + (n & 1) * QR, u[0]);
+        uint32_t x[32];
 #pragma unroll
         for (int k = 0; k < QR / 32; ++k) {
+          tc_ld32(tm + (n & 1) * QR + k * 32, x);
           tc_wait_ld();
-          uint32_t(&x)[32] = u[k & 1];
 #pragma unroll
           for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(x[i]));
-          if (k + 1 < QR / 32) {
-            tc_ld32(tm + (n & 1) * QR + (k + 1) * 32, u[(k + 1) & 1]);
-          } else {  // the buffer is read
+          if (k + 1 == QR / 32) {  // the buffer is read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[C::S_FREE + (n & 1)]);
@@ -285,10 +296,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
           }
         }
       }
-      if (pos < it.r.ctx) {
-        float *dst = p.weights + ((size_t)page * f.num_kv_heads + it.kvh) * bs + pos % bs;
-        const float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        *dst = p.accumulate && pos < prefix ? *dst + w : w;
+      n = behind;
+      // The other group's sum.  (A group that writes here for the next item but one has
+      // stored the item between, behind the other's reading of this one.)
+      float *add = s_sum + (item & 1) * kBN + th;
+      const float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (!store) {
+        *add = w;
+        named_arrive(4 + (item & 1), 256);
+      } else {
+        named_sync(4 + (item & 1), 256);
+        if (pos < it.r.ctx) {
+          float *dst = p.weights + ((size_t)page * f.num_kv_heads + it.kvh) * bs + pos % bs;
+          const float all = *add + w;
+          *dst = p.accumulate && pos < prefix ? *dst + all : all;
+        }
       }
     }
   }
