@@ -612,7 +612,8 @@ pa_status pa_cache_write_slots(const void *k_new, const void *v_new,
  *                      below -1): that token and those below it
  * Asynchronous on `stream`, one launch, no workspace; capturable after the first
  * call on a device.  Errors: PA_ERR_INVALID_ARG for null pointers with nonzero
- * sizes, negative sizes, mask_words < 1 or pointers not aligned to their element.
+ * sizes, negative sizes, mask_words < 1 or pointers not aligned to their element;
+ * PA_ERR_UNSUPPORTED for more than 2^30 tokens.
  */
 pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_start_loc,
                         const int32_t *seq_lens, uint64_t *tree_mask,
@@ -651,7 +652,7 @@ pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_start_loc,
  * not 4-byte aligned, or a workspace that is not 256-byte aligned;
  * PA_ERR_WORKSPACE when the workspace is NULL or too small, or when the first call
  * on a device is made during capture; PA_ERR_UNSUPPORTED for extents whose units of
- * work pass 2^31.  num_tokens == 0 launches nothing.
+ * work pass 2^31, or a max_seq_len above 2^30.  num_tokens == 0 launches nothing.
  */
 pa_status pa_forward_tree(const void *q, const void *k_cache, const void *v_cache,
                           const int32_t *block_table, const int32_t *seq_lens,
@@ -692,7 +693,8 @@ size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tok
  *                   each request, in request order (a list that pa_block_tables
  *                   takes pages from); num_freed: device pointer to one int32, their
  *                   number.  Both NULL: not wanted
- *  head_dim x element size a multiple of 16 bytes, at most 16384; any block_size
+ *  head_dim x element size a multiple of 16 bytes, at most 16384 (and max_path of
+ *  them at most 2^34); any block_size
  * Bad device metadata: PA_DEV_BAD_QSL (a decreasing pair of starts),
  * PA_DEV_BAD_SEQLEN, PA_DEV_BAD_QLEN, PA_DEV_BAD_TREE (a path_len or path out of its
  * range): that request is left as it is, its length too.  PA_DEV_BAD_BLOCK: a row
@@ -790,7 +792,8 @@ size_t pa_forward_weights_workspace_bytes(pa_dtype dtype, int num_seqs,
  * PA_DEV_OVERFLOW as for pa_cache_accept.
  * Asynchronous on `stream`, two launches; capturable after the first call on a
  * device.  Errors as for pa_cache_write; PA_ERR_WORKSPACE as for pa_forward_tree;
- * PA_ERR_UNSUPPORTED also for extents beyond 2^31 moved runs.
+ * PA_ERR_UNSUPPORTED also for extents beyond 2^31 moved runs, or a max_seq_len above
+ * 2^30.
  */
 pa_status pa_cache_evict(void *k_cache, void *v_cache, const float *weights,
                          float *weights_out, const int32_t *block_table,

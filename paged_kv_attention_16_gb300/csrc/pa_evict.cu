@@ -19,6 +19,7 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+constexpr int kMaxEvictLen = 1 << 30;  // positions some steps behind the end count in 32 bits
 constexpr int kSelectThreads = 1024;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMoveThreads = 256;
@@ -477,7 +478,7 @@ EvictLayout evict_layout(int head_bytes, int num_seqs, int num_kv_heads, int max
   const long long S = std::max(num_seqs, 1), units = S * num_kv_heads, msl = std::max(max_seq_len, 1);
   l.chunk_rows = std::max(1, kChunkPieces / std::max(head_bytes / 16, 1));
   l.max_chunks = (int)ceil_div_ll(msl, l.chunk_rows);
-  l.ok = units < (1ll << 30) && units * l.max_chunks < (1ll << 31);
+  l.ok = units < (1ll << 30) && units * l.max_chunks < (1ll << 31) && msl <= kMaxEvictLen;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;

@@ -684,7 +684,7 @@ SpanLayout span_layout(int dtype, int num_seqs, int num_tokens, int num_heads, i
   const long long units =
       Hk * std::min(ceil_div_ll(T * G, kSpanRows) + S, S * ceil_div_ll(most * G, kSpanRows));
   const long long tiles = ceil_div_ll(msl, kSpanTile) * kSpanWide + kSpanOverhead;
-  l.ok = units * tiles < (1ll << 31) - (1 << 20);
+  l.ok = units * tiles < (1ll << 31) - (1 << 20) && msl <= kSpanMaxLen;
   // two rows of partials for each row of a unit of up to 128
   l.slot_rows = most * G <= 128 ? (int)(2 * ceil_div_ll(most * G, 4) * 4) : kSpanRows;
   const long long slots = units + kMaxGrid;

@@ -15,6 +15,8 @@
 
 namespace pa {
 
+// Longest context taken: positions some tiles behind its end still count in 32 bits.
+constexpr int kSpanMaxLen = 1 << 30;
 constexpr int kSpanRows = 256;
 constexpr int kSpanTile = 128;
 // Work is laid out in half tiles: a tile of a unit of more than 128 rows, which keeps

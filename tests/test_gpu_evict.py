@@ -73,6 +73,21 @@ def test_windows_of_rows(n, dtype, output):
     check_votes([n, n], [n, n + 300], (8, 2, 64, 16), dtype, seed=n, output=output, accumulate=False)
 
 
+@pytest.mark.parametrize("output", [True, False])
+@pytest.mark.parametrize("shape", [(16, 1, 64, 16), (8, 2, 128, 32), (4, 2, 64, 64)])
+def test_windows_of_all_sizes_in_one_call(shape, output):
+    """Kept scores, rows whose sums stay in shared memory and rows whose sums pass."""
+    check_votes([1, 150, 40, 300, 9, 0, 33, 200], [700, 150, 41, 900, 500, 8, 260, 1000], shape, "bf16", "nhd", 44,
+                output=output)
+
+
+@pytest.mark.parametrize("S", [28, 29])
+def test_batches_around_the_planned_sizes(S):
+    rng = np.random.default_rng(S)
+    q = rng.integers(0, 12, S)
+    check_votes(q.tolist(), (q + rng.integers(0, 500, S)).tolist(), (8, 2, 64, 16), seed=S)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_whole_prompt(dtype):
     check_votes([300], [300], (4, 2, 64, 16), dtype, seed=4)
@@ -361,6 +376,26 @@ def test_evict_without_a_list_on_another_stream():
     torch.cuda.synchronize()
     assert after.tolist() == [100, 300] and pa.pa_get_device_status(st) == 0
     assert np.array_equal(inputs.storage_array(d.k_cache.cpu()), want[0])
+
+
+def test_evict_offsets_past_32_bits():
+    """Pages whose element offsets pass 2^31."""
+    Hk, D, bs = 8, 128, 64
+    pages = (1 << 31) // (bs * Hk * D) + 40
+    b, w = evict_case(17, [180], Hk, D, bs)
+    want = orc.cache_evict(inputs.storage_array(b.k_cache), inputs.storage_array(b.v_cache), w, w,
+                           b.block_table.numpy(), b.seq_lens.numpy(), [70], bs, b.num_blocks, 10, 180, 2, 9)
+    far, old = torch.tensor([pages - 1, pages - 7, pages - 3]), b.block_table[0, :3].long()
+    k = torch.zeros((pages, bs, Hk, D), dtype=torch.bfloat16, device="cuda")
+    v, d_w = torch.zeros_like(k), torch.zeros((pages, Hk, bs), device="cuda")
+    at = far.cuda()
+    k[at], v[at], d_w[at] = b.k_cache[old].cuda(), b.v_cache[old].cuda(), torch.from_numpy(w)[old].cuda()
+    after = i32([0])
+    pa.pa_cache_evict(k, v, d_w, far.to(torch.int32).view(1, 3).cuda(), b.seq_lens.cuda(), i32([70]), after, bs,
+                      max_seq_len=180, num_first=2, num_recent=9)
+    assert pa.pa_get_device_status() == 0 and after.tolist() == [70]
+    for got, ref in ((k, want[0]), (v, want[1]), (d_w, want[2])):
+        assert np.array_equal(inputs.storage_array(got[at].cpu()), ref[old.numpy()])
 
 
 def test_evictions_captured_and_replayed_at_once():

@@ -147,6 +147,32 @@ def test_many_requests():
     check_tree(q, rng.integers(0, 90, 300).tolist(), (4, 2, 64, 16), seed=9)
 
 
+@pytest.mark.parametrize("S", [27, 28, 29, 32, 33])
+def test_batches_around_the_planned_sizes(S):
+    """Up to 28 requests are planned in the kernel itself."""
+    rng = np.random.default_rng(S)
+    q = rng.integers(0, 20, S).tolist()
+    q[-1] = 0 if S % 2 else 3
+    check_tree(q, rng.integers(0, 400, S).tolist(), (8, 2, 64, 16), seed=S)
+
+
+@pytest.mark.parametrize("S", [28, 40])
+def test_bad_requests_among_many(S):
+    q_lens = [6] * S
+    b = spans.batch(q_lens, [90] * S, 8, 2, 64, 16, seed=S)
+    mask = np.full((6 * S, 1), 0x3f, np.uint64)
+    want = spans.oracle(b, mask)
+    b.seq_lens[S - 1] = 5
+    b.seq_lens[3] = b.max_seq_len + 1
+    b.block_table[9, 2] = b.num_blocks
+    got = spans.run_tree(b, mask, expect=7)
+    b.seq_lens[S - 1] = b.seq_lens[3] = 90
+    zero_rows(b, got, want, {3, 9, S - 1}, "bf16")
+    spans.check_out(b, got, want, "bf16")
+    b.query_start_loc[S // 2] = 1
+    assert not spans.run_tree(b, mask, expect=pa.PA_DEV_BAD_QSL).any()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_any_mask(dtype):
     """Masks that are no trees: later tokens seen, own ones hidden, rows without any."""
@@ -504,6 +530,83 @@ def test_accept_list_overflow_and_no_list():
     pa.pa_cache_accept(d.k_cache, d.v_cache, d.block_table, d.seq_lens, d.query_start_loc, i32(path),
                        i32(lens), after, 16)
     assert after.tolist() == [5 + lens[0], 9 + lens[1]] and pa.pa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("S,n", [(1, 1), (256, 8), (257, 8), (64, 32), (65, 32)])
+def test_accept_lists_in_one_launch_or_two(S, n):
+    b, path, lens = accept_case(S + n, [n] * S, [11] * S, 1, 64, 16, "bf16", "nhd", n)
+    check_accept(b, path, lens, expect=0)
+
+
+def test_accept_bad_paths_leave_their_pages():
+    b, path, lens = accept_case(33, [40] * 30, [16] * 30, 2, 64, 16, "bf16", "hnd", 8)
+    lens[:] = 3
+    path[:, :3] = [0, 7, 39]
+    path[4, 1] = 0
+    path[9, 2] = 40
+    lens[11] = 9
+    b.block_table[20, 3] = b.num_blocks
+    want = check_accept(b, path, lens, expect=0x101)
+    assert want[2][4] == want[2][9] == want[2][11] == 56 and want[2][5] == 19
+
+
+def test_accepts_captured_and_on_two_streams():
+    cases = []
+    for seed in (34, 35):
+        b, path, lens = accept_case(seed, [30] * 20, [50] * 20, 2, 128, 16, "bf16", "nhd", 12)
+        want = orc.cache_accept(inputs.storage_array(b.k_cache), inputs.storage_array(b.v_cache),
+                                b.block_table.numpy(), b.seq_lens.numpy(), b.query_start_loc.numpy(), path,
+                                lens, 16, b.num_blocks, 200, "nhd")
+        d, after, freed, count = pa.to_device(b), i32([0] * 20), i32([-9] * 200), i32([-9])
+        d_path, d_lens, st = i32(path), i32(lens), torch.cuda.Stream()
+        saved = d.k_cache.clone(), d.v_cache.clone()
+
+        def call(d=d, p=d_path, n=d_lens, after=after, freed=freed, count=count):
+            pa.pa_cache_accept(d.k_cache, d.v_cache, d.block_table, d.seq_lens, d.query_start_loc, p, n, after,
+                               16, freed_pages=freed, num_freed=count)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        cases.append((want, d, saved, after, freed, count, st, g, d_path, d_lens))
+    for _ in range(3):
+        for _, d, saved, after, freed, count, *_ in cases:
+            d.k_cache.copy_(saved[0])
+            d.v_cache.copy_(saved[1])
+            for t in (after, freed, count):
+                t.fill_(-9)
+        torch.cuda.synchronize()
+        for c in cases:
+            with torch.cuda.stream(c[6]):
+                c[7].replay()
+        torch.cuda.synchronize()
+        for want, d, _, after, freed, count, *_ in cases:
+            assert after.tolist() == want[2] and int(count) == len(want[3])
+            assert freed.tolist()[:len(want[3])] == want[3]
+            assert np.array_equal(inputs.storage_array(d.k_cache.cpu()).view(np.uint8), want[0].view(np.uint8))
+            assert np.array_equal(inputs.storage_array(d.v_cache.cpu()).view(np.uint8), want[1].view(np.uint8))
+    assert pa.pa_get_device_status() == 0
+
+
+def test_accept_offsets_past_32_bits():
+    """Pages whose element offsets pass 2^31."""
+    Hk, D, bs = 8, 128, 64
+    pages = (1 << 31) // (bs * Hk * D) + 40
+    b, path, lens = accept_case(36, [100], [60], Hk, D, bs, "bf16", "nhd", 50)
+    want = orc.cache_accept(inputs.storage_array(b.k_cache), inputs.storage_array(b.v_cache),
+                            b.block_table.numpy(), b.seq_lens.numpy(), b.query_start_loc.numpy(), path, lens,
+                            bs, b.num_blocks, 8, "nhd")
+    far, old = torch.tensor([pages - 1, pages - 7, pages - 3]), b.block_table[0, :3].long()
+    k = torch.zeros((pages, bs, Hk, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[far.cuda()], v[far.cuda()] = b.k_cache[old].cuda(), b.v_cache[old].cuda()
+    after = i32([0])
+    pa.pa_cache_accept(k, v, far.to(torch.int32).view(1, 3).cuda(), b.seq_lens.cuda(), b.query_start_loc.cuda(),
+                       i32(path), i32(lens), after, bs)
+    assert pa.pa_get_device_status() == 0 and after.tolist() == want[2]
+    for got, ref in ((k, want[0]), (v, want[1])):
+        assert np.array_equal(inputs.storage_array(got[far.cuda()].cpu()), ref[old.numpy()])
 
 
 # ---------------------------------------------------------------------------

@@ -32,7 +32,7 @@ MASKS = ("par qsl sl mask pos st S T W", dict(par=P, qsl=P, sl=P, mask=P, pos=P,
     (dict(W=0), 1), (dict(W=-1), 1), (dict(S=-1), 1), (dict(T=-1), 1), (dict(par=None), 1),
     (dict(mask=None), 1), (dict(qsl=None), 1), (dict(sl=None), 1), (dict(mask=P + 4), 1),
     (dict(par=P + 2), 1), (dict(qsl=P + 1), 1), (dict(sl=P + 2), 1), (dict(pos=P + 2), 1),
-    (dict(T=0), 0), (dict(T=0, mask=None, par=None), 0),
+    (dict(T=0), 0), (dict(T=0, mask=None, par=None), 0), (dict(T=(1 << 30) + 1), 2),
 ])
 def test_masks_argument_checks(lib, kw, want):
     assert call(lib.pa_tree_masks, *MASKS, kw) == want
@@ -53,6 +53,7 @@ BOTH = [
     (dict(k=P + 8), 1), (dict(v=P + 8), 1), (dict(out=P + 8), 1), (dict(ws=None), 3), (dict(wsb=100), 3),
     (dict(ws=P + 128), 1), (dict(bt=P + 1), 1), (dict(sl=P + 2), 1), (dict(qsl=P + 3), 1),
     (dict(S=1 << 20, T=1 << 20, msl=1 << 30), 2), (dict(msl=-1), 1),
+    (dict(S=1, T=1, H=1, Hk=1, msl=(1 << 30) + 1), 2), (dict(S=1, T=1, H=1, Hk=1, msl=1 << 30, ws=None), 3),
 ]
 
 
@@ -95,7 +96,7 @@ ACCEPT = ("k v bt sl qsl path pl out freed count Hk D bs st dt S mp mbps nb cap 
     (dict(path=None), 1), (dict(pl=None), 1), (dict(out=None), 1), (dict(mbps=0), 1), (dict(nb=0), 1),
     (dict(k=P + 8), 1), (dict(v=P + 8), 1), (dict(bt=P + 2), 1), (dict(out=P), 1), (dict(out=P + 2), 1),
     (dict(freed=P + 1), 1), (dict(count=P + 2), 1), (dict(path=P + 2), 1),
-    (dict(S=0, freed=None, count=None, cap=0), 0),
+    (dict(S=0, freed=None, count=None, cap=0), 0), (dict(mp=1 << 27), 2),
 ])
 def test_accept_argument_checks(lib, kw, want):
     assert call(lib.pa_cache_accept, *ACCEPT, kw) == want
@@ -116,6 +117,7 @@ EVICT = ("k v w wo bt sl keep out freed count first recent Hk D bs st dt S mbps 
     (dict(nb=0), 1), (dict(k=P + 8), 1), (dict(w=P + 2), 1), (dict(wo=P + 1), 1), (dict(out=P), 1),
     (dict(out=P + 32), 1), (dict(keep=P + 2), 1), (dict(ws=None), 3), (dict(wsb=100), 3),
     (dict(ws=P + 16), 1), (dict(S=1 << 20, Hk=1 << 10, msl=1 << 20), 2),
+    (dict(S=1, Hk=1, D=8, msl=(1 << 30) + 1), 2), (dict(S=1, Hk=1, D=8, msl=1 << 30, ws=None), 3),
     (dict(S=0, freed=None, count=None, cap=0), 0),
 ])
 def test_evict_argument_checks(lib, kw, want):
