@@ -23,6 +23,7 @@ constexpr int kMaxEvictLen = 1 << 30;  // positions some steps behind the end co
 constexpr int kSelectThreads = 1024;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMoveThreads = 256;
+constexpr int kMoveSeqs = 256;  // requests whose chunks and lengths a block keeps at hand
 constexpr int kMovePieces = 4;  // 16-byte pieces of K, and of V, that a thread copies
 constexpr int kChunkPieces = kMoveThreads * kMovePieces;
 
@@ -373,11 +374,19 @@ __device__ inline unsigned load_acquire(const unsigned *p) {
 
 __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const EvictArgs a) {
   __shared__ uint4 s_k[kChunkPieces], s_v[kChunkPieces];
-  __shared__ unsigned s_ticket;
+  __shared__ unsigned s_ticket, s_end[kMoveSeqs];
+  __shared__ int s_after[kMoveSeqs];
   const int tid = threadIdx.x, Hk = a.num_kv_heads, bs = a.block_size, ppr = a.head_bytes / 16;
   pdl_trigger();
   pdl_wait();
   const unsigned chunks = a.head->chunks;
+  // (in shared memory: an acquire empties L1, and these loads follow one another)
+  const bool few = a.num_seqs <= kMoveSeqs;
+  for (int s = tid; few && s < a.num_seqs; s += kMoveThreads) {
+    s_end[s] = a.chunk_end[s];
+    s_after[s] = min(a.seq_lens[s], a.keep_lens[s]);
+  }
+  auto end_of = [&](int s) { return few ? s_end[s] : a.chunk_end[s]; };
   for (;;) {
     __syncthreads();  // s_ticket and the rows of the chunk before are read
     if (tid == 0) s_ticket = atomicAdd(&a.head->ticket, 1u);
@@ -387,11 +396,11 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     int lo = 0, hi = a.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (a.chunk_end[mid] > t) hi = mid; else lo = mid + 1;
+      if (end_of(mid) > t) hi = mid; else lo = mid + 1;
     }
-    const int s = lo, after = min(a.seq_lens[s], a.keep_lens[s]);
+    const int s = lo, after = few ? s_after[s] : min(a.seq_lens[s], a.keep_lens[s]);
     const int nc = divide(after + a.chunk_rows - 1, a.by_rows);
-    const int local = (int)(t - (a.chunk_end[s] - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
+    const int local = (int)(t - (end_of(s) - (unsigned)(Hk * nc))), h = local / nc, c = local - h * nc;
     const int unit = s * Hk + h;
     const int32_t *bt = a.block_table + (size_t)s * a.max_blocks_per_seq;
     const int32_t *kept = a.kept + (size_t)unit * a.max_seq_len;
@@ -400,29 +409,36 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     const int below = a.below[(size_t)unit * a.max_chunks + c];
     // -- this chunk's rows into shared memory
     unsigned flags = 0;
+    long long into[kMovePieces];  // -1: not moved
 #pragma unroll
     for (int u = 0; u < kMovePieces; ++u) {
       const int e = u * kMoveThreads + tid, row = divide(e, a.by_ppr), piece = e - row * ppr;
+      into[u] = -1;
       if (row >= rows) continue;
       const int src = kept[i0 + row];
       if (src == i0 + row) continue;
-      const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
-      if (from < 0) continue;
+      const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes),
+                      to = row_offset(bt, i0 + row, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
+      if (from < 0 || to < 0) {
+        flags |= PA_DEV_BAD_BLOCK;
+        continue;
+      }
       copy16(s_k + e, a.k_cache + from + piece * 16);
       copy16(s_v + e, a.v_cache + from + piece * 16);
-    }
-    // -- meanwhile its weights (select has read them all)
-    for (int i = i0 + tid; i < i0 + rows; i += kMoveThreads) {
-      const int from = kept[i], page = bt[divide(from, a.by_bs)],
-                lp = divide(i, a.by_bs), into = bt[lp];
-      if (page >= 0 && page < a.num_blocks && into >= 0 && into < a.num_blocks)
-        a.weights_out[((long long)into * Hk + h) * bs + (i - lp * bs)] = a.kept_w[(size_t)unit * a.max_seq_len + i];
+      into[u] = to + piece * 16;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (tid == 0) {
       __threadfence();
       atomicExch(ready + c, 1u);
+    }
+    // -- meanwhile its weights (select has read them all)
+    for (int i = i0 + tid; i < i0 + rows; i += kMoveThreads) {
+      const int from = kept[i], page = bt[divide(from, a.by_bs)],
+                lp = divide(i, a.by_bs), dst = bt[lp];
+      if (page >= 0 && page < a.num_blocks && dst >= 0 && dst < a.num_blocks)
+        a.weights_out[((long long)dst * Hk + h) * bs + (i - lp * bs)] = a.kept_w[(size_t)unit * a.max_seq_len + i];
     }
     // -- the chunks whose rows lie where this one writes: those that hold the kept
     // positions from i0 on, from the first one's chunk on; they were handed out
@@ -443,18 +459,9 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     if (!__syncthreads_or(late)) {
 #pragma unroll
       for (int u = 0; u < kMovePieces; ++u) {
-        const int e = u * kMoveThreads + tid, row = divide(e, a.by_ppr), piece = e - row * ppr;
-        if (row >= rows) continue;
-        const int src = kept[i0 + row];
-        if (src == i0 + row) continue;
-        const long long from = row_offset(bt, src, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
-        const long long into = row_offset(bt, i0 + row, h, Hk, bs, a.by_bs, a.num_blocks, a.hnd, a.head_bytes);
-        if (from < 0 || into < 0) {
-          flags |= PA_DEV_BAD_BLOCK;
-          continue;
-        }
-        *reinterpret_cast<uint4 *>(a.k_cache + into + piece * 16) = s_k[e];
-        *reinterpret_cast<uint4 *>(a.v_cache + into + piece * 16) = s_v[e];
+        if (into[u] < 0) continue;
+        *reinterpret_cast<uint4 *>(a.k_cache + into[u]) = s_k[u * kMoveThreads + tid];
+        *reinterpret_cast<uint4 *>(a.v_cache + into[u]) = s_v[u * kMoveThreads + tid];
       }
     }
     if (flags) atomicOr(a.status, flags);
