@@ -308,8 +308,8 @@ struct SpanRow {
   bool pairs;
 };
 
-// Row of token i and head h of request r.  *done: a unit of more than 128 rows in one
-// piece, which the tensor-core kernel has finished.
+// Row of token i and head h of request r.  *done: of a unit in one piece, which the
+// tensor-core kernel has finished.
 __device__ inline SpanRow span_locate(const SpanParams &p, const SpanPlan &plan, const SpanReq &r, int i, int h,
                                       int lg, bool causal, bool *done) {
   SpanRow x;
@@ -319,15 +319,14 @@ __device__ inline SpanRow span_locate(const SpanParams &p, const SpanPlan &plan,
   x.unit = (long long)r.unit0 + kvh * r.nblk + b;
   x.u0 = r.cost0 + (unsigned)kvh * r.kcost + (unsigned)b * r.ucost;
   x.len = last ? r.ulast : r.ucost;
-  x.w = last ? r.wlast : r.wcost;
+  x.w = span_tile_cost(r, b, p.overhead);
   x.ntile = r.ntile;
   x.c0 = (int)(x.u0 / plan.run);
   x.blk_end = span_block_end(r, b * tq, tq, causal);
   x.n = (int)((x.u0 + x.len - 1) / plan.run) - x.c0 + 1;
-  // (such a unit has one partial a piece, in the row's own place)
   x.pairs = p.halves && (r.q_len - b * tq) << lg <= 128;
   *done = false;
-  if (p.halves && !x.pairs) {
+  if (p.halves && (p.join || !x.pairs)) {
     for (int c = x.c0; c < x.c0 + x.n; ++c) {  // (pieces before it may have no tile)
       const int t1 = span_tile_at(p, r, min(x.u0 + x.len, (unsigned)(c + 1) * plan.run) - x.u0, x.w);
       if (t1 == r.ntile) *done = true;
@@ -369,7 +368,7 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
     const int at = (int)(item / units) * kKeptChunk, sh = (int)(item - (long long)at / kKeptChunk * units);
     const int s = sh / Hk, kvh = sh - s * Hk, pos = at + tid * 4;
     const SpanReq r = p.req[s];
-    if (!r.valid || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
+    if (r.nblk == 0 || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
     const int R = r.q_len << lg;
     const bool mine = pos < r.ctx;
     // (what does not wait for the sums is on its way before them)
@@ -391,7 +390,11 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
       const int h = (kvh << lg) + (tid & ((1 << lg) - 1));
       const SpanRow row = span_locate(p, plan, r, tid >> lg, h, lg, true, &done);
       float m = -INFINITY, l = 0.f;
-      for (int e = 0; e < row.n; ++e) {
+      if (done) {  // (the sink in it)
+        m = __ldcg(p.row_lse + (size_t)(r.q_start + (tid >> lg)) * f.num_heads + h);
+        l = 1.f;
+      }
+      for (int e = 0; e < row.n && !done; ++e) {
         const long long from = span_partial(p, plan, row, e);
         const float v = from < 0 ? -INFINITY : __ldcg(p.part_lse + from);
         if (v == -INFINITY) continue;
@@ -399,7 +402,7 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
         l = l * (m == top ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - top)) + (v == top ? 1.f : fast_exp2(v - top));
         m = top;
       }
-      if (f.sinks && m != INFINITY && m != -INFINITY) {
+      if (f.sinks && !done && m != INFINITY && m != -INFINITY) {
         const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = max_nan(m, sink2);
         l = l * fast_exp2(m - top) + fast_exp2(sink2 - top);
         m = top;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
       const SpanReq r = p.req[lo];
       const int i = tok - r.q_start;
       mine = i < r.q_len;
-      if (mine && r.valid) {
+      if (mine && r.nblk > 0) {
         bool done;
         at = span_locate(p, plan, r, i, h, lg, CAUSAL, &done);
         n = done ? 0 : at.n;
@@ -670,7 +673,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SpanLayout {
   size_t plan, req, vote_end, part_o, part_lse, row_lse, scores, total;
-  int slot_rows;
+  int slot_rows, one;
   bool ok;  // the extents are ones that the kernels count in 32 bits
 };
 
@@ -686,7 +689,8 @@ SpanLayout span_layout(int dtype, int num_seqs, int num_tokens, int num_heads, i
   const long long tiles = ceil_div_ll(msl, kSpanTile) * kSpanWide + kSpanOverhead;
   l.ok = units * tiles < (1ll << 31) - (1 << 20) && msl <= kSpanMaxLen;
   // two rows of partials for each row of a unit of up to 128
-  l.slot_rows = most * G <= 128 ? (int)(2 * ceil_div_ll(most * G, 4) * 4) : kSpanRows;
+  l.one = most * G <= 128;
+  l.slot_rows = l.one ? (int)(2 * ceil_div_ll(most * G, 4) * 4) : kSpanRows;
   const long long slots = units + kMaxGrid;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -791,9 +795,15 @@ pa_status span_call(const SpanCall &sc) {
   p.num_sms = num_sms;
   p.grid = std::min(num_sms, kMaxGrid);
   p.halves = c.dtype == PA_BF16;
+  p.one = lay.one;
   const long long units = (long long)c.num_kv_heads *
                           std::max<long long>(c.num_seqs, ceil_div_ll((long long)c.num_tokens * (c.num_heads / c.num_kv_heads), kSpanRows));
   p.overhead = units >= p.grid ? kSpanOverhead : 0;
+  // Units of up to 128 rows finished in one row tile: where they are many, and have the
+  // rows of trees (64 trees of 16 tokens, 4 heads each: 206 us, 200 so; the rows of
+  // decode steps are few, 64 of them 222 us, 226 so, and the code that small calls wait
+  // for grows: one tree 11.2 us, 12.3 so).
+  p.join = p.halves && !votes && p.overhead > 0;
   p.slot_rows = lay.slot_rows;
   p.plan = reinterpret_cast<SpanPlan *>(ws + lay.plan);
   p.req = reinterpret_cast<SpanReq *>(ws + lay.req);
@@ -819,13 +829,13 @@ pa_status span_call(const SpanCall &sc) {
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
   // partials that a row may have: two of each block that shares its unit
-  const long long blocks = 2 * (ceil_div_ll(c.max_seq_len, kSpanTile) + 1);
+  const long long blocks = 2 * std::min<long long>(ceil_div_ll(c.max_seq_len, kSpanTile) + 1, p.grid);
   // rows of a KV head that one request may have
   const int most_rows = (int)std::min<long long>(
       (long long)(c.max_query_len > 0 ? std::min(c.max_query_len, c.num_tokens) : c.num_tokens) *
           (c.num_heads / c.num_kv_heads), 1 << 30);
   slot = prof_begin(PA_K_MERGE, st);
-  err = launch_merge<MODE>(p, std::min<long long>(blocks, 2 * p.grid), most_rows, st);
+  err = launch_merge<MODE>(p, blocks, most_rows, st);
   prof_end(slot, st);
   if (err != cudaSuccess) return PA_ERR_CUDA;
   if (votes && most_rows > kSpanStoredRows) {

@@ -47,16 +47,19 @@ enum SpanMode : int {
 struct SpanReq {
   int q_start, q_len;  // its token rows
   int ctx;             // positions, the new tokens among them
-  int valid;
-  int nblk;            // blocks of kSpanRows rows of a KV head (0: nothing to do)
+  int nblk;            // blocks of kSpanRows rows of a KV head (0: bad, or nothing to do)
   int ntile;           // tiles of its context
   int unit0;           // first unit; unit = unit0 + kv head * nblk + block
   unsigned cost0;      // where its first unit begins in the laid-out work
   int kcost;           // laid-out work of a KV head: its blocks' one after the other,
   int ucost, ulast;    // a block's, and the last one's
-  int wcost, wlast;    // a tile of a block's, and of the last one's
   long long score0;    // first kept score, -1: not kept
 };
+
+// Laid-out work of a tile of block b of a request.
+__device__ inline int span_tile_cost(const SpanReq &r, int b, int overhead) {
+  return b < r.nblk - 1 || r.ulast - overhead > r.ntile ? kSpanWide : 1;
+}
 
 struct SpanPlan {
   unsigned total;  // laid-out work
@@ -74,7 +77,9 @@ struct SpanParams {
   float *weights;                  // [num_blocks][num_kv_heads][block_size], or null
   int accumulate;
   int keep_scores;
-  int num_sms, grid, halves;       // halves: see span_row
+  int num_sms, grid;
+  int halves, join;                // see span_row
+  int one;                         // no unit has more than 128 rows
   int overhead;                    // kSpanOverhead, or 0
   int fused;                       // no planner: see span_plan_warp
   int slot_rows;
@@ -89,7 +94,8 @@ struct SpanParams {
 
 // Where row r of a unit lies among the partials of slot `slot`.  The tensor-core
 // kernel gives a unit of up to 128 rows to both of its row tiles, every other tile
-// of positions each: x tells them apart (else x = 0).
+// of positions each: x tells them apart (else x = 0).  It finishes units in one piece
+// by itself: those of more than 128 rows, and (join) the others too.
 __device__ inline long long span_row(const SpanParams &p, long long slot, int x, int r) {
   return slot * p.slot_rows + x * (p.slot_rows / 2) + r;
 }
@@ -97,7 +103,7 @@ __device__ inline long long span_row(const SpanParams &p, long long slot, int x,
 // Batches of up to this many requests (bf16) have no planner's launch: every block of
 // the span kernel works the plan out for itself, a request a lane (and as many as its
 // shared memory has room for).
-constexpr int kSpanFusedSeqs = 28;
+constexpr int kSpanFusedSeqs = 20;
 
 // Request s as its metadata say, without the sums over the requests before it; cnt:
 // its units, laid-out work, kept scores and tiles of the KV heads that are summed up
@@ -118,17 +124,15 @@ __device__ inline SpanReq span_request(const SpanParams &p, int s, unsigned &fla
   const bool q_ok = r.q_len <= r.ctx && (f.max_qlen <= 0 || r.q_len <= f.max_qlen) &&
                     (!p.mask || r.q_len <= 64ll * p.mask_words);
   if (r.q_len != 0) flags |= (len_ok ? 0u : PA_DEV_BAD_SEQLEN) | (q_ok ? 0u : PA_DEV_BAD_QLEN);
-  r.valid = r.q_len > 0 && len_ok && q_ok;
   r.score0 = -1;
   cnt[0] = cnt[1] = cnt[2] = cnt[3] = 0;
-  if (r.valid) {
+  if (r.q_len > 0 && len_ok && q_ok) {
     const long long rows = (long long)r.q_len * G;
     r.nblk = (int)((rows + kSpanRows - 1) / kSpanRows);
     r.ntile = (r.ctx + kSpanTile - 1) / kSpanTile;
-    r.wcost = kSpanWide;
-    r.wlast = rows - (r.nblk - 1ll) * kSpanRows > 128 ? kSpanWide : span_narrow(r.nblk, f.head_dim);
-    r.ulast = r.ntile * r.wlast + p.overhead;
-    r.ucost = r.nblk > 1 ? r.ntile * r.wcost + p.overhead : r.ulast;
+    const int wlast = rows - (r.nblk - 1ll) * kSpanRows > 128 ? kSpanWide : span_narrow(r.nblk, f.head_dim);
+    r.ulast = r.ntile * wlast + p.overhead;
+    r.ucost = r.nblk > 1 ? r.ntile * kSpanWide + p.overhead : r.ulast;
     r.kcost = (r.nblk - 1) * r.ucost + r.ulast;
     cnt[0] = (long long)Hk * r.nblk;
     cnt[1] = (long long)Hk * r.kcost;
@@ -242,7 +246,7 @@ struct SpanCursor {
   // heads of a KV head.
   __device__ bool make(const SpanParams &p, int lg, bool causal, const SpanReq &q, int req, int h, int b,
                        unsigned begin, unsigned from, unsigned to, SpanPiece &it) const {
-    const int w = b == q.nblk - 1 ? q.wlast : q.wcost;
+    const int w = span_tile_cost(q, b, p.overhead);
     const int lo = span_tile_at(p, q, from - begin, w), hi = span_tile_at(p, q, to - begin, w);
     it.q_start = q.q_start;
     it.q_len = q.q_len;

@@ -57,10 +57,12 @@ struct Cfg {
   static constexpr int Q_FULL = 0, Q_FREE = 1, S_FULL = 2, O_HALF = 4, O_DONE = 6, P_HALF = 8,
                        P_FULL = 10, O_FREE = 12, TURN = 14, END = 16, K_FULL = 17, V_FULL = K_FULL + KST,
                        K_FREE = V_FULL + VST, V_FREE = K_FREE + KST, V_OK = V_FREE + VST,
-                       PIECE = V_OK + VST, PIECE_FREE = PIECE + kPieces, NBAR = PIECE_FREE + kPieces;
+                       PAIR = V_OK + VST, PIECE = PAIR + 1, PIECE_FREE = PIECE + kPieces,
+                       NBAR = PIECE_FREE + kPieces;
   static constexpr int OFF_PIECE = (OFF_BAR + NBAR * 8 + 15) & ~15;
   static constexpr int OFF_MISC = OFF_PIECE + kPieces * (int)sizeof(SpanPiece);
-  static constexpr int OFF_REQ = (OFF_MISC + 144 + 15) & ~15;  // requests, where this kernel plans
+  static constexpr int OFF_PAIR = OFF_MISC + 144;     // references and sums of the second row tile
+  static constexpr int OFF_REQ = OFF_PAIR + 128 * 8;  // requests, where this kernel plans
   static constexpr int SMEM = OFF_REQ + kSpanFusedSeqs * (int)sizeof(SpanReq);
   static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kBN, 0);
   static constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, 1);
@@ -121,7 +123,7 @@ __device__ inline bool not_finite(uint4 v) {  // of eight bf16 values, any
 // The values that were zeroed, for one row that may see some of them: added to its
 // partial or its finished output (DONE), normalised by inv, in memory.  Rare and slow.
 template <int D, bool CAUSAL, bool DONE>
-__device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it, int row, bool pairs,
+__device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it, int row, bool half,
                                         int x, float ref, float inv, void *out) {
   const FwdParams &f = p.f;
   const int Hk = f.num_kv_heads, G = f.num_heads / Hk, bs = f.block_size, prefix = it.ctx - it.q_len;
@@ -130,7 +132,7 @@ __device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it,
       static_cast<const __nv_bfloat16 *>(f.q) + ((size_t)(it.q_start + tl) * f.num_heads + head) * D;
   const int32_t *bt = f.block_table + (size_t)it.req * f.max_blocks_per_seq;
   for (int pos = max(it.kv_lo, first_hidden<CAUSAL>(it)); pos < it.kv_hi; ++pos) {
-    if (pairs && (((pos - it.kv_lo) / kBN) & 1) != x) continue;
+    if (half && (((pos - it.kv_lo) / kBN) & 1) != x) continue;
     const int n = pos - prefix;
     if (n >= 0) {
       const bool seen = CAUSAL ? n <= tl
@@ -161,7 +163,8 @@ __device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it,
   }
 }
 
-template <int D, int MODE, bool ONE>
+// JOIN: units of up to 128 rows in one piece are finished here too, in one row tile.
+template <int D, int MODE, bool ONE, bool JOIN>
 __global__ void __launch_bounds__(kThreads, 1)
     span_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ SpanParams p,
@@ -188,14 +191,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensor_map(&tm_q);
     prefetch_tensor_map(&tm_k);
     if (VALUES) prefetch_tensor_map(&tm_v);
-    for (int b = 0; b < C::NBAR; ++b) {
-      // P and O: the row tile's four warps; a ring stage: two loading warps, two
-      // issuing ones, two that look at the values
-      const bool softmax = b >= C::P_HALF && b < C::TURN, ring = b >= C::K_FULL;
-      const int readers = VALUES ? 15 : 11;  // warps that read the pieces
-      mbar_init(&bar[b], b >= C::PIECE_FREE ? readers : b >= C::PIECE ? 1 : softmax ? 4
-                         : ring || b == C::Q_FREE || b == C::END ? 2 : 1);
-    }
+  }
+  // (a barrier a thread: one thread's loop over them takes a small call half a microsecond)
+  if (tid < C::NBAR) {
+    // P and O: the row tile's four warps; a ring stage: two loading warps, two
+    // issuing ones, two that look at the values
+    const int b = tid;
+    const bool softmax = (b >= C::P_HALF && b < C::TURN) || b == C::PAIR, ring = b >= C::K_FULL;
+    const int readers = VALUES ? 15 : 11;  // warps that read the pieces
+    mbar_init(&bar[b], b >= C::PIECE_FREE ? readers : b >= C::PIECE ? 1 : softmax ? 4
+                       : ring || b == C::Q_FREE || b == C::END ? 2 : 1);
     fence_mbar_init();
   }
   if (tid < 32) s_fix[tid] = 0;
@@ -205,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   bool dead = false;
+  float2 *const s_pair = reinterpret_cast<float2 *>(smem + C::OFF_PAIR);
   SpanPiece *const s_piece = reinterpret_cast<SpanPiece *>(smem + C::OFF_PIECE);
   SpanPiece it;
   uint32_t pieces = 0;  // taken by this warp
@@ -513,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 2^(c s - ref) as one multiply-add needs c > 0 (the maximum is then c max s)
     const bool fold = c2 > 0.f;
     const float cs = fold ? c2 : 1.f;
-    uint32_t n = 0;
+    uint32_t n = 0, joined = 0;
     // The first round is dry: a tile of whatever TMEM holds, no barrier touched
     // and nothing stored, run before the plan is awaited.  It brings this
     // code into the instruction cache.
@@ -700,11 +706,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!dry) mbar_wait(&bar[C::O_DONE + x], (n - 1) & 1, dead, f.status);
           tc_fence_after();
         }
+        // Both row tiles' halves of a whole unit of up to 128 rows: the first one's threads
+        // join them, the second one's O read from tensor memory (the same lanes).
+        const bool joint = JOIN && !dry && !two && it.whole && it.kv_lo + kBN < it.kv_hi;
+        if (joint && x == 1) {
+          s_pair[r] = make_float2(ref, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::PAIR]);
+          // (s_pair is read when O is free again, and O written again only then)
+          goto next;
+        }
+        float a0 = 1.f, a1 = 0.f;
+        if (joint) {
+          mbar_wait(&bar[C::PAIR], joined++ & 1, dead, f.status);
+          tc_fence_after();
+          const float2 other = s_pair[r];
+          if (l == 0.f) {
+            ref = other.x;
+            l = other.y;
+            a1 = 1.f;
+          } else if (other.y != 0.f) {
+            const float top = other.x > ref || other.x != other.x ? other.x : ref;
+            a0 = ref == top ? 1.f : fast_exp2(ref - top);
+            a1 = other.x == top ? 1.f : fast_exp2(other.x - top);
+            l = l * a0 + other.y * a1;
+            ref = top;
+          }
+        }
         const bool bad = !dry && s_bad[k & 15] == k + 1, none = l == 0.f;
         const long long prow = span_row(p, it.slot, x, r);
         float lse = bad ? INFINITY : none ? -INFINITY : ref + log2f(l), inv = bad || none ? 0.f : 1.f / l;
         const bool real = r < rows && !dry;
-        if (!ONE && two && it.whole) {
+        if (it.whole && (JOIN || (!ONE && two))) {
           const int row = row0 + r, head = it.kvh * G + (row & (G - 1));
           const long long orow = (long long)(it.q_start + tl) * f.num_heads + head;
           if (f.sinks && !bad && !none && real) {
@@ -716,16 +750,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (VALUES) {
             if (warp_active) {
               __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(f.out) + orow * D;
+              const float f0 = a0 * inv, f1 = a1 * inv;
 #pragma unroll 1
               for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t raw[32], packed[16];
                 tc_ld32(tm_o + c0, raw);
-                tc_wait_ld();
+                if (joint) {
+                  uint32_t more[32];
+                  tc_ld32(tm_o + 128 + c0, more);
+                  wait_ld(raw, more);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    raw[i] = __float_as_uint(fmaf(__uint_as_float(raw[i]), f0, __uint_as_float(more[i]) * f1));
+                } else {
+                  tc_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * f0);
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   // one rounding to nearest even, of the finished output
-                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(raw[2 * i]) * inv,
-                                                                  __uint_as_float(raw[2 * i + 1]) * inv);
+                  const __nv_bfloat162 h2 =
+                      __floats2bfloat162_rn(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
                   packed[i] = bad || none ? 0u : *reinterpret_cast<const uint32_t *>(&h2);
                 }
                 if (real) {
@@ -762,9 +808,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (dry || VALUES) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[C::O_FREE + x]);
+          if (lane == 0) {
+            mbar_arrive(&bar[C::O_FREE + x]);
+            if (joint) mbar_arrive(&bar[C::O_FREE + 1]);
+          }
         }
       }
+    next:
       if (dry) pdl_wait();  // the plan
       if (!next_piece()) break;
       ++k;
@@ -776,11 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kIssueWarp) tc_dealloc(tmem, kTmemCols);
 }
 
-template <int D, int MODE, bool ONE>
+template <int D, int MODE, bool ONE, bool JOIN = false>
 cudaError_t launch_d(const SpanParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                      const CUtensorMap &tv, int box, cudaStream_t stream) {
   using C = Cfg<D, ONE>;
-  auto kern = span_mma_kernel<D, MODE, ONE>;
+  auto kern = span_mma_kernel<D, MODE, ONE, JOIN>;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_attrs_once(kern, C::SMEM, done);
   if (e != cudaSuccess) return e;
@@ -790,8 +840,15 @@ cudaError_t launch_d(const SpanParams &p, const CUtensorMap &tq, const CUtensorM
 template <int MODE>
 cudaError_t launch_mode(const SpanParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                         const CUtensorMap &tv, int box, cudaStream_t stream) {
-  // (slots of fewer rows: the caller's bound says that no piece has more than 128)
-  const bool one = p.slot_rows < kSpanRows;
+  const bool one = p.one;
+  if constexpr (MODE == kSpanTree) {
+    if (p.join && p.f.head_dim == 128)
+      return one ? launch_d<128, MODE, true, true>(p, tq, tk, tv, box, stream)
+                 : launch_d<128, MODE, false, true>(p, tq, tk, tv, box, stream);
+    if (p.join)
+      return one ? launch_d<64, MODE, true, true>(p, tq, tk, tv, box, stream)
+                 : launch_d<64, MODE, false, true>(p, tq, tk, tv, box, stream);
+  }
   if (p.f.head_dim == 128)
     return one ? launch_d<128, MODE, true>(p, tq, tk, tv, box, stream)
                : launch_d<128, MODE, false>(p, tq, tk, tv, box, stream);

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
     const int sh = (int)(item % ((long long)f.num_seqs * Hk)), s = sh / Hk, kvh = sh % Hk;
     const int at = (int)(item / ((long long)f.num_seqs * Hk)) * kPos;
     const SpanReq r = p.req[s];
-    if (!r.valid || r.score0 >= 0 || at >= r.ctx) continue;
+    if (r.nblk == 0 || r.score0 >= 0 || at >= r.ctx) continue;
     if (request_bad(p, r)) continue;
     const int32_t *bt = f.block_table + (size_t)s * f.max_blocks_per_seq;
     const int R = r.q_len * G, prefix = r.ctx - r.q_len;

@@ -64,7 +64,7 @@ struct VoteCursor {
 
   __device__ void take(const SpanParams &p) {
     r = p.req[s];
-    skip = r.valid && __ldcg(p.row_lse + (size_t)(r.q_start + r.q_len - 1) * p.f.num_heads) == INFINITY;
+    skip = r.nblk > 0 && __ldcg(p.row_lse + (size_t)(r.q_start + r.q_len - 1) * p.f.num_heads) == INFINITY;
   }
   __device__ void start(const SpanParams &p) {
     const unsigned total = p.plan->vote_tiles;
@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   if (tid == 0) {
     prefetch_tensor_map(&tm_q);
     prefetch_tensor_map(&tm_k);
-    for (int b = 0; b < C::NBAR; ++b) mbar_init(&bar[b], b >= C::S_FREE && b < C::END ? 4 : 1);
+  }
+  if (tid < C::NBAR) {
+    mbar_init(&bar[tid], tid >= C::S_FREE && tid < C::END ? 4 : 1);
     fence_mbar_init();
   }
   if (warp == kIssueWarp) tc_alloc(s_tmem, C::COLS);

@@ -81,7 +81,7 @@ def test_windows_of_all_sizes_in_one_call(shape, output):
                 output=output)
 
 
-@pytest.mark.parametrize("S", [28, 29])
+@pytest.mark.parametrize("S", [20, 21, 28, 29])
 def test_batches_around_the_planned_sizes(S):
     rng = np.random.default_rng(S)
     q = rng.integers(0, 12, S)

@@ -147,9 +147,9 @@ def test_many_requests():
     check_tree(q, rng.integers(0, 90, 300).tolist(), (4, 2, 64, 16), seed=9)
 
 
-@pytest.mark.parametrize("S", [27, 28, 29, 32, 33])
+@pytest.mark.parametrize("S", [20, 21, 27, 28, 29, 32, 33])
 def test_batches_around_the_planned_sizes(S):
-    """Up to 28 requests are planned in the kernel itself."""
+    """Some requests are planned in the kernel itself, more by a kernel before it."""
     rng = np.random.default_rng(S)
     q = rng.integers(0, 20, S).tolist()
     q[-1] = 0 if S % 2 else 3
@@ -257,6 +257,38 @@ def test_a_bad_value_reaches_those_that_see_it(value, dtype):
         assert (np.isnan(hit) if value != value else hit == value).all()
         g[np.ix_(seen, np.arange(4), [7])] = want[s]["out"][np.ix_(seen, np.arange(4), [7])]
     spans.check_out(b, got, want, dtype)
+
+
+@pytest.mark.parametrize("max_query_len", [0, 8])
+@pytest.mark.parametrize("shape,S", [((32, 8, 128, 16), 60), ((64, 4, 128, 64), 80), ((16, 8, 64, 32), 70),
+                                     ((8, 8, 128, 128), 50)])
+def test_units_that_one_block_finishes(shape, S, max_query_len):
+    """More units than blocks, several tiles each: hidden tokens that hold anything, values
+    that are not finite where some see them, a bad page and sinks among them."""
+    H, Hk, D, bs = shape
+    G = H // Hk
+    rng = np.random.default_rng(S)
+    q_lens = rng.integers(1, 9, S).tolist()
+    q_lens[3:8] = [8, 1, 8, 6, 7]
+    cached = rng.integers(60, 700, S).tolist()
+    b = spans.batch(q_lens, [n + c for n, c in zip(q_lens, cached)], H, Hk, D, bs, seed=S)
+    qsl = b.query_start_loc.numpy()
+    mask = orc.tree_masks(spans.random_trees(rng, q_lens), qsl, b.num_tokens, 1)[0]
+    mask[qsl[3]:qsl[4]] &= ~np.uint64(1)
+    sinks = rng.standard_normal(H)
+    want = spans.oracle(b, mask, sinks)
+    page, slot = spans.slots_of(b, 3)
+    b.k_cache[page[cached[3]], slot[cached[3]]] = float("nan")
+    b.v_cache[page[cached[3]], slot[cached[3]]] = float("inf")
+    page, slot = spans.slots_of(b, 5)
+    b.v_cache[page[-1], slot[-1], 0, 7] = float("inf")  # (the last token's: itself alone sees it)
+    b.block_table[7, 0] = -1
+    got = spans.run_tree(b, mask, sinks=sinks, expect=1, max_query_len=max_query_len)
+    row = qsl[6] - 1
+    assert (got[row, :G, 7] == np.inf).all()
+    got[row, :G, 7] = want[5]["out"][-1, :G, 7]
+    zero_rows(b, got, want, {7}, "bf16")
+    spans.check_out(b, got, want, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
