@@ -83,7 +83,10 @@ __device__ inline float weight_of(uint32_t key) {
 // A cluster of C blocks for each (request, KV head), each with its share of the
 // positions, whose weights it reads once, as keys in shared memory.  Three passes
 // over them count the keys' leading bits, a fourth lists what is kept; counts are summed
-// over the cluster through distributed shared memory.
+// over the cluster through distributed shared memory.  Bound by latency: the pages, the
+// weights, a barrier or two between the steps of a pass.  16 requests of up to 8192
+// positions, 8 KV heads: 14 us; 4 of up to 131072 in clusters of 16 blocks 22 (a
+// call 36, 42 in clusters of 8; what digits the keys have changes it by 3).
 
 constexpr int kMostCluster = 16;
 
@@ -365,6 +368,11 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
 // ---------------------------------------------------------------------------
 // move
 // ---------------------------------------------------------------------------
+// A chunk is 16 KB of K and as much of V: read into shared memory, marked read, then
+// written when the chunks whose rows lie there are marked.  Six blocks an SM, so that
+// the reads of some run beside the writes of others.  Bound by HBM and by the chain of
+// a chunk (ticket, list, page, row, flags): 16 requests cut to 2048 positions, 8 KV heads
+// of 128, 238 MB read and written in 51 us, 4.7 TB/s, 70 % of the measured copy rate.
 
 __device__ inline unsigned load_acquire(const unsigned *p) {
   unsigned v;

@@ -70,13 +70,17 @@ __global__ void __launch_bounds__(kPlanThreads) span_plan_kernel(const SpanParam
 // the pass over keys and values on CUDA cores (fp32)
 // ---------------------------------------------------------------------------
 // Eight threads share up to four rows (each every eighth 16-byte group of their
-// head_dim values), 128 rows a pass; 32 keys and values at a time in shared
+// head_dim values), 128 rows a pass; 64 keys and values at a time in shared
 // memory, the next ones loaded meanwhile, each load of them used for the four
 // rows.  The scores of 8 keys are reduced over the eight threads so that each ends
 // up with one key's, join the running maximum and sum there, and the weights are
-// handed round again.
+// handed round again.  Bound by the multiply-adds and the shuffles between them:
+// 64 trees of up to 16 tokens, 32/8 heads of 128, up to 8192 positions: 3.06 ms, 17
+// TFLOP/s.  Up to 16 rows are taken by 2, 4 or 8 sets of warps, each on its share of a
+// tile's keys (64 decodes on those positions, 4 rows: 0.58 ms, 4.0 TB/s; with all warps
+// on the same keys 2.76 ms).
 constexpr int kSimtThreads = 256;
-constexpr int kSimtKeys = 32;
+constexpr int kSimtKeys = 64;
 constexpr int kSimtRows = 4;  // rows of a thread, 32 apart
 constexpr uint32_t kHidden = 0x80000000u;  // -0, the weight of a hidden position
 
@@ -115,10 +119,13 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
     // (a pass of fewer rows than threads' rows holds one or two a thread)
     auto pass = [&](int row0, auto rows_c) {
       constexpr int R = decltype(rows_c)::value;
+      // up to 16 rows: 2, 4 or 8 sets of warps take them, each its share of the keys
+      const int left = rows - row0, sets = R > 1 || left > 16 ? 1 : left > 8 ? 2 : left > 4 ? 4 : 8;
+      const int per = 32 / sets, set = (tid >> 3) / per, row1 = row0 + (tid >> 3) % per;
       float qv[R][N], o[R][VALUES ? N : 1], m[R], l[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int row = min(row0 + r * 32 + (tid >> 3), rows - 1);
+        const int row = min(row1 + r * 32, rows - 1);
         const int tok = it.q_start + it.t0 + row / G, head = it.kvh * G + row % G;
         const float *q = static_cast<const float *>(f.q) + ((size_t)tok * f.num_heads + head) * D;
         m[r] = -INFINITY;
@@ -135,23 +142,33 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
       }
       int bad = 0;
       auto load = [&](SpanTileBuf<D> &t, int lo) {
-#pragma unroll 4
-        for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
-          const int j = e / (D / 4), x = e % (D / 4) * 4, pos = lo + j;
-          bool in = pos < it.kv_hi;
-          size_t row = 0;
-          if (in) {
-            const int page = bt[pos / bs], slot = pos % bs;
-            if (page < 0 || page >= f.num_blocks) {
-              bad = 1;
-              in = false;
-            } else {
-              row = p.hnd ? ((size_t)page * Hk + it.kvh) * bs + slot
-                          : ((size_t)page * bs + slot) * Hk + it.kvh;
-            }
+        // a run of 16 positions lies in one page
+        constexpr int STEP = kSimtThreads / (D / 4);  // keys of one round of the threads
+        const int x = tid % (D / 4) * 4;
+        int page[kSimtKeys / 16];
+#pragma unroll
+        for (int run = 0; run < kSimtKeys / 16; ++run) {
+          const int at = lo + run * 16;
+          page[run] = at < it.kv_hi ? bt[at / bs] : -1;
+          if (at < it.kv_hi && (page[run] < 0 || page[run] >= f.num_blocks)) {
+            bad = 1;
+            page[run] = -1;
           }
-          copy4(&t.k[j][x], kc + row * D + x, in);
-          if constexpr (VALUES) copy4(&t.v[j][x], vc + row * D + x, in);
+        }
+#pragma unroll
+        for (int run = 0; run < kSimtKeys / 16; ++run) {
+          const int slot = (lo + run * 16) % bs;
+          const size_t row = page[run] < 0 ? 0
+                             : p.hnd       ? ((size_t)page[run] * Hk + it.kvh) * bs + slot
+                                           : ((size_t)page[run] * bs + slot) * Hk + it.kvh;
+#pragma unroll
+          for (int i = tid / (D / 4); i < 16; i += STEP) {
+            const int j = run * 16 + i;
+            const bool in = page[run] >= 0 && lo + j < it.kv_hi;
+            const size_t at = (in ? row + (size_t)i * (p.hnd ? 1 : Hk) : 0) * D + x;
+            copy4(&t.k[j][x], kc + at, in);
+            if constexpr (VALUES) copy4(&t.v[j][x], vc + at, in);
+          }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
@@ -162,7 +179,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
         __syncthreads();  // the tile is there, and the other one has been read
         const SpanTileBuf<D> &t = s_tile[buf];
         if (lo + kSimtKeys < it.kv_hi) load(s_tile[buf ^ 1], lo + kSimtKeys);
-        for (int j0 = 0; j0 < kSimtKeys && lo + j0 < it.kv_hi; j0 += 8) {
+        for (int j0 = set * 8; j0 < kSimtKeys && lo + j0 < it.kv_hi; j0 += sets * 8) {
           float w[R][8];  // the thread's shares of 8 scores, then its key's weight in [0]
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -194,7 +211,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
                 w[r][j] = keep + __shfl_xor_sync(0xffffffffu, send, h);
               }
             }
-            const int row = row0 + r * 32 + (tid >> 3);
+            const int row = row1 + r * 32;
             const int tl = it.t0 + min(row, rows - 1) / G;
             bool seen = in;
             if (in && pos >= prefix) {
@@ -247,12 +264,35 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
       }
       bad = __syncthreads_or(bad);  // (and both tiles have been read)
       if (bad && tid == 0) atomicOr(f.status, PA_DEV_BAD_BLOCK);
+      if (R == 1 && sets > 1) {  // the sets' sums meet in the tiles' place
+        constexpr int LD = (VALUES ? N : 0) + 2;
+        float *own = reinterpret_cast<float *>(s_raw) + tid * LD;
+        own[0] = m[0];
+        own[1] = l[0];
+        if constexpr (VALUES) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) own[2 + i] = o[0][i];
+        }
+        __syncthreads();
+        for (int k = 1; set == 0 && k < sets; ++k) {
+          const float *other = own + k * per * 8 * LD;
+          const float top = fmaxf(m[0], other[0]);
+          const float a = m[0] == top ? 1.f : exp2f(m[0] - top), b = other[0] == top ? 1.f : exp2f(other[0] - top);
+          m[0] = top;
+          l[0] = l[0] * a + other[1] * b;
+          if constexpr (VALUES) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[0][i] = o[0][i] * a + other[2 + i] * b;
+          }
+        }
+        __syncthreads();  // (read, before the next pass's tiles)
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int h = 4; h >= 1; h >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], h);
-        const int row = row0 + r * 32 + (tid >> 3);
-        if (row < rows) {
+        const int row = row1 + r * 32;
+        if (row < rows && set == 0) {
           const long long at = span_row(p, it.slot, 0, row);
           if constexpr (VALUES) {
             const float inv = l[r] == 0.f || bad ? 0.f : 1.f / l[r];
@@ -280,7 +320,9 @@ __global__ void __launch_bounds__(kSimtThreads, 1) span_simt_kernel(const SpanPa
 // A row is one (token, query head).  Its partials are those of its unit's pieces:
 //   L = log2(sum_i 2^(lse_i) [+ 2^sink]),  out = sum_i 2^(lse_i - L) O_i.
 // Eight lanes hold a row's head_dim values and walk its partials four at a time;
-// W such groups share a row's partials and meet in shared memory.
+// W such groups share a row's partials and meet in shared memory.  Rows of units that
+// the pass has finished are passed over.  Bound by the reads of the partials, which are
+// in L2, and with few rows by its latency (5 us by itself for one tree of 8 tokens).
 
 template <typename T>
 __device__ inline void store4(T *dst, float a, float b, float c, float d);
