@@ -22,11 +22,12 @@ __device__ inline bool request_bad(const SpanParams &p, const SpanReq &r) {
   return __ldcg(p.row_lse + (size_t)(r.q_start + r.q_len - 1) * p.f.num_heads) == INFINITY;
 }
 
-// fp32: 64 positions x 32 rows a step, a thread 4 positions x 2 rows; a block's keys
+// fp32: 64 positions x 64 rows a step, a thread 4 positions x 4 rows; a block's keys
 // stay in shared memory while all rows pass.  Bound by the multiply-adds and the shared
 // memory that feeds them: 16 windows of 64 tokens, 16/4 heads of 64, up to 16384
-// positions: 1.79 ms, 7.4 TFLOP/s.
-constexpr int kPos = 64, kRows = 32;
+// positions: 0.81 ms, 16 TFLOP/s (two rows a thread and neighbouring positions, whose
+// keys met in one bank: 1.79).
+constexpr int kPos = 64, kRows = 64, kOwn = kRows / 16;  // kOwn: rows of a thread, 16 apart
 
 __device__ inline float4 load4f(const float *src) { return *reinterpret_cast<const float4 *>(src); }
 
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
   __shared__ float s_lse[kRows], s_sum[kVoteThreads / 16][kPos];
   const FwdParams &f = p.f;
   const int tid = threadIdx.x, H = f.num_heads, Hk = f.num_kv_heads, G = H / Hk, bs = f.block_size;
-  const int tx = tid & 15, ty = tid >> 4;  // positions 4 tx .., rows ty and ty + 16
+  const int tx = tid & 15, ty = tid >> 4;  // positions tx, tx + 16, .. (no two in a bank), rows ty, ty + 16, ..
   pdl_trigger();
   pdl_wait();
   if (p.plan->all_bad) return;
@@ -83,35 +84,33 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
                              : -INFINITY;
       }
       __syncthreads();
-      float acc[2][4] = {};
-#pragma unroll 4
+      float even[kOwn][4] = {}, odd[kOwn][4] = {};  // sums over even and odd columns
+#pragma unroll 2
       for (int x = 0; x < D; x += 4) {
-        float4 a[2], b[4];
+        float4 a[kOwn], b[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4 *>(&s_q[(ty + 16 * i) * LD + x]);
+        for (int i = 0; i < kOwn; ++i) a[i] = *reinterpret_cast<const float4 *>(&s_q[(ty + 16 * i) * LD + x]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(&s_k[(tx * 4 + j) * LD + x]);
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(&s_k[(tx + 16 * j) * LD + x]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kOwn; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-            acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-            acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-            acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+            ffma2(even[i][j], odd[i][j], a[i].x, a[i].y, b[j].x, b[j].y);
+            ffma2(even[i][j], odd[i][j], a[i].z, a[i].w, b[j].z, b[j].w);
           }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kOwn; ++i) {
         const int row = r0 + ty + 16 * i, own = prefix + min(row, R - 1) / G;
         const float l = s_lse[ty + 16 * i];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (at + tx * 4 + j <= own) sum[j] += vote(acc[i][j], l);
+          if (at + tx + 16 * j <= own) sum[j] += vote(even[i][j] + odd[i][j], l);
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_sum[ty][tx * 4 + j] = sum[j];
+    for (int j = 0; j < 4; ++j) s_sum[ty][tx + 16 * j] = sum[j];
     __syncthreads();
     if (tid < kPos / 4 && at + tid * 4 < r.ctx) {
       float tot[4];
