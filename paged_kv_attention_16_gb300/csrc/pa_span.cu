@@ -467,8 +467,10 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
   if (!waited) pdl_wait();
 }
 
-__global__ void __launch_bounds__(kMergeThreads) votes_kept_kernel(const SpanParams p, int chunks) {
-  pdl_trigger();
+// more: another kernel of the call follows.  (A next call's blocks would only take
+// these ones' places: 64 decodes 223.7 us, 222.5 without.)
+__global__ void __launch_bounds__(kMergeThreads) votes_kept_kernel(const SpanParams p, int chunks, int more) {
+  if (more) pdl_trigger();
   votes_kept<false>(p, blockIdx.x, gridDim.x, chunks);
 }
 
@@ -484,17 +486,18 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
   const FwdParams &f = p.f;
   const int S = f.num_seqs, H = f.num_heads, lg = __ffs(H / f.num_kv_heads) - 1;
   const int tid = threadIdx.x, lane = tid & 7, grp = tid >> 3, part = grp % W;
-  pdl_trigger();
+  const long long rows = (long long)f.num_tokens * H;
+  // The plan is done (every block of the kernel before awaited it): a block of one
+  // step works out where its partials lie while they are made.
+  const bool early = (long long)merge_blocks * ROWS >= rows;
+  // (blocks of several steps keep their places to themselves: 12 wide trees 558 us, 555 so)
+  if (early) pdl_trigger();
   if constexpr (MODE != kSpanTree) {
     if ((int)blockIdx.x >= merge_blocks) {
       votes_kept<true>(p, blockIdx.x - merge_blocks, gridDim.x - merge_blocks, chunks);
       return;
     }
   }
-  const long long rows = (long long)f.num_tokens * H;
-  // The plan is done (every block of the kernel before awaited it): a block of one
-  // step works out where its partials lie while they are made.
-  const bool early = (long long)merge_blocks * ROWS >= rows;
   if (early) __threadfence();
   else pdl_wait();
   T *out = static_cast<T *>(f.out);
@@ -677,7 +680,7 @@ cudaError_t launch_merge_d(const SpanParams &p, long long most, int most_rows, c
       launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p, (int)blocks, (int)chunks);
   if (e != cudaSuccess) return e;
   return launch_dependent(votes_kept_kernel, dim3((unsigned)std::min(items, 8 * sms)), dim3(kMergeThreads), 0, st,
-                          p, (int)chunks);
+                          p, (int)chunks, (int)(most_rows > kSpanStoredRows));
 }
 
 template <int D, int MODE>

@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
   __shared__ unsigned long long s_mask[2][kMaskTokens][kMaskWords];
   __shared__ int s_up[2][kMaskTokens];
   const int S = a.num_seqs, T = a.num_tokens, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  pdl_wait();
+  pdl_wait();  // (the next kernel's blocks come in behind these: 256 trees one call
+               // after the other 8.2 us, 14.1 with a trigger here)
   int bad = 0;
   for (int s = tid; s < S; s += kMaskThreads) {
     const int q0 = a.qsl[s], q1 = a.qsl[s + 1];
