@@ -402,9 +402,8 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
   __shared__ float s_lse[kSpanStoredRows];
   const FwdParams &f = p.f;
   const int tid = threadIdx.x, Hk = f.num_kv_heads, lg = __ffs(f.num_heads / Hk) - 1, bs = f.block_size;
-  __threadfence();  // (the plan is done: every block of the kernel before awaited it)
+  pdl_wait();  // the plan, and what else the kernel before has left
   const SpanPlan plan = *p.plan;
-  bool waited = false;
   const int units = f.num_seqs * Hk;
   for (long long item = block; !plan.all_bad && item < (long long)chunks * units; item += blocks) {
     const int at = (int)(item / units) * kKeptChunk, sh = (int)(item - (long long)at / kKeptChunk * units);
@@ -413,10 +412,7 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
     if (r.nblk == 0 || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
     const int R = r.q_len << lg;
     const bool mine = pos < r.ctx;
-    // (what does not wait for the sums is on its way before them)
     const int page = mine ? f.block_table[(size_t)s * f.max_blocks_per_seq + pos / bs] : 0;
-    if (!waited) pdl_wait();
-    waited = true;
     const long long pad = (long long)r.ntile * kSpanTile;
     const float *src = p.scores + r.score0 + (long long)kvh * R * pad + pos;
     float4 x[4];
@@ -463,8 +459,6 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
       span_vote(__ldcg(reinterpret_cast<const float4 *>(src + i * pad)), s_lse[i], sum);
     span_add_votes(p, r, page, kvh, pos, sum);
   }
-  // (whatever waits for this kernel waits for the one before it too)
-  if (!waited) pdl_wait();
 }
 
 // more: another kernel of the call follows.  (A next call's blocks would only take
@@ -487,19 +481,16 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
   const int S = f.num_seqs, H = f.num_heads, lg = __ffs(H / f.num_kv_heads) - 1;
   const int tid = threadIdx.x, lane = tid & 7, grp = tid >> 3, part = grp % W;
   const long long rows = (long long)f.num_tokens * H;
-  // The plan is done (every block of the kernel before awaited it): a block of one
-  // step works out where its partials lie while they are made.
-  const bool early = (long long)merge_blocks * ROWS >= rows;
   // (blocks of several steps keep their places to themselves: 12 wide trees 558 us, 555 so)
-  if (early) pdl_trigger();
+  if ((long long)merge_blocks * ROWS >= rows) pdl_trigger();
   if constexpr (MODE != kSpanTree) {
     if ((int)blockIdx.x >= merge_blocks) {
       votes_kept<true>(p, blockIdx.x - merge_blocks, gridDim.x - merge_blocks, chunks);
       return;
     }
   }
-  if (early) __threadfence();
-  else pdl_wait();
+  // The plan too: where the span kernel makes it, it is a running kernel's until here.
+  pdl_wait();
   T *out = static_cast<T *>(f.out);
   const SpanPlan plan = *p.plan;
   // a decode batch: token tok is most likely request tok's, no search
@@ -537,7 +528,6 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
         if (done) mine = false;
       }
     }
-    if (early) pdl_wait();  // the partials
     for (int e0 = part; e0 < n; e0 += 4 * W) {
       float lse[4];
       float4 x[4][V];

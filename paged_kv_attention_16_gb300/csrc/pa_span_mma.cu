@@ -112,7 +112,6 @@ __device__ inline SpanPlan span_plan_warp(const SpanParams &p, SpanReq *req, int
     if (flags) atomicOr(p.f.status, flags);
   }
   __syncwarp();
-  if (leave) __threadfence();
   return plan;
 }
 
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = f.num_heads / f.num_kv_heads, TQ = 128 / G, bs = f.block_size, lg = __ffs(G) - 1;
   if (smem_u32(smem) & 1023) {  // the same for every thread: all leave together
     if (tid == 0) atomicOr(f.status, PA_DEV_INTERNAL);
-    pdl_wait();  // (the merge counts on the plan being done)
+    pdl_wait();  // (the plan's words are the call's before until then)
     if (p.fused && blockIdx.x == 0 && tid == 0) *p.plan = SpanPlan{0, 1, 0, 1};
     return;
   }
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         SpanReq *const s_req = reinterpret_cast<SpanReq *>(smem + C::OFF_REQ);
         if (p.fused) cur.start(p, s_req, span_plan_warp(p, s_req, lane, blockIdx.x == 0), blockIdx.x);
         else cur.start(p, p.req, *p.plan, blockIdx.x);
-        pdl_trigger();  // (the merge counts on the plan being done)
+        pdl_trigger();
       }
       auto make_piece = [&]() {
         if (!cur.next(p, lg, CAUSAL, it)) it.kv_lo = it.kv_hi = 0;
