@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "pa_join.h"
 #include "pa_span.h"
 
 namespace pa {
@@ -338,9 +339,6 @@ __device__ inline void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float a, float 
                                                *reinterpret_cast<const uint32_t *>(&y));
 }
 
-// The larger one, but a NaN stays.
-__device__ inline float max_nan(float a, float b) { return b > a || b != b ? b : a; }
-
 // Where the partials of one row lie.
 struct SpanRow {
   unsigned u0, len;     // its unit's laid-out work
@@ -436,12 +434,12 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
         const long long from = span_partial(p, plan, row, e);
         const float v = from < 0 ? -INFINITY : __ldcg(p.part_lse + from);
         if (v == -INFINITY) continue;
-        const float top = max_nan(m, v);
+        const float top = join_top(m, v);
         l = l * (m == top ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - top)) + (v == top ? 1.f : fast_exp2(v - top));
         m = top;
       }
       if (f.sinks && !done && m != INFINITY && m != -INFINITY) {
-        const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = max_nan(m, sink2);
+        const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = join_top(m, sink2);
         l = l * fast_exp2(m - top) + fast_exp2(sink2 - top);
         m = top;
       }
@@ -547,7 +545,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (lse[u] == -INFINITY) continue;  // no such partial, or one without a visible position
-        const float top = max_nan(m, lse[u]);
+        const float top = join_top(m, lse[u]);
         // (equal infinities: a bad page, which m tells)
         const float a = m == -INFINITY || m == top ? (m == top ? 1.f : 0.f) : fast_exp2(m - top);
         const float wt = lse[u] == top ? 1.f : fast_exp2(lse[u] - top);
@@ -577,7 +575,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
       __syncthreads();
       if (part == 0) {
         float top = m;
-        for (int k = 1; k < W; ++k) top = max_nan(top, s_m[grp + k]);
+        for (int k = 1; k < W; ++k) top = join_top(top, s_m[grp + k]);
         const float a = m == top ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - top);
         l *= a;
         if constexpr (VALUES) {
@@ -613,7 +611,7 @@ __global__ void __launch_bounds__(kMergeThreads) span_merge_kernel(const SpanPar
       // nothing, or a bad page, is zero
       const bool bad = m == INFINITY, none = m == -INFINITY;
       if (!bad && !none && f.sinks) {
-        const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = max_nan(m, sink2);
+        const float sink2 = __ldg(f.sinks + h) * kLog2eF, top = join_top(m, sink2);
         const float k = fast_exp2(m - top);
         l = l * k + fast_exp2(sink2 - top);
         m = top;

@@ -325,9 +325,11 @@ __device__ inline void span_vote(const float4 x, float lse, float (&sum)[4]) {
 }
 
 // Adds `sum`, of the four positions from pos on, to their slots of `page`.  Positions
-// of the new tokens start at their sum; positions from ctx on have no slot.
+// of the new tokens start at their sum; positions from ctx on have no slot, nor has a
+// page beyond the pool (its request is passed over; no access goes by that alone).
 __device__ inline void span_add_votes(const SpanParams &p, const SpanReq &r, int page, int kvh, int pos,
                                       const float (&sum)[4]) {
+  if (page < 0 || page >= p.f.num_blocks) return;
   const int bs = p.f.block_size;  // (bs % 16 == 0: one page)
   float *dst = p.weights + ((size_t)page * p.f.num_kv_heads + kvh) * bs + pos % bs;
   const int fresh = p.accumulate ? r.ctx - r.q_len : 0;

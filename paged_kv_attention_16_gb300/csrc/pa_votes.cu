@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(kVoteThreads) votes_simt_kernel(const SpanPara
     for (int e = tid; e < kPos * (D / 4); e += kVoteThreads) {
       const int j = e / (D / 4), x = e % (D / 4) * 4, pos = at + j;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (pos < r.ctx) {
-        const int page = bt[pos / bs], slot = pos % bs;
+      const int page = pos < r.ctx ? bt[pos / bs] : -1, slot = pos % bs;
+      if (page >= 0 && page < f.num_blocks) {
         const size_t row = p.hnd ? ((size_t)page * Hk + kvh) * bs + slot : ((size_t)page * bs + slot) * Hk + kvh;
         v = load4f(static_cast<const float *>(p.k_cache) + row * D + x);
       }

@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     while (!dead && cur.next(p, lg, QR, it)) {
       const int32_t *bt = f.block_table + (size_t)it.s * f.max_blocks_per_seq;
       const int pos = it.at + run * box;
-      const int page = mine && pos < it.r.ctx ? bt[pos / bs] : f.num_blocks;  // past the pool: zeros
+      int page = mine && pos < it.r.ctx ? bt[pos / bs] : f.num_blocks;  // past the pool: zeros
+      if (page < 0 || page > f.num_blocks) page = f.num_blocks;
       if (lane == 0) {
         if (kr > 0) mbar_wait(&bar[C::K_FREE + ks], (kr - 1) & 1, dead, f.status);
         if (!dead) mbar_arrive_expect_tx(&bar[C::K_FULL + ks], C::K_BYTES);
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         at_kvh = it.kvh;
       }
       const bool store = (item & 1) == grp;  // the groups take turns
-      const int page = store && pos < it.r.ctx ? f.block_table[(size_t)it.s * f.max_blocks_per_seq + pos / bs] : 0;
+      const int page = store && pos < it.r.ctx ? f.block_table[(size_t)it.s * f.max_blocks_per_seq + pos / bs] : -1;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       const uint32_t behind = n + (it.nb - it.b0);
       n += mine - it.b0;
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         named_arrive(4 + (item & 1), 256);
       } else {
         named_sync(4 + (item & 1), 256);
-        if (pos < it.r.ctx) {
+        if (page >= 0 && page < f.num_blocks) {
           float *dst = p.weights + ((size_t)page * f.num_kv_heads + it.kvh) * bs + pos % bs;
           const float all = *add + w;
           *dst = p.accumulate && pos < prefix ? *dst + all : all;
