@@ -197,6 +197,9 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
     }
     return;
   }
+  // The cluster's blocks are all there before any of them reaches into another's shared
+  // memory, whether or not there is something to count; the weights are read meanwhile.
+  if (C > 1) cluster_arrive_all();
   const int first = min(a.num_first, after), recent = min(a.num_recent, after - first);
   const int need = after - first - recent, lo = first, hi = len - recent;  // candidates [lo, hi)
   for (int c = part * kSelectThreads + tid; c < (after + a.chunk_rows - 1) / a.chunk_rows; c += C * kSelectThreads)
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
     }
     __syncthreads();
   }
+  if (C > 1) cluster_wait_all();
   auto key_of = [&](int pos) { return pos < c1 ? s_key[pos - p0] : order_of(read(pos)); };
 
   // -- the candidate of rank `need` from the top: `prefix` its leading bits
