@@ -612,7 +612,8 @@ pa_status pa_cache_write_slots(const void *k_new, const void *v_new,
  *                      below -1): that token and those below it
  * Asynchronous on `stream`, one launch, no workspace; capturable after the first
  * call on a device.  Errors: PA_ERR_INVALID_ARG for null pointers with nonzero
- * sizes, negative sizes, mask_words < 1 or pointers not aligned to their element;
+ * sizes, negative sizes, mask_words < 1, pointers not aligned to their element, or an
+ * array written that overlaps another one of the call (positions over parents, say);
  * PA_ERR_UNSUPPORTED for more than 2^30 tokens.
  */
 pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_start_loc,
@@ -649,8 +650,8 @@ pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_start_loc,
  * blocks (tokens x query heads of a KV head) that meet the bad page.
  * Errors: as for pa_forward; PA_ERR_INVALID_ARG also for no request with
  * num_tokens > 0, a NULL or misaligned mask or mask_words < 1, int32 arrays that are
- * not 4-byte aligned, or a workspace that is not 256-byte aligned;
- * PA_ERR_WORKSPACE when the workspace is NULL or too small, or when the first call
+ * not 4-byte aligned, an out that overlaps q, or a workspace that is not 256-byte
+ * aligned; PA_ERR_WORKSPACE when the workspace is NULL or too small, or when the first call
  * on a device is made during capture; PA_ERR_UNSUPPORTED for extents whose units of
  * work pass 2^31, or a max_seq_len above 2^30.  num_tokens == 0 launches nothing.
  */
@@ -687,7 +688,7 @@ size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tok
  *  path             [num_seqs, max_path] int32, strictly rising; entries from
  *                   path_lens[s] on are not read
  *  path_lens        [num_seqs] int32, 0 .. min(q_len, max_path)
- *  seq_lens_out     [num_seqs] int32, written; another array than seq_lens
+ *  seq_lens_out     [num_seqs] int32, written
  *  freed_pages      [freed_capacity] int32: the ids of the pages from
  *                   ceil(new length / block_size) to ceil(seq_len / block_size) of
  *                   each request, in request order (a list that pa_block_tables
@@ -702,7 +703,9 @@ size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tok
  * written as -1.  PA_DEV_OVERFLOW: more freed pages than freed_capacity; the first
  * ones are listed.
  * Asynchronous on `stream`, one launch, two for the list of many paths, no
- * workspace; capturable after the first call on a device.  Errors as for pa_cache_write.
+ * workspace; capturable after the first call on a device.  Errors as for pa_cache_write;
+ * PA_ERR_INVALID_ARG also for an int32 array written that overlaps another one of the
+ * call.
  */
 pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_table,
                           const int32_t *seq_lens, const int32_t *query_start_loc,
@@ -779,8 +782,7 @@ size_t pa_forward_weights_workspace_bytes(pa_dtype dtype, int num_seqs,
  *  block_table      read only, as for pa_cache_accept
  *  seq_lens         [num_seqs] int32, at most max_seq_len
  *  keep_lens        [num_seqs] int32, the most positions each may keep (0 and more)
- *  seq_lens_out     [num_seqs] int32, written: min(seq_len, keep_len); another array
- *                   than seq_lens and keep_lens
+ *  seq_lens_out     [num_seqs] int32, written: min(seq_len, keep_len)
  *  freed_pages, num_freed, freed_capacity: as for pa_cache_accept
  *  max_seq_len      host-known bound on seq_lens (sizes the workspace)
  *  workspace        as for pa_forward_tree, pa_cache_evict_workspace_bytes()
@@ -791,7 +793,9 @@ size_t pa_forward_weights_workspace_bytes(pa_dtype dtype, int num_seqs,
  * weights from or to it are not moved; in the list of freed pages it is -1.
  * PA_DEV_OVERFLOW as for pa_cache_accept.
  * Asynchronous on `stream`, two launches; capturable after the first call on a
- * device.  Errors as for pa_cache_write; PA_ERR_WORKSPACE as for pa_forward_tree;
+ * device.  Errors as for pa_cache_write; PA_ERR_INVALID_ARG also for an int32 array
+ * written that overlaps another one of the call, or weights that overlap weights_out
+ * without being the same; PA_ERR_WORKSPACE as for pa_forward_tree;
  * PA_ERR_UNSUPPORTED also for extents beyond 2^31 moved runs, or a max_seq_len above
  * 2^30.
  */

@@ -592,12 +592,20 @@ pa_status pa_cache_evict(void *k_cache, void *v_cache, const float *weights, flo
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 4) ||
       !aligned(weights_out, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
       !aligned(keep_lens, 4) || !aligned(seq_lens_out, 4) || !aligned(freed_pages, 4) ||
-      !aligned(num_freed, 4) || seq_lens_out == seq_lens || seq_lens_out == keep_lens)
+      !aligned(num_freed, 4))
     return PA_ERR_INVALID_ARG;
   const EvictLayout lay = evict_layout(head_dim * es, num_seqs, num_kv_heads, max_seq_len);
   if (!lay.ok) return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_INVALID_ARG;
+  const MemRange from(weights, (long long)num_blocks * num_kv_heads, block_size * 4ll),
+      to(weights_out, (long long)num_blocks * num_kv_heads, block_size * 4ll);
+  if (any_overlap({{seq_lens_out, num_seqs, 4}, {freed_pages, freed_capacity, 4}, {num_freed, 1, 4}},
+                  {{block_table, (long long)num_seqs * max_blocks_per_seq, 4},
+                   {seq_lens, num_seqs, 4},
+                   {keep_lens, num_seqs, 4}}) ||
+      (weights != weights_out && from.meets(to)))
+    return PA_ERR_INVALID_ARG;
   EvictArgs a{};
   void *lib_ws = nullptr;
   int num_sms = 0;

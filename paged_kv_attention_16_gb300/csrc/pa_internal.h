@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 
 #include "pa_common.cuh"
 
@@ -126,6 +127,28 @@ pa_status launch_rows_and_tiles(const FwdCall &c, FwdParams &p, int num_sms, cud
                                 bool timed);
 // Resident CTAs per SM of the row kernel that serves these rows.
 int row_ctas_per_sm(int dtype, int head_dim, int group);
+
+// Memory that a call's argument names: n elements of `size` bytes at p (null: none).
+struct MemRange {
+  uintptr_t at;
+  unsigned long long bytes;
+  MemRange(const void *p, long long n, long long size)
+      : at(reinterpret_cast<uintptr_t>(p)), bytes(p && n > 0 ? (unsigned long long)n * size : 0) {}
+  bool meets(const MemRange &o) const {
+    return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes;
+  }
+};
+// Whether what a call writes meets what it reads, or anything else that it writes: then
+// other blocks of the call, or other launches, would read what it has just written.
+inline bool any_overlap(std::initializer_list<MemRange> written, std::initializer_list<MemRange> read) {
+  for (const MemRange *w = written.begin(); w != written.end(); ++w) {
+    for (const MemRange *x = w + 1; x != written.end(); ++x)
+      if (w->meets(*x)) return true;
+    for (const MemRange &x : read)
+      if (w->meets(x)) return true;
+  }
+  return false;
+}
 
 // True while `stream` is capturing a CUDA graph.
 bool stream_capturing(cudaStream_t stream);

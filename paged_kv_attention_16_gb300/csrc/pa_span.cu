@@ -790,6 +790,9 @@ pa_status span_call(const SpanCall &sc) {
   if (!lay.ok) return PA_ERR_UNSUPPORTED;
   if (!sc.workspace || sc.workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(sc.workspace) & 255) return PA_ERR_INVALID_ARG;
+  // (queries are read again behind the first outputs' stores)
+  const long long rows = (long long)c.num_tokens * c.num_heads, row_bytes = c.head_dim * (c.dtype == PA_F32 ? 4 : 2);
+  if (any_overlap({{c.out, rows, row_bytes}}, {{c.q, rows, row_bytes}})) return PA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(sc.stream);
   SpanParams p{};
   void *lib_ws = nullptr;

@@ -333,6 +333,9 @@ extern "C" pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_
     return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
   if (num_tokens > 1 << 30) return PA_ERR_UNSUPPORTED;
+  if (any_overlap({{tree_mask, (long long)num_tokens * mask_words, 8}, {positions, num_tokens, 4}},
+                  {{parents, num_tokens, 4}, {query_start_loc, num_seqs + 1ll, 4}, {seq_lens, num_seqs, 4}}))
+    return PA_ERR_INVALID_ARG;
   MaskArgs a{};
   void *ws = nullptr;
   int num_sms = 0;
@@ -382,7 +385,14 @@ extern "C" pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(path, 4) ||
       !aligned(path_lens, 4) || !aligned(seq_lens_out, 4) || !aligned(freed_pages, 4) ||
-      !aligned(num_freed, 4) || seq_lens_out == seq_lens)
+      !aligned(num_freed, 4))
+    return PA_ERR_INVALID_ARG;
+  if (any_overlap({{seq_lens_out, num_seqs, 4}, {freed_pages, freed_capacity, 4}, {num_freed, 1, 4}},
+                  {{block_table, (long long)num_seqs * max_blocks_per_seq, 4},
+                   {seq_lens, num_seqs, 4},
+                   {query_start_loc, num_seqs + 1ll, 4},
+                   {path, (long long)num_seqs * max_path, 4},
+                   {path_lens, num_seqs, 4}}))
     return PA_ERR_INVALID_ARG;
   AcceptArgs a{};
   void *ws = nullptr;
