@@ -614,7 +614,7 @@ pa_status pa_cache_write_slots(const void *k_new, const void *v_new,
  * call on a device.  Errors: PA_ERR_INVALID_ARG for null pointers with nonzero
  * sizes, negative sizes, mask_words < 1, pointers not aligned to their element, or an
  * array written that overlaps another one of the call (positions over parents, say);
- * PA_ERR_UNSUPPORTED for more than 2^30 tokens.
+ * PA_ERR_UNSUPPORTED for more than 2^30 tokens or requests.
  */
 pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_start_loc,
                         const int32_t *seq_lens, uint64_t *tree_mask,
@@ -705,7 +705,7 @@ size_t pa_forward_tree_workspace_bytes(pa_dtype dtype, int num_seqs, int num_tok
  * Asynchronous on `stream`, one launch, two for the list of many paths, no
  * workspace; capturable after the first call on a device.  Errors as for pa_cache_write;
  * PA_ERR_INVALID_ARG also for an int32 array written that overlaps another one of the
- * call.
+ * call, PA_ERR_UNSUPPORTED also for more than 2^30 requests.
  */
 pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_table,
                           const int32_t *seq_lens, const int32_t *query_start_loc,

@@ -332,7 +332,7 @@ extern "C" pa_status pa_tree_masks(const int32_t *parents, const int32_t *query_
       !aligned(positions, 4) || !aligned(tree_mask, 8))
     return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
-  if (num_tokens > 1 << 30) return PA_ERR_UNSUPPORTED;
+  if (num_tokens > 1 << 30 || num_seqs > 1 << 30) return PA_ERR_UNSUPPORTED;
   if (any_overlap({{tree_mask, (long long)num_tokens * mask_words, 8}, {positions, num_tokens, 4}},
                   {{parents, num_tokens, 4}, {query_start_loc, num_seqs + 1ll, 4}, {seq_lens, num_seqs, 4}}))
     return PA_ERR_INVALID_ARG;
@@ -375,7 +375,8 @@ extern "C" pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t
     return PA_ERR_INVALID_ARG;
   const int es = dtype == PA_F32 ? 4 : 2;
   if ((long long)head_dim * es % 16 != 0 || (long long)head_dim * es > kMaxHeadBytes ||
-      (long long)max_path * (head_dim * es / 16) > 1 << 30)  // pieces of a path, counted in 32 bits
+      (long long)max_path * (head_dim * es / 16) > 1 << 30 ||  // pieces of a path, counted in 32 bits
+      num_seqs > 1 << 30)
     return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0 && !num_freed) return PA_OK;
   if (num_seqs > 0 &&

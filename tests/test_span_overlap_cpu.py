@@ -1,6 +1,6 @@
 """Arrays that a call writes and that overlap others of the same call are refused on the
-host: blocks and launches of one call read what others of it write.  Nothing is launched,
-no GPU needed."""
+host: blocks and launches of one call read what others of it write.  Counts that would
+pass the kernels' 32-bit counters are refused too.  Nothing is launched, no GPU needed."""
 import ctypes
 
 import pytest
@@ -41,6 +41,7 @@ WEIGHT_ARGS = apart(WEIGHTS, "q k v bt sl qsl out w ws")
     (dict(pos=at(0)), 1), (dict(pos=at(0, 8)), 1), (dict(pos=at(0, -8)), 1),  # over parents
     (dict(pos=at(1, 8)), 1), (dict(pos=at(2, 4)), 1), (dict(pos=at(3, 20)), 1),
     (dict(mask=at(0)), 1), (dict(mask=at(1, -16)), 1), (dict(mask=at(2)), 1),
+    (dict(S=(1 << 30) + 1), 2),
 ])
 def test_masks(lib, kw, want):
     assert call(lib.pa_tree_masks, *MASK_ARGS, kw) == want
@@ -51,6 +52,7 @@ def test_masks(lib, kw, want):
     (dict(out=at(4, 8)), 1), (dict(out=at(5, 28)), 1), (dict(out=at(6)), 1), (dict(out=at(2, 28)), 1),
     (dict(freed=at(2)), 1), (dict(freed=at(3, -28)), 1), (dict(freed=at(6)), 1),
     (dict(count=at(6, 4)), 1), (dict(count=at(7)), 1), (dict(count=at(8, 28)), 1), (dict(freed=at(7, -4)), 1),
+    (dict(S=(1 << 30) + 1), 2),
 ])
 def test_accept(lib, kw, want):
     assert call(lib.pa_cache_accept, *ACCEPT_ARGS, kw) == want
