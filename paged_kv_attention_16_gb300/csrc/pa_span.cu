@@ -408,7 +408,7 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
     const int s = sh / Hk, kvh = sh - s * Hk, pos = at + tid * 4;
     const SpanReq r = p.req[s];
     if (r.nblk == 0 || r.score0 < 0 || at >= r.ctx) continue;  // (the same for all threads)
-    const int R = r.q_len << lg;
+    const int R = r.q_len << lg, prefix = r.ctx - r.q_len;
     const bool mine = pos < r.ctx;
     const int page = mine ? f.block_table[(size_t)s * f.max_blocks_per_seq + pos / bs] : 0;
     const long long pad = (long long)r.ntile * kSpanTile;
@@ -451,10 +451,10 @@ __device__ inline void votes_kept(const SpanParams &p, int block, int blocks, in
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < R) span_vote(x[i], s_lse[i], sum);
+      if (i < R) span_vote(x[i], s_lse[i], pos, prefix + (i >> lg), sum);
 #pragma unroll 4
     for (int i = 4; i < R; ++i)
-      span_vote(__ldcg(reinterpret_cast<const float4 *>(src + i * pad)), s_lse[i], sum);
+      span_vote(__ldcg(reinterpret_cast<const float4 *>(src + i * pad)), s_lse[i], pos, prefix + (i >> lg), sum);
     span_add_votes(p, r, page, kvh, pos, sum);
   }
 }

@@ -315,9 +315,17 @@ __device__ inline unsigned long long span_causal_bits(int at, int own) {
 // The pass over keys and values on the tensor cores (bf16; mode: a SpanMode).
 cudaError_t launch_span_mma(const SpanParams &p, int mode, cudaStream_t stream);
 
-// The weight of four scores of one row; a row that sees nothing (-inf) has none.
-__device__ inline void span_vote(const float4 x, float lse, float (&sum)[4]) {
+// The weight of four scores of one row, of the positions from pos on; `own`: the row's
+// token's.  A row that sees nothing (-inf) has none, and one that is not a number has
+// none at the positions that it does not see (whose scores are -inf).
+__device__ inline void span_vote(const float4 x, float lse, int pos, int own, float (&sum)[4]) {
   if (lse == -INFINITY) return;
+  if (lse != lse) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (pos + c <= own) sum[c] += lse;
+    return;
+  }
   sum[0] += fast_exp2(x.x - lse);
   sum[1] += fast_exp2(x.y - lse);
   sum[2] += fast_exp2(x.z - lse);
