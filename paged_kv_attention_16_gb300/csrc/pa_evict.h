@@ -9,9 +9,12 @@ namespace pa {
 
 constexpr int kMaxHeadBytes = 16384;  // of one KV head's row: 1024 pieces of 16 bytes
 
-// Division of 0 <= n < 2^31 by d >= 1, the same for a whole call: one high product
-// instead of the twenty instructions of a division (these kernels run once over
-// little data, so they are as fast as their code comes in).
+// Division of 0 <= n < 2^31 by d >= 1, the same for a whole call, by a high product
+// (Granlund and Montgomery, "Division by invariant integers using multiplication",
+// 1994): with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1,
+//   floor(n / d) = (floor(n m / 2^32) + n) >> s,
+// whose sum stays below 2^32 for these n.  These kernels run once over little data,
+// so they are as fast as their code comes in: a few instructions for a division's many.
 struct FastDiv {
   unsigned mul, shift;
 };

@@ -188,7 +188,7 @@ struct AcceptArgs {
   const int32_t *block_table, *seq_lens, *qsl, *path, *path_lens;
   int32_t *seq_lens_out;
   FreeList free;
-  int num_seqs, num_tokens, max_path, num_kv_heads, head_bytes, block_size, max_blocks_per_seq,
+  int num_seqs, max_path, num_kv_heads, head_bytes, block_size, max_blocks_per_seq,
       num_blocks, hnd;
   FastDiv by_bs, by_ppr;
   unsigned int *status;
