@@ -724,7 +724,8 @@ pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_tab
  * pa_forward_weights -- pa_forward (causal), and for every KV head k and position j
  *   W[k][j] = sum over the request's rows i and the query heads h of k of
  *             softmax_j(scale * <q[i][h], K_j>)
- * in fp32.  The rows given are those that vote: one token a request in decoding, or
+ * in fp32 (a row that is not a number makes W so at the positions that it sees, not at
+ * later ones).  The rows given are those that vote: one token a request in decoding, or
  * the last tokens of a prompt whose output another call has made.
  *
  *  q, k_cache, block_table, seq_lens, num_heads, num_kv_heads, head_dim, block_size,
@@ -734,12 +735,13 @@ pa_status pa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_tab
  *  v_cache, out    as for pa_forward.  out may be NULL: the weights alone, v_cache
  *                  is then not read and may be NULL
  *  weights         [num_blocks, num_kv_heads, block_size] fp32, 16-byte aligned: the
- *                  accumulated weight of each cache slot.  A slot that two requests
- *                  of the call share (a common page) ends up with either one's sum
+ *                  accumulated weight of each cache slot.  What a slot that two
+ *                  requests of the call share (a common page) ends up with is not
+ *                  determined: one's sum, or both
  *  accumulate      1: W is added to the slots of the positions before the new tokens,
  *                  and set in those of the new tokens (whose weight begins here);
  *                  0: set in all of the request's slots.  Other slots are left as
- *                  they were
+ *                  they were, those of a request without new tokens too
  *  options         sinks (in the denominators), kv_layout, max_query_len as for
  *                  pa_forward_ex; a sliding window or ALiBi is PA_ERR_UNSUPPORTED
  *  workspace       as for pa_forward_tree, pa_forward_weights_workspace_bytes()

@@ -521,7 +521,9 @@ cudaError_t launch_select(const EvictArgs &a, int num_sms, cudaStream_t st) {
   int C = 1;
   while (C < kMostCluster && units * C * 2 <= num_sms && a.max_seq_len / (2 * C) >= kSelectThreads) C *= 2;
   const long long share = ceil_div_ll(std::max(a.max_seq_len, 1), C);
-  // (keys beyond 192 KB are read from memory in every pass)
+  // (keys beyond 192 KB are read from memory in every pass, one behind the other: 16
+  // requests of up to 131072 positions, 8 KV heads, take 727 us a call, 287 of them the
+  // bytes; 16 of up to 65536 323 and 144)
   const int cached = (int)std::min<long long>(share, 48 * 1024);
   static std::atomic<unsigned long long> done{0};
   int dev = 0;

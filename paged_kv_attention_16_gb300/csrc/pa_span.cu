@@ -653,9 +653,9 @@ cudaError_t launch_merge_d(const SpanParams &p, long long most, int most_rows, c
   if (MODE == kSpanTree)
     return launch_dependent(kern, dim3((unsigned)blocks), dim3(kMergeThreads), 0, st, p, (int)blocks, 0);
   // The sums over rows of kept scores beside the merge where the two blocks an SM that
-  // its registers leave hold them at once (4 decodes of up to 1000 positions 17.8 us,
-  // 20.5 behind it); else behind it, eight blocks an SM (64 decodes of up to 8192
-  // positions 219 us, 242 beside it).
+  // its registers leave hold them at once (4 decodes of up to 1000 positions 16.5 us,
+  // 18.5 behind it); else behind it, eight blocks an SM (64 decodes of up to 8192
+  // positions 223 us, 249 beside it).
   const long long chunks = ceil_div_ll(std::max(p.f.max_seq_len, 1), kKeptChunk);
   const long long items = chunks * p.f.num_seqs * p.f.num_kv_heads;
   if (items + blocks <= 2 * sms) {
@@ -838,7 +838,7 @@ pa_status span_call(const SpanCall &sc) {
   // Units of up to 128 rows finished in one row tile: where they are many, and have the
   // rows of trees (64 trees of 16 tokens, 4 heads each: 206 us, 200 so; the rows of
   // decode steps are few, 64 of them 222 us, 226 so, and the code that small calls wait
-  // for grows: one tree 11.2 us, 12.3 so).
+  // for grows: one tree 1.1 us more).
   p.join = p.halves && !votes && p.overhead > 0;
   p.slot_rows = lay.slot_rows;
   p.plan = reinterpret_cast<SpanPlan *>(ws + lay.plan);
@@ -849,8 +849,8 @@ pa_status span_call(const SpanCall &sc) {
   p.row_lse = votes ? reinterpret_cast<float *>(ws + lay.row_lse) : nullptr;
   p.scores = votes ? reinterpret_cast<float *>(ws + lay.scores) : nullptr;
 
-  // A launch less for few requests: one user's tree of 8 tokens 12.4 -> 11.4 us in a
-  // graph, 24 -> 21 launched one by one.
+  // A launch less for few requests: one user's tree of 8 tokens 13.7 -> 12.9 us in a
+  // graph, 23.4 -> 21.7 launched one by one.
   p.fused = c.dtype == PA_BF16 && c.num_seqs <= kSpanFusedSeqs;
   int slot;
   cudaError_t err = cudaSuccess;

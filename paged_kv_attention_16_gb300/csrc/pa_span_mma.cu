@@ -26,11 +26,11 @@
 // the pool, which TMA fills with zeros: every tile has the same byte count.
 //
 // What bounds it: units of up to 128 rows at head_dim 128 the stream of keys and
-// values (64 trees of up to 16 tokens, 32/8 heads, up to 8192 positions: 188 us for
-// 1.15 GB, 6.2 TB/s, 92 % of the measured copy rate); units of 256 rows the chain of a
+// values (64 trees of up to 16 tokens, 32/8 heads, up to 8192 positions: 188 to 192 us for
+// 1.15 GB, 6.0 to 6.2 TB/s, 90 to 92 % of the measured copy rate); units of 256 rows the chain of a
 // row tile's scores, softmax and value product, the two row tiles in turns (12 trees of
-// up to 250 tokens, 64/4 heads, up to 16384 positions: 543 us, 1.2 PFLOP/s, a tile some
-// 3100 clocks of which the products are 2200; the tensor pipe is busy 58 % of the
+// up to 250 tokens, 64/4 heads, up to 16384 positions: 530 to 545 us, 1.2 PFLOP/s, a tile
+// some 3100 clocks of which the products are 2200; the tensor pipe is busy 58 % of the
 // time); one small tree the latencies from the plan to the partials (8 us).
 #include "pa_span.h"
 #include "pa_umma.cuh"

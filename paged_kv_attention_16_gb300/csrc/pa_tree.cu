@@ -23,7 +23,9 @@ bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 // block's (shared memory); beyond that a thread walks its token's chain, which only
 // goes down, and writes its row's words from the top one to the bottom one.
 // Bound by latency (lengths, parents, the steps): 64 trees of up to 16 tokens 2.8 us in
-// a graph, 256 of up to 250 9.0 (27 with a chain a thread for all of them).
+// a graph, 256 of up to 250 9.0 (27 with a chain a thread for all of them).  Beyond
+// kMaskTokens the chain's loads follow one another: 64 trees of 512 tokens, each under a
+// random one before it, 7.5 us, as one chain 87; of 1000 tokens 17 and 284.
 constexpr int kMaskThreads = 256, kMaskTokens = 256, kMaskWords = kMaskTokens / 64;
 
 struct MaskArgs {
@@ -173,8 +175,9 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
 // in place.  A block takes one KV head of a request and walks its path upwards, some
 // rows at a time, all of them read before the first is written; what a step writes
 // lies below everything that later steps read.  500 paths of up to 200 rows of 256
-// bytes, four KV heads, take 39 us: 181 MB read and written, 4.6 TB/s (the steps of a
-// path follow one another; 75 us with pages and rows loaded one behind the other).  The block of KV head 0 writes the new
+// bytes, four KV heads, take 39 us: 181 MB read and written, 4.6 TB/s (a step's rows are
+// awaited before they are written, and written before the next step's are asked for;
+// 75 us with pages and rows loaded one behind the other).  The block of KV head 0 writes the new
 // length; a second launch lists the pages from the lengths.  Where the paths are few
 // and short in all (kListEntries) a block more of the first one lists them, looking
 // through every path itself.  Two launches against one: 1 path of 8 4.2 and 2.7 us, 64 of

@@ -15,10 +15,10 @@
 // scores go to two TMEM buffers in turn, a group of warps to each.  The groups' sums
 // meet in shared memory.
 //
-// Bound by the instructions around the exponentials and the waits for the scores:
-// 16 requests of 64 tokens, 4 heads a KV head of 64, 16384 positions: 38 us (268 million
-// exponentials, 2 instructions of the 3.2 issued for each; 56 % of the issue slots, the
-// tensor cores at 22 %, 71 MB from DRAM).  One group a CTA: 42 us, its scores fetched 32
+// No unit is full; what a tile waits for is the chain between the roles (keys and rows,
+// scores, sums): 16 requests of 64 tokens, 4 heads a KV head of 64, 16384 positions: 38
+// to 40 us (268 million exponentials, the exponential unit at 38 %, 56 % of the issue
+// slots, the tensor cores at 23 %, 71 MB from DRAM).  One group a CTA: 42 us, its scores fetched 32
 // columns ahead; with two groups that prefetch costs registers and time (40).
 #include "pa_span.h"
 #include "pa_umma.cuh"
