@@ -21,7 +21,7 @@
 // Values that a row does not see must not reach it, but 0 x NaN would: in tiles that
 // reach hidden positions, warps 14 and 15 look at the values and zero the rows that
 // are not finite; rows that see such a position get it back behind the piece, from
-// memory (fix_values).
+// memory (each_zeroed).
 // A box that lies past the piece, or on a bad page, is loaded from a page beyond
 // the pool, which TMA fills with zeros: every tile has the same byte count.
 //
@@ -127,11 +127,11 @@ __device__ inline bool not_finite(uint4 v) {  // of eight bf16 values, any
   return ((x | y | z | w) & 0x80008000u) != 0;
 }
 
-// The values that were zeroed, for one row that may see some of them: added to its
-// partial or its finished output (DONE), normalised by inv, in memory.  Rare and slow.
-template <int D, bool CAUSAL, bool DONE>
-__device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it, int row, bool half,
-                                        int x, float ref, float inv, void *out) {
+// The positions whose values were zeroed and which one row sees: use(w, v), w the row's
+// weight of the position, normalised by inv, v the values.  Rare and slow.
+template <int D, bool CAUSAL, typename Use>
+__device__ inline void each_zeroed(const SpanParams &p, const SpanPiece &it, int row, bool half, int x,
+                                   float ref, float inv, Use use) {
   const FwdParams &f = p.f;
   const int Hk = f.num_kv_heads, G = f.num_heads / Hk, bs = f.block_size, prefix = it.ctx - it.q_len;
   const int tl = it.t0 + row / G, head = it.kvh * G + row % G;
@@ -156,18 +156,28 @@ __device__ __noinline__ void fix_values(const SpanParams &p, const SpanPiece it,
     const __nv_bfloat16 *vv = static_cast<const __nv_bfloat16 *>(p.v_cache) + at;
     float s = 0.f;
     for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
-    const float w = fast_exp2(s * f.scale_log2 - ref) * inv;
-    // (what it adds is not finite where it matters: a finished output's rounding does not)
-    for (int d = 0; d < D; ++d) {
-      const float add = w * __bfloat162float(vv[d]);
-      if (DONE) {
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(out) + d;
-        *dst = __float2bfloat16_rn(__bfloat162float(*dst) + add);
-      } else {
-        static_cast<float *>(out)[d] += add;
-      }
-    }
+    use(fast_exp2(s * f.scale_log2 - ref) * inv, vv);
   }
+}
+
+// They are added to the row's partial.
+template <int D, bool CAUSAL>
+__device__ __noinline__ void fix_partial(const SpanParams &p, const SpanPiece it, int row, bool half,
+                                         int x, float ref, float inv, float *out) {
+  each_zeroed<D, CAUSAL>(p, it, row, half, x, ref, inv, [&](float w, const __nv_bfloat16 *v) {
+    for (int d = 0; d < D; ++d) out[d] += w * __bfloat162float(v[d]);
+  });
+}
+
+// They are added to a finished row that was left in its partial's place, `sum`, before it
+// is rounded, once.
+template <int D, bool CAUSAL>
+__device__ __noinline__ void fix_finished(const SpanParams &p, const SpanPiece it, int row, float ref,
+                                          float inv, float *sum, __nv_bfloat16 *out) {
+  each_zeroed<D, CAUSAL>(p, it, row, false, 0, ref, inv, [&](float w, const __nv_bfloat16 *v) {
+    for (int d = 0; d < D; ++d) sum[d] += w * __bfloat162float(v[d]);
+  });
+  for (int d = 0; d < D; ++d) out[d] = __float2bfloat16_rn(sum[d]);
 }
 
 // JOIN: units of up to 128 rows in one piece are finished here too, in one row tile.
@@ -758,9 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp_active) {
               __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(f.out) + orow * D;
               const float f0 = a0 * inv, f1 = a1 * inv;
+              const bool later = real && s_fix[k & 15] == k + 1 && !bad && !none;  // fix_finished rounds it
 #pragma unroll 1
               for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t raw[32], packed[16];
+                __syncwarp();
                 tc_ld32(tm_o + c0, raw);
                 if (joint) {
                   uint32_t more[32];
@@ -781,15 +793,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                       __floats2bfloat162_rn(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
                   packed[i] = bad || none ? 0u : *reinterpret_cast<const uint32_t *>(&h2);
                 }
-                if (real) {
+                if (later) {
+#pragma unroll
+                  for (int i = 0; i < 32; i += 8) store32(p.part_o + prow * D + c0 + i, raw, i, 1.f);
+                } else if (real) {
 #pragma unroll
                   for (int i = 0; i < 16; i += 4)
                     *reinterpret_cast<uint4 *>(dst + c0 + 2 * i) =
                         make_uint4(packed[i], packed[i + 1], packed[i + 2], packed[i + 3]);
                 }
               }
-              if (real && s_fix[k & 15] == k + 1 && !bad && !none)
-                fix_values<D, CAUSAL, true>(p, it, row, false, x, ref, inv, dst);
+              if (later) fix_finished<D, CAUSAL>(p, it, row, ref, inv, p.part_o + prow * D, dst);
             }
           }
           if (VOTES && real) p.row_lse[orow] = lse;
@@ -807,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               if (real && s_fix[k & 15] == k + 1 && !bad && !none)
-                fix_values<D, CAUSAL, false>(p, it, row0 + r, !two, x, ref, inv, p.part_o + prow * D);
+                fix_partial<D, CAUSAL>(p, it, row0 + r, !two, x, ref, inv, p.part_o + prow * D);
             }
           }
           if (real) p.part_lse[prow] = lse;
